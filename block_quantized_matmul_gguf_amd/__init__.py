@@ -49,6 +49,13 @@ SIGNATURES = {
     "qmatmul_run_group": (_int, [ctypes.POINTER(_p), _int, ctypes.POINTER(_p), _p, ctypes.POINTER(_p), _i64, _p]),
     "qmatmul_run_noalloc": (_int, [_int, _i64, _i64, _i64, _int, _p, _p, _p, _p]),
     "qmatmul_quantize_q4_k_search": (_int, [_p, _i64, _i64, _p, _p]),
+    "qmatmul_route_experts": (_int, [_p, _int, _i64, _i64, _p, _int, _int, _int, _int, _int, _int, ctypes.c_float, _p, _p, _p]),
+    "qmatmul_experts_workspace_bytes": (_i64, [_int, _int, _i64, _i64, _i64, _i64, _i64, _int]),
+    "qmatmul_experts_run": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _int, _int, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
+    "qmatmul_experts_glu": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _int, _int, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
+    "qmatmul_experts_combine": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
+    "qmatmul_w4_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64, _int]),
+    "qmatmul_w4_run": (_int, [_i64, _i64, _i64, _i64, _int, _int, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
     "qmatmul_check": (_int, [_int, _i64, _i64, _i64, _int]),
     "qmatmul_row_bytes": (_i64, [_int, _i64]),
     "qmatmul_block_sums_per_row": (_i64, [_int, _i64]),
@@ -356,3 +363,238 @@ def dequantize_weights(fmt: int, w, n: int, k: int, out=None, stream=None):
     _check(lib().qmatmul_dequantize_weights(fmt, _ptr(w), n, k, _ptr(out), _stream(stream)),
            "qmatmul_dequantize_weights")
     return out
+
+
+# ------------------------------------- mixture of experts, 4-bit groups ----
+#
+# These calls take no plan.  A call's scratch tensor and, unless the caller
+# gives them, its outputs come from torch's allocator on the stream of the
+# call, so calls may overlap on different streams and be captured in graphs
+# that run side by side.
+
+F32, F16, BF16 = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {"silu": 0, "gelu": 1}
+EXPERTS_RUN, EXPERTS_GLU, EXPERTS_COMBINE = 0, 1, 2
+_TYPES = None
+
+
+def _type_of(t, name):
+    global _TYPES
+    if _TYPES is None:
+        torch = _torch()
+        _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _tensor(t, dtype, dims, name, device=None):
+    """Checks a tensor argument: on the GPU (on ``device``), contiguous, of
+    ``dtype`` (None: a float type) and ``dims`` dimensions."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU, got {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if dims is not None and t.dim() not in (dims if isinstance(dims, tuple) else (dims,)):
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _out(t, shape, dtype, device, name):
+    """A given output, checked, or a new one on the current stream."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    _tensor(t, dtype, None, name, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _on_device(device, stream, body):
+    """Runs body(stream handle) with ``device`` current and ``stream`` (None:
+    that device's current stream) as the stream of allocations."""
+    torch = _torch()
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if stream is None and torch.cuda.current_device() == device.index:
+        return body(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return body(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
+
+
+def _scratch(nbytes, device, where):
+    """(pointer, bytes, the tensor that owns them) of a call's workspace."""
+    if nbytes < 0:
+        raise QmmError(EINVAL, where, last_error())
+    if nbytes == 0:
+        return None, 0, None
+    ws = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+    return ws.data_ptr(), nbytes, ws
+
+
+def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int | None = None,
+                  group_top: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """The experts of each row of logits (float32, float16 or bfloat16 [T, E]):
+    (ids int32 [T, top_k], weights float32 [T, top_k]).
+
+    Scores are softmax or sigmoid of the logits; the choice is by score + bias
+    (float32 [E]), within the ``top_groups`` best of ``groups`` groups of
+    neighbouring experts (a group's score: the sum of its ``group_top`` best
+    choices), ties to the lower index.  Experts with a -inf or NaN logit are
+    never chosen; slots left over have id -1 and weight 0.  Weights are the
+    scores, divided by their sum if ``renormalize``, times ``scale``."""
+    torch = _torch()
+    _tensor(logits, None, 2, "logits")
+    code = _type_of(logits, "logits")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    dev = logits.device
+    t, e = logits.shape
+    if bias is not None:
+        _tensor(bias, torch.float32, 1, "bias", dev)
+        if bias.shape[0] != e:
+            raise ValueError(f"bias must have shape ({e},), got {tuple(bias.shape)}")
+
+    def body(s):
+        i = _out(ids, (t, top_k), torch.int32, dev, "ids")
+        w = _out(weights, (t, top_k), torch.float32, dev, "weights")
+        _check(lib().qmatmul_route_experts(
+            logits.data_ptr(), code, t, e, None if bias is None else bias.data_ptr(), SCORES[score], top_k, groups,
+            groups if top_groups is None else top_groups, group_top, int(renormalize), scale, i.data_ptr(),
+            w.data_ptr(), s), "qmatmul_route_experts")
+        return i, w
+
+    if not 1 <= top_k <= min(64, e):
+        raise ValueError(f"top_k must be in 1..{min(64, e)}, got {top_k}")
+    return _on_device(dev, stream, body)
+
+
+def _expert_args(fmt, w, x, ids, x_dims, name):
+    """Checks what the experts' products share; (E, N, K, T, top_k, type)."""
+    torch = _torch()
+    _tensor(x, None, x_dims, name)
+    code = _type_of(x, name)
+    dev = x.device
+    _tensor(ids, torch.int32, 2, "ids", dev)
+    t, k = ids.shape
+    if x.shape[0] != t or (x.dim() == 3 and x.shape[1] != k):
+        raise ValueError(f"{name} {tuple(x.shape)} and ids {tuple(ids.shape)} differ in tokens or slots")
+    kk = x.shape[-1]
+    rb = row_bytes(fmt, kk)
+    if rb < 0:
+        raise ValueError(f"K={kk} is not a multiple of the block size of format {fmt}")
+    e = n = None
+    for t_w, w_name in w:
+        _tensor(t_w, torch.uint8, 3, w_name, dev)
+        if t_w.shape[2] != rb or (e is not None and (t_w.shape[0] != e or t_w.shape[1] != n)):
+            raise ValueError(f"{w_name} must be [E, N, {rb}] uint8, got {tuple(t_w.shape)}")
+        e, n = t_w.shape[0], t_w.shape[1]
+    return e, n, kk, t, k, code
+
+
+def experts_matmul(fmt: int, w, x, ids, y=None, stream=None):
+    """y[t, s] = x[t] . W[ids[t, s]]^T: the products of tokens with the weights
+    of their experts.  w: uint8 [E, N, row_bytes(fmt, K)] GGUF blocks; x:
+    float32, float16 or bfloat16 [T, K], or [T, top_k, K] with a row per slot;
+    ids: int32 [T, top_k], values outside 0..E-1 meaning no expert (zeros).
+    Returns [T, top_k, N] in x's type."""
+    e, n, kk, t, k, code = _expert_args(fmt, ((w, "w"),), x, ids, (2, 3), "x")
+    dev = x.device
+
+    def body(s):
+        out = _out(y, (t, k, n), x.dtype, dev, "y")
+        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_RUN, fmt, e, n, kk, t, k, code), dev,
+                                "qmatmul_experts_run")
+        _check(lib().qmatmul_experts_run(fmt, e, n, kk, t, k, code, int(x.dim() == 3), w.data_ptr(), x.data_ptr(),
+                                         ids.data_ptr(), out.data_ptr(), ws, nb, s), "qmatmul_experts_run")
+        return out
+
+    return _on_device(dev, stream, body)
+
+
+def experts_glu(fmt: int, w_gate, w_up, x, ids, act: str = "silu", h=None, stream=None):
+    """h[t, s] = act(x[t] . Wg^T) * (x[t] . Wu^T) with the gate and up weights
+    of expert ids[t, s] (both uint8 [E, N, row_bytes(fmt, K)]); act "silu" or
+    "gelu" (the tanh form).  Returns [T, top_k, N] in x's type."""
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    e, n, kk, t, k, code = _expert_args(fmt, ((w_gate, "w_gate"), (w_up, "w_up")), x, ids, 2, "x")
+    dev = x.device
+
+    def body(s):
+        out = _out(h, (t, k, n), x.dtype, dev, "h")
+        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_GLU, fmt, e, n, kk, t, k, code), dev,
+                                "qmatmul_experts_glu")
+        _check(lib().qmatmul_experts_glu(fmt, e, n, kk, t, k, code, ACTS[act], w_gate.data_ptr(), w_up.data_ptr(),
+                                         x.data_ptr(), ids.data_ptr(), out.data_ptr(), ws, nb, s), "qmatmul_experts_glu")
+        return out
+
+    return _on_device(dev, stream, body)
+
+
+def experts_combine(fmt: int, w, h, ids, weights, y=None, stream=None):
+    """y[t] = sum_s weights[t, s] * (h[t, s] . W[ids[t, s]]^T): the experts'
+    last product and the weighted sum over a token's slots.  h: [T, top_k, K],
+    weights: float32 [T, top_k].  Returns [T, N] in h's type."""
+    e, n, kk, t, k, code = _expert_args(fmt, ((w, "w"),), h, ids, 3, "h")
+    dev = h.device
+    _tensor(weights, _torch().float32, 2, "weights", dev)
+    if tuple(weights.shape) != (t, k):
+        raise ValueError(f"weights must have shape {(t, k)}, got {tuple(weights.shape)}")
+
+    def body(s):
+        out = _out(y, (t, n), h.dtype, dev, "y")
+        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_COMBINE, fmt, e, n, kk, t, k, code), dev,
+                                "qmatmul_experts_combine")
+        _check(lib().qmatmul_experts_combine(fmt, e, n, kk, t, k, code, w.data_ptr(), h.data_ptr(), ids.data_ptr(),
+                                             weights.data_ptr(), out.data_ptr(), ws, nb, s), "qmatmul_experts_combine")
+        return out
+
+    return _on_device(dev, stream, body)
+
+
+def w4_matmul(q, scales, x, zeros=None, y=None, stream=None):
+    """y = x . W^T with 4-bit weights in groups: W[n, k] = scales[n, k // G] *
+    (q[n, k] - z), z = zeros[n, k // G] or 8.  q: uint8 [N, K/2], element 2i in
+    the low nibble of byte i; scales: float32, float16 or bfloat16 [N, K/G],
+    G a multiple of 32; zeros: uint8 [N, K/G]; x: float32, float16 or bfloat16
+    [M, K].  Returns [M, N] in x's type."""
+    torch = _torch()
+    _tensor(x, None, 2, "x")
+    code = _type_of(x, "x")
+    dev = x.device
+    m, kk = x.shape
+    _tensor(q, torch.uint8, 2, "q", dev)
+    n = q.shape[0]
+    if q.shape[1] * 2 != kk:
+        raise ValueError(f"q must be [N, {kk // 2}] for K={kk}, got {tuple(q.shape)}")
+    _tensor(scales, None, 2, "scales", dev)
+    scode = _type_of(scales, "scales")
+    ng = scales.shape[1]
+    if scales.shape[0] != n or ng == 0 or kk % ng:
+        raise ValueError(f"scales must be [{n}, K / group], got {tuple(scales.shape)} for K={kk}")
+    if zeros is not None:
+        _tensor(zeros, torch.uint8, 2, "zeros", dev)
+        if zeros.shape != scales.shape:
+            raise ValueError(f"zeros must have the scales' shape {tuple(scales.shape)}, got {tuple(zeros.shape)}")
+    g = kk // ng
+
+    def body(s):
+        out = _out(y, (m, n), x.dtype, dev, "y")
+        ws, nb, keep = _scratch(lib().qmatmul_w4_workspace_bytes(n, kk, m, g, code), dev, "qmatmul_w4_run")
+        _check(lib().qmatmul_w4_run(n, kk, m, g, code, scode, q.data_ptr(), scales.data_ptr(),
+                                    None if zeros is None else zeros.data_ptr(), x.data_ptr(), out.data_ptr(), ws, nb, s),
+               "qmatmul_w4_run")
+        return out
+
+    return _on_device(dev, stream, body)

@@ -68,6 +68,13 @@ QMM_DEV void vm_wait_ahead(int ahead)
         else vm_wait_ahead<T, I - 1>(ahead);
     }
 }
+// Orders this wave's LDS writes before its later LDS reads by other lanes.
+QMM_DEV void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 QMM_DEV void lgkm_wait0() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // Byte count for a buffer resource, saturated to its 32-bit field.
 QMM_DEV uint32_t clamp_u32(int64_t v) { return v > 0xffffffffll ? 0xffffffffu : (uint32_t)v; }

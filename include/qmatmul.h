@@ -264,6 +264,112 @@ int qmatmul_run_traced(const qmm_plan* plan, const void* w_blocks, const float* 
 int qmatmul_run_block_sums(const qmm_plan* plan, const void* w_blocks, const float* x,
                            int32_t* sums, int64_t M, void* stream);
 
+/*
+ * Mixture-of-experts layers and 4-bit group weights, on activations of any of
+ * three types, for one token or a long prompt.  These calls need no plan and
+ * allocate nothing: where one needs scratch memory the caller passes it (ws,
+ * ws_bytes >= the matching *_workspace_bytes, 16-byte aligned; NULL when that
+ * is 0), so calls with scratch of their own may overlap on different streams
+ * and be captured in graphs that run side by side.  Nothing has to be kept in
+ * ws between calls, and only kernels are enqueued (no memset, no host copy, no
+ * synchronization); run a shape once eagerly before capturing it, as with
+ * qmatmul_run.
+ */
+
+/* activation and scale types */
+#define QMM_F32 0
+#define QMM_F16 1
+#define QMM_BF16 2
+
+/* scores of qmatmul_route_experts */
+#define QMM_SCORE_SOFTMAX 0
+#define QMM_SCORE_SIGMOID 1
+
+/* activations of qmatmul_experts_glu */
+#define QMM_ACT_SILU 0
+#define QMM_ACT_GELU 1 /* 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+
+/* products of qmatmul_experts_workspace_bytes */
+#define QMM_EXPERTS_RUN 0
+#define QMM_EXPERTS_GLU 1
+#define QMM_EXPERTS_COMBINE 2
+
+/*
+ * Choose experts: per row of logits [T x E] (type QMM_F32, QMM_F16 or
+ * QMM_BF16; any alignment of that type), the top_k experts and their weights.
+ *   s = softmax(logits) or sigmoid(logits); choice c = s + bias (bias: device
+ *   f32 [E] or NULL).  An expert whose logit or c is NaN or -inf is masked: it
+ *   has no score and is never chosen.
+ *   groups > 1 (a divisor of E, at most 64): experts form that many groups of
+ *   neighbours; a group's score is the sum of its group_top (1 or 2) largest
+ *   c; only the top_groups best groups (ties: the lower index) stay.
+ *   ids [T x top_k]: the remaining experts by descending c, ties to the lower
+ *   index; -1 in the slots for which no expert is left.
+ *   weights [T x top_k]: s of the chosen experts (without the bias), divided
+ *   by their sum if renormalize (0 if that sum is 0), times scale; 0 where the
+ *   id is -1.
+ * Scores, sums and comparisons are carried in 64 bits; weights are rounded
+ * once, to f32.  1 <= top_k <= 64, top_k <= E <= 1024, 0 <= T <= 2^24.  A +inf logit
+ * gives softmax its limit: the +inf experts share the whole weight.
+ */
+int qmatmul_route_experts(const void* logits, int type, int64_t T, int64_t E, const float* bias, int score,
+                          int top_k, int groups, int top_groups, int group_top, int renormalize, float scale,
+                          int32_t* ids, float* weights, void* stream);
+
+/*
+ * Products with the weights of chosen experts.  w holds E matrices one after
+ * another, each N x K in GGUF blocks as qmatmul_run takes them (E * N *
+ * qmatmul_row_bytes(format, K) bytes, 16-byte aligned); ids: device int32
+ * [T x top_k]; an id outside 0..E-1 means no expert; the same id may come
+ * twice in a row.  x, h and y have the type `type`; x and h 16-byte aligned.
+ * Activations are not quantized (mode (a)), products are summed in f32 and
+ * each output is rounded once, to `type`.
+ *
+ * qmatmul_experts_run: y[t][s] = x[t] . W[ids[t][s]]^T, y [T x top_k x N];
+ *   per_slot = 0: x [T x K], one row for a token's slots; per_slot = 1:
+ *   x [T x top_k x K].  Slots without an expert give zeros.
+ * qmatmul_experts_glu: h[t][s] = act(x[t] . Wg^T) * (x[t] . Wu^T) for the
+ *   slot's expert, h [T x top_k x N]; no expert: zeros.
+ * qmatmul_experts_combine: y[t] = sum_s weights[t][s] * (h[t][s] .
+ *   W[ids[t][s]]^T), y [T x N], h [T x top_k x K], weights device f32
+ *   [T x top_k]; slots without an expert add nothing, whatever their h and
+ *   weight hold.
+ *
+ * A row of x with an infinity or NaN makes the outputs computed from it
+ * non-finite (NaN where the sum holds inf - inf or 0 * inf) and no others.
+ * Limits: E <= 1024, top_k <= 64, T * top_k <= 2^24, and qmatmul_create's
+ * limits on N and K.  T == 0 enqueues nothing.  Outputs must not overlap
+ * inputs.
+ */
+int64_t qmatmul_experts_workspace_bytes(int product, int format, int64_t E, int64_t N, int64_t K, int64_t T,
+                                        int64_t top_k, int type); /* -1 if invalid */
+int qmatmul_experts_run(int format, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int type, int per_slot,
+                        const void* w, const void* x, const int32_t* ids, void* y, void* ws, size_t ws_bytes,
+                        void* stream);
+int qmatmul_experts_glu(int format, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int type, int act,
+                        const void* w_gate, const void* w_up, const void* x, const int32_t* ids, void* h, void* ws,
+                        size_t ws_bytes, void* stream);
+int qmatmul_experts_combine(int format, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int type,
+                            const void* w, const void* h, const int32_t* ids, const float* weights, void* y, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * y [M x N] = x [M x K] . W^T with W in 4-bit codes and one scale (and zero
+ * point) per group of `group` values of a row:
+ *   W[n][k] = scales[n][k / group] * (q[n][k] - z), z = zeros[n][k / group]
+ *   or, zeros == NULL, 8.
+ * q: device, N x K/2 bytes, element 2i in the low nibble of byte i and 2i + 1
+ * in its high nibble, 16-byte aligned.  scales: device [N x K/group] of
+ * scale_type (QMM_F32, QMM_F16 or QMM_BF16).  zeros: device uint8 [N x
+ * K/group], 0..15 (other values are used as they are).  group: a multiple of
+ * 32 that divides K.  x (16-byte aligned) and y have the type `type`.  M >= 0;
+ * M == 0 enqueues nothing.  Sums and rounding as qmatmul_experts_run.
+ */
+int64_t qmatmul_w4_workspace_bytes(int64_t N, int64_t K, int64_t M, int64_t group, int type); /* -1 if invalid */
+int qmatmul_w4_run(int64_t N, int64_t K, int64_t M, int64_t group, int type, int scale_type, const void* q,
+                   const void* scales, const uint8_t* zeros, const void* x, void* y, void* ws, size_t ws_bytes,
+                   void* stream);
+
 /* Host-only helpers (no HIP calls; safe without a GPU). */
 int qmatmul_check(int format, int64_t N, int64_t K, int64_t M_max, int mode); /* what create validates */
 int64_t qmatmul_row_bytes(int format, int64_t K);           /* bytes of one row of blocks, -1 if invalid */
