@@ -12,23 +12,62 @@ enum { FMT_W4 = 100 };  // 4-bit codes, scales and zero points in planes of thei
 enum { MOE_RUN = 0, MOE_GLU = 1, MOE_COMBINE = 2 };
 enum { TYPE_F32 = 0, TYPE_F16 = 1, TYPE_BF16 = 2 };
 
+// A tile of pairs on one expert (e < 0: pairs without an expert, count <= 0:
+// no tile): order[start .. start + count - 1].
+struct MoeTile {
+    int e, start, count, pad;
+};
+
 // One call.  P = T * top_k pairs of a token and a slot; pair p has the
 // activations of row p (per_slot) or p / top_k and the weights of expert
 // ids[p] (ids == nullptr: one matrix, every pair on it).
 struct MoeArgs {
     int fmt, op, type, act, per_slot;
-    int64_t E, N, K, T;
-    int top_k;
+    int E, top_k;
+    int64_t N, K, T;
     int64_t row_bytes;        // bytes of a weight row (W4: of its codes)
     const uint8_t* w0;        // weights (GLU: gate)
     const uint8_t* w1;        // GLU: up
     const void* scales;       // W4
     const uint8_t* zeros;     // W4, or null
-    int group, scale_type;    // W4
+    int scale_type;           // W4
+    int group_blocks;         // W4: 32-value blocks per group,
+    uint32_t group_magic;     // and ceil(2^32 / group_blocks), 0 when that is 1
     const void* x;
     const int32_t* ids;
     const float* weights;     // COMBINE
-    void* y;
+    void* y;                  // outputs, or the f32 products a combine sums later
+    int y_type;
+    // workspace of the paths that sort the pairs
+    int32_t* order;           // [P]
+    MoeTile* tiles;           // [max_tiles]
+    int max_tiles;
+    // prepared activations (tile path): f16 planes in operand order, the hi
+    // parts and for f32 the lo parts, [rows][Kp] each; 1/scale per row; Q4_K:
+    // hi and lo of the sub-block sums / 32, [rows][K/256][16]
+    _Float16* xp;
+    int64_t x_rows, Kp;
+    float* xinv;
+    _Float16* xsum;
 };
+
+// Streaming kernel: up to 16 pairs of an expert per workgroup, weights straight
+// from memory to the matrix cores.  one: a workgroup has one pair (or, for a
+// combine, one token and its slots); waves: waves along K per workgroup.
+hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s);
+// Tile kernel: mt * 16 pairs of an expert against 128 weight rows (GLU: 64 of
+// each matrix) per workgroup, prepared activations through LDS.
+hipError_t launch_tile(const MoeArgs& a, int mt, hipStream_t s);
+
+#define QMM_MOE_DECLARE(F)                                                              \
+    hipError_t launch_stream_##F(const MoeArgs& a, bool one, int waves, hipStream_t s); \
+    hipError_t launch_tile_##F(const MoeArgs& a, int mt, hipStream_t s);
+QMM_MOE_DECLARE(q8_0)
+QMM_MOE_DECLARE(q4_0)
+QMM_MOE_DECLARE(q5_0)
+QMM_MOE_DECLARE(q4_k)
+QMM_MOE_DECLARE(q6_k)
+QMM_MOE_DECLARE(w4)
+#undef QMM_MOE_DECLARE
 
 }  // namespace qmm

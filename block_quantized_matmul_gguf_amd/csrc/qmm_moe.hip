@@ -1,130 +1,161 @@
 // qmm_moe.hip -- the experts' products and the 4-bit group products: argument
-// checks and the kernel that computes them.
-//
-// One wave per output: its lanes take the 32-value blocks of the weight row in
-// turn, decode them to f32 and multiply them with the activations.
+// checks, the choice of the kernel, and the kernels around the products (the
+// sort of the pairs by expert, the weighted sum over a token's slots).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "../../include/qmatmul.h"
-#include "qmm_device.h"
-#include "qmm_moe.h"
+#include "qmm_moe_unit.h"
 
 namespace qmm {
 namespace {
 
-QMM_DEV float load_act(const void* p, int type, int64_t i)
-{
-    if (type == TYPE_F32) return ((const float*)p)[i];
-    if (type == TYPE_F16) return (float)((const _Float16*)p)[i];
-    return __builtin_bit_cast(float, (uint32_t)((const uint16_t*)p)[i] << 16);
-}
-QMM_DEV void store_act(void* p, int type, int64_t i, float v)
-{
-    if (type == TYPE_F32) ((float*)p)[i] = v;
-    else if (type == TYPE_F16) ((_Float16*)p)[i] = (_Float16)v;
-    else ((__bf16*)p)[i] = (__bf16)v;
-}
-QMM_DEV float half_at(const uint8_t* p) { return (float)*(const _Float16*)p; }
+constexpr int SORT_THREADS = 1024;
+constexpr int MAX_E = 1024;
 
-// 32-value block b of row n of matrix w, as f32.
-QMM_DEV void decode32(const MoeArgs& a, const uint8_t* w, int64_t n, int b, float v[32])
+// Sorts the pairs by expert: order[] holds them expert by expert (those
+// without one last), tiles[] the runs of up to tm pairs of one expert.  One
+// workgroup: a histogram, its prefix sums and a scatter in LDS.  The order of
+// an expert's pairs among themselves comes from atomics and may differ from
+// run to run; every output depends on its own pair alone.
+__global__ __launch_bounds__(SORT_THREADS) void moe_sort(MoeArgs a, int tm)
 {
-    const uint8_t* row = w + n * a.row_bytes;
-    if (a.fmt == FMT_Q8_0) {
-        const uint8_t* p = row + b * 34;
-        const float d = half_at(p);
-        for (int j = 0; j < 32; ++j) v[j] = d * (float)(int8_t)p[2 + j];
-    } else if (a.fmt == FMT_Q4_0) {
-        const uint8_t* p = row + b * 18;
-        const float d = half_at(p);
-        for (int j = 0; j < 16; ++j) {
-            v[j] = d * (float)((p[2 + j] & 15) - 8);
-            v[j + 16] = d * (float)((p[2 + j] >> 4) - 8);
+    __shared__ int cnt[MAX_E + 1], off[MAX_E + 1], tile0[MAX_E + 2];
+    const int tid = (int)threadIdx.x, E = a.E, B = E + 1, P = (int)(a.T * a.top_k);
+    for (int b = tid; b < B; b += SORT_THREADS) cnt[b] = 0;
+    __syncthreads();
+    for (int p = tid; p < P; p += SORT_THREADS) {
+        const int e = a.ids[p];
+        atomicAdd(&cnt[e >= 0 && e < E ? e : E], 1);
+    }
+    __syncthreads();
+    if (tid < 64) {
+        const int per = (B + 63) / 64, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+        int c = 0, t = 0;
+        for (int b = b0; b < b1; ++b) {
+            c += cnt[b];
+            t += (cnt[b] + tm - 1) / tm;
         }
-    } else if (a.fmt == FMT_Q5_0) {
-        const uint8_t* p = row + b * 22;
-        const float d = half_at(p);
-        const uint32_t h = p[2] | (p[3] << 8) | (p[4] << 16) | ((uint32_t)p[5] << 24);
-        for (int j = 0; j < 16; ++j) {
-            v[j] = d * (float)(int)(((p[6 + j] & 15) | (((h >> j) & 1) << 4)) - 16);
-            v[j + 16] = d * (float)(int)(((p[6 + j] >> 4) | (((h >> (j + 16)) & 1) << 4)) - 16);
+        int ci = c, ti = t;
+        for (int d = 1; d < 64; d *= 2) {
+            const int cu = __shfl_up(ci, d), tu = __shfl_up(ti, d);
+            if (tid >= d) {
+                ci += cu;
+                ti += tu;
+            }
         }
-    } else if (a.fmt == FMT_Q4_K) {
-        const uint8_t* p = row + (b / 8) * 144;
-        const uint32_t* s = (const uint32_t*)(p + 4);
-        int sc, mn;
-        q4k_scale_min(s[0], s[1], s[2], b % 8, sc, mn);
-        const float d = half_at(p) * (float)sc, m = half_at(p + 2) * (float)mn;
-        const int sh = (b & 1) * 4;
-        for (int j = 0; j < 32; ++j) v[j] = d * (float)((p[16 + (b % 8) / 2 * 32 + j] >> sh) & 15) - m;
-    } else if (a.fmt == FMT_Q6_K) {
-        const uint8_t* p = row + (b / 8) * 210;
-        const int h = (b % 8) / 4, t = b % 4;
-        const float d = half_at(p + 208);
-        for (int j = 0; j < 32; ++j) {
-            const int lo = (p[64 * h + 32 * (t & 1) + j] >> (4 * (t >> 1))) & 15;
-            const int hi = (p[128 + 32 * h + j] >> (2 * t)) & 3;
-            v[j] = d * (float)(int8_t)p[192 + 8 * h + 2 * t + j / 16] * (float)((lo | (hi << 4)) - 32);
+        c = ci - c;
+        t = ti - t;
+        for (int b = b0; b < b1; ++b) {
+            off[b] = c;
+            tile0[b] = t;
+            c += cnt[b];
+            t += (cnt[b] + tm - 1) / tm;
         }
-    } else {
-        const int64_t g = n * (a.K / a.group) + b * 32 / a.group;
-        const float d = load_act(a.scales, a.scale_type, g);
-        const int z = a.zeros ? a.zeros[g] : 8;
-        for (int j = 0; j < 16; ++j) {
-            const int q = row[16 * b + j];
-            v[2 * j] = d * (float)((q & 15) - z);
-            v[2 * j + 1] = d * (float)((q >> 4) - z);
+        if (tid == 63) tile0[B] = ti;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.max_tiles; i += SORT_THREADS) {
+        MoeTile t = {-1, 0, 0, 0};
+        if (i < tile0[B]) {
+            int lo = 0, hi = B;  // the last bucket whose first tile is <= i
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (tile0[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            const int k = (i - tile0[lo]) * tm;
+            t.e = lo < E ? lo : -1;
+            t.start = off[lo] + k;
+            t.count = min(tm, cnt[lo] - k);
         }
+        a.tiles[i] = t;
+    }
+    __syncthreads();
+    for (int p = tid; p < P; p += SORT_THREADS) {
+        const int e = a.ids[p];
+        a.order[atomicAdd(&off[e >= 0 && e < E ? e : E], 1)] = p;
     }
 }
 
-// Dot product of row n of w with activation row r, in every lane.
-QMM_DEV float dot(const MoeArgs& a, const uint8_t* w, int64_t n, int64_t r)
+// y[t][n] = sum over the slots with an expert of weights[t][s] * prod[t][s][n]
+__global__ __launch_bounds__(256) void moe_combine(MoeArgs a, const float* prod)
 {
-    float s = 0.0f;
-    for (int b = (int)__lane_id(); b < a.K / 32; b += 64) {
-        float v[32];
-        decode32(a, w, n, b, v);
-        for (int j = 0; j < 32; ++j) s = fmaf(v[j], load_act(a.x, a.type, r * a.K + b * 32 + j), s);
-    }
-    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-    return s;
-}
-
-QMM_DEV float activate(float v, int act)
-{
-    if (act == QMM_ACT_SILU) return v / (1.0f + expf(-v));
-    const float t = 0.7978845608028654f * (v + 0.044715f * v * v * v);
-    return v / (1.0f + expf(-2.0f * t));
-}
-
-__global__ __launch_bounds__(256) void moe_simple(MoeArgs a)
-{
-    const int64_t outs = (a.op == MOE_COMBINE ? a.T : a.T * a.top_k) * a.N;
-    const int64_t o = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (o >= outs) return;
-    const int64_t n = o % a.N, p = o / a.N, stride = a.N * a.row_bytes;
-    float r = 0.0f;
-    if (a.op == MOE_COMBINE) {
+    const int64_t outs = a.T * a.N, stride = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < outs; i += stride) {
+        const int64_t t = i / a.N, n = i - t * a.N;
+        float v = 0.0f;
         for (int s = 0; s < a.top_k; ++s) {
-            const int e = a.ids[p * a.top_k + s];
-            if (e >= 0 && e < a.E) r = fmaf(a.weights[p * a.top_k + s], dot(a, a.w0 + e * stride, n, p * a.top_k + s), r);
+            const int64_t p = t * a.top_k + s;
+            const int e = a.ids[p];
+            if (e >= 0 && e < a.E) v = fmaf(a.weights[p], prod[p * a.N + n], v);
         }
-    } else {
-        const int e = a.ids ? a.ids[p] : 0;
-        if (e >= 0 && e < a.E) {
-            const int64_t src = a.per_slot ? p : p / a.top_k;
-            r = dot(a, a.w0 + e * stride, n, src);
-            if (a.op == MOE_GLU) r = activate(r, a.act) * dot(a, a.w1 + e * stride, n, src);
-        }
+        store_out(a.y, a.y_type, i, v);
     }
-    if (__lane_id() == 0) store_act(a.y, a.type, o, r);
 }
 
-hipError_t launch_moe(const MoeArgs& a, hipStream_t s)
+enum { PATH_ONE, PATH_SCAN, PATH_STREAM };
+
+// What a call runs and what it needs of the workspace.
+struct MoePlan {
+    int path, waves;
+    bool sort;
+    int tm, max_tiles;
+    size_t order, tiles, products, bytes;  // offsets
+};
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+MoePlan plan_of(const MoeArgs& a)
 {
-    const int64_t outs = (a.op == MOE_COMBINE ? a.T : a.T * a.top_k) * a.N;
-    moe_simple<<<dim3((unsigned)((outs + 3) / 4)), dim3(256), 0, s>>>(a);
+    MoePlan p = {};
+    const int64_t P = a.T * a.top_k;
+    const bool dense = a.fmt == FMT_W4;
+    p.path = dense ? (a.T == 1 ? PATH_ONE : PATH_STREAM) : a.T == 1 ? PATH_ONE : P <= 64 ? PATH_SCAN : PATH_STREAM;
+    p.waves = 4;
+    p.sort = !dense && p.path == PATH_STREAM;
+    p.tm = 16;
+    size_t off = 0;
+    if (p.sort) {
+        p.max_tiles = (int)(P / p.tm + std::min<int64_t>(a.E + 1, P));
+        p.order = off;
+        off += align256((size_t)P * 4);
+        p.tiles = off;
+        off += align256((size_t)p.max_tiles * sizeof(MoeTile));
+    }
+    if (a.op == MOE_COMBINE && p.path != PATH_ONE) {
+        p.products = off;
+        off += align256((size_t)P * (size_t)a.N * 4);
+    }
+    p.bytes = off;
+    return p;
+}
+
+hipError_t launch_moe(const MoeArgs& call, const MoePlan& p, char* ws, hipStream_t s)
+{
+    MoeArgs a = call;
+    a.y_type = a.type;
+    if (p.sort) {
+        a.order = (int32_t*)(ws + p.order);
+        a.tiles = (MoeTile*)(ws + p.tiles);
+        a.max_tiles = p.max_tiles;
+        moe_sort<<<dim3(1), dim3(SORT_THREADS), 0, s>>>(a, p.tm);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const bool summed = a.op == MOE_COMBINE && p.path != PATH_ONE;
+    float* products = (float*)(ws + p.products);
+    if (summed) {
+        a.op = MOE_RUN;
+        a.y = products;
+        a.y_type = TYPE_F32;
+    }
+    hipError_t e = launch_stream(a, p.path == PATH_ONE, p.waves, s);
+    if (e != hipSuccess || !summed) return e;
+    a = call;
+    a.y_type = a.type;
+    moe_combine<<<dim3((unsigned)std::min<int64_t>((a.T * a.N + 255) / 256, 1 << 16)), dim3(256), 0, s>>>(a, products);
     return hipGetLastError();
 }
 
@@ -162,7 +193,7 @@ MoeArgs experts_args(int op, int format, int64_t E, int64_t N, int64_t K, int64_
     a.fmt = format;
     a.op = op;
     a.type = type;
-    a.E = E;
+    a.E = (int)E;
     a.N = N;
     a.K = K;
     a.T = T;
@@ -171,19 +202,32 @@ MoeArgs experts_args(int op, int format, int64_t E, int64_t N, int64_t K, int64_
     return a;
 }
 
-int64_t workspace_bytes(const MoeArgs& a) { return 0; }
+int64_t workspace_bytes(const MoeArgs& a) { return a.T == 0 ? 0 : (int64_t)plan_of(a).bytes; }
 
 int run(const MoeArgs& a, void* ws, size_t ws_bytes, void* stream)
 {
-    const int64_t need = workspace_bytes(a);
-    if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < (size_t)need)) return bad("ws must be 16-byte aligned and hold the call's workspace bytes");
-    const hipError_t e = launch_moe(a, (hipStream_t)stream);
+    const MoePlan p = plan_of(a);
+    if (p.bytes > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < p.bytes)) return bad("ws must be 16-byte aligned and hold the call's workspace bytes");
+    const hipError_t e = launch_moe(a, p, (char*)ws, (hipStream_t)stream);
     return e == hipSuccess ? QMM_OK : set_error(QMM_EHIP, hipGetErrorString(e));
 }
 
 bool off16(const void* p) { return (uintptr_t)p % 16 != 0; }
 
 }  // namespace
+
+hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s)
+{
+    switch (a.fmt) {
+    case FMT_Q8_0: return launch_stream_q8_0(a, one, waves, s);
+    case FMT_Q4_0: return launch_stream_q4_0(a, one, waves, s);
+    case FMT_Q5_0: return launch_stream_q5_0(a, one, waves, s);
+    case FMT_Q4_K: return launch_stream_q4_k(a, one, waves, s);
+    case FMT_Q6_K: return launch_stream_q6_k(a, one, waves, s);
+    default: return launch_stream_w4(a, one, waves, s);
+    }
+}
+
 }  // namespace qmm
 
 using namespace qmm;
@@ -266,7 +310,8 @@ static MoeArgs w4_args(int64_t N, int64_t K, int64_t M, int64_t group, int type)
     a.T = M;
     a.top_k = 1;
     a.row_bytes = K / 2;
-    a.group = (int)group;
+    a.group_blocks = (int)(group / 32);
+    a.group_magic = group == 32 ? 0 : (uint32_t)(((1ull << 32) + (uint64_t)(group / 32) - 1) / (uint64_t)(group / 32));
     return a;
 }
 

@@ -1,0 +1,556 @@
+// qmm_moe_unit.h -- block-quantized weight rows as matrix-core operands.
+//
+// v_mfma_f32_16x16x32_f16 multiplies 16 rows of activations (A) with 16 rows of
+// weights (B): lane (r = lane & 15, g = lane >> 4) holds eight k values of
+// activation row r and eight of weight row r, and on return the sums of weight
+// row r with activation rows 4g .. 4g+3.  So the lane that decodes a weight
+// row also owns that row's sums, and a block's scale is a per-lane factor.
+//
+// Which eight k values a lane group takes is free as long as A and B agree.
+// Weights enter as exact integers in f16 (the scales multiply sums, in f32),
+// so products are exact and sums are f32.
+//
+// A unit is what a wave loads of 16 rows at a time, each lane whole 16-byte
+// words (the blocks' two-byte alignment is the hardware's to deal with):
+//   32-value formats: four blocks, lane group g loading block g whole; a 4 x 4
+//     transposition across lane groups (v_permlane32_swap, v_permlane16_swap)
+//     then gives every group a quarter of each block, so one product covers
+//     one block and one scale;
+//   Q4_K and Q6_K: a super-block, lane group g loading two (four) sub-blocks
+//     whole; the sub-block scales are small integers and go into the operand
+//     (Q4_K: sc q <= 945; Q6_K: (16 s1 + s0) (q - 32) as the two exact parts
+//     16 s1 (q - 32) and s0 (q - 32)), so products may mix sub-blocks and the
+//     super-block's scale multiplies their sum.
+#pragma once
+#include "qmm_device.h"
+#include "qmm_moe.h"
+
+namespace qmm {
+
+// dw with the upper half-wave of a and the lower half-wave of b exchanged
+QMM_DEV void swap32(uint32_t& a, uint32_t& b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+// odd 16-lane rows of a exchanged with even rows of b
+QMM_DEV void swap16(uint32_t& a, uint32_t& b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+// c[j] of lane group g  <->  c[g] of lane group j
+QMM_DEV void transpose4(uint32_t c[4])
+{
+    swap32(c[0], c[2]);
+    swap32(c[1], c[3]);
+    swap16(c[0], c[1]);
+    swap16(c[2], c[3]);
+}
+// v of lane groups 0..3, in every lane
+QMM_DEV void gather4(uint32_t v, uint32_t o[4])
+{
+    uint32_t a = v, b = v;
+    swap32(a, b);
+    o[0] = a;
+    o[1] = a;
+    o[2] = b;
+    o[3] = b;
+    swap16(o[0], o[1]);
+    swap16(o[2], o[3]);
+}
+QMM_DEV float f32_of(uint32_t v) { return __builtin_bit_cast(float, v); }
+QMM_DEV uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
+QMM_DEV half2_t half2_of(uint32_t v) { return __builtin_bit_cast(half2_t, v); }
+
+// loads at any byte alignment
+QMM_DEV void load16(const uint8_t* p, uint32_t c[4])
+{
+    u32x4_t v;
+    __builtin_memcpy(&v, p, 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = v[i];
+}
+QMM_DEV uint32_t load4(const uint8_t* p)
+{
+    uint32_t v;
+    __builtin_memcpy(&v, p, 4);
+    return v;
+}
+QMM_DEV uint32_t load2(const uint8_t* p)
+{
+    uint16_t v;
+    __builtin_memcpy(&v, p, 2);
+    return v;
+}
+
+QMM_DEV half8_t join8(half2_t a, half2_t b, half2_t c, half2_t d)
+{
+    half8_t r;
+    r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+    r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+    return r;
+}
+
+// A weight matrix as a wave reads it: what is common to its rows.
+struct MoeMatrix {
+    const uint8_t* w;
+    int64_t row_bytes;
+    int blocks;  // 32-value blocks of a row
+    // W4
+    const void* scales;
+    const uint8_t* zeros;
+    int scale_type, groups, group_blocks;
+    uint32_t group_magic;
+};
+
+// Per format:
+//   UNIT   values of a unit;  HALVES  steps of 128 values in it
+//   CHAIN  products of a step share one scale (and so one accumulator)
+//   PARTS  operands per product;  MINS  Q4_K's minima
+//   o0, o1, slot: the k values of lane group g in product j of step h are
+//     o0 .. o0+3 and o1 .. o1+3; slot i of the operand holds number slot(i)
+template <int FMT>
+struct Unit;
+
+// ---------------------------------------------------- four 32-value blocks
+
+template <int FMT>
+struct Unit32 {
+    static constexpr int UNIT = 128, HALVES = 1, PARTS = 1;
+    static constexpr bool CHAIN = false, MINS = false;
+    static QMM_DEV int o0(int, int j, int g) { return 32 * j + 4 * g; }
+    static QMM_DEV int o1(int, int j, int g) { return 32 * j + 16 + 4 * g; }
+    // position of value k of a unit in operand order [step][j][g][slot]
+    static QMM_DEV int place(int k)
+    {
+        const int e = k & 31, i = (e & 3) | ((e & 16) >> 2);  // number within the operand's eight
+        return (((k >> 5) * 4 + ((e >> 2) & 3)) << 3) | (FMT == FMT_Q8_0 ? i : nib_perm(i));
+    }
+    float s[4];  // scales of the four blocks
+    QMM_DEV float scale(int j) const { return s[j]; }
+    QMM_DEV void gather_scales(float own)
+    {
+        uint32_t o[4];
+        gather4(bits_of(own), o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = f32_of(o[j]);
+    }
+};
+
+// four nibbles of v (bits 0..3 of its bytes after the shift) in the order 0,2
+// (first pair) and 1,3, as 1024 + q
+QMM_DEV uint32_t nib_pair(uint32_t v, int shift) { return ((v >> shift) & 0x000f000fu) | 0x64006400u; }
+
+template <>
+struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
+    uint32_t c[8], d;
+    static QMM_DEV int slot(int i) { return i; }
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    {
+        const int b = 4 * u + g;
+        const uint8_t* p = m.w + n * m.row_bytes + b * 34;
+        d = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = 0;
+        if (b < m.blocks) {
+            load16(p + 2, c);
+            load16(p + 18, c + 4);
+            d = load2(p);
+        }
+    }
+    QMM_DEV void unpack(int)
+    {
+        transpose4(c);
+        transpose4(c + 4);
+        gather_scales(f16lo(d));
+    }
+    QMM_DEV half8_t operand(int, int j, int) const
+    {
+        uint32_t p[4];
+        i8x4_to_f16(c[j], p[0], p[1]);
+        i8x4_to_f16(c[4 + j], p[2], p[3]);
+        return join8(half2_of(p[0]), half2_of(p[1]), half2_of(p[2]), half2_of(p[3]));
+    }
+};
+
+template <>
+struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
+    uint32_t c[4], d;
+    static QMM_DEV int slot(int i) { return nib_perm(i); }
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    {
+        const int b = 4 * u + g;
+        const uint8_t* p = m.w + n * m.row_bytes + b * 18;
+        d = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = 0;
+        if (b < m.blocks) {
+            load16(p + 2, c);
+            d = load2(p);
+        }
+    }
+    QMM_DEV void unpack(int)
+    {
+        transpose4(c);
+        gather_scales(f16lo(d));
+    }
+    QMM_DEV half8_t operand(int, int j, int) const
+    {
+        const half2_t bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+        const uint32_t v = c[j];
+        return join8(half2_of(nib_pair(v, 0)) + bias, half2_of(nib_pair(v, 8)) + bias, half2_of(nib_pair(v, 4)) + bias,
+                     half2_of(nib_pair(v, 12)) + bias);
+    }
+};
+
+template <>
+struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
+    uint32_t c[4], d, qh, h[4];
+    static QMM_DEV int slot(int i) { return nib_perm(i); }
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    {
+        const int b = 4 * u + g;
+        const uint8_t* p = m.w + n * m.row_bytes + b * 22;
+        d = 0;
+        qh = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = 0;
+        if (b < m.blocks) {
+            load16(p + 6, c);
+            qh = load4(p + 2);
+            d = load2(p);
+        }
+    }
+    // h[j]: the fifth bits of this lane group's values of block j, the first
+    // four in bits 0..3, the last four in bits 16..19
+    QMM_DEV void unpack(int g)
+    {
+        transpose4(c);
+        gather_scales(f16lo(d));
+        gather4(qh, h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = (h[j] >> (4 * g)) & 0x000f000fu;
+    }
+    QMM_DEV half8_t operand(int, int j, int) const
+    {
+        const half2_t bias = {(_Float16)-1040.0f, (_Float16)-1040.0f};
+        const uint32_t v = c[j], lo = h[j] & 15u, hi = h[j] >> 16;
+        // bits 0 and 2 of a group of four, to bits 4 and 20
+        const uint32_t k = (1u << 4) | (1u << 18), m = 0x00100010u;
+        const uint32_t p0 = nib_pair(v, 0) | (__umul24(lo, k) & m), p1 = nib_pair(v, 8) | (__umul24(lo >> 1, k) & m);
+        const uint32_t p2 = nib_pair(v, 4) | (__umul24(hi, k) & m), p3 = nib_pair(v, 12) | (__umul24(hi >> 1, k) & m);
+        return join8(half2_of(p0) + bias, half2_of(p1) + bias, half2_of(p2) + bias, half2_of(p3) + bias);
+    }
+};
+
+template <>
+struct Unit<FMT_W4> : Unit32<FMT_W4> {
+    uint32_t c[4], d, z;
+    half2_t bias[4];
+    static QMM_DEV int o0(int, int j, int g) { return 32 * j + 8 * g; }
+    static QMM_DEV int o1(int, int j, int g) { return 32 * j + 8 * g + 4; }
+    static QMM_DEV int slot(int i) { return (i >> 1) | ((i & 1) << 2); }
+    static QMM_DEV int place(int k) { return (k & ~7) | ((k & 3) << 1) | ((k >> 2) & 1); }
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    {
+        const int b = 4 * u + g;
+        d = 0;
+        z = 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = 0;
+        if (b < m.blocks) {
+            const u32x4_t v = *(const u32x4_t*)(m.w + n * m.row_bytes + 16 * b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = v[i];
+            const int64_t at = n * m.groups + (m.group_magic ? (int)__umulhi((uint32_t)b, m.group_magic) : b);
+            if (m.scale_type == TYPE_F32) d = ((const uint32_t*)m.scales)[at];
+            else if (m.scale_type == TYPE_F16) d = bits_of((float)((const _Float16*)m.scales)[at]);
+            else d = (uint32_t)((const uint16_t*)m.scales)[at] << 16;
+            if (m.zeros) z = m.zeros[at];
+        }
+    }
+    QMM_DEV void unpack(int)
+    {
+        transpose4(c);
+        gather_scales(f32_of(d));
+        // -(1024 + z) in both halves
+        uint32_t o[4];
+        gather4((0xe400u | z) * 0x00010001u, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bias[j] = half2_of(o[j]);
+    }
+    QMM_DEV half8_t operand(int, int j, int) const
+    {
+        const uint32_t v = c[j];
+        return join8(half2_of(nib_pair(v, 0)) + bias[j], half2_of(nib_pair(v, 4)) + bias[j], half2_of(nib_pair(v, 8)) + bias[j],
+                     half2_of(nib_pair(v, 12)) + bias[j]);
+    }
+};
+
+// ------------------------------------------------------- a super-block
+
+template <>
+struct Unit<FMT_Q4_K> {
+    static constexpr int UNIT = 256, HALVES = 2, PARTS = 1;
+    static constexpr bool CHAIN = true, MINS = true;
+    // lane group g: sub-blocks 2g (low nibbles, step 0) and 2g + 1 (high, step 1)
+    static QMM_DEV int o0(int h, int j, int g) { return 64 * g + 32 * h + 8 * j; }
+    static QMM_DEV int o1(int h, int j, int g) { return o0(h, j, g) + 4; }
+    static QMM_DEV int slot(int i) { return nib_perm(i); }
+    static QMM_DEV int place(int k) { return ((((k >> 5) & 1) * 4 + ((k >> 3) & 3)) * 4 + (k >> 6)) * 8 + nib_perm(k & 7); }
+    uint32_t c[8], hd[4];
+    half2_t sc[2], off[2];  // sub-block scale, -1024 * scale
+    uint32_t mn;            // the two minima, one per byte
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    {
+        const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 144;
+        const u32x4_t a = *(const u32x4_t*)p;
+        const u32x4_t v0 = *(const u32x4_t*)(p + 16 + 32 * g), v1 = *(const u32x4_t*)(p + 32 + 32 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hd[i] = a[i];
+            c[i] = v0[i];
+            c[4 + i] = v1[i];
+        }
+    }
+    QMM_DEV void unpack(int g)
+    {
+        const int sh = 16 * (g & 1);
+        const uint32_t a = hd[1] >> sh, b = hd[2] >> sh, e = hd[3] >> sh;
+        const uint32_t s2 = g < 2 ? a & 0x3f3fu : (e & 0x0f0fu) | ((a >> 2) & 0x3030u);
+        mn = g < 2 ? b & 0x3f3fu : ((e >> 4) & 0x0f0fu) | ((b >> 2) & 0x3030u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const _Float16 f = (_Float16)(float)((s2 >> (8 * i)) & 0xffu);
+            sc[i] = half2_t{f, f};
+            off[i] = sc[i] * half2_t{(_Float16)-1024.0f, (_Float16)-1024.0f};
+        }
+    }
+    QMM_DEV half8_t operand(int h, int j, int) const
+    {
+        const uint32_t v = c[2 * j] >> (4 * h), w = c[2 * j + 1] >> (4 * h);
+        return join8(__builtin_elementwise_fma(half2_of(nib_pair(v, 0)), sc[h], off[h]),
+                     __builtin_elementwise_fma(half2_of(nib_pair(v, 8)), sc[h], off[h]),
+                     __builtin_elementwise_fma(half2_of(nib_pair(w, 0)), sc[h], off[h]),
+                     __builtin_elementwise_fma(half2_of(nib_pair(w, 8)), sc[h], off[h]));
+    }
+    QMM_DEV float scale(int) const { return f16lo(hd[0]); }
+    // against {S_2g hi, S_2g+1 hi, S_2g lo, S_2g+1 lo, 0, ..}, S the sub-block sums / 32
+    QMM_DEV half8_t mins() const
+    {
+        const _Float16 a = (_Float16)(float)(mn & 0xffu), b = (_Float16)(float)(mn >> 8), z = (_Float16)0.0f;
+        return join8(half2_t{a, b}, half2_t{a, b}, half2_t{z, z}, half2_t{z, z});
+    }
+    QMM_DEV float mins_scale() const { return -32.0f * f16hi(hd[0]); }
+};
+
+template <>
+struct Unit<FMT_Q6_K> {
+    static constexpr int UNIT = 256, HALVES = 2, PARTS = 2;
+    static constexpr bool CHAIN = true, MINS = false;
+    // lane group g: of half g >> 1 of the super-block, in each of its four
+    // 32-value quarters the 16 values at 16 (g & 1); product 4h + j takes the
+    // first or second eight of quarter (4h + j) / 2
+    static QMM_DEV int o0(int h, int j, int g)
+    {
+        const int jj = 4 * h + j;
+        return 128 * (g >> 1) + 32 * (jj >> 1) + 16 * (g & 1) + 8 * (jj & 1);
+    }
+    static QMM_DEV int o1(int h, int j, int g) { return o0(h, j, g) + 4; }
+    static QMM_DEV int slot(int i) { return i; }
+    static QMM_DEV int place(int k)
+    {
+        const int jj = 2 * ((k >> 5) & 3) + ((k >> 3) & 1), g = 2 * (k >> 7) + ((k >> 4) & 1);
+        return (jj * 4 + g) * 8 + (k & 7);
+    }
+    uint32_t l0[4], l1[4], qh[4], s0, s1, d;
+    half2_t hi[4], lo[4];  // 16 s1 and s0 of the four quarters' scales
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    {
+        const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 210;
+        const uint8_t* q = p + 64 * (g >> 1) + 16 * (g & 1);
+        load16(q, l0);
+        load16(q + 32, l1);
+        load16(p + 128 + 32 * (g >> 1) + 16 * (g & 1), qh);
+        s0 = load4(p + 192 + 8 * (g >> 1));
+        s1 = load4(p + 196 + 8 * (g >> 1));
+        d = load2(p + 208);
+    }
+    QMM_DEV void unpack(int g)
+    {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int v = (int)(int8_t)(((t < 2 ? s0 : s1) >> (16 * (t & 1) + 8 * (g & 1))) & 0xffu);
+            const _Float16 a = (_Float16)(float)(v & ~15), b = (_Float16)(float)(v & 15);
+            hi[t] = half2_t{a, a};
+            lo[t] = half2_t{b, b};
+        }
+    }
+    QMM_DEV half8_t operand(int h, int j, int part) const
+    {
+        const int jj = 4 * h + j, t = jj >> 1, w = 2 * (jj & 1);
+        const half2_t f = part ? lo[t] : hi[t];
+        half2_t p[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t ql = (t & 1 ? l1[w + i] : l0[w + i]) >> (t >= 2 ? 4 : 0);
+            const uint32_t q = (ql & 0x0f0f0f0fu) | (((qh[w + i] >> (2 * t)) & 0x03030303u) << 4);
+            const half2_t bias = {(_Float16)-1056.0f, (_Float16)-1056.0f};
+            p[2 * i] = (half2_of(__builtin_amdgcn_perm(0x64646464u, q, 0x05010400u)) + bias) * f;
+            p[2 * i + 1] = (half2_of(__builtin_amdgcn_perm(0x64646464u, q, 0x07030602u)) + bias) * f;
+        }
+        return join8(p[0], p[1], p[2], p[3]);
+    }
+    QMM_DEV float scale(int) const { return f16lo(d); }
+};
+
+// ------------------------------------------------------------ activations
+
+QMM_DEV void act4(const void* x, int type, int64_t i, float v[4])
+{
+    if (type == TYPE_F32) {
+        const f32x4_t t = *(const f32x4_t*)((const float*)x + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = t[k];
+    } else {
+        const u32x2_t t = *(const u32x2_t*)((const uint16_t*)x + i);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            v[2 * k] = type == TYPE_F16 ? f16lo(t[k]) : f32_of(t[k] << 16);
+            v[2 * k + 1] = type == TYPE_F16 ? f16hi(t[k]) : f32_of(t[k] & 0xffff0000u);
+        }
+    }
+}
+
+// The power of two that brings values of magnitude up to amax into f16's
+// range, the largest to [2^14, 2^15) (less where that would need a factor
+// above 2^126), and its inverse.  Scaled f16 parts then hold bf16 values
+// exactly and f32 values, as hi + lo, to 2^-22, but for values 2^-29 and more
+// below the largest, which are off by at most 2^-40 of it.  (An infinite amax
+// only has to leave its row non-finite.)
+QMM_DEV void act_scale(float amax, float& s, float& inv)
+{
+    const int eb = (int)(bits_of(amax) >> 23);
+    const int sb = min(268 - eb, 253);
+    s = f32_of((uint32_t)sb << 23);
+    inv = f32_of((uint32_t)(254 - sb) << 23);
+}
+
+// Eight scaled values (in operand order) as f16 parts.
+template <int PL>
+QMM_DEV void split8(const float v[8], half8_t p[PL])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[0][i] = (_Float16)v[i];
+        if constexpr (PL == 2) p[1][i] = (_Float16)(v[i] - (float)p[0][i]);
+    }
+}
+
+// The operand of Unit::mins: hi and lo parts of two sums.
+QMM_DEV half8_t sums_operand(const float s[2])
+{
+    const _Float16 a = (_Float16)s[0], b = (_Float16)s[1], z = (_Float16)0.0f;
+    return join8(half2_t{a, b}, half2_t{(_Float16)(s[0] - (float)a), (_Float16)(s[1] - (float)b)}, half2_t{z, z}, half2_t{z, z});
+}
+
+QMM_DEV f32x4_t mfma(half8_t a, half8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// One step (128 values) of NT units against MT groups of 16 activation rows:
+// acc[m][t] += the step's sums.  A(m, j, part) gives activation operands.
+template <int FMT, int PL, int MT, int NT, class AF>
+QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[MT][NT])
+{
+    using U = Unit<FMT>;
+    if constexpr (U::CHAIN) {
+        f32x4_t d[MT][NT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) d[m][t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            half8_t b[NT][U::PARTS];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int q = 0; q < U::PARTS; ++q) b[t][q] = un[t].operand(h, j, q);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int p = 0; p < PL; ++p) {
+                    const half8_t a = A(m, j, p);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int q = 0; q < U::PARTS; ++q) d[m][t] = mfma(a, b[t][q], d[m][t]);
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float s = un[t].scale(0);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(s, d[m][t][i], acc[m][t][i]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            half8_t b[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) b[t] = un[t].operand(h, j, 0);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                f32x4_t d[NT];
+#pragma unroll
+                for (int p = 0; p < PL; ++p) {
+                    const half8_t a = A(m, j, p);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) d[t] = mfma(a, b[t], p ? d[t] : f32x4_t{0, 0, 0, 0});
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float s = un[t].scale(j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(s, d[t][i], acc[m][t][i]);
+                }
+            }
+        }
+    }
+}
+
+QMM_DEV void store_out(void* y, int type, int64_t i, float v)
+{
+    if (type == TYPE_F32) ((float*)y)[i] = v;
+    else if (type == TYPE_F16) ((_Float16*)y)[i] = (_Float16)v;
+    else ((__bf16*)y)[i] = (__bf16)v;
+}
+
+// act 0: v / (1 + e^-v); 1: 0.5 v (1 + tanh t) = v / (1 + e^-2t), t = sqrt(2/pi) (v + 0.044715 v^3)
+QMM_DEV float activate(float v, int act)
+{
+    const float t = act == 0 ? -v : -1.5957691216057308f * (v + 0.044715f * v * v * v);
+    return v / (1.0f + expf(t));
+}
+
+QMM_DEV MoeMatrix moe_matrix(const MoeArgs& a, const uint8_t* w)
+{
+    MoeMatrix m;
+    m.w = w;
+    m.row_bytes = a.row_bytes;
+    m.blocks = (int)(a.K / 32);
+    m.scales = a.scales;
+    m.zeros = a.zeros;
+    m.scale_type = a.scale_type;
+    m.groups = 0;
+    m.group_blocks = a.group_blocks;
+    m.group_magic = a.group_magic;
+    if (a.fmt == FMT_W4) m.groups = m.blocks / a.group_blocks;
+    return m;
+}
+
+}  // namespace qmm

@@ -1,0 +1,6 @@
+// qmm_moe_w4.hip -- the experts' product kernels, 4-bit group weights.
+#include "qmm_moe_stream.h"
+
+namespace qmm {
+QMM_MOE_STREAM(w4, FMT_W4)
+}  // namespace qmm
