@@ -375,7 +375,7 @@ def dequantize_weights(fmt: int, w, n: int, k: int, out=None, stream=None):
 F32, F16, BF16 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
 ACTS = {"silu": 0, "gelu": 1}
-EXPERTS_RUN, EXPERTS_GLU, EXPERTS_COMBINE = 0, 1, 2
+EXPERTS_RUN, EXPERTS_GLU, EXPERTS_COMBINE, EXPERTS_RUN_SLOTS = 0, 1, 2, 3
 _TYPES = None
 
 
@@ -513,8 +513,8 @@ def experts_matmul(fmt: int, w, x, ids, y=None, stream=None):
 
     def body(s):
         out = _out(y, (t, k, n), x.dtype, dev, "y")
-        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_RUN, fmt, e, n, kk, t, k, code), dev,
-                                "qmatmul_experts_run")
+        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_RUN if x.dim() == 2 else EXPERTS_RUN_SLOTS, fmt,
+                                                                      e, n, kk, t, k, code), dev, "qmatmul_experts_run")
         _check(lib().qmatmul_experts_run(fmt, e, n, kk, t, k, code, int(x.dim() == 3), w.data_ptr(), x.data_ptr(),
                                          ids.data_ptr(), out.data_ptr(), ws, nb, s), "qmatmul_experts_run")
         return out

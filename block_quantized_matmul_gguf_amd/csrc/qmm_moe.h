@@ -55,13 +55,16 @@ struct MoeArgs {
 // from memory to the matrix cores.  one: a workgroup has one pair (or, for a
 // combine, one token and its slots); waves: waves along K per workgroup.
 hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s);
-// Tile kernel: mt * 16 pairs of an expert against 128 weight rows (GLU: 64 of
-// each matrix) per workgroup, prepared activations through LDS.
-hipError_t launch_tile(const MoeArgs& a, int mt, hipStream_t s);
+// Tile kernel: tile_rows(type) pairs of an expert against 128 weight rows (GLU:
+// 64 of each matrix) per workgroup, prepared activations through LDS.
+inline int tile_rows(int type) { return type == TYPE_F32 ? 64 : 128; }
+hipError_t launch_prep(const MoeArgs& a, hipStream_t s);
+hipError_t launch_tile(const MoeArgs& a, hipStream_t s);
 
 #define QMM_MOE_DECLARE(F)                                                              \
     hipError_t launch_stream_##F(const MoeArgs& a, bool one, int waves, hipStream_t s); \
-    hipError_t launch_tile_##F(const MoeArgs& a, int mt, hipStream_t s);
+    hipError_t launch_prep_##F(const MoeArgs& a, hipStream_t s);                        \
+    hipError_t launch_tile_##F(const MoeArgs& a, hipStream_t s);
 QMM_MOE_DECLARE(q8_0)
 QMM_MOE_DECLARE(q4_0)
 QMM_MOE_DECLARE(q5_0)

@@ -95,14 +95,15 @@ __global__ __launch_bounds__(256) void moe_combine(MoeArgs a, const float* prod)
     }
 }
 
-enum { PATH_ONE, PATH_SCAN, PATH_STREAM };
+enum { PATH_ONE, PATH_SCAN, PATH_STREAM, PATH_TILE };
 
 // What a call runs and what it needs of the workspace.
 struct MoePlan {
     int path, waves;
     bool sort;
     int tm, max_tiles;
-    size_t order, tiles, products, bytes;  // offsets
+    int64_t x_rows, Kp;
+    size_t order, tiles, products, xp, xinv, xsum, bytes;  // offsets
 };
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -112,22 +113,32 @@ MoePlan plan_of(const MoeArgs& a)
     MoePlan p = {};
     const int64_t P = a.T * a.top_k;
     const bool dense = a.fmt == FMT_W4;
-    p.path = dense ? (a.T == 1 ? PATH_ONE : PATH_STREAM) : a.T == 1 ? PATH_ONE : P <= 64 ? PATH_SCAN : PATH_STREAM;
+    if (a.T == 1) p.path = PATH_ONE;
+    else if (P > 24 * (int64_t)(dense ? 4 : a.E)) p.path = PATH_TILE;
+    else p.path = dense || P > 64 ? PATH_STREAM : PATH_SCAN;
     p.waves = 4;
-    p.sort = !dense && p.path == PATH_STREAM;
-    p.tm = 16;
+    p.tm = p.path == PATH_TILE ? tile_rows(a.type) : 16;
+    p.max_tiles = (int)(dense ? (P + p.tm - 1) / p.tm : P / p.tm + std::min<int64_t>(a.E + 1, P));
+    p.sort = !dense && p.path >= PATH_STREAM;
     size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += align256(bytes);
+        return at;
+    };
     if (p.sort) {
-        p.max_tiles = (int)(P / p.tm + std::min<int64_t>(a.E + 1, P));
-        p.order = off;
-        off += align256((size_t)P * 4);
-        p.tiles = off;
-        off += align256((size_t)p.max_tiles * sizeof(MoeTile));
+        p.order = take((size_t)P * 4);
+        p.tiles = take((size_t)p.max_tiles * sizeof(MoeTile));
     }
-    if (a.op == MOE_COMBINE && p.path != PATH_ONE) {
-        p.products = off;
-        off += align256((size_t)P * (size_t)a.N * 4);
+    if (p.path == PATH_TILE) {
+        const int64_t unit = a.fmt == FMT_Q4_K || a.fmt == FMT_Q6_K ? 256 : 128;
+        p.x_rows = a.per_slot ? P : a.T;
+        p.Kp = (a.K + unit - 1) / unit * unit;
+        p.xp = take((size_t)p.x_rows * p.Kp * (a.type == TYPE_F32 ? 4 : 2));
+        p.xinv = take((size_t)p.x_rows * 4);
+        if (a.fmt == FMT_Q4_K) p.xsum = take((size_t)p.x_rows * (p.Kp / 256) * 32);
     }
+    if (a.op == MOE_COMBINE && p.path != PATH_ONE) p.products = take((size_t)P * (size_t)a.N * 4);
     p.bytes = off;
     return p;
 }
@@ -135,14 +146,22 @@ MoePlan plan_of(const MoeArgs& a)
 hipError_t launch_moe(const MoeArgs& call, const MoePlan& p, char* ws, hipStream_t s)
 {
     MoeArgs a = call;
+    hipError_t e = hipSuccess;
     a.y_type = a.type;
+    a.max_tiles = p.max_tiles;
     if (p.sort) {
         a.order = (int32_t*)(ws + p.order);
         a.tiles = (MoeTile*)(ws + p.tiles);
-        a.max_tiles = p.max_tiles;
         moe_sort<<<dim3(1), dim3(SORT_THREADS), 0, s>>>(a, p.tm);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (p.path == PATH_TILE) {
+        a.xp = (_Float16*)(ws + p.xp);
+        a.xinv = (float*)(ws + p.xinv);
+        a.xsum = (_Float16*)(ws + p.xsum);
+        a.x_rows = p.x_rows;
+        a.Kp = p.Kp;
+        if ((e = launch_prep(a, s)) != hipSuccess) return e;
     }
     const bool summed = a.op == MOE_COMBINE && p.path != PATH_ONE;
     float* products = (float*)(ws + p.products);
@@ -151,7 +170,7 @@ hipError_t launch_moe(const MoeArgs& call, const MoePlan& p, char* ws, hipStream
         a.y = products;
         a.y_type = TYPE_F32;
     }
-    hipError_t e = launch_stream(a, p.path == PATH_ONE, p.waves, s);
+    e = p.path == PATH_TILE ? launch_tile(a, s) : launch_stream(a, p.path == PATH_ONE, p.waves, s);
     if (e != hipSuccess || !summed) return e;
     a = call;
     a.y_type = a.type;
@@ -167,11 +186,13 @@ int type_bytes(int t) { return t == QMM_F32 ? 4 : 2; }
 // Sizes and types of an experts' product; no pointers.
 int check_experts(int product, int format, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int type)
 {
-    if (product != QMM_EXPERTS_RUN && product != QMM_EXPERTS_GLU && product != QMM_EXPERTS_COMBINE)
+    if (product != QMM_EXPERTS_RUN && product != QMM_EXPERTS_GLU && product != QMM_EXPERTS_COMBINE &&
+        product != QMM_EXPERTS_RUN_SLOTS)
         return set_error(QMM_EUNSUPPORTED, "unknown product");
     const int st = qmatmul_check(format, N, K, 1, QMM_MODE_F32ACT);
     if (st != QMM_OK) return st;
     if (!known_type(type)) return set_error(QMM_EUNSUPPORTED, "unknown activation type");
+    if (N > (1ll << 24)) return bad("N must be at most 2^24");
     if (E < 1 || E > 1024) return bad("E must be in 1..1024");
     if (top_k < 1 || top_k > 64) return bad("top_k must be in 1..64");
     if (T < 0 || T > (1ll << 24) || T * top_k > (1ll << 24)) return bad("T must not be negative and T * top_k at most 2^24");
@@ -183,7 +204,7 @@ int check_w4(int64_t N, int64_t K, int64_t M, int64_t group, int type)
     if (!known_type(type)) return set_error(QMM_EUNSUPPORTED, "unknown activation type");
     if (N <= 0 || K <= 0 || M < 0) return bad("N and K must be positive, M not negative");
     if (group <= 0 || group % 32 || K % group) return set_error(QMM_EBLOCK, "group must be a multiple of 32 that divides K");
-    if (N > (1ll << 30) || K > (1ll << 20) || M > (1ll << 24) || N * (K / 2) > (1ll << 40)) return bad("shape too large");
+    if (N > (1ll << 24) || K > (1ll << 20) || M > (1ll << 24) || N * (K / 2) > (1ll << 40)) return bad("shape too large");
     return QMM_OK;
 }
 
@@ -216,16 +237,32 @@ bool off16(const void* p) { return (uintptr_t)p % 16 != 0; }
 
 }  // namespace
 
+#define QMM_MOE_DISPATCH(CALL)                  \
+    switch (a.fmt) {                            \
+    case FMT_Q8_0: return CALL(q8_0);           \
+    case FMT_Q4_0: return CALL(q4_0);           \
+    case FMT_Q5_0: return CALL(q5_0);           \
+    case FMT_Q4_K: return CALL(q4_k);           \
+    case FMT_Q6_K: return CALL(q6_k);           \
+    default: return CALL(w4);                   \
+    }
 hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s)
 {
-    switch (a.fmt) {
-    case FMT_Q8_0: return launch_stream_q8_0(a, one, waves, s);
-    case FMT_Q4_0: return launch_stream_q4_0(a, one, waves, s);
-    case FMT_Q5_0: return launch_stream_q5_0(a, one, waves, s);
-    case FMT_Q4_K: return launch_stream_q4_k(a, one, waves, s);
-    case FMT_Q6_K: return launch_stream_q6_k(a, one, waves, s);
-    default: return launch_stream_w4(a, one, waves, s);
-    }
+#define CALL(F) launch_stream_##F(a, one, waves, s)
+    QMM_MOE_DISPATCH(CALL)
+#undef CALL
+}
+hipError_t launch_prep(const MoeArgs& a, hipStream_t s)
+{
+#define CALL(F) launch_prep_##F(a, s)
+    QMM_MOE_DISPATCH(CALL)
+#undef CALL
+}
+hipError_t launch_tile(const MoeArgs& a, hipStream_t s)
+{
+#define CALL(F) launch_tile_##F(a, s)
+    QMM_MOE_DISPATCH(CALL)
+#undef CALL
 }
 
 }  // namespace qmm
@@ -237,7 +274,9 @@ extern "C" int64_t qmatmul_experts_workspace_bytes(int product, int format, int6
 {
     set_error(QMM_OK, "");
     if (check_experts(product, format, E, N, K, T, top_k, type) != QMM_OK) return -1;
-    return workspace_bytes(experts_args(product, format, E, N, K, T, top_k, type));
+    MoeArgs a = experts_args(product == QMM_EXPERTS_RUN_SLOTS ? MOE_RUN : product, format, E, N, K, T, top_k, type);
+    a.per_slot = product >= QMM_EXPERTS_COMBINE;
+    return workspace_bytes(a);
 }
 
 extern "C" int qmatmul_experts_run(int format, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int type,

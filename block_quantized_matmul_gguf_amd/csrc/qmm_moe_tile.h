@@ -1,0 +1,260 @@
+// qmm_moe_tile.h -- products of many activation rows with an expert's weights,
+// bound by the matrix cores and by the vector work that feeds them.
+//
+// A workgroup multiplies MT * 16 pairs of one expert with 128 weight rows
+// (GLU: 64 rows of the gate and the same 64 of the up matrix).  Its four waves
+// own 32 of them each: a weight row is decoded once per workgroup, from
+// registers, and never staged; the activations, prepared once per call in
+// operand order, are copied straight into LDS one step (128 values of K) ahead
+// and read by all four waves.
+#pragma once
+#include "qmm_moe_unit.h"
+
+namespace qmm {
+
+constexpr int TILE_N = 128;
+
+typedef const __attribute__((address_space(1))) void* gptr_t;
+typedef __attribute__((address_space(3))) void* lptr_t;
+
+// 16 bytes per lane from p (per lane) to LDS at base + 16 * lane
+QMM_DEV void copy_to_lds(const void* p, void* base)
+{
+    __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)base, 16, 0, 0);
+}
+
+template <int FMT, int PL, int MT, bool GLU>
+__global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
+{
+    using U = Unit<FMT>;
+    constexpr int UNIT = U::UNIT, H = U::HALVES, MW = MT / 4;  // row groups a wave copies
+    __shared__ __align__(16) _Float16 ta[2][PL][MT][4][64][8];
+    __shared__ __align__(16) _Float16 ts[U::MINS ? 2 : 1][U::MINS ? MT : 1][2][16][8];
+
+    const int lane = (int)__lane_id(), r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    constexpr int BN = GLU ? TILE_N / 2 : TILE_N;
+    const int nb = (int)((a.N + BN - 1) / BN);
+
+    // Workgroups go to the eight XCDs in turn.  Experts: an XCD takes all
+    // weight tiles of its row tiles, so a row tile's activations enter one L2.
+    // One matrix: an XCD takes all row tiles of its weight tiles.
+    const int64_t id = blockIdx.x, seq = id >> 3;
+    int64_t b, tile;
+    if (a.ids) {
+        tile = seq / nb * 8 + (id & 7);
+        b = seq % nb;
+    } else {
+        b = seq / a.max_tiles * 8 + (id & 7);
+        tile = seq % a.max_tiles;
+    }
+    if (b >= nb || tile >= a.max_tiles) return;
+    MoeTile t;
+    if (a.ids) {
+        t = a.tiles[tile];
+    } else {
+        t.e = 0;
+        t.start = (int)tile * MT * 16;
+        t.count = (int)min((int64_t)MT * 16, a.T - t.start);
+    }
+    if (t.count <= 0) return;
+    const int64_t n0 = b * BN;
+
+    // the pair of row 16 m + r, and where its activations are
+    auto pair_of = [&](int m) {
+        const int i = t.start + min(m * 16 + r, t.count - 1);
+        return a.ids ? a.order[i] : i;
+    };
+    auto row_of = [&](int pair) { return a.per_slot ? pair : pair / a.top_k; };
+
+    f32x4_t acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[m][c] = f32x4_t{0, 0, 0, 0};
+
+    if (t.e >= 0) {
+        const int units = (int)(a.Kp / UNIT), steps = units * H;
+        const int64_t plane = a.x_rows * a.Kp;
+        const _Float16* src[MW];
+        const _Float16* ssrc = nullptr;
+#pragma unroll
+        for (int i = 0; i < MW; ++i) src[i] = a.xp + (int64_t)row_of(pair_of(wave * MW + i)) * a.Kp + g * 8;
+        // sums: 16 halves per row and unit; waves below MT / 2 copy [m][p][r] of m = 2 wave, 2 wave + 1
+        if constexpr (U::MINS) {
+            const int sm = (wave * 2 + (lane >> 5)) & (MT - 1);
+            const int i = t.start + min(sm * 16 + r, t.count - 1);
+            ssrc = a.xsum + (int64_t)row_of(a.ids ? a.order[i] : i) * units * 16 + ((lane >> 4) & 1) * 8;
+        }
+        auto stage = [&](int s) {
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+#pragma unroll
+                for (int i = 0; i < MW; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        copy_to_lds(src[i] + p * plane + (int64_t)s * 128 + j * 32, &ta[s & 1][p][wave * MW + i][j][0][0]);
+            if constexpr (U::MINS) {
+                if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + (int64_t)(s >> 1) * 16, &ts[(s >> 1) & 1][wave * 2][0][0][0]);
+            }
+        };
+        const int64_t matrix = a.N * a.row_bytes;
+        MoeMatrix mat = moe_matrix(a, a.w0 + t.e * matrix);
+        int64_t n[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) n[c] = min(n0 + (GLU ? wave * 16 : wave * 32 + c * 16) + r, a.N - 1);
+        auto fetch = [&](int u, Unit<FMT> (&un)[2]) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (GLU) mat.w = (c ? a.w1 : a.w0) + t.e * matrix;
+                un[c].load(mat, n[c], u, g);
+            }
+        };
+        Unit<FMT> cur[2], next[2];
+        stage(0);
+        fetch(0, next);
+        for (int u = 0; u < units; ++u) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int s = u * H + h;
+                vm_wait<0>();
+                __syncthreads();
+                if (s + 1 < steps) stage(s + 1);
+                if (h == 0) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        cur[c] = next[c];
+                        cur[c].unpack(g);
+                    }
+                    if (u + 1 < units) fetch(u + 1, next);
+                }
+                step<FMT, PL, MT, 2>(cur, h, [&](int m, int j, int p) { return *(const half8_t*)&ta[s & 1][p][m][j][lane][0]; }, acc);
+                if constexpr (U::MINS) {
+                    if (h == 0) {
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const u32x2_t q = *(const u32x2_t*)&ts[u & 1][m][g >> 1][r][(g & 1) * 4];
+                            const half8_t sa = join8(half2_of(q[0]), half2_of(q[1]), half2_of(0u), half2_of(0u));
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const f32x4_t d = mfma(sa, cur[c].mins(), f32x4_t{0, 0, 0, 0});
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) acc[m][c][i] = fmaf(cur[c].mins_scale(), d[i], acc[m][c][i]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // sums 4g + i of row group m are those of rows 16 m + 4 g + i
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (m * 16 >= t.count) break;
+        const int pair = pair_of(m);
+        const float inv = t.e >= 0 ? a.xinv[row_of(pair)] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * g + i;
+            const int64_t p = __shfl(pair, row);
+            const float f = __shfl(inv, row);
+            if (m * 16 + row >= t.count) continue;
+            if constexpr (GLU) {
+                const int64_t n = n0 + wave * 16 + r;
+                const float v = t.e < 0 ? 0.0f : activate(acc[m][0][i] * f, a.act) * (acc[m][1][i] * f);
+                if (n < a.N) store_out(a.y, a.y_type, p * a.N + n, v);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int64_t n = n0 + wave * 32 + c * 16 + r;
+                    if (n < a.N) store_out(a.y, a.y_type, p * a.N + n, acc[m][c][i] * f);
+                }
+            }
+        }
+    }
+}
+
+// Activations in operand order.  One wave per row: its largest magnitude, then
+// eight values per lane at a time, scaled, as f16 parts.
+template <int FMT, int PL>
+__global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
+{
+    using U = Unit<FMT>;
+    const int lane = (int)__lane_id();
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= a.x_rows) return;
+    float am = 0.0f;
+    for (int64_t k = lane * 4; k < a.K; k += 256) {
+        float v[4];
+        act4(a.x, a.type, row * a.K + k, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) am = fmaxf(am, fabsf(v[i]));
+    }
+    float s, inv;
+    act_scale(wave_max(am), s, inv);
+    if (lane == 0) a.xinv[row] = inv;
+    const int64_t plane = a.x_rows * a.Kp;
+    for (int64_t q = lane; q < a.Kp / 8; q += 64) {  // piece [unit][step][j][g]
+        constexpr int PIECES = U::UNIT / 8;
+        const int64_t u = q / PIECES;
+        const int i = (int)(q % PIECES), h = i >> 4, j = (i >> 2) & 3, g = i & 3;
+        float v[8];
+        half8_t p[PL];
+        float sum = 0.0f;
+        if (u * U::UNIT + U::o0(h, j, g) < a.K) {
+            float e[8];
+            act4(a.x, a.type, row * a.K + u * U::UNIT + U::o0(h, j, g), e);
+            act4(a.x, a.type, row * a.K + u * U::UNIT + U::o1(h, j, g), e + 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = e[U::slot(k)] * s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        }
+        split8<PL>(v, p);
+#pragma unroll
+        for (int k = 0; k < PL; ++k) *(half8_t*)(a.xp + k * plane + row * a.Kp + q * 8) = p[k];
+        if constexpr (U::MINS) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += v[k];
+            sum += __shfl_xor(sum, 4);
+            sum += __shfl_xor(sum, 8);
+            sum *= 0.03125f;
+            if (j == 0) {
+                _Float16* o = a.xsum + (row * (a.Kp / 256) + u) * 16 + g * 4 + h;
+                const _Float16 hi = (_Float16)sum;
+                o[0] = hi;
+                o[2] = (_Float16)(sum - (float)hi);
+            }
+        }
+    }
+}
+
+template <int FMT, int PL, int MT>
+hipError_t launch_tile_t(const MoeArgs& a, hipStream_t s)
+{
+    const int64_t bn = a.op == MOE_GLU ? TILE_N / 2 : TILE_N, nb = (a.N + bn - 1) / bn;
+    const int64_t grid = a.ids ? (a.max_tiles + 7) / 8 * 8 * nb : (nb + 7) / 8 * 8 * a.max_tiles;
+    if (a.op == MOE_GLU) moe_tile<FMT, PL, MT, true><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
+    else moe_tile<FMT, PL, MT, false><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int FMT>
+hipError_t launch_prep_t(const MoeArgs& a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.x_rows + 3) / 4)), block(256);
+    if (a.type == TYPE_F32) moe_prep<FMT, 2><<<grid, block, 0, s>>>(a);
+    else moe_prep<FMT, 1><<<grid, block, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+#define QMM_MOE_TILE(NAME, FMT)                                                                        \
+    hipError_t launch_prep_##NAME(const MoeArgs& a, hipStream_t s) { return launch_prep_t<FMT>(a, s); } \
+    hipError_t launch_tile_##NAME(const MoeArgs& a, hipStream_t s)                                      \
+    {                                                                                                   \
+        return a.type == TYPE_F32 ? launch_tile_t<FMT, 2, 4>(a, s) : launch_tile_t<FMT, 1, 8>(a, s);    \
+    }
+
+}  // namespace qmm

@@ -1,6 +1,8 @@
 // qmm_moe_w4.hip -- the experts' product kernels, 4-bit group weights.
 #include "qmm_moe_stream.h"
+#include "qmm_moe_tile.h"
 
 namespace qmm {
 QMM_MOE_STREAM(w4, FMT_W4)
+QMM_MOE_TILE(w4, FMT_W4)
 }  // namespace qmm

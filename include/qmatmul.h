@@ -293,6 +293,7 @@ int qmatmul_run_block_sums(const qmm_plan* plan, const void* w_blocks, const flo
 #define QMM_EXPERTS_RUN 0
 #define QMM_EXPERTS_GLU 1
 #define QMM_EXPERTS_COMBINE 2
+#define QMM_EXPERTS_RUN_SLOTS 3 /* qmatmul_experts_run with per_slot = 1 */
 
 /*
  * Choose experts: per row of logits [T x E] (type QMM_F32, QMM_F16 or
@@ -337,8 +338,8 @@ int qmatmul_route_experts(const void* logits, int type, int64_t T, int64_t E, co
  *
  * A row of x with an infinity or NaN makes the outputs computed from it
  * non-finite (NaN where the sum holds inf - inf or 0 * inf) and no others.
- * Limits: E <= 1024, top_k <= 64, T * top_k <= 2^24, and qmatmul_create's
- * limits on N and K.  T == 0 enqueues nothing.  Outputs must not overlap
+ * Limits: E <= 1024, top_k <= 64, T * top_k <= 2^24, N <= 2^24, and
+ * qmatmul_create's limit on K.  T == 0 enqueues nothing.  Outputs must not overlap
  * inputs.
  */
 int64_t qmatmul_experts_workspace_bytes(int product, int format, int64_t E, int64_t N, int64_t K, int64_t T,
@@ -362,7 +363,7 @@ int qmatmul_experts_combine(int format, int64_t E, int64_t N, int64_t K, int64_t
  * in its high nibble, 16-byte aligned.  scales: device [N x K/group] of
  * scale_type (QMM_F32, QMM_F16 or QMM_BF16).  zeros: device uint8 [N x
  * K/group], 0..15 (other values are used as they are).  group: a multiple of
- * 32 that divides K.  x (16-byte aligned) and y have the type `type`.  M >= 0;
+ * 32 that divides K; N and M at most 2^24.  x (16-byte aligned) and y have the type `type`.  M >= 0;
  * M == 0 enqueues nothing.  Sums and rounding as qmatmul_experts_run.
  */
 int64_t qmatmul_w4_workspace_bytes(int64_t N, int64_t K, int64_t M, int64_t group, int type); /* -1 if invalid */

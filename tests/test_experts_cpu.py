@@ -90,12 +90,12 @@ def test_w4_refusals(kw, status):
 
 def test_workspace_sizes():
     lib = qmm.lib()
-    for product in (qmm.EXPERTS_RUN, qmm.EXPERTS_GLU, qmm.EXPERTS_COMBINE):
+    for product in (qmm.EXPERTS_RUN, qmm.EXPERTS_GLU, qmm.EXPERTS_COMBINE, qmm.EXPERTS_RUN_SLOTS):
         for t in (0, 1, 3, 40, 700, 5000):
             assert lib.qmatmul_experts_workspace_bytes(product, qmm.Q4_K, 64, 1024, 2048, t, 8, qmm.BF16) >= 0
         assert lib.qmatmul_experts_workspace_bytes(product, qmm.Q4_K, 64, 1024, 2047, 1, 8, qmm.BF16) == -1
         assert lib.qmatmul_experts_workspace_bytes(product, qmm.Q4_K, 0, 1024, 2048, 1, 8, qmm.BF16) == -1
-    assert lib.qmatmul_experts_workspace_bytes(3, qmm.Q4_K, 64, 1024, 2048, 1, 8, qmm.BF16) == -1
+    assert lib.qmatmul_experts_workspace_bytes(4, qmm.Q4_K, 64, 1024, 2048, 1, 8, qmm.BF16) == -1
     for m in (0, 1, 17, 64, 4000):
         assert lib.qmatmul_w4_workspace_bytes(1537, 1536, m, 32, qmm.F32) >= 0
     assert lib.qmatmul_w4_workspace_bytes(1537, 1536, 4, 48, qmm.F32) == -1
