@@ -43,8 +43,10 @@ struct MoeArgs {
     MoeTile* tiles;           // [max_tiles]
     int max_tiles;
     // prepared activations (tile path): f16 planes in operand order, the hi
-    // parts and for f32 the lo parts, [rows][Kp] each; 1/scale per row; Q4_K:
-    // hi and lo of the sub-block sums / 32, [rows][K/256][16]
+    // parts and for f32 the lo parts, [Kp/128][rows][128] each (a step of many
+    // rows is one run of memory: rows a power of two apart would share an L2
+    // channel); 1/scale per row; Q4_K: hi and lo of the sub-block sums / 32,
+    // [K/256][rows][16]
     _Float16* xp;
     int64_t x_rows, Kp;
     float* xinv;

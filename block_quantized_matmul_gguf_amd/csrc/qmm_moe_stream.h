@@ -107,15 +107,18 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
         const int nslots = combine ? a.top_k : 1;
         const int items = nslots * units;
         const int64_t matrix = a.N * a.row_bytes;
+        const MoeMatrix mat = moe_matrix(a, nullptr);
         int64_t n[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) n[t] = min(n0 + r + (GLU ? 0 : 16 * t), a.N - 1);
 
-        constexpr int XV = UNIT / 64;
+        constexpr int XV = UNIT / 64;  // ONE: values of a unit per lane
         struct Loaded {
             Unit<FMT> u[NT];
-            float x[ONE ? XV : 1];
-            float w;  // factor of the item's sums; 0 without an expert
+            // ONE: lane's XV neighbours (the first half of a Raw4 for two)
+            // else: the operand's values, [step][j][run]
+            Raw4<PL> x[ONE ? 1 : H][ONE ? 1 : 4][2];
+            float w;  // factor of the item's sums
             bool live;
         };
         auto fetch = [&](int it, Loaded& l) {
@@ -134,26 +137,36 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
             if constexpr (ONE) {
                 const int64_t row = combine ? (int64_t)rows.pair * a.top_k + slot : a.per_slot ? rows.pair : rows.pair / a.top_k;
                 const int k = u * UNIT + lane * XV;  // XV divides 32: a piece is inside the row or past its end
-#pragma unroll
-                for (int i = 0; i < XV; ++i) l.x[i] = 0.0f;
+                l.x[0][0][0].clear();
                 if (k < a.K) {
                     const int64_t at = row * a.K + k;
                     if constexpr (XV == 4) {
-                        act4(a.x, a.type, at, l.x);
+                        l.x[0][0][0].load(a.x, at);
+                    } else if constexpr (PL == 2) {
+                        const u32x2_t t = *(const u32x2_t*)((const uint32_t*)a.x + at);
+                        l.x[0][0][0].r[0] = t[0];
+                        l.x[0][0][0].r[1] = t[1];
                     } else {
-                        if (a.type == TYPE_F32) {
-                            const float2 t = *(const float2*)((const float*)a.x + at);
-                            l.x[0] = t.x;
-                            l.x[1] = t.y;
-                        } else {
-                            const uint32_t t = *(const uint32_t*)((const uint16_t*)a.x + at);
-                            l.x[0] = a.type == TYPE_F16 ? f16lo(t) : f32_of(t << 16);
-                            l.x[1] = a.type == TYPE_F16 ? f16hi(t) : f32_of(t & 0xffff0000u);
-                        }
+                        l.x[0][0][0].r[0] = *(const uint32_t*)((const uint16_t*)a.x + at);
                     }
                 }
+            } else {
+                const int64_t row = a.per_slot ? rows.pair : rows.pair / a.top_k;
+                const int64_t base = row * a.K + (int64_t)u * UNIT;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        l.x[h][j][0].clear();
+                        l.x[h][j][1].clear();
+                        if (UNIT == 256 || u * 4 + j < a.K / 32) {
+                            l.x[h][j][0].load(a.x, base + U::o0(h, j, g));
+                            l.x[h][j][1].load(a.x, base + U::o1(h, j, g));
+                        }
+                    }
             }
-            MoeMatrix m = moe_matrix(a, a.w0 + e * matrix);
+            MoeMatrix m = mat;
+            m.w = a.w0 + e * matrix;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (GLU && t == 1) m.w = a.w1 + e * matrix;
@@ -164,15 +177,15 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
         auto multiply = [&](int it, Loaded& l) {
             if constexpr (ONE) {
                 if (!l.live) return;
-                float am = 0.0f;
+                float v[4], am = 0.0f, sum = 0.0f;
+                l.x[0][0][0].values(a.type, v);
 #pragma unroll
-                for (int i = 0; i < XV; ++i) am = fmaxf(am, fabsf(l.x[i]));
+                for (int i = 0; i < XV; ++i) am = fmaxf(am, fabsf(v[i]));
                 float s, inv;
                 act_scale(wave_max(am), s, inv);
-                float v[XV], sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < XV; ++i) {
-                    v[i] = l.x[i] * s;
+                    v[i] *= s;
                     sum += v[i];
                 }
                 // to operand order: [step][j][g][slot]
@@ -196,7 +209,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     d[0][t] = f32x4_t{0, 0, 0, 0};
-                    l.u[t].unpack(g);
+                    l.u[t].unpack(mat, g);
                 }
 #pragma unroll
                 for (int h = 0; h < H; ++h)
@@ -216,22 +229,15 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
                 for (int t = 0; t < NT; ++t) acc[0][t][0] = fmaf(l.w, inv * d[0][t][0], acc[0][t][0]);
                 wave_sync();  // the next item's values go where these were
             } else {
-                const int64_t row = a.per_slot ? rows.pair : rows.pair / a.top_k;
-                const int64_t base = row * a.K + (int64_t)it * UNIT;
                 float v[H][4][8];
                 float am = 0.0f;
 #pragma unroll
                 for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (UNIT == 128 && it * 4 + j >= a.K / 32) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[h][j][i] = 0.0f;
-                            continue;
-                        }
                         float e[8];
-                        act4(a.x, a.type, base + U::o0(h, j, g), e);
-                        act4(a.x, a.type, base + U::o1(h, j, g), e + 4);
+                        l.x[h][j][0].values(a.type, e);
+                        l.x[h][j][1].values(a.type, e + 4);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[h][j][i] = e[U::slot(i)];
                     }
@@ -267,7 +273,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     d[0][t] = f32x4_t{0, 0, 0, 0};
-                    l.u[t].unpack(g);
+                    l.u[t].unpack(mat, g);
                 }
 #pragma unroll
                 for (int h = 0; h < H; ++h) step<FMT, PL, 1, NT>(l.u, h, [&](int, int j, int p) { return xa[h][j][p]; }, d);

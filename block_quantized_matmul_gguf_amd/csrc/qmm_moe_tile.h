@@ -79,23 +79,28 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
         const _Float16* src[MW];
         const _Float16* ssrc = nullptr;
 #pragma unroll
-        for (int i = 0; i < MW; ++i) src[i] = a.xp + (int64_t)row_of(pair_of(wave * MW + i)) * a.Kp + g * 8;
+        for (int i = 0; i < MW; ++i) src[i] = a.xp + (int64_t)row_of(pair_of(wave * MW + i)) * 128 + g * 8;
         // sums: 16 halves per row and unit; waves below MT / 2 copy [m][p][r] of m = 2 wave, 2 wave + 1
         if constexpr (U::MINS) {
             const int sm = (wave * 2 + (lane >> 5)) & (MT - 1);
             const int i = t.start + min(sm * 16 + r, t.count - 1);
-            ssrc = a.xsum + (int64_t)row_of(a.ids ? a.order[i] : i) * units * 16 + ((lane >> 4) & 1) * 8;
+            ssrc = a.xsum + (int64_t)row_of(a.ids ? a.order[i] : i) * 16 + ((lane >> 4) & 1) * 8;
         }
-        auto stage = [&](int s) {
+        // The walk along K starts at another unit in every workgroup: all of them at one place of
+        // rows a power of two apart would ask the same L2 channel.
+        const int first = (int)((b * 5 + tile) % units);
+        auto place_of = [&](int u) { return u + first < units ? u + first : u + first - units; };
+        auto stage = [&](int s) {  // step s of the walk
+            const int64_t su = place_of(s / H), at = su * H + s % H;
 #pragma unroll
             for (int p = 0; p < PL; ++p)
 #pragma unroll
                 for (int i = 0; i < MW; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        copy_to_lds(src[i] + p * plane + (int64_t)s * 128 + j * 32, &ta[s & 1][p][wave * MW + i][j][0][0]);
+                        copy_to_lds(src[i] + p * plane + at * a.x_rows * 128 + j * 32, &ta[s & 1][p][wave * MW + i][j][0][0]);
             if constexpr (U::MINS) {
-                if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + (int64_t)(s >> 1) * 16, &ts[(s >> 1) & 1][wave * 2][0][0][0]);
+                if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + su * a.x_rows * 16, &ts[(s >> 1) & 1][wave * 2][0][0][0]);
             }
         };
         const int64_t matrix = a.N * a.row_bytes;
@@ -107,7 +112,7 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 if (GLU) mat.w = (c ? a.w1 : a.w0) + t.e * matrix;
-                un[c].load(mat, n[c], u, g);
+                un[c].load(mat, n[c], place_of(u), g);
             }
         };
         Unit<FMT> cur[2], next[2];
@@ -124,7 +129,7 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         cur[c] = next[c];
-                        cur[c].unpack(g);
+                        cur[c].unpack(mat, g);
                     }
                     if (u + 1 < units) fetch(u + 1, next);
                 }
@@ -187,7 +192,9 @@ __global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
     float am = 0.0f;
     for (int64_t k = lane * 4; k < a.K; k += 256) {
         float v[4];
-        act4(a.x, a.type, row * a.K + k, v);
+        Raw4<PL> w;
+        w.load(a.x, row * a.K + k);
+        w.values(a.type, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) am = fmaxf(am, fabsf(v[i]));
     }
@@ -204,8 +211,11 @@ __global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
         float sum = 0.0f;
         if (u * U::UNIT + U::o0(h, j, g) < a.K) {
             float e[8];
-            act4(a.x, a.type, row * a.K + u * U::UNIT + U::o0(h, j, g), e);
-            act4(a.x, a.type, row * a.K + u * U::UNIT + U::o1(h, j, g), e + 4);
+            Raw4<PL> w0, w1;
+            w0.load(a.x, row * a.K + u * U::UNIT + U::o0(h, j, g));
+            w1.load(a.x, row * a.K + u * U::UNIT + U::o1(h, j, g));
+            w0.values(a.type, e);
+            w1.values(a.type, e + 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = e[U::slot(k)] * s;
         } else {
@@ -214,7 +224,7 @@ __global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
         }
         split8<PL>(v, p);
 #pragma unroll
-        for (int k = 0; k < PL; ++k) *(half8_t*)(a.xp + k * plane + row * a.Kp + q * 8) = p[k];
+        for (int k = 0; k < PL; ++k) *(half8_t*)(a.xp + k * plane + ((q >> 4) * a.x_rows + row) * 128 + (q & 15) * 8) = p[k];
         if constexpr (U::MINS) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum += v[k];
@@ -222,7 +232,7 @@ __global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
             sum += __shfl_xor(sum, 8);
             sum *= 0.03125f;
             if (j == 0) {
-                _Float16* o = a.xsum + (row * (a.Kp / 256) + u) * 16 + g * 4 + h;
+                _Float16* o = a.xsum + (u * a.x_rows + row) * 16 + g * 4 + h;
                 const _Float16 hi = (_Float16)sum;
                 o[0] = hi;
                 o[2] = (_Float16)(sum - (float)hi);

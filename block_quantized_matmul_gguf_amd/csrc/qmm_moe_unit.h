@@ -161,7 +161,7 @@ struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
             d = load2(p);
         }
     }
-    QMM_DEV void unpack(int)
+    QMM_DEV void unpack(const MoeMatrix&, int)
     {
         transpose4(c);
         transpose4(c + 4);
@@ -192,7 +192,7 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
             d = load2(p);
         }
     }
-    QMM_DEV void unpack(int)
+    QMM_DEV void unpack(const MoeMatrix&, int)
     {
         transpose4(c);
         gather_scales(f16lo(d));
@@ -226,7 +226,7 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
     }
     // h[j]: the fifth bits of this lane group's values of block j, the first
     // four in bits 0..3, the last four in bits 16..19
-    QMM_DEV void unpack(int g)
+    QMM_DEV void unpack(const MoeMatrix&, int g)
     {
         transpose4(c);
         gather_scales(f16lo(d));
@@ -266,16 +266,16 @@ struct Unit<FMT_W4> : Unit32<FMT_W4> {
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = v[i];
             const int64_t at = n * m.groups + (m.group_magic ? (int)__umulhi((uint32_t)b, m.group_magic) : b);
+            // as they are: a conversion here would wait for the load
             if (m.scale_type == TYPE_F32) d = ((const uint32_t*)m.scales)[at];
-            else if (m.scale_type == TYPE_F16) d = bits_of((float)((const _Float16*)m.scales)[at]);
-            else d = (uint32_t)((const uint16_t*)m.scales)[at] << 16;
+            else d = ((const uint16_t*)m.scales)[at];
             if (m.zeros) z = m.zeros[at];
         }
     }
-    QMM_DEV void unpack(int)
+    QMM_DEV void unpack(const MoeMatrix& m, int)
     {
         transpose4(c);
-        gather_scales(f32_of(d));
+        gather_scales(m.scale_type == TYPE_F16 ? f16lo(d) : f32_of(m.scale_type == TYPE_F32 ? d : d << 16));
         // -(1024 + z) in both halves
         uint32_t o[4];
         gather4((0xe400u | z) * 0x00010001u, o);
@@ -316,7 +316,7 @@ struct Unit<FMT_Q4_K> {
             c[4 + i] = v1[i];
         }
     }
-    QMM_DEV void unpack(int g)
+    QMM_DEV void unpack(const MoeMatrix&, int g)
     {
         const int sh = 16 * (g & 1);
         const uint32_t a = hd[1] >> sh, b = hd[2] >> sh, e = hd[3] >> sh;
@@ -379,7 +379,7 @@ struct Unit<FMT_Q6_K> {
         s1 = load4(p + 196 + 8 * (g >> 1));
         d = load2(p + 208);
     }
-    QMM_DEV void unpack(int g)
+    QMM_DEV void unpack(const MoeMatrix&, int g)
     {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -409,21 +409,43 @@ struct Unit<FMT_Q6_K> {
 
 // ------------------------------------------------------------ activations
 
-QMM_DEV void act4(const void* x, int type, int64_t i, float v[4])
-{
-    if (type == TYPE_F32) {
-        const f32x4_t t = *(const f32x4_t*)((const float*)x + i);
+// Four neighbouring activations as they are in memory (PL = 2: f32, PL = 1: two
+// bytes each), and as f32.  Loading and converting are apart so that a wave
+// can have many loads in flight.
+template <int PL>
+struct Raw4 {
+    uint32_t r[2 * PL];
+    QMM_DEV void clear()
+    {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = t[k];
-    } else {
-        const u32x2_t t = *(const u32x2_t*)((const uint16_t*)x + i);
+        for (int k = 0; k < 2 * PL; ++k) r[k] = 0;
+    }
+    QMM_DEV void load(const void* x, int64_t i)
+    {
+        if constexpr (PL == 2) {
+            const u32x4_t t = *(const u32x4_t*)((const uint32_t*)x + i);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            v[2 * k] = type == TYPE_F16 ? f16lo(t[k]) : f32_of(t[k] << 16);
-            v[2 * k + 1] = type == TYPE_F16 ? f16hi(t[k]) : f32_of(t[k] & 0xffff0000u);
+            for (int k = 0; k < 4; ++k) r[k] = t[k];
+        } else {
+            const u32x2_t t = *(const u32x2_t*)((const uint16_t*)x + i);
+            r[0] = t[0];
+            r[1] = t[1];
         }
     }
-}
+    QMM_DEV void values(int type, float v[4]) const
+    {
+        if constexpr (PL == 2) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = f32_of(r[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                v[2 * k] = type == TYPE_F16 ? f16lo(r[k]) : f32_of(r[k] << 16);
+                v[2 * k + 1] = type == TYPE_F16 ? f16hi(r[k]) : f32_of(r[k] & 0xffff0000u);
+            }
+        }
+    }
+};
 
 // The power of two that brings values of magnitude up to amax into f16's
 // range, the largest to [2^14, 2^15) (less where that would need a factor
