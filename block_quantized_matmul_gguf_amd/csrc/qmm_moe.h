@@ -8,7 +8,9 @@
 
 namespace qmm {
 
-enum { FMT_W4 = 100 };  // 4-bit codes, scales and zero points in planes of their own
+// 4-bit codes, scales and zero points in planes of their own; groups of any
+// multiple of 32 values, or of 128
+enum { FMT_W4 = 100, FMT_W4_WIDE = 101 };
 enum { MOE_RUN = 0, MOE_GLU = 1, MOE_COMBINE = 2 };
 enum { TYPE_F32 = 0, TYPE_F16 = 1, TYPE_BF16 = 2 };
 
@@ -73,6 +75,7 @@ QMM_MOE_DECLARE(q5_0)
 QMM_MOE_DECLARE(q4_k)
 QMM_MOE_DECLARE(q6_k)
 QMM_MOE_DECLARE(w4)
+QMM_MOE_DECLARE(w4_wide)
 #undef QMM_MOE_DECLARE
 
 }  // namespace qmm

@@ -91,7 +91,8 @@ __global__ __launch_bounds__(256) void moe_combine(MoeArgs a, const float* prod)
             const int e = a.ids[p];
             if (e >= 0 && e < a.E) v = fmaf(a.weights[p], prod[p * a.N + n], v);
         }
-        store_out(a.y, a.y_type, i, v);
+        if (a.y_type == TYPE_F32) store_out<true>(a.y, a.y_type, i, v);
+        else store_out<false>(a.y, a.y_type, i, v);
     }
 }
 
@@ -112,7 +113,7 @@ MoePlan plan_of(const MoeArgs& a)
 {
     MoePlan p = {};
     const int64_t P = a.T * a.top_k;
-    const bool dense = a.fmt == FMT_W4;
+    const bool dense = a.fmt == FMT_W4 || a.fmt == FMT_W4_WIDE;
     if (a.T == 1) p.path = PATH_ONE;
     else if (P > 24 * (int64_t)(dense ? 4 : a.E)) p.path = PATH_TILE;
     else p.path = dense || P > 64 ? PATH_STREAM : PATH_SCAN;
@@ -244,6 +245,7 @@ bool off16(const void* p) { return (uintptr_t)p % 16 != 0; }
     case FMT_Q5_0: return CALL(q5_0);           \
     case FMT_Q4_K: return CALL(q4_k);           \
     case FMT_Q6_K: return CALL(q6_k);           \
+    case FMT_W4_WIDE: return CALL(w4_wide);     \
     default: return CALL(w4);                   \
     }
 hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s)
@@ -340,7 +342,7 @@ extern "C" int qmatmul_experts_combine(int format, int64_t E, int64_t N, int64_t
 static MoeArgs w4_args(int64_t N, int64_t K, int64_t M, int64_t group, int type)
 {
     MoeArgs a = {};
-    a.fmt = FMT_W4;
+    a.fmt = group % 128 ? FMT_W4 : FMT_W4_WIDE;
     a.op = MOE_RUN;
     a.type = type;
     a.E = 1;

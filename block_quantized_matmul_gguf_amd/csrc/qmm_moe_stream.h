@@ -59,7 +59,7 @@ QMM_DEV StreamRows scan_rows(const MoeArgs& a, int P, int p, int lane, int* list
     return s;
 }
 
-template <int FMT, int PL, bool ONE, int NT, bool GLU>
+template <int FMT, int PL, bool ONE, int NT, bool GLU, bool WIDE>
 __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 {
     using U = Unit<FMT>;
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
         if constexpr (GLU) v = rows.e < 0 ? 0.0f : activate(v, a.act) * w;
         // the pair of row `row`: lane `row` of this wave holds it
         const int pair = ONE ? rows.pair : __shfl(rows.pair, row);
-        if (row < rows.cnt && n < a.N) store_out(a.y, a.y_type, (int64_t)pair * a.N + n, v);
+        if (row < rows.cnt && n < a.N) store_out<WIDE>(a.y, a.y_type, (int64_t)pair * a.N + n, v);
     }
 }
 
@@ -340,11 +340,11 @@ hipError_t launch_stream_t(const MoeArgs& a, int waves, hipStream_t s)
     const int64_t P = a.T * a.top_k;
     const int64_t ny = ONE ? (a.op == MOE_COMBINE ? a.T : P) : !a.ids ? (a.T + 15) / 16 : a.tiles ? a.max_tiles : P;
     const dim3 block(64 * waves);
-    if (a.op == MOE_GLU) {
-        moe_stream<FMT, PL, ONE, 2, true><<<dim3((unsigned)((a.N + 15) / 16), (unsigned)ny), block, 0, s>>>(a);
-    } else {
-        moe_stream<FMT, PL, ONE, 1, false><<<dim3((unsigned)((a.N + 15) / 16), (unsigned)ny), block, 0, s>>>(a);
-    }
+    constexpr bool experts = FMT != FMT_W4 && FMT != FMT_W4_WIDE;
+    const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)ny);
+    if (experts && a.op == MOE_GLU) moe_stream<FMT, PL, ONE, experts ? 2 : 1, experts, PL == 2><<<grid, block, 0, s>>>(a);
+    else if (PL == 2 || a.y_type != TYPE_F32) moe_stream<FMT, PL, ONE, 1, false, PL == 2><<<grid, block, 0, s>>>(a);
+    else moe_stream<FMT, PL, ONE, 1, false, PL == 2 || (experts && !ONE)><<<grid, block, 0, s>>>(a);  // a combine's products
     return hipGetLastError();
 }
 

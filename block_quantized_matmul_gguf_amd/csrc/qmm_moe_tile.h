@@ -1,18 +1,17 @@
 // qmm_moe_tile.h -- products of many activation rows with an expert's weights,
 // bound by the matrix cores and by the vector work that feeds them.
 //
-// A workgroup multiplies MT * 16 pairs of one expert with 128 weight rows
-// (GLU: 64 rows of the gate and the same 64 of the up matrix).  Its four waves
-// own 32 of them each: a weight row is decoded once per workgroup, from
-// registers, and never staged; the activations, prepared once per call in
-// operand order, are copied straight into LDS one step (128 values of K) ahead
-// and read by all four waves.
+// A workgroup multiplies MT * 16 pairs of one expert with 32 weight rows per
+// wave (GLU: 16 rows of the gate and the same 16 of the up matrix): a weight
+// row is decoded once per workgroup, from registers, and never staged.  The
+// activations, prepared once per call in operand order, are copied straight
+// into LDS, one step (128 values of K) being 32 KB, two steps ahead of their
+// use, and read by every wave; the next unit's weights are loaded while one is
+// multiplied.
 #pragma once
 #include "qmm_moe_unit.h"
 
 namespace qmm {
-
-constexpr int TILE_N = 128;
 
 typedef const __attribute__((address_space(1))) void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;
@@ -23,17 +22,21 @@ QMM_DEV void copy_to_lds(const void* p, void* base)
     __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)base, 16, 0, 0);
 }
 
-template <int FMT, int PL, int MT, bool GLU>
-__global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
+template <int FMT, int PL, int MT, int NW, bool GLU, bool WIDE>
+__global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 {
     using U = Unit<FMT>;
-    constexpr int UNIT = U::UNIT, H = U::HALVES, MW = MT / 4;  // row groups a wave copies
-    __shared__ __align__(16) _Float16 ta[2][PL][MT][4][64][8];
+    constexpr int UNIT = U::UNIT, H = U::HALVES;
+    constexpr int RING = 3;              // steps in LDS: one in use, two on their way
+    constexpr int GW = PL * MT / NW;     // row groups (of one plane) a wave copies,
+    constexpr int COPIES = GW * 4;       // 16 bytes per lane each, in a step
+    static_assert(PL * MT % NW == 0 && MT / 2 <= NW, "waves share the copies evenly");
+    __shared__ __align__(16) _Float16 ta[RING][PL * MT][4][64][8];
     __shared__ __align__(16) _Float16 ts[U::MINS ? 2 : 1][U::MINS ? MT : 1][2][16][8];
 
     const int lane = (int)__lane_id(), r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    constexpr int BN = GLU ? TILE_N / 2 : TILE_N;
+    constexpr int BN = NW * (GLU ? 16 : 32);
     const int nb = (int)((a.N + BN - 1) / BN);
 
     // Workgroups go to the eight XCDs in turn.  Experts: an XCD takes all
@@ -76,10 +79,13 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
     if (t.e >= 0) {
         const int units = (int)(a.Kp / UNIT), steps = units * H;
         const int64_t plane = a.x_rows * a.Kp;
-        const _Float16* src[MW];
+        const _Float16* src[GW];
         const _Float16* ssrc = nullptr;
 #pragma unroll
-        for (int i = 0; i < MW; ++i) src[i] = a.xp + (int64_t)row_of(pair_of(wave * MW + i)) * 128 + g * 8;
+        for (int i = 0; i < GW; ++i) {
+            const int q = wave * GW + i;  // plane q / MT, rows of group q % MT
+            src[i] = a.xp + (q / MT) * plane + (int64_t)row_of(pair_of(q % MT)) * 128 + g * 8;
+        }
         // sums: 16 halves per row and unit; waves below MT / 2 copy [m][p][r] of m = 2 wave, 2 wave + 1
         if constexpr (U::MINS) {
             const int sm = (wave * 2 + (lane >> 5)) & (MT - 1);
@@ -90,15 +96,13 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
         // rows a power of two apart would ask the same L2 channel.
         const int first = (int)((b * 5 + tile) % units);
         auto place_of = [&](int u) { return u + first < units ? u + first : u + first - units; };
-        auto stage = [&](int s) {  // step s of the walk
+        auto stage = [&](int s, int buf) {  // step s of the walk
             const int64_t su = place_of(s / H), at = su * H + s % H;
 #pragma unroll
-            for (int p = 0; p < PL; ++p)
+            for (int i = 0; i < GW; ++i)
 #pragma unroll
-                for (int i = 0; i < MW; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        copy_to_lds(src[i] + p * plane + at * a.x_rows * 128 + j * 32, &ta[s & 1][p][wave * MW + i][j][0][0]);
+                for (int j = 0; j < 4; ++j)
+                    copy_to_lds(src[i] + at * a.x_rows * 128 + j * 32, &ta[buf][wave * GW + i][j][0][0]);
             if constexpr (U::MINS) {
                 if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + su * a.x_rows * 16, &ts[(s >> 1) & 1][wave * 2][0][0][0]);
             }
@@ -115,25 +119,34 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
                 un[c].load(mat, n[c], place_of(u), g);
             }
         };
+        // Loads and copies are issued in every step, past the last one again for it, so that their
+        // number in flight is known: weights first, then copies.
         Unit<FMT> cur[2], next[2];
-        stage(0);
+        stage(0, 0);
         fetch(0, next);
+        stage(min(1, steps - 1), 1);
+        int buf = 0;
         for (int u = 0; u < units; ++u) {
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int s = u * H + h;
-                vm_wait<0>();
-                __syncthreads();
-                if (s + 1 < steps) stage(s + 1);
+                // Operations retire in order: once no more than one step's copies are outstanding,
+                // step s and the weights of its unit have landed.
+                vm_wait<COPIES>();
+                lgkm_wait0();
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");  // no LDS access moves across
+                // everyone is past step s - 1, whose buffer is free
                 if (h == 0) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         cur[c] = next[c];
                         cur[c].unpack(mat, g);
                     }
-                    if (u + 1 < units) fetch(u + 1, next);
+                    fetch(min(u + 1, units - 1), next);
                 }
-                step<FMT, PL, MT, 2>(cur, h, [&](int m, int j, int p) { return *(const half8_t*)&ta[s & 1][p][m][j][lane][0]; }, acc);
+                stage(min(s + 2, steps - 1), buf == 0 ? 2 : buf - 1);
+                step<FMT, PL, MT, 2>(cur, h, [&](int m, int j, int p) { return *(const half8_t*)&ta[buf][p * MT + m][j][lane][0]; }, acc);
                 if constexpr (U::MINS) {
                     if (h == 0) {
 #pragma unroll
@@ -149,9 +162,12 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
                         }
                     }
                 }
+                buf = buf == 2 ? 0 : buf + 1;
             }
         }
     }
+
+    vm_wait<0>();  // copies past the last step: none may land in LDS that is no longer this workgroup's
 
     // sums 4g + i of row group m are those of rows 16 m + 4 g + i
 #pragma unroll
@@ -168,12 +184,12 @@ __global__ __launch_bounds__(256, 2) void moe_tile(MoeArgs a)
             if constexpr (GLU) {
                 const int64_t n = n0 + wave * 16 + r;
                 const float v = t.e < 0 ? 0.0f : activate(acc[m][0][i] * f, a.act) * (acc[m][1][i] * f);
-                if (n < a.N) store_out(a.y, a.y_type, p * a.N + n, v);
+                if (n < a.N) store_out<WIDE>(a.y, a.y_type, p * a.N + n, v);
             } else {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int64_t n = n0 + wave * 32 + c * 16 + r;
-                    if (n < a.N) store_out(a.y, a.y_type, p * a.N + n, acc[m][c][i] * f);
+                    if (n < a.N) store_out<WIDE>(a.y, a.y_type, p * a.N + n, acc[m][c][i] * f);
                 }
             }
         }
@@ -241,13 +257,16 @@ __global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
     }
 }
 
-template <int FMT, int PL, int MT>
+template <int FMT, int PL, int MT, int NW>
 hipError_t launch_tile_t(const MoeArgs& a, hipStream_t s)
 {
-    const int64_t bn = a.op == MOE_GLU ? TILE_N / 2 : TILE_N, nb = (a.N + bn - 1) / bn;
+    constexpr bool experts = FMT != FMT_W4 && FMT != FMT_W4_WIDE;
+    const int64_t bn = NW * (a.op == MOE_GLU ? 16 : 32), nb = (a.N + bn - 1) / bn;
     const int64_t grid = a.ids ? (a.max_tiles + 7) / 8 * 8 * nb : (nb + 7) / 8 * 8 * a.max_tiles;
-    if (a.op == MOE_GLU) moe_tile<FMT, PL, MT, true><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
-    else moe_tile<FMT, PL, MT, false><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
+    const dim3 g((unsigned)grid), block(64 * NW);
+    if (experts && a.op == MOE_GLU) moe_tile<FMT, PL, MT, NW, experts, PL == 2><<<g, block, 0, s>>>(a);
+    else if (PL == 2 || a.y_type != TYPE_F32) moe_tile<FMT, PL, MT, NW, false, PL == 2><<<g, block, 0, s>>>(a);
+    else moe_tile<FMT, PL, MT, NW, false, PL == 2 || experts><<<g, block, 0, s>>>(a);  // a combine's products
     return hipGetLastError();
 }
 
@@ -264,7 +283,7 @@ hipError_t launch_prep_t(const MoeArgs& a, hipStream_t s)
     hipError_t launch_prep_##NAME(const MoeArgs& a, hipStream_t s) { return launch_prep_t<FMT>(a, s); } \
     hipError_t launch_tile_##NAME(const MoeArgs& a, hipStream_t s)                                      \
     {                                                                                                   \
-        return a.type == TYPE_F32 ? launch_tile_t<FMT, 2, 4>(a, s) : launch_tile_t<FMT, 1, 8>(a, s);    \
+        return a.type == TYPE_F32 ? launch_tile_t<FMT, 2, 4, 8>(a, s) : launch_tile_t<FMT, 1, 8, 8>(a, s);\
     }
 
 }  // namespace qmm

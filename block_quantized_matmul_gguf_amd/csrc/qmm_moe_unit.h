@@ -129,6 +129,9 @@ struct Unit32 {
         const int e = k & 31, i = (e & 3) | ((e & 16) >> 2);  // number within the operand's eight
         return (((k >> 5) * 4 + ((e >> 2) & 3)) << 3) | (FMT == FMT_Q8_0 ? i : nib_perm(i));
     }
+    // Block 4u + g, or the row's last: past the end activations are zero, and a
+    // load that always happens keeps the wave's count of loads in flight known.
+    static QMM_DEV int block_of(const MoeMatrix& m, int u, int g) { return min(4 * u + g, m.blocks - 1); }
     float s[4];  // scales of the four blocks
     QMM_DEV float scale(int j) const { return s[j]; }
     QMM_DEV void gather_scales(float own)
@@ -140,9 +143,22 @@ struct Unit32 {
     }
 };
 
-// four nibbles of v (bits 0..3 of its bytes after the shift) in the order 0,2
-// (first pair) and 1,3, as 1024 + q
-QMM_DEV uint32_t nib_pair(uint32_t v, int shift) { return ((v >> shift) & 0x000f000fu) | 0x64006400u; }
+// Two nibbles of v as f16 in one dword: bits 0..3 and 16..19 as 1024 + q
+// (nib_lo), bits 4..7 and 20..23 as 1024 + 16 q (nib_hi: no shift; the fused
+// multiply-add that takes the 1024 off divides by 16 as well).  The f16
+// pattern is kept in a vector register, so masking and joining are one
+// instruction.
+QMM_DEV uint32_t f16_pattern()
+{
+    uint32_t c = 0x64006400u;
+    asm("" : "+v"(c));
+    return c;
+}
+QMM_DEV half2_t nib_lo(uint32_t v, uint32_t pattern) { return half2_of((v & 0x000f000fu) | pattern); }
+QMM_DEV half2_t nib_hi(uint32_t v, uint32_t pattern) { return half2_of((v & 0x00f000f0u) | pattern); }
+QMM_DEV half2_t both(float v) { return half2_t{(_Float16)v, (_Float16)v}; }
+// p / 16 + bias
+QMM_DEV half2_t sixteenth(half2_t p, half2_t bias) { return __builtin_elementwise_fma(p, both(0.0625f), bias); }
 
 template <>
 struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
@@ -150,16 +166,10 @@ struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
     static QMM_DEV int slot(int i) { return i; }
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
-        const int b = 4 * u + g;
-        const uint8_t* p = m.w + n * m.row_bytes + b * 34;
-        d = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = 0;
-        if (b < m.blocks) {
-            load16(p + 2, c);
-            load16(p + 18, c + 4);
-            d = load2(p);
-        }
+        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 34;
+        load16(p + 2, c);
+        load16(p + 18, c + 4);
+        d = load2(p);
     }
     QMM_DEV void unpack(const MoeMatrix&, int)
     {
@@ -182,15 +192,9 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
     static QMM_DEV int slot(int i) { return nib_perm(i); }
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
-        const int b = 4 * u + g;
-        const uint8_t* p = m.w + n * m.row_bytes + b * 18;
-        d = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = 0;
-        if (b < m.blocks) {
-            load16(p + 2, c);
-            d = load2(p);
-        }
+        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 18;
+        load16(p + 2, c);
+        d = load2(p);
     }
     QMM_DEV void unpack(const MoeMatrix&, int)
     {
@@ -199,10 +203,9 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
     }
     QMM_DEV half8_t operand(int, int j, int) const
     {
-        const half2_t bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-        const uint32_t v = c[j];
-        return join8(half2_of(nib_pair(v, 0)) + bias, half2_of(nib_pair(v, 8)) + bias, half2_of(nib_pair(v, 4)) + bias,
-                     half2_of(nib_pair(v, 12)) + bias);
+        const uint32_t v = c[j], w = v >> 8, k = f16_pattern();
+        return join8(nib_lo(v, k) + both(-1032.0f), nib_lo(w, k) + both(-1032.0f), sixteenth(nib_hi(v, k), both(-72.0f)),
+                     sixteenth(nib_hi(w, k), both(-72.0f)));
     }
 };
 
@@ -212,17 +215,10 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
     static QMM_DEV int slot(int i) { return nib_perm(i); }
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
-        const int b = 4 * u + g;
-        const uint8_t* p = m.w + n * m.row_bytes + b * 22;
-        d = 0;
-        qh = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = 0;
-        if (b < m.blocks) {
-            load16(p + 6, c);
-            qh = load4(p + 2);
-            d = load2(p);
-        }
+        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 22;
+        load16(p + 6, c);
+        qh = load4(p + 2);
+        d = load2(p);
     }
     // h[j]: the fifth bits of this lane group's values of block j, the first
     // four in bits 0..3, the last four in bits 16..19
@@ -236,13 +232,40 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
     }
     QMM_DEV half8_t operand(int, int j, int) const
     {
-        const half2_t bias = {(_Float16)-1040.0f, (_Float16)-1040.0f};
-        const uint32_t v = c[j], lo = h[j] & 15u, hi = h[j] >> 16;
-        // bits 0 and 2 of a group of four, to bits 4 and 20
-        const uint32_t k = (1u << 4) | (1u << 18), m = 0x00100010u;
-        const uint32_t p0 = nib_pair(v, 0) | (__umul24(lo, k) & m), p1 = nib_pair(v, 8) | (__umul24(lo >> 1, k) & m);
-        const uint32_t p2 = nib_pair(v, 4) | (__umul24(hi, k) & m), p3 = nib_pair(v, 12) | (__umul24(hi >> 1, k) & m);
-        return join8(half2_of(p0) + bias, half2_of(p1) + bias, half2_of(p2) + bias, half2_of(p3) + bias);
+        const uint32_t v = c[j], w = v >> 8, k = f16_pattern(), lo = h[j] & 15u, hi = h[j] >> 16;
+        // bits 0 and 2 of a group of four go to bits 4 and 20 (nib_lo) or 8 and 24 (nib_hi)
+        const uint32_t fl = (1u << 4) | (1u << 18), fh = (1u << 8) | (1u << 22);
+        const half2_t p0 = nib_lo(v, k | (__umul24(lo, fl) & 0x00100010u)), p1 = nib_lo(w, k | (__umul24(lo >> 1, fl) & 0x00100010u));
+        const half2_t p2 = nib_hi(v, k | (__umul24(hi, fh) & 0x01000100u)), p3 = nib_hi(w, k | (__umul24(hi >> 1, fh) & 0x01000100u));
+        return join8(p0 + both(-1040.0f), p1 + both(-1040.0f), sixteenth(p2, both(-80.0f)), sixteenth(p3, both(-80.0f)));
+    }
+};
+
+// Codes of W4 rows: eight neighbours per dword, lowest nibble first.
+struct UnitW4 {
+    static QMM_DEV int o0(int, int j, int g) { return 32 * j + 8 * g; }
+    static QMM_DEV int o1(int, int j, int g) { return 32 * j + 8 * g + 4; }
+    static QMM_DEV int slot(int i) { return (i >> 1) | ((i & 1) << 2); }
+    static QMM_DEV int place(int k) { return (k & ~7) | ((k & 3) << 1) | ((k >> 2) & 1); }
+    // -(1024 + z) and -(64 + z), in both halves of a dword
+    static QMM_DEV uint32_t bias_lo(uint32_t z) { return (0xe400u | z) * 0x00010001u; }
+    static QMM_DEV half2_t bias_hi(half2_t lo) { return lo + both(960.0f); }
+    static QMM_DEV half8_t values(uint32_t v, half2_t lo, half2_t hi)
+    {
+        const uint32_t w = v >> 8, k = f16_pattern();
+        return join8(nib_lo(v, k) + lo, sixteenth(nib_hi(v, k), hi), nib_lo(w, k) + lo, sixteenth(nib_hi(w, k), hi));
+    }
+    static QMM_DEV void scale_at(const MoeMatrix& m, int64_t n, int block, uint32_t& d, uint32_t& z)
+    {
+        const int64_t at = n * m.groups + (m.group_magic ? (int)__umulhi((uint32_t)block, m.group_magic) : block);
+        // as they are: a conversion here would wait for the load
+        if (m.scale_type == TYPE_F32) d = ((const uint32_t*)m.scales)[at];
+        else d = ((const uint16_t*)m.scales)[at];
+        if (m.zeros) z = m.zeros[at];
+    }
+    static QMM_DEV float scale_value(const MoeMatrix& m, uint32_t d)
+    {
+        return m.scale_type == TYPE_F16 ? f16lo(d) : f32_of(m.scale_type == TYPE_F32 ? d : d << 16);
     }
 };
 
@@ -250,44 +273,62 @@ template <>
 struct Unit<FMT_W4> : Unit32<FMT_W4> {
     uint32_t c[4], d, z;
     half2_t bias[4];
-    static QMM_DEV int o0(int, int j, int g) { return 32 * j + 8 * g; }
-    static QMM_DEV int o1(int, int j, int g) { return 32 * j + 8 * g + 4; }
-    static QMM_DEV int slot(int i) { return (i >> 1) | ((i & 1) << 2); }
-    static QMM_DEV int place(int k) { return (k & ~7) | ((k & 3) << 1) | ((k >> 2) & 1); }
+    static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
+    static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
+    static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
+    static QMM_DEV int place(int k) { return UnitW4::place(k); }
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
-        const int b = 4 * u + g;
-        d = 0;
+        const int b = block_of(m, u, g);
+        const u32x4_t v = *(const u32x4_t*)(m.w + n * m.row_bytes + 16 * b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = v[i];
         z = 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = 0;
-        if (b < m.blocks) {
-            const u32x4_t v = *(const u32x4_t*)(m.w + n * m.row_bytes + 16 * b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[i] = v[i];
-            const int64_t at = n * m.groups + (m.group_magic ? (int)__umulhi((uint32_t)b, m.group_magic) : b);
-            // as they are: a conversion here would wait for the load
-            if (m.scale_type == TYPE_F32) d = ((const uint32_t*)m.scales)[at];
-            else d = ((const uint16_t*)m.scales)[at];
-            if (m.zeros) z = m.zeros[at];
-        }
+        UnitW4::scale_at(m, n, b, d, z);
     }
     QMM_DEV void unpack(const MoeMatrix& m, int)
     {
         transpose4(c);
-        gather_scales(m.scale_type == TYPE_F16 ? f16lo(d) : f32_of(m.scale_type == TYPE_F32 ? d : d << 16));
-        // -(1024 + z) in both halves
+        gather_scales(UnitW4::scale_value(m, d));
         uint32_t o[4];
-        gather4((0xe400u | z) * 0x00010001u, o);
+        gather4(UnitW4::bias_lo(z), o);
 #pragma unroll
         for (int j = 0; j < 4; ++j) bias[j] = half2_of(o[j]);
     }
-    QMM_DEV half8_t operand(int, int j, int) const
+    QMM_DEV half8_t operand(int, int j, int) const { return UnitW4::values(c[j], bias[j], UnitW4::bias_hi(bias[j])); }
+};
+
+// W4 with groups of whole units (group a multiple of 128): one scale and zero
+// point per unit, so its four products share an accumulator (a quarter of the
+// multiply-adds) and nothing is gathered.
+template <>
+struct Unit<FMT_W4_WIDE> {
+    static constexpr int UNIT = 128, HALVES = 1, PARTS = 1;
+    static constexpr bool CHAIN = true, MINS = false;
+    static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
+    static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
+    static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
+    static QMM_DEV int place(int k) { return UnitW4::place(k); }
+    uint32_t c[4], d, z;
+    float s;
+    half2_t lo, hi;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
-        const uint32_t v = c[j];
-        return join8(half2_of(nib_pair(v, 0)) + bias[j], half2_of(nib_pair(v, 4)) + bias[j], half2_of(nib_pair(v, 8)) + bias[j],
-                     half2_of(nib_pair(v, 12)) + bias[j]);
+        const u32x4_t v = *(const u32x4_t*)(m.w + n * m.row_bytes + 64 * u + 16 * g);
+        z = 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = v[i];
+        UnitW4::scale_at(m, n, 4 * u, d, z);
     }
+    QMM_DEV void unpack(const MoeMatrix& m, int)
+    {
+        transpose4(c);
+        s = UnitW4::scale_value(m, d);
+        lo = half2_of(UnitW4::bias_lo(z));
+        hi = UnitW4::bias_hi(lo);
+    }
+    QMM_DEV half8_t operand(int, int j, int) const { return UnitW4::values(c[j], lo, hi); }
+    QMM_DEV float scale(int) const { return s; }
 };
 
 // ------------------------------------------------------- a super-block
@@ -302,7 +343,7 @@ struct Unit<FMT_Q4_K> {
     static QMM_DEV int slot(int i) { return nib_perm(i); }
     static QMM_DEV int place(int k) { return ((((k >> 5) & 1) * 4 + ((k >> 3) & 3)) * 4 + (k >> 6)) * 8 + nib_perm(k & 7); }
     uint32_t c[8], hd[4];
-    half2_t sc[2], off[2];  // sub-block scale, -1024 * scale
+    half2_t sc[2], off[2];  // sub-block scale and -1024 times it; the second's / 16 and -64 times it
     uint32_t mn;            // the two minima, one per byte
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
@@ -324,18 +365,16 @@ struct Unit<FMT_Q4_K> {
         mn = g < 2 ? b & 0x3f3fu : ((e >> 4) & 0x0f0fu) | ((b >> 2) & 0x3030u);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const _Float16 f = (_Float16)(float)((s2 >> (8 * i)) & 0xffu);
-            sc[i] = half2_t{f, f};
-            off[i] = sc[i] * half2_t{(_Float16)-1024.0f, (_Float16)-1024.0f};
+            const half2_t f = both((float)((s2 >> (8 * i)) & 0xffu));
+            sc[i] = f * both(i ? 0.0625f : 1.0f);
+            off[i] = f * both(i ? -64.0f : -1024.0f);
         }
     }
     QMM_DEV half8_t operand(int h, int j, int) const
     {
-        const uint32_t v = c[2 * j] >> (4 * h), w = c[2 * j + 1] >> (4 * h);
-        return join8(__builtin_elementwise_fma(half2_of(nib_pair(v, 0)), sc[h], off[h]),
-                     __builtin_elementwise_fma(half2_of(nib_pair(v, 8)), sc[h], off[h]),
-                     __builtin_elementwise_fma(half2_of(nib_pair(w, 0)), sc[h], off[h]),
-                     __builtin_elementwise_fma(half2_of(nib_pair(w, 8)), sc[h], off[h]));
+        const uint32_t k = f16_pattern(), v = c[2 * j], w = c[2 * j + 1];
+        auto part = [&](uint32_t x) { return __builtin_elementwise_fma(h ? nib_hi(x, k) : nib_lo(x, k), sc[h], off[h]); };
+        return join8(part(v), part(v >> 8), part(w), part(w >> 8));
     }
     QMM_DEV float scale(int) const { return f16lo(hd[0]); }
     // against {S_2g hi, S_2g+1 hi, S_2g lo, S_2g+1 lo, 0, ..}, S the sub-block sums / 32
@@ -384,9 +423,8 @@ struct Unit<FMT_Q6_K> {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int v = (int)(int8_t)(((t < 2 ? s0 : s1) >> (16 * (t & 1) + 8 * (g & 1))) & 0xffu);
-            const _Float16 a = (_Float16)(float)(v & ~15), b = (_Float16)(float)(v & 15);
-            hi[t] = half2_t{a, a};
-            lo[t] = half2_t{b, b};
+            hi[t] = both((float)(v & ~15));
+            lo[t] = both((float)(v & 15));
         }
     }
     QMM_DEV half8_t operand(int h, int j, int part) const
@@ -520,6 +558,9 @@ QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[MT][NT]
                 for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(s, d[m][t][i], acc[m][t][i]);
         }
     } else {
+        // a product's sums are scaled while the next ones are formed
+        f32x4_t d[2][NT];
+        float s[2][NT];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             half8_t b[NT];
@@ -527,29 +568,42 @@ QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[MT][NT]
             for (int t = 0; t < NT; ++t) b[t] = un[t].operand(h, j, 0);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                f32x4_t d[NT];
+                const int at = (j * MT + m) & 1;
 #pragma unroll
                 for (int p = 0; p < PL; ++p) {
                     const half8_t a = A(m, j, p);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) d[t] = mfma(a, b[t], p ? d[t] : f32x4_t{0, 0, 0, 0});
+                    for (int t = 0; t < NT; ++t) d[at][t] = mfma(a, b[t], p ? d[at][t] : f32x4_t{0, 0, 0, 0});
                 }
+                const int q = (j * MT + m - 1) % MT;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const float s = un[t].scale(j);
+                    s[at][t] = un[t].scale(j);
+                    if (j + m > 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(s, d[t][i], acc[m][t][i]);
+                        for (int i = 0; i < 4; ++i) acc[q][t][i] = fmaf(s[at ^ 1][t], d[at ^ 1][t][i], acc[q][t][i]);
+                    }
                 }
             }
         }
+        constexpr int last = (4 * MT - 1) & 1;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[MT - 1][t][i] = fmaf(s[last][t], d[last][t][i], acc[MT - 1][t][i]);
     }
 }
 
+// Rounds v to the output type: WIDE f32, else f16 or bf16.
+template <bool WIDE>
 QMM_DEV void store_out(void* y, int type, int64_t i, float v)
 {
-    if (type == TYPE_F32) ((float*)y)[i] = v;
-    else if (type == TYPE_F16) ((_Float16*)y)[i] = (_Float16)v;
-    else ((__bf16*)y)[i] = (__bf16)v;
+    if constexpr (WIDE) {
+        ((float*)y)[i] = v;
+    } else {
+        const uint16_t h = f16bits(v), b = __builtin_bit_cast(uint16_t, (__bf16)v);
+        ((uint16_t*)y)[i] = type == TYPE_F16 ? h : b;
+    }
 }
 
 // act 0: v / (1 + e^-v); 1: 0.5 v (1 + tanh t) = v / (1 + e^-2t), t = sqrt(2/pi) (v + 0.044715 v^3)
@@ -571,7 +625,7 @@ QMM_DEV MoeMatrix moe_matrix(const MoeArgs& a, const uint8_t* w)
     m.groups = 0;
     m.group_blocks = a.group_blocks;
     m.group_magic = a.group_magic;
-    if (a.fmt == FMT_W4) m.groups = m.blocks / a.group_blocks;
+    if (a.fmt == FMT_W4 || a.fmt == FMT_W4_WIDE) m.groups = m.blocks / a.group_blocks;
     return m;
 }
 

@@ -5,4 +5,6 @@
 namespace qmm {
 QMM_MOE_STREAM(w4, FMT_W4)
 QMM_MOE_TILE(w4, FMT_W4)
+QMM_MOE_STREAM(w4_wide, FMT_W4_WIDE)
+QMM_MOE_TILE(w4_wide, FMT_W4_WIDE)
 }  // namespace qmm
