@@ -99,9 +99,9 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
     }
     if (rows.cnt <= 0) return;  // the same in every wave
 
-    f32x4_t acc[1][NT];
+    f32x4_t acc[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[0][t] = f32x4_t{0, 0, 0, 0};
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4_t{0, 0, 0, 0};
 
     if (rows.e >= 0) {
         const int nslots = combine ? a.top_k : 1;
@@ -205,15 +205,15 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
                     if ((lane & 7) == 0) xsum[wave][lane >> 3] = sum;
                 }
                 wave_sync();
-                f32x4_t d[1][NT];
+                f32x4_t d[NT];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    d[0][t] = f32x4_t{0, 0, 0, 0};
+                    d[t] = f32x4_t{0, 0, 0, 0};
                     l.u[t].unpack(mat, g);
                 }
 #pragma unroll
                 for (int h = 0; h < H; ++h)
-                    step<FMT, PL, 1, NT>(l.u, h, [&](int, int j, int p) {
+                    step<FMT, PL, NT>(l.u, h, [&](int j, int p) {
                         return *(const half8_t*)&xw[p * UNIT + ((h * 4 + j) * 4 + g) * 8];
                     }, d);
                 if constexpr (U::MINS) {
@@ -222,11 +222,11 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const f32x4_t q = mfma(sa, l.u[t].mins(), f32x4_t{0, 0, 0, 0});
-                        d[0][t][0] = fmaf(l.u[t].mins_scale(), q[0], d[0][t][0]);
+                        d[t][0] = fmaf(l.u[t].mins_scale(), q[0], d[t][0]);
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < NT; ++t) acc[0][t][0] = fmaf(l.w, inv * d[0][t][0], acc[0][t][0]);
+                for (int t = 0; t < NT; ++t) acc[t][0] = fmaf(l.w, inv * d[t][0], acc[t][0]);
                 wave_sync();  // the next item's values go where these were
             } else {
                 float v[H][4][8];
@@ -269,14 +269,14 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
                         }
                         split8<PL>(v[h][j], xa[h][j]);
                     }
-                f32x4_t d[1][NT];
+                f32x4_t d[NT];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    d[0][t] = f32x4_t{0, 0, 0, 0};
+                    d[t] = f32x4_t{0, 0, 0, 0};
                     l.u[t].unpack(mat, g);
                 }
 #pragma unroll
-                for (int h = 0; h < H; ++h) step<FMT, PL, 1, NT>(l.u, h, [&](int, int j, int p) { return xa[h][j][p]; }, d);
+                for (int h = 0; h < H; ++h) step<FMT, PL, NT>(l.u, h, [&](int j, int p) { return xa[h][j][p]; }, d);
                 if constexpr (U::MINS) {
                     sv[0] *= 0.03125f;
                     sv[1] *= 0.03125f;
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
                     for (int t = 0; t < NT; ++t) {
                         const f32x4_t q = mfma(sa, l.u[t].mins(), f32x4_t{0, 0, 0, 0});
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) d[0][t][i] = fmaf(l.u[t].mins_scale(), q[i], d[0][t][i]);
+                        for (int i = 0; i < 4; ++i) d[t][i] = fmaf(l.u[t].mins_scale(), q[i], d[t][i]);
                     }
                 }
                 // back to the rows' own scales (lane 4g + i holds that of sum i)
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
                 for (int i = 0; i < 4; ++i) {
                     const float f = __shfl(inv, 4 * g + i);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) acc[0][t][i] = fmaf(f, d[0][t][i], acc[0][t][i]);
+                    for (int t = 0; t < NT; ++t) acc[t][i] = fmaf(f, d[t][i], acc[t][i]);
                 }
             }
         };
@@ -311,10 +311,10 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         if constexpr (ONE) {
-            if (g == 0) red[wave][t][r] = acc[0][t][0];
+            if (g == 0) red[wave][t][r] = acc[t][0];
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) red[wave][t][(4 * g + i) * 16 + r] = acc[0][t][i];
+            for (int i = 0; i < 4; ++i) red[wave][t][(4 * g + i) * 16 + r] = acc[t][i];
         }
     }
     __syncthreads();

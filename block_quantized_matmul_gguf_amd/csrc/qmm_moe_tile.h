@@ -22,6 +22,80 @@ QMM_DEV void copy_to_lds(const void* p, void* base)
     __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)base, 16, 0, 0);
 }
 
+// One step (128 values) of two weight units against MT groups of 16 activation
+// rows in LDS (operands [part * MT + m][j][lane]): acc[m][t] += the step's sums.
+//
+// The step goes in eight pieces of four operand reads and eight products (two
+// pieces per product index j).  With the products of a piece run the next
+// piece's reads, the scaling of the piece before and half of the decoding for
+// the next j, issued between them: a matrix product occupies its unit for four
+// issue slots, three of which are free for vector work.
+constexpr int VALU_PER_PRODUCT = 6;
+
+template <int FMT, int PL, int MT>
+QMM_DEV void tile_step(const Unit<FMT> (&un)[2], int h, const _Float16* lds, f32x4_t (&acc)[MT][2])
+{
+    using U = Unit<FMT>;
+    static_assert(PL * MT == 8, "two pieces of four reads per product index");
+    constexpr int GM = MT / 2;  // row groups of a piece
+    half8_t a[2][GM][PL];
+    auto read = [&](int q, half8_t (&o)[GM][PL]) {
+#pragma unroll
+        for (int m = 0; m < GM; ++m)
+#pragma unroll
+            for (int p = 0; p < PL; ++p) o[m][p] = *(const half8_t*)(lds + ((p * MT + (q & 1) * GM + m) * 4 + (q >> 1)) * 512);
+    };
+    f32x4_t d[2][GM][2];
+    half8_t b[2][2][U::PARTS];
+    auto scale = [&](int q) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float s = un[t].scale(q >> 1);
+#pragma unroll
+            for (int m = 0; m < GM; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (q & 1) * GM + m;
+                    acc[r][t][i] = fmaf(s, d[q & 1][m][t][i], acc[r][t][i]);
+                }
+        }
+    };
+    auto decode = [&](int j, int t) {
+#pragma unroll
+        for (int k = 0; k < U::PARTS; ++k) b[j & 1][t][k] = un[t].operand(h, j, k);
+    };
+    read(0, a[0]);
+    decode(0, 0);
+    decode(0, 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const int j = q >> 1;
+        if (q < 7) read(q + 1, a[(q + 1) & 1]);
+#pragma unroll
+        for (int m = 0; m < GM; ++m)
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+#pragma unroll
+                for (int k = 0; k < U::PARTS; ++k)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const bool first = p + k == 0 && (!U::CHAIN || j == 0);
+                        d[q & 1][m][t] = mfma(a[q & 1][m][p], b[j & 1][t][k], first ? f32x4_t{0, 0, 0, 0} : d[q & 1][m][t]);
+                    }
+        if (q > 0 && (!U::CHAIN || q == 7)) scale(q - 1);
+        if (j < 3) decode(j + 1, q & 1);
+#pragma unroll
+        for (int i = 0; i < 8 * U::PARTS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read
+            __builtin_amdgcn_sched_group_barrier(0x002, VALU_PER_PRODUCT, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    scale(7);
+}
+
 template <int FMT, int PL, int MT, int NW, bool GLU, bool WIDE>
 __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 {
@@ -31,8 +105,9 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
     constexpr int GW = PL * MT / NW;     // row groups (of one plane) a wave copies,
     constexpr int COPIES = GW * 4;       // 16 bytes per lane each, in a step
     static_assert(PL * MT % NW == 0 && MT / 2 <= NW, "waves share the copies evenly");
-    __shared__ __align__(16) _Float16 ta[RING][PL * MT][4][64][8];
-    __shared__ __align__(16) _Float16 ts[U::MINS ? 2 : 1][U::MINS ? MT : 1][2][16][8];
+    // operands [RING][part * MT + m][j][lane][8], then (Q4_K) the sums of two units [2][m][2][16][8]
+    constexpr int STEP = PL * MT * 4 * 512, SUMS = U::MINS ? MT * 256 : 0;
+    __shared__ __align__(16) _Float16 lds[RING * STEP + 2 * SUMS];
 
     const int lane = (int)__lane_id(), r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -102,9 +177,9 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
             for (int i = 0; i < GW; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    copy_to_lds(src[i] + at * a.x_rows * 128 + j * 32, &ta[buf][wave * GW + i][j][0][0]);
+                    copy_to_lds(src[i] + at * a.x_rows * 128 + j * 32, lds + buf * STEP + ((wave * GW + i) * 4 + j) * 512);
             if constexpr (U::MINS) {
-                if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + su * a.x_rows * 16, &ts[(s >> 1) & 1][wave * 2][0][0][0]);
+                if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + su * a.x_rows * 16, lds + RING * STEP + ((s >> 1) & 1) * SUMS + wave * 512);
             }
         };
         const int64_t matrix = a.N * a.row_bytes;
@@ -141,17 +216,18 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         cur[c] = next[c];
+                        cur[c].pin();
                         cur[c].unpack(mat, g);
                     }
                     fetch(min(u + 1, units - 1), next);
                 }
                 stage(min(s + 2, steps - 1), buf == 0 ? 2 : buf - 1);
-                step<FMT, PL, MT, 2>(cur, h, [&](int m, int j, int p) { return *(const half8_t*)&ta[buf][p * MT + m][j][lane][0]; }, acc);
+                tile_step<FMT, PL, MT>(cur, h, lds + buf * STEP + lane * 8, acc);
                 if constexpr (U::MINS) {
                     if (h == 0) {
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            const u32x2_t q = *(const u32x2_t*)&ts[u & 1][m][g >> 1][r][(g & 1) * 4];
+                            const u32x2_t q = *(const u32x2_t*)(lds + RING * STEP + (u & 1) * SUMS + ((m * 2 + (g >> 1)) * 16 + r) * 8 + (g & 1) * 4);
                             const half8_t sa = join8(half2_of(q[0]), half2_of(q[1]), half2_of(0u), half2_of(0u));
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {

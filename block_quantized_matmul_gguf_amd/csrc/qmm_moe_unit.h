@@ -86,6 +86,16 @@ QMM_DEV uint32_t load2(const uint8_t* p)
     return v;
 }
 
+// Keeps the values in registers as they are up to here: nothing computed from
+// them moves ahead of this point (and with it the wait for their loads).
+template <int N>
+QMM_DEV void pin_regs(uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+QMM_DEV void pin_reg(uint32_t& v) { asm volatile("" : "+v"(v)); }
+
 QMM_DEV half8_t join8(half2_t a, half2_t b, half2_t c, half2_t d)
 {
     half8_t r;
@@ -171,6 +181,11 @@ struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
         load16(p + 18, c + 4);
         d = load2(p);
     }
+    QMM_DEV void pin()
+    {
+        pin_regs(c);
+        pin_reg(d);
+    }
     QMM_DEV void unpack(const MoeMatrix&, int)
     {
         transpose4(c);
@@ -196,6 +211,11 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
         load16(p + 2, c);
         d = load2(p);
     }
+    QMM_DEV void pin()
+    {
+        pin_regs(c);
+        pin_reg(d);
+    }
     QMM_DEV void unpack(const MoeMatrix&, int)
     {
         transpose4(c);
@@ -219,6 +239,12 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
         load16(p + 6, c);
         qh = load4(p + 2);
         d = load2(p);
+    }
+    QMM_DEV void pin()
+    {
+        pin_regs(c);
+        pin_reg(d);
+        pin_reg(qh);
     }
     // h[j]: the fifth bits of this lane group's values of block j, the first
     // four in bits 0..3, the last four in bits 16..19
@@ -286,6 +312,12 @@ struct Unit<FMT_W4> : Unit32<FMT_W4> {
         z = 8;
         UnitW4::scale_at(m, n, b, d, z);
     }
+    QMM_DEV void pin()
+    {
+        pin_regs(c);
+        pin_reg(d);
+        pin_reg(z);
+    }
     QMM_DEV void unpack(const MoeMatrix& m, int)
     {
         transpose4(c);
@@ -319,6 +351,12 @@ struct Unit<FMT_W4_WIDE> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = v[i];
         UnitW4::scale_at(m, n, 4 * u, d, z);
+    }
+    QMM_DEV void pin()
+    {
+        pin_regs(c);
+        pin_reg(d);
+        pin_reg(z);
     }
     QMM_DEV void unpack(const MoeMatrix& m, int)
     {
@@ -357,6 +395,11 @@ struct Unit<FMT_Q4_K> {
             c[4 + i] = v1[i];
         }
     }
+    QMM_DEV void pin()
+    {
+        pin_regs(c);
+        pin_regs(hd);
+    }
     QMM_DEV void unpack(const MoeMatrix&, int g)
     {
         const int sh = 16 * (g & 1);
@@ -389,7 +432,8 @@ struct Unit<FMT_Q4_K> {
 template <>
 struct Unit<FMT_Q6_K> {
     static constexpr int UNIT = 256, HALVES = 2, PARTS = 2;
-    static constexpr bool CHAIN = true, MINS = false;
+    // its sums could share an accumulator over a step, but that takes more registers than there are
+    static constexpr bool CHAIN = false, MINS = false;
     // lane group g: of half g >> 1 of the super-block, in each of its four
     // 32-value quarters the 16 values at 16 (g & 1); product 4h + j takes the
     // first or second eight of quarter (4h + j) / 2
@@ -417,6 +461,15 @@ struct Unit<FMT_Q6_K> {
         s0 = load4(p + 192 + 8 * (g >> 1));
         s1 = load4(p + 196 + 8 * (g >> 1));
         d = load2(p + 208);
+    }
+    QMM_DEV void pin()
+    {
+        pin_regs(l0);
+        pin_regs(l1);
+        pin_regs(qh);
+        pin_reg(s0);
+        pin_reg(s1);
+        pin_reg(d);
     }
     QMM_DEV void unpack(const MoeMatrix&, int g)
     {
@@ -519,78 +572,30 @@ QMM_DEV half8_t sums_operand(const float s[2])
 
 QMM_DEV f32x4_t mfma(half8_t a, half8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// One step (128 values) of NT units against MT groups of 16 activation rows:
-// acc[m][t] += the step's sums.  A(m, j, part) gives activation operands.
-template <int FMT, int PL, int MT, int NT, class AF>
-QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[MT][NT])
+// One step (128 values) of NT units against 16 activation rows: acc[t] += the
+// step's sums.  A(j, part) gives activation operands.
+template <int FMT, int PL, int NT, class AF>
+QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[NT])
 {
     using U = Unit<FMT>;
-    if constexpr (U::CHAIN) {
-        f32x4_t d[MT][NT];
+    f32x4_t d[NT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) d[m][t] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            half8_t b[NT][U::PARTS];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int q = 0; q < U::PARTS; ++q) b[t][q] = un[t].operand(h, j, q);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int p = 0; p < PL; ++p) {
-                    const half8_t a = A(m, j, p);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int q = 0; q < U::PARTS; ++q) d[m][t] = mfma(a, b[t][q], d[m][t]);
-                }
-        }
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float s = un[t].scale(0);
+            if (!U::CHAIN || j == 0) d[t] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int q = 0; q < U::PARTS; ++q) {
+                const half8_t b = un[t].operand(h, j, q);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(s, d[m][t][i], acc[m][t][i]);
-        }
-    } else {
-        // a product's sums are scaled while the next ones are formed
-        f32x4_t d[2][NT];
-        float s[2][NT];
+                for (int p = 0; p < PL; ++p) d[t] = mfma(A(j, p), b, d[t]);
+            }
+            if (!U::CHAIN || j == 3) {
+                const float s = un[t].scale(j);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            half8_t b[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) b[t] = un[t].operand(h, j, 0);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int at = (j * MT + m) & 1;
-#pragma unroll
-                for (int p = 0; p < PL; ++p) {
-                    const half8_t a = A(m, j, p);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) d[at][t] = mfma(a, b[t], p ? d[at][t] : f32x4_t{0, 0, 0, 0});
-                }
-                const int q = (j * MT + m - 1) % MT;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    s[at][t] = un[t].scale(j);
-                    if (j + m > 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[q][t][i] = fmaf(s[at ^ 1][t], d[at ^ 1][t][i], acc[q][t][i]);
-                    }
-                }
+                for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(s, d[t][i], acc[t][i]);
             }
         }
-        constexpr int last = (4 * MT - 1) & 1;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[MT - 1][t][i] = fmaf(s[last][t], d[last][t][i], acc[MT - 1][t][i]);
     }
 }
 
