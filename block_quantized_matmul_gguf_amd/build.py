@@ -16,7 +16,7 @@ SOURCES = ["qmm_capi.cpp", "qmm_quant.hip", "qmm_gemv.hip", "qmm_gemv_row.hip", 
            "qmm_dequant.hip", "qmm_ext.hip", "qmm_noalloc.hip", "qmm_gemv_b.hip", "qmm_gemv_emit.hip", "qmm_gemv_reg.hip",
            "qmm_gemm_s.hip", "qmm_route.hip", "qmm_moe.hip",
            "qmm_moe_q8_0.hip", "qmm_moe_q4_0.hip", "qmm_moe_q5_0.hip", "qmm_moe_q4_k.hip", "qmm_moe_q6_k.hip",
-           "qmm_moe_w4.hip"]
+           "qmm_moe_w4.hip", "qmm_moe_w4_s32.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -9,8 +9,8 @@
 namespace qmm {
 
 // 4-bit codes, scales and zero points in planes of their own; groups of any
-// multiple of 32 values, or of 128
-enum { FMT_W4 = 100, FMT_W4_WIDE = 101 };
+// multiple of 32 values, or (wide) of 128; scales of 16 or of 32 bits
+enum { FMT_W4 = 100, FMT_W4_WIDE = 101, FMT_W4_S32 = 102, FMT_W4_WIDE_S32 = 103 };
 enum { MOE_RUN = 0, MOE_GLU = 1, MOE_COMBINE = 2 };
 enum { TYPE_F32 = 0, TYPE_F16 = 1, TYPE_BF16 = 2 };
 
@@ -76,6 +76,8 @@ QMM_MOE_DECLARE(q4_k)
 QMM_MOE_DECLARE(q6_k)
 QMM_MOE_DECLARE(w4)
 QMM_MOE_DECLARE(w4_wide)
+QMM_MOE_DECLARE(w4_s32)
+QMM_MOE_DECLARE(w4_wide_s32)
 #undef QMM_MOE_DECLARE
 
 }  // namespace qmm

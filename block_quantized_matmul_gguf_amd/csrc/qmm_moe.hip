@@ -113,7 +113,7 @@ MoePlan plan_of(const MoeArgs& a)
 {
     MoePlan p = {};
     const int64_t P = a.T * a.top_k;
-    const bool dense = a.fmt == FMT_W4 || a.fmt == FMT_W4_WIDE;
+    const bool dense = a.fmt >= FMT_W4;
     if (a.T == 1) p.path = PATH_ONE;
     else if (P > 24 * (int64_t)(dense ? 4 : a.E)) p.path = PATH_TILE;
     else p.path = dense || P > 64 ? PATH_STREAM : PATH_SCAN;
@@ -132,9 +132,8 @@ MoePlan plan_of(const MoeArgs& a)
         p.tiles = take((size_t)p.max_tiles * sizeof(MoeTile));
     }
     if (p.path == PATH_TILE) {
-        const int64_t unit = a.fmt == FMT_Q4_K || a.fmt == FMT_Q6_K ? 256 : 128;
         p.x_rows = a.per_slot ? P : a.T;
-        p.Kp = (a.K + unit - 1) / unit * unit;
+        p.Kp = (a.K + 255) / 256 * 256;
         p.xp = take((size_t)p.x_rows * p.Kp * (a.type == TYPE_F32 ? 4 : 2));
         p.xinv = take((size_t)p.x_rows * 4);
         if (a.fmt == FMT_Q4_K) p.xsum = take((size_t)p.x_rows * (p.Kp / 256) * 32);
@@ -246,6 +245,8 @@ bool off16(const void* p) { return (uintptr_t)p % 16 != 0; }
     case FMT_Q4_K: return CALL(q4_k);           \
     case FMT_Q6_K: return CALL(q6_k);           \
     case FMT_W4_WIDE: return CALL(w4_wide);     \
+    case FMT_W4_S32: return CALL(w4_s32);       \
+    case FMT_W4_WIDE_S32: return CALL(w4_wide_s32); \
     default: return CALL(w4);                   \
     }
 hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s)
@@ -376,6 +377,7 @@ extern "C" int qmatmul_w4_run(int64_t N, int64_t K, int64_t M, int64_t group, in
     if (off16(q) || off16(x) || (uintptr_t)scales % type_bytes(scale_type) || (uintptr_t)y % type_bytes(type)) return bad("q and x must be 16-byte aligned, scales and y aligned to their type");
     MoeArgs a = w4_args(N, K, M, group, type);
     a.scale_type = scale_type;
+    if (scale_type == QMM_F32) a.fmt = a.fmt == FMT_W4 ? FMT_W4_S32 : FMT_W4_WIDE_S32;
     a.w0 = (const uint8_t*)q;
     a.scales = scales;
     a.zeros = zeros;

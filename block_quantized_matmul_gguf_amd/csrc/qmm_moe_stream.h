@@ -340,7 +340,7 @@ hipError_t launch_stream_t(const MoeArgs& a, int waves, hipStream_t s)
     const int64_t P = a.T * a.top_k;
     const int64_t ny = ONE ? (a.op == MOE_COMBINE ? a.T : P) : !a.ids ? (a.T + 15) / 16 : a.tiles ? a.max_tiles : P;
     const dim3 block(64 * waves);
-    constexpr bool experts = FMT != FMT_W4 && FMT != FMT_W4_WIDE;
+    constexpr bool experts = FMT < FMT_W4;
     const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)ny);
     if (experts && a.op == MOE_GLU) moe_stream<FMT, PL, ONE, experts ? 2 : 1, experts, PL == 2><<<grid, block, 0, s>>>(a);
     else if (PL == 2 || a.y_type != TYPE_F32) moe_stream<FMT, PL, ONE, 1, false, PL == 2><<<grid, block, 0, s>>>(a);

@@ -22,56 +22,92 @@ QMM_DEV void copy_to_lds(const void* p, void* base)
     __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)base, 16, 0, 0);
 }
 
+// What a wave of the tile kernel loads of 16 weight rows at a time: 256 values,
+// in two steps.  The 32-value formats' units come in pairs, the second unpacked
+// when it is used.
+template <int FMT, bool PAIR = Unit<FMT>::UNIT == 128>
+struct TileUnit : Unit<FMT> {
+    static constexpr int LOADS = Unit<FMT>::LOADS;
+    QMM_DEV void unpack_step(const MoeMatrix& m, int g, int h)
+    {
+        if (h == 0) this->unpack(m, g);
+    }
+    QMM_DEV half8_t operand_of(int h, int j, int part) const { return this->operand(h, j, part); }
+    QMM_DEV float scale_of(int, int j) const { return this->scale(j); }
+};
+template <int FMT>
+struct TileUnit<FMT, true> {
+    using U = Unit<FMT>;
+    static constexpr int LOADS = 2 * U::LOADS;
+    U u[2];
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int at, int g)
+    {
+        const int last = (m.blocks + 3) / 4 - 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) u[h].load(m, n, min(2 * at + h, last), g);
+    }
+    QMM_DEV void pin()
+    {
+        u[0].pin();
+        u[1].pin();
+    }
+    QMM_DEV void unpack_step(const MoeMatrix& m, int g, int h) { u[h].unpack(m, g); }
+    QMM_DEV half8_t operand_of(int h, int j, int part) const { return u[h].operand(0, j, part); }
+    QMM_DEV float scale_of(int h, int j) const { return u[h].scale(j); }
+};
+
 // One step (128 values) of two weight units against MT groups of 16 activation
 // rows in LDS (operands [part * MT + m][j][lane]): acc[m][t] += the step's sums.
 //
-// The step goes in eight pieces of four operand reads and eight products (two
-// pieces per product index j).  With the products of a piece run the next
-// piece's reads, the scaling of the piece before and half of the decoding for
-// the next j, issued between them: a matrix product occupies its unit for four
-// issue slots, three of which are free for vector work.
+// The step goes in pieces of two operand reads and four products (four pieces
+// per product index j).  With the products of a piece run the reads of the
+// piece after next, the scaling of the piece before and a part of the decoding
+// for the next j, issued between them: a matrix product occupies its unit for
+// four issue slots, three of which are free for vector work.
 constexpr int VALU_PER_PRODUCT = 6;
-
 template <int FMT, int PL, int MT>
-QMM_DEV void tile_step(const Unit<FMT> (&un)[2], int h, const _Float16* lds, f32x4_t (&acc)[MT][2])
+QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds, f32x4_t (&acc)[MT][2])
 {
     using U = Unit<FMT>;
-    static_assert(PL * MT == 8, "two pieces of four reads per product index");
-    constexpr int GM = MT / 2;  // row groups of a piece
-    half8_t a[2][GM][PL];
-    auto read = [&](int q, half8_t (&o)[GM][PL]) {
+    static_assert(PL * MT == 8, "four pieces of two reads per product index");
+    constexpr int GM = 2 / PL;  // row groups of a piece
+    half8_t a[3][GM][PL];
+    auto read = [&](int q) {
 #pragma unroll
         for (int m = 0; m < GM; ++m)
 #pragma unroll
-            for (int p = 0; p < PL; ++p) o[m][p] = *(const half8_t*)(lds + ((p * MT + (q & 1) * GM + m) * 4 + (q >> 1)) * 512);
+            for (int p = 0; p < PL; ++p)
+                a[q % 3][m][p] = *(const half8_t*)(lds + ((p * MT + (q & 3) * GM + m) * 4 + (q >> 2)) * 512);
     };
-    f32x4_t d[2][GM][2];
+    f32x4_t d[U::CHAIN ? 4 : 2][GM][2];
+    constexpr int DM = U::CHAIN ? 3 : 1;
     half8_t b[2][2][U::PARTS];
     auto scale = [&](int q) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float s = un[t].scale(q >> 1);
+            const float s = un[t].scale_of(h, q >> 2);
 #pragma unroll
             for (int m = 0; m < GM; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = (q & 1) * GM + m;
-                    acc[r][t][i] = fmaf(s, d[q & 1][m][t][i], acc[r][t][i]);
+                    const int r = (q & 3) * GM + m;
+                    acc[r][t][i] = fmaf(s, d[q & DM][m][t][i], acc[r][t][i]);
                 }
         }
     };
     auto decode = [&](int j, int t) {
 #pragma unroll
-        for (int k = 0; k < U::PARTS; ++k) b[j & 1][t][k] = un[t].operand(h, j, k);
+        for (int k = 0; k < U::PARTS; ++k) b[j & 1][t][k] = un[t].operand_of(h, j, k);
     };
-    read(0, a[0]);
+    read(0);
+    read(1);
     decode(0, 0);
     decode(0, 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const int j = q >> 1;
-        if (q < 7) read(q + 1, a[(q + 1) & 1]);
+    for (int q = 0; q < 16; ++q) {
+        const int j = q >> 2;
+        if (q < 14) read(q + 2);
 #pragma unroll
         for (int m = 0; m < GM; ++m)
 #pragma unroll
@@ -81,26 +117,25 @@ QMM_DEV void tile_step(const Unit<FMT> (&un)[2], int h, const _Float16* lds, f32
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const bool first = p + k == 0 && (!U::CHAIN || j == 0);
-                        d[q & 1][m][t] = mfma(a[q & 1][m][p], b[j & 1][t][k], first ? f32x4_t{0, 0, 0, 0} : d[q & 1][m][t]);
+                        d[q & DM][m][t] = mfma(a[q % 3][m][p], b[j & 1][t][k], first ? f32x4_t{0, 0, 0, 0} : d[q & DM][m][t]);
                     }
-        if (q > 0 && (!U::CHAIN || q == 7)) scale(q - 1);
-        if (j < 3) decode(j + 1, q & 1);
+        if (q > (U::CHAIN ? 12 : 0)) scale(q - 1);
+        if (j < 3 && (q & 1) == 0) decode(j + 1, (q >> 1) & 1);
 #pragma unroll
-        for (int i = 0; i < 8 * U::PARTS; ++i) {
+        for (int i = 0; i < 4 * U::PARTS; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read
             __builtin_amdgcn_sched_group_barrier(0x002, VALU_PER_PRODUCT, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
-    scale(7);
+    scale(15);
 }
 
 template <int FMT, int PL, int MT, int NW, bool GLU, bool WIDE>
 __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 {
     using U = Unit<FMT>;
-    constexpr int UNIT = U::UNIT, H = U::HALVES;
     constexpr int RING = 3;              // steps in LDS: one in use, two on their way
     constexpr int GW = PL * MT / NW;     // row groups (of one plane) a wave copies,
     constexpr int COPIES = GW * 4;       // 16 bytes per lane each, in a step
@@ -152,7 +187,7 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
         for (int c = 0; c < 2; ++c) acc[m][c] = f32x4_t{0, 0, 0, 0};
 
     if (t.e >= 0) {
-        const int units = (int)(a.Kp / UNIT), steps = units * H;
+        const int units = (int)(a.Kp / 256), steps = 2 * units;
         const int64_t plane = a.x_rows * a.Kp;
         const _Float16* src[GW];
         const _Float16* ssrc = nullptr;
@@ -172,7 +207,7 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
         const int first = (int)((b * 5 + tile) % units);
         auto place_of = [&](int u) { return u + first < units ? u + first : u + first - units; };
         auto stage = [&](int s, int buf) {  // step s of the walk
-            const int64_t su = place_of(s / H), at = su * H + s % H;
+            const int64_t su = place_of(s >> 1), at = 2 * su + (s & 1);
 #pragma unroll
             for (int i = 0; i < GW; ++i)
 #pragma unroll
@@ -187,7 +222,7 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
         int64_t n[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) n[c] = min(n0 + (GLU ? wave * 16 : wave * 32 + c * 16) + r, a.N - 1);
-        auto fetch = [&](int u, Unit<FMT> (&un)[2]) {
+        auto fetch = [&](int u, TileUnit<FMT> (&un)[2]) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 if (GLU) mat.w = (c ? a.w1 : a.w0) + t.e * matrix;
@@ -195,19 +230,19 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
             }
         };
         // Loads and copies are issued in every step, past the last one again for it, so that their
-        // number in flight is known: weights first, then copies.
-        Unit<FMT> cur[2], next[2];
-        stage(0, 0);
+        // number in flight is known, and both two steps before their use.  Operations retire in order:
+        // once no more are outstanding than the step before issued, all earlier ones have landed.
+        TileUnit<FMT> cur[2], next[2];
         fetch(0, next);
-        stage(min(1, steps - 1), 1);
+        stage(0, 0);
+        stage(1, 1);
         int buf = 0;
         for (int u = 0; u < units; ++u) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                const int s = u * H + h;
-                // Operations retire in order: once no more than one step's copies are outstanding,
-                // step s and the weights of its unit have landed.
-                vm_wait<COPIES>();
+            for (int h = 0; h < 2; ++h) {
+                const int s = 2 * u + h;
+                if (h) vm_wait<COPIES + 2 * TileUnit<FMT>::LOADS>();
+                else vm_wait<COPIES>();
                 lgkm_wait0();
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");  // no LDS access moves across
@@ -217,10 +252,11 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
                     for (int c = 0; c < 2; ++c) {
                         cur[c] = next[c];
                         cur[c].pin();
-                        cur[c].unpack(mat, g);
                     }
                     fetch(min(u + 1, units - 1), next);
                 }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) cur[c].unpack_step(mat, g, h);
                 stage(min(s + 2, steps - 1), buf == 0 ? 2 : buf - 1);
                 tile_step<FMT, PL, MT>(cur, h, lds + buf * STEP + lane * 8, acc);
                 if constexpr (U::MINS) {
@@ -336,7 +372,7 @@ __global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
 template <int FMT, int PL, int MT, int NW>
 hipError_t launch_tile_t(const MoeArgs& a, hipStream_t s)
 {
-    constexpr bool experts = FMT != FMT_W4 && FMT != FMT_W4_WIDE;
+    constexpr bool experts = FMT < FMT_W4;
     const int64_t bn = NW * (a.op == MOE_GLU ? 16 : 32), nb = (a.N + bn - 1) / bn;
     const int64_t grid = a.ids ? (a.max_tiles + 7) / 8 * 8 * nb : (nb + 7) / 8 * 8 * a.max_tiles;
     const dim3 g((unsigned)grid), block(64 * NW);

@@ -22,6 +22,8 @@
 //     16 s1 (q - 32) and s0 (q - 32)), so products may mix sub-blocks and the
 //     super-block's scale multiplies their sum.
 #pragma once
+#include <type_traits>
+
 #include "qmm_device.h"
 #include "qmm_moe.h"
 
@@ -66,12 +68,11 @@ QMM_DEV uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
 QMM_DEV half2_t half2_of(uint32_t v) { return __builtin_bit_cast(half2_t, v); }
 
 // loads at any byte alignment
-QMM_DEV void load16(const uint8_t* p, uint32_t c[4])
+QMM_DEV u32x4_t load16(const uint8_t* p)
 {
     u32x4_t v;
     __builtin_memcpy(&v, p, 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = v[i];
+    return v;
 }
 QMM_DEV uint32_t load4(const uint8_t* p)
 {
@@ -88,11 +89,16 @@ QMM_DEV uint32_t load2(const uint8_t* p)
 
 // Keeps the values in registers as they are up to here: nothing computed from
 // them moves ahead of this point (and with it the wait for their loads).
-template <int N>
-QMM_DEV void pin_regs(uint32_t (&v)[N])
+// (Words loaded together are kept together, as vectors: taken apart before this
+// point, they would be copied, and waited for, where they were loaded.)
+QMM_DEV void pin_reg(u32x4_t& v) { asm volatile("" : "+v"(v)); }
+QMM_DEV void pin_reg(u32x2_t& v) { asm volatile("" : "+v"(v)); }
+QMM_DEV void pin_reg(uint16_t& v) { asm volatile("" : "+v"(v)); }
+QMM_DEV void pin_reg(uint8_t& v)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+    uint16_t w = v;
+    asm volatile("" : "+v"(w));
+    v = (uint8_t)w;
 }
 QMM_DEV void pin_reg(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
@@ -111,13 +117,15 @@ struct MoeMatrix {
     int blocks;  // 32-value blocks of a row
     // W4
     const void* scales;
-    const uint8_t* zeros;
+    const uint8_t* zeros;  // without zero points: any readable bytes, as many
+    bool has_zeros;
     int scale_type, groups, group_blocks;
     uint32_t group_magic;
 };
 
 // Per format:
 //   UNIT   values of a unit;  HALVES  steps of 128 values in it
+//   LOADS  load instructions of a unit, at least
 //   CHAIN  products of a step share one scale (and so one accumulator)
 //   PARTS  operands per product;  MINS  Q4_K's minima
 //   o0, o1, slot: the k values of lane group g in product j of step h are
@@ -172,22 +180,30 @@ QMM_DEV half2_t sixteenth(half2_t p, half2_t bias) { return __builtin_elementwis
 
 template <>
 struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
-    uint32_t c[8], d;
+    u32x4_t r0, r1;  // as loaded
+    uint32_t d, c[8];
     static QMM_DEV int slot(int i) { return i; }
+    static constexpr int LOADS = 3;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
         const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 34;
-        load16(p + 2, c);
-        load16(p + 18, c + 4);
+        r0 = load16(p + 2);
+        r1 = load16(p + 18);
         d = load2(p);
     }
     QMM_DEV void pin()
     {
-        pin_regs(c);
+        pin_reg(r0);
+        pin_reg(r1);
         pin_reg(d);
     }
     QMM_DEV void unpack(const MoeMatrix&, int)
     {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = r0[i];
+            c[4 + i] = r1[i];
+        }
         transpose4(c);
         transpose4(c + 4);
         gather_scales(f16lo(d));
@@ -203,21 +219,25 @@ struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
 
 template <>
 struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
-    uint32_t c[4], d;
+    u32x4_t r0;
+    uint32_t d, c[4];
     static QMM_DEV int slot(int i) { return nib_perm(i); }
+    static constexpr int LOADS = 2;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
         const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 18;
-        load16(p + 2, c);
+        r0 = load16(p + 2);
         d = load2(p);
     }
     QMM_DEV void pin()
     {
-        pin_regs(c);
+        pin_reg(r0);
         pin_reg(d);
     }
     QMM_DEV void unpack(const MoeMatrix&, int)
     {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = r0[i];
         transpose4(c);
         gather_scales(f16lo(d));
     }
@@ -231,18 +251,20 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
 
 template <>
 struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
-    uint32_t c[4], d, qh, h[4];
+    u32x4_t r0;
+    uint32_t d, qh, c[4], h[4];
     static QMM_DEV int slot(int i) { return nib_perm(i); }
+    static constexpr int LOADS = 3;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
         const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 22;
-        load16(p + 6, c);
+        r0 = load16(p + 6);
         qh = load4(p + 2);
         d = load2(p);
     }
     QMM_DEV void pin()
     {
-        pin_regs(c);
+        pin_reg(r0);
         pin_reg(d);
         pin_reg(qh);
     }
@@ -250,6 +272,8 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
     // four in bits 0..3, the last four in bits 16..19
     QMM_DEV void unpack(const MoeMatrix&, int g)
     {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = r0[i];
         transpose4(c);
         gather_scales(f16lo(d));
         gather4(qh, h);
@@ -281,93 +305,114 @@ struct UnitW4 {
         const uint32_t w = v >> 8, k = f16_pattern();
         return join8(nib_lo(v, k) + lo, sixteenth(nib_hi(v, k), hi), nib_lo(w, k) + lo, sixteenth(nib_hi(w, k), hi));
     }
-    static QMM_DEV void scale_at(const MoeMatrix& m, int64_t n, int block, uint32_t& d, uint32_t& z)
+    template <bool S32>
+    using scale_t = std::conditional_t<S32, uint32_t, uint16_t>;
+    template <bool S32>
+    static QMM_DEV void scale_at(const MoeMatrix& m, int64_t n, int block, scale_t<S32>& d, uint8_t& z)
     {
         const int64_t at = n * m.groups + (m.group_magic ? (int)__umulhi((uint32_t)block, m.group_magic) : block);
         // as they are: a conversion here would wait for the load
-        if (m.scale_type == TYPE_F32) d = ((const uint32_t*)m.scales)[at];
-        else d = ((const uint16_t*)m.scales)[at];
-        if (m.zeros) z = m.zeros[at];
+        d = ((const scale_t<S32>*)m.scales)[at];
+        z = m.zeros[at];
     }
-    static QMM_DEV float scale_value(const MoeMatrix& m, uint32_t d)
+    static QMM_DEV uint32_t zero_value(const MoeMatrix& m, uint32_t z) { return m.has_zeros ? z : 8; }
+    template <bool S32>
+    static QMM_DEV float scale_value(const MoeMatrix& m, scale_t<S32> d)
     {
-        return m.scale_type == TYPE_F16 ? f16lo(d) : f32_of(m.scale_type == TYPE_F32 ? d : d << 16);
+        if constexpr (S32) return f32_of(d);
+        return m.scale_type == TYPE_F16 ? f16lo(d) : f32_of((uint32_t)d << 16);
     }
 };
 
-template <>
-struct Unit<FMT_W4> : Unit32<FMT_W4> {
-    uint32_t c[4], d, z;
+template <bool S32>
+struct UnitW4Narrow : Unit32<FMT_W4> {
+    u32x4_t r0;
+    UnitW4::scale_t<S32> d;
+    uint8_t z;
+    uint32_t c[4];
     half2_t bias[4];
     static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
     static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
     static QMM_DEV int place(int k) { return UnitW4::place(k); }
+    static constexpr int LOADS = 3;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
         const int b = block_of(m, u, g);
-        const u32x4_t v = *(const u32x4_t*)(m.w + n * m.row_bytes + 16 * b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = v[i];
-        z = 8;
-        UnitW4::scale_at(m, n, b, d, z);
+        r0 = *(const u32x4_t*)(m.w + n * m.row_bytes + 16 * b);
+        UnitW4::scale_at<S32>(m, n, b, d, z);
     }
     QMM_DEV void pin()
     {
-        pin_regs(c);
+        pin_reg(r0);
         pin_reg(d);
         pin_reg(z);
     }
     QMM_DEV void unpack(const MoeMatrix& m, int)
     {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = r0[i];
         transpose4(c);
-        gather_scales(UnitW4::scale_value(m, d));
+        gather_scales(UnitW4::scale_value<S32>(m, d));
         uint32_t o[4];
-        gather4(UnitW4::bias_lo(z), o);
+        gather4(UnitW4::bias_lo(UnitW4::zero_value(m, z)), o);
 #pragma unroll
         for (int j = 0; j < 4; ++j) bias[j] = half2_of(o[j]);
     }
     QMM_DEV half8_t operand(int, int j, int) const { return UnitW4::values(c[j], bias[j], UnitW4::bias_hi(bias[j])); }
 };
 
+template <>
+struct Unit<FMT_W4> : UnitW4Narrow<false> {};
+template <>
+struct Unit<FMT_W4_S32> : UnitW4Narrow<true> {};
+
 // W4 with groups of whole units (group a multiple of 128): one scale and zero
 // point per unit, so its four products share an accumulator (a quarter of the
 // multiply-adds) and nothing is gathered.
-template <>
-struct Unit<FMT_W4_WIDE> {
+template <bool S32>
+struct UnitW4Wide {
     static constexpr int UNIT = 128, HALVES = 1, PARTS = 1;
     static constexpr bool CHAIN = true, MINS = false;
     static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
     static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
     static QMM_DEV int place(int k) { return UnitW4::place(k); }
-    uint32_t c[4], d, z;
+    u32x4_t r0;
+    UnitW4::scale_t<S32> d;
+    uint8_t z;
+    uint32_t c[4];
     float s;
     half2_t lo, hi;
+    static constexpr int LOADS = 3;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
-        const u32x4_t v = *(const u32x4_t*)(m.w + n * m.row_bytes + 64 * u + 16 * g);
-        z = 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = v[i];
-        UnitW4::scale_at(m, n, 4 * u, d, z);
+        r0 = *(const u32x4_t*)(m.w + n * m.row_bytes + 64 * u + 16 * g);
+        UnitW4::scale_at<S32>(m, n, 4 * u, d, z);
     }
     QMM_DEV void pin()
     {
-        pin_regs(c);
+        pin_reg(r0);
         pin_reg(d);
         pin_reg(z);
     }
     QMM_DEV void unpack(const MoeMatrix& m, int)
     {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = r0[i];
         transpose4(c);
-        s = UnitW4::scale_value(m, d);
-        lo = half2_of(UnitW4::bias_lo(z));
+        s = UnitW4::scale_value<S32>(m, d);
+        lo = half2_of(UnitW4::bias_lo(UnitW4::zero_value(m, z)));
         hi = UnitW4::bias_hi(lo);
     }
     QMM_DEV half8_t operand(int, int j, int) const { return UnitW4::values(c[j], lo, hi); }
     QMM_DEV float scale(int) const { return s; }
 };
+
+template <>
+struct Unit<FMT_W4_WIDE> : UnitW4Wide<false> {};
+template <>
+struct Unit<FMT_W4_WIDE_S32> : UnitW4Wide<true> {};
 
 // ------------------------------------------------------- a super-block
 
@@ -380,25 +425,22 @@ struct Unit<FMT_Q4_K> {
     static QMM_DEV int o1(int h, int j, int g) { return o0(h, j, g) + 4; }
     static QMM_DEV int slot(int i) { return nib_perm(i); }
     static QMM_DEV int place(int k) { return ((((k >> 5) & 1) * 4 + ((k >> 3) & 3)) * 4 + (k >> 6)) * 8 + nib_perm(k & 7); }
-    uint32_t c[8], hd[4];
+    u32x4_t hd, r0, r1;
     half2_t sc[2], off[2];  // sub-block scale and -1024 times it; the second's / 16 and -64 times it
     uint32_t mn;            // the two minima, one per byte
+    static constexpr int LOADS = 3;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
         const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 144;
-        const u32x4_t a = *(const u32x4_t*)p;
-        const u32x4_t v0 = *(const u32x4_t*)(p + 16 + 32 * g), v1 = *(const u32x4_t*)(p + 32 + 32 * g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hd[i] = a[i];
-            c[i] = v0[i];
-            c[4 + i] = v1[i];
-        }
+        hd = *(const u32x4_t*)p;
+        r0 = *(const u32x4_t*)(p + 16 + 32 * g);
+        r1 = *(const u32x4_t*)(p + 32 + 32 * g);
     }
     QMM_DEV void pin()
     {
-        pin_regs(c);
-        pin_regs(hd);
+        pin_reg(hd);
+        pin_reg(r0);
+        pin_reg(r1);
     }
     QMM_DEV void unpack(const MoeMatrix&, int g)
     {
@@ -415,7 +457,7 @@ struct Unit<FMT_Q4_K> {
     }
     QMM_DEV half8_t operand(int h, int j, int) const
     {
-        const uint32_t k = f16_pattern(), v = c[2 * j], w = c[2 * j + 1];
+        const uint32_t k = f16_pattern(), v = j < 2 ? r0[2 * j & 3] : r1[2 * j & 3], w = j < 2 ? r0[(2 * j + 1) & 3] : r1[(2 * j + 1) & 3];
         auto part = [&](uint32_t x) { return __builtin_elementwise_fma(h ? nib_hi(x, k) : nib_lo(x, k), sc[h], off[h]); };
         return join8(part(v), part(v >> 8), part(w), part(w >> 8));
     }
@@ -449,33 +491,34 @@ struct Unit<FMT_Q6_K> {
         const int jj = 2 * ((k >> 5) & 3) + ((k >> 3) & 1), g = 2 * (k >> 7) + ((k >> 4) & 1);
         return (jj * 4 + g) * 8 + (k & 7);
     }
-    uint32_t l0[4], l1[4], qh[4], s0, s1, d;
+    u32x4_t l0, l1, qh;
+    u32x2_t sc;
+    uint32_t d;
     half2_t hi[4], lo[4];  // 16 s1 and s0 of the four quarters' scales
+    static constexpr int LOADS = 5;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
     {
         const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 210;
         const uint8_t* q = p + 64 * (g >> 1) + 16 * (g & 1);
-        load16(q, l0);
-        load16(q + 32, l1);
-        load16(p + 128 + 32 * (g >> 1) + 16 * (g & 1), qh);
-        s0 = load4(p + 192 + 8 * (g >> 1));
-        s1 = load4(p + 196 + 8 * (g >> 1));
+        l0 = load16(q);
+        l1 = load16(q + 32);
+        qh = load16(p + 128 + 32 * (g >> 1) + 16 * (g & 1));
+        __builtin_memcpy(&sc, p + 192 + 8 * (g >> 1), 8);
         d = load2(p + 208);
     }
     QMM_DEV void pin()
     {
-        pin_regs(l0);
-        pin_regs(l1);
-        pin_regs(qh);
-        pin_reg(s0);
-        pin_reg(s1);
+        pin_reg(l0);
+        pin_reg(l1);
+        pin_reg(qh);
+        pin_reg(sc);
         pin_reg(d);
     }
     QMM_DEV void unpack(const MoeMatrix&, int g)
     {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int v = (int)(int8_t)(((t < 2 ? s0 : s1) >> (16 * (t & 1) + 8 * (g & 1))) & 0xffu);
+            const int v = (int)(int8_t)((sc[t >> 1] >> (16 * (t & 1) + 8 * (g & 1))) & 0xffu);
             hi[t] = both((float)(v & ~15));
             lo[t] = both((float)(v & 15));
         }
@@ -625,12 +668,13 @@ QMM_DEV MoeMatrix moe_matrix(const MoeArgs& a, const uint8_t* w)
     m.row_bytes = a.row_bytes;
     m.blocks = (int)(a.K / 32);
     m.scales = a.scales;
-    m.zeros = a.zeros;
+    m.has_zeros = a.zeros != nullptr;
+    m.zeros = a.zeros ? a.zeros : (const uint8_t*)a.scales;
     m.scale_type = a.scale_type;
     m.groups = 0;
     m.group_blocks = a.group_blocks;
     m.group_magic = a.group_magic;
-    if (a.fmt == FMT_W4 || a.fmt == FMT_W4_WIDE) m.groups = m.blocks / a.group_blocks;
+    if (a.fmt >= FMT_W4) m.groups = m.blocks / a.group_blocks;
     return m;
 }
 

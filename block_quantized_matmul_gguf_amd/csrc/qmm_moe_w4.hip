@@ -1,4 +1,4 @@
-// qmm_moe_w4.hip -- the experts' product kernels, 4-bit group weights.
+// qmm_moe_w4.hip -- the product kernels, 4-bit group weights with 16-bit scales.
 #include "qmm_moe_stream.h"
 #include "qmm_moe_tile.h"
 
