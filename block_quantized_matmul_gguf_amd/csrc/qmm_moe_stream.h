@@ -66,6 +66,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
     constexpr int UNIT = U::UNIT, H = U::HALVES;
     constexpr int RED = ONE ? 16 : 256;  // sums per tile and wave
     __shared__ float red[STREAM_MAX_WAVES][NT][RED];
+    __shared__ __align__(16) uint32_t areas[STREAM_MAX_WAVES][U::AREA];
     __shared__ int lists[STREAM_MAX_WAVES][16];
     __shared__ __align__(16) _Float16 xs[ONE ? STREAM_MAX_WAVES : 1][ONE ? PL * UNIT : 8];
     __shared__ __align__(16) float xsum[ONE && U::MINS ? STREAM_MAX_WAVES : 1][8];
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
         const MoeMatrix mat = moe_matrix(a, nullptr);
         int64_t n[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) n[t] = min(n0 + r + (GLU ? 0 : 16 * t), a.N - 1);
+        for (int t = 0; t < NT; ++t) n[t] = min(n0 + (lane >> 2) + (GLU ? 0 : 16 * t), a.N - 1);
 
         constexpr int XV = UNIT / 64;  // ONE: values of a unit per lane
         struct Loaded {
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (GLU && t == 1) m.w = a.w1 + e * matrix;
-                l.u[t].load(m, n[t], u, g);
+                l.u[t].load(m, n[t], u, lane & 3);
             }
         };
         // multiplies a fetched item
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     d[t] = f32x4_t{0, 0, 0, 0};
-                    l.u[t].unpack(mat, g);
+                    l.u[t].unpack(mat, areas[wave], lane);
                 }
 #pragma unroll
                 for (int h = 0; h < H; ++h)
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(64 * STREAM_MAX_WAVES) void moe_stream(MoeArgs a)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     d[t] = f32x4_t{0, 0, 0, 0};
-                    l.u[t].unpack(mat, g);
+                    l.u[t].unpack(mat, areas[wave], lane);
                 }
 #pragma unroll
                 for (int h = 0; h < H; ++h) step<FMT, PL, NT>(l.u, h, [&](int j, int p) { return xa[h][j][p]; }, d);

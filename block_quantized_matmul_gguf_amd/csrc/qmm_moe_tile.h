@@ -28,9 +28,9 @@ QMM_DEV void copy_to_lds(const void* p, void* base)
 template <int FMT, bool PAIR = Unit<FMT>::UNIT == 128>
 struct TileUnit : Unit<FMT> {
     static constexpr int LOADS = Unit<FMT>::LOADS;
-    QMM_DEV void unpack_step(const MoeMatrix& m, int g, int h)
+    QMM_DEV void unpack_step(const MoeMatrix& m, uint32_t* area, int lane, int h)
     {
-        if (h == 0) this->unpack(m, g);
+        if (h == 0) this->unpack(m, area, lane);
     }
     QMM_DEV half8_t operand_of(int h, int j, int part) const { return this->operand(h, j, part); }
     QMM_DEV float scale_of(int, int j) const { return this->scale(j); }
@@ -40,24 +40,24 @@ struct TileUnit<FMT, true> {
     using U = Unit<FMT>;
     static constexpr int LOADS = 2 * U::LOADS;
     U u[2];
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int at, int g)
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int at, int q)
     {
         const int last = (m.blocks + 3) / 4 - 1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) u[h].load(m, n, min(2 * at + h, last), g);
+        for (int h = 0; h < 2; ++h) u[h].load(m, n, min(2 * at + h, last), q);
     }
     QMM_DEV void pin()
     {
         u[0].pin();
         u[1].pin();
     }
-    QMM_DEV void unpack_step(const MoeMatrix& m, int g, int h) { u[h].unpack(m, g); }
+    QMM_DEV void unpack_step(const MoeMatrix& m, uint32_t* area, int lane, int h) { u[h].unpack(m, area, lane); }
     QMM_DEV half8_t operand_of(int h, int j, int part) const { return u[h].operand(0, j, part); }
     QMM_DEV float scale_of(int h, int j) const { return u[h].scale(j); }
 };
 
 // One step (128 values) of two weight units against MT groups of 16 activation
-// rows in LDS (operands [part * MT + m][j][lane]): acc[m][t] += the step's sums.
+// rows in LDS (see moe_tile; at[j] is the lane's offset for product j): acc[m][t] += the step's sums.
 //
 // The step goes in pieces of two operand reads and four products (four pieces
 // per product index j).  With the products of a piece run the reads of the
@@ -66,7 +66,7 @@ struct TileUnit<FMT, true> {
 // four issue slots, three of which are free for vector work.
 constexpr int VALU_PER_PRODUCT = 6;
 template <int FMT, int PL, int MT>
-QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds, f32x4_t (&acc)[MT][2])
+QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds, const int (&at)[4], f32x4_t (&acc)[MT][2])
 {
     using U = Unit<FMT>;
     static_assert(PL * MT == 8, "four pieces of two reads per product index");
@@ -77,7 +77,7 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
         for (int m = 0; m < GM; ++m)
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-                a[q % 3][m][p] = *(const half8_t*)(lds + ((p * MT + (q & 3) * GM + m) * 4 + (q >> 2)) * 512);
+                a[q % 3][m][p] = *(const half8_t*)(lds + (p * MT + (q & 3) * GM + m) * 2048 + at[q >> 2]);
     };
     f32x4_t d[U::CHAIN ? 4 : 2][GM][2];
     constexpr int DM = U::CHAIN ? 3 : 1;
@@ -140,9 +140,13 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
     constexpr int GW = PL * MT / NW;     // row groups (of one plane) a wave copies,
     constexpr int COPIES = GW * 4;       // 16 bytes per lane each, in a step
     static_assert(PL * MT % NW == 0 && MT / 2 <= NW, "waves share the copies evenly");
-    // operands [RING][part * MT + m][j][lane][8], then (Q4_K) the sums of two units [2][m][2][16][8]
+    // Activations [RING][part * MT + m][row][16 places of 8 values]: value group j * 4 + g of row r is
+    // in place (j * 4 + g) ^ r, so that the lanes of an operand read without bank conflicts and those
+    // of a copy read 256 neighbouring bytes.  Then (Q4_K) the sums of two units [2][m][2][16][8].
     constexpr int STEP = PL * MT * 4 * 512, SUMS = U::MINS ? MT * 256 : 0;
-    __shared__ __align__(16) _Float16 lds[RING * STEP + 2 * SUMS];
+    // Then the waves' exchange areas.  (One array: beside another one, reads of this would be made
+    // to wait for every copy in flight.)
+    __shared__ __align__(16) _Float16 lds[RING * STEP + 2 * SUMS + NW * U::AREA * 2];
 
     const int lane = (int)__lane_id(), r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -189,13 +193,17 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
     if (t.e >= 0) {
         const int units = (int)(a.Kp / 256), steps = 2 * units;
         const int64_t plane = a.x_rows * a.Kp;
-        const _Float16* src[GW];
+        // a copy takes four rows: lane's row lane >> 4 of them, place lane & 15
+        const _Float16* src[GW][4];
         const _Float16* ssrc = nullptr;
 #pragma unroll
-        for (int i = 0; i < GW; ++i) {
-            const int q = wave * GW + i;  // plane q / MT, rows of group q % MT
-            src[i] = a.xp + (q / MT) * plane + (int64_t)row_of(pair_of(q % MT)) * 128 + g * 8;
-        }
+        for (int i = 0; i < GW; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int q = wave * GW + i, row = 4 * k + g;  // plane q / MT, rows of group q % MT
+                const int at = t.start + min(q % MT * 16 + row, t.count - 1);
+                src[i][k] = a.xp + (q / MT) * plane + (int64_t)row_of(a.ids ? a.order[at] : at) * 128 + (r ^ row) * 8;
+            }
         // sums: 16 halves per row and unit; waves below MT / 2 copy [m][p][r] of m = 2 wave, 2 wave + 1
         if constexpr (U::MINS) {
             const int sm = (wave * 2 + (lane >> 5)) & (MT - 1);
@@ -211,8 +219,8 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 #pragma unroll
             for (int i = 0; i < GW; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    copy_to_lds(src[i] + at * a.x_rows * 128 + j * 32, lds + buf * STEP + ((wave * GW + i) * 4 + j) * 512);
+                for (int k = 0; k < 4; ++k)
+                    copy_to_lds(src[i][k] + at * a.x_rows * 128, lds + buf * STEP + (wave * GW + i) * 2048 + k * 512);
             if constexpr (U::MINS) {
                 if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + su * a.x_rows * 16, lds + RING * STEP + ((s >> 1) & 1) * SUMS + wave * 512);
             }
@@ -221,17 +229,20 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
         MoeMatrix mat = moe_matrix(a, a.w0 + t.e * matrix);
         int64_t n[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) n[c] = min(n0 + (GLU ? wave * 16 : wave * 32 + c * 16) + r, a.N - 1);
+        for (int c = 0; c < 2; ++c) n[c] = min(n0 + (GLU ? wave * 16 : wave * 32 + c * 16) + (lane >> 2), a.N - 1);
         auto fetch = [&](int u, TileUnit<FMT> (&un)[2]) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 if (GLU) mat.w = (c ? a.w1 : a.w0) + t.e * matrix;
-                un[c].load(mat, n[c], place_of(u), g);
+                un[c].load(mat, n[c], place_of(u), lane & 3);
             }
         };
         // Loads and copies are issued in every step, past the last one again for it, so that their
         // number in flight is known, and both two steps before their use.  Operations retire in order:
         // once no more are outstanding than the step before issued, all earlier ones have landed.
+        int operand_at[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) operand_at[j] = r * 128 + ((j * 4 + g) ^ r) * 8;
         TileUnit<FMT> cur[2], next[2];
         fetch(0, next);
         stage(0, 0);
@@ -256,9 +267,9 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
                     fetch(min(u + 1, units - 1), next);
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) cur[c].unpack_step(mat, g, h);
+                for (int c = 0; c < 2; ++c) cur[c].unpack_step(mat, (uint32_t*)(lds + RING * STEP + 2 * SUMS) + wave * U::AREA, lane, h);
                 stage(min(s + 2, steps - 1), buf == 0 ? 2 : buf - 1);
-                tile_step<FMT, PL, MT>(cur, h, lds + buf * STEP + lane * 8, acc);
+                tile_step<FMT, PL, MT>(cur, h, lds + buf * STEP, operand_at, acc);
                 if constexpr (U::MINS) {
                     if (h == 0) {
 #pragma unroll

@@ -10,15 +10,18 @@
 // Weights enter as exact integers in f16 (the scales multiply sums, in f32),
 // so products are exact and sums are f32.
 //
-// A unit is what a wave loads of 16 rows at a time, each lane whole 16-byte
-// words (the blocks' two-byte alignment is the hardware's to deal with):
-//   32-value formats: four blocks, lane group g loading block g whole; a 4 x 4
-//     transposition across lane groups (v_permlane32_swap, v_permlane16_swap)
-//     then gives every group a quarter of each block, so one product covers
+// A unit is what a wave loads of 16 rows at a time, lane (R = lane >> 2, q =
+// lane & 3) whole 16-byte words of row R's quarter q: neighbouring lanes read
+// neighbouring bytes (with a row per lane every lane costs the address unit a
+// cycle of its own: about 64 per load, measured as half of a tile kernel's
+// time).  The blocks' two-byte alignment is the hardware's to deal with.  A
+// pass through the wave's own LDS hands the words to the operand's lanes:
+//   32-value formats: quarter q is block q; the words are transposed on the
+//     way, lane group g getting word g of each block, so one product covers
 //     one block and one scale;
-//   Q4_K and Q6_K: a super-block, lane group g loading two (four) sub-blocks
-//     whole; the sub-block scales are small integers and go into the operand
-//     (Q4_K: sc q <= 945; Q6_K: (16 s1 + s0) (q - 32) as the two exact parts
+//   Q4_K and Q6_K: a super-block, quarter q two (four) sub-blocks, kept whole;
+//     the sub-block scales are small integers and go into the operand (Q4_K:
+//     sc q <= 945; Q6_K: (16 s1 + s0) (q - 32) as the two exact parts
 //     16 s1 (q - 32) and s0 (q - 32)), so products may mix sub-blocks and the
 //     super-block's scale multiplies their sum.
 #pragma once
@@ -43,26 +46,21 @@ QMM_DEV void swap16(uint32_t& a, uint32_t& b)
     a = r[0];
     b = r[1];
 }
-// c[j] of lane group g  <->  c[g] of lane group j
-QMM_DEV void transpose4(uint32_t c[4])
+// The exchange through a wave's LDS.  A word area holds 16 bytes per (row,
+// quarter), the quarters of a row permuted so that neither side has bank
+// conflicts; a row area holds a dword per (row, quarter).
+constexpr int WORD_AREA = 256, ROW_AREA = 64;  // dwords
+QMM_DEV int word_at(int row, int quarter) { return row * 16 + ((quarter ^ ((row >> 1) & 3)) << 2); }
+QMM_DEV void put_word(uint32_t* area, int lane, u32x4_t v) { *(u32x4_t*)(area + word_at(lane >> 2, lane & 3)) = v; }
+// word i of the lane's four goes to quarter i of the row, at the lane's place in it
+QMM_DEV void put_transposed(uint32_t* area, int lane, u32x4_t v)
 {
-    swap32(c[0], c[2]);
-    swap32(c[1], c[3]);
-    swap16(c[0], c[1]);
-    swap16(c[2], c[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) area[word_at(lane >> 2, i) + (lane & 3)] = v[i];
 }
-// v of lane groups 0..3, in every lane
-QMM_DEV void gather4(uint32_t v, uint32_t o[4])
-{
-    uint32_t a = v, b = v;
-    swap32(a, b);
-    o[0] = a;
-    o[1] = a;
-    o[2] = b;
-    o[3] = b;
-    swap16(o[0], o[1]);
-    swap16(o[2], o[3]);
-}
+QMM_DEV u32x4_t get_word(const uint32_t* area, int lane) { return *(const u32x4_t*)(area + word_at(lane & 15, lane >> 4)); }
+QMM_DEV void put_row(uint32_t* area, int lane, uint32_t v) { area[lane] = v; }
+QMM_DEV u32x4_t get_row(const uint32_t* area, int lane) { return *(const u32x4_t*)(area + (lane & 15) * 4); }
 QMM_DEV float f32_of(uint32_t v) { return __builtin_bit_cast(float, v); }
 QMM_DEV uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
 QMM_DEV half2_t half2_of(uint32_t v) { return __builtin_bit_cast(half2_t, v); }
@@ -125,7 +123,8 @@ struct MoeMatrix {
 
 // Per format:
 //   UNIT   values of a unit;  HALVES  steps of 128 values in it
-//   LOADS  load instructions of a unit, at least
+//   load   of row n: lane quarter q's words;  unpack  the exchange, and scales
+//   LOADS  load instructions of a unit, at least;  AREA  dwords of LDS to exchange in
 //   CHAIN  products of a step share one scale (and so one accumulator)
 //   PARTS  operands per product;  MINS  Q4_K's minima
 //   o0, o1, slot: the k values of lane group g in product j of step h are
@@ -147,17 +146,15 @@ struct Unit32 {
         const int e = k & 31, i = (e & 3) | ((e & 16) >> 2);  // number within the operand's eight
         return (((k >> 5) * 4 + ((e >> 2) & 3)) << 3) | (FMT == FMT_Q8_0 ? i : nib_perm(i));
     }
-    // Block 4u + g, or the row's last: past the end activations are zero, and a
+    // Block 4u + q, or the row's last: past the end activations are zero, and a
     // load that always happens keeps the wave's count of loads in flight known.
-    static QMM_DEV int block_of(const MoeMatrix& m, int u, int g) { return min(4 * u + g, m.blocks - 1); }
+    static QMM_DEV int block_of(const MoeMatrix& m, int u, int q) { return min(4 * u + q, m.blocks - 1); }
     float s[4];  // scales of the four blocks
     QMM_DEV float scale(int j) const { return s[j]; }
-    QMM_DEV void gather_scales(float own)
+    QMM_DEV void half_scales(u32x4_t v)
     {
-        uint32_t o[4];
-        gather4(bits_of(own), o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = f32_of(o[j]);
+        for (int j = 0; j < 4; ++j) s[j] = f16lo(v[j]);
     }
 };
 
@@ -183,10 +180,10 @@ struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
     u32x4_t r0, r1;  // as loaded
     uint32_t d, c[8];
     static QMM_DEV int slot(int i) { return i; }
-    static constexpr int LOADS = 3;
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    static constexpr int LOADS = 3, AREA = 2 * WORD_AREA + ROW_AREA;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
-        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 34;
+        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, q) * 34;
         r0 = load16(p + 2);
         r1 = load16(p + 18);
         d = load2(p);
@@ -197,16 +194,20 @@ struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
         pin_reg(r1);
         pin_reg(d);
     }
-    QMM_DEV void unpack(const MoeMatrix&, int)
+    QMM_DEV void unpack(const MoeMatrix& m, uint32_t* area, int lane)
     {
+        put_transposed(area, lane, r0);
+        put_transposed(area + WORD_AREA, lane, r1);
+        put_row(area + 2 * WORD_AREA, lane, d);
+        wave_sync();
+        const u32x4_t v = get_word(area, lane), w = get_word(area + WORD_AREA, lane);
+        half_scales(get_row(area + 2 * WORD_AREA, lane));
+        wave_sync();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            c[i] = r0[i];
-            c[4 + i] = r1[i];
+            c[i] = v[i];
+            c[4 + i] = w[i];
         }
-        transpose4(c);
-        transpose4(c + 4);
-        gather_scales(f16lo(d));
     }
     QMM_DEV half8_t operand(int, int j, int) const
     {
@@ -222,10 +223,10 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
     u32x4_t r0;
     uint32_t d, c[4];
     static QMM_DEV int slot(int i) { return nib_perm(i); }
-    static constexpr int LOADS = 2;
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    static constexpr int LOADS = 2, AREA = WORD_AREA + ROW_AREA;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
-        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 18;
+        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, q) * 18;
         r0 = load16(p + 2);
         d = load2(p);
     }
@@ -234,12 +235,16 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
         pin_reg(r0);
         pin_reg(d);
     }
-    QMM_DEV void unpack(const MoeMatrix&, int)
+    QMM_DEV void unpack(const MoeMatrix& m, uint32_t* area, int lane)
     {
+        put_transposed(area, lane, r0);
+        put_row(area + WORD_AREA, lane, d);
+        wave_sync();
+        const u32x4_t v = get_word(area, lane);
+        half_scales(get_row(area + WORD_AREA, lane));
+        wave_sync();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = r0[i];
-        transpose4(c);
-        gather_scales(f16lo(d));
+        for (int i = 0; i < 4; ++i) c[i] = v[i];
     }
     QMM_DEV half8_t operand(int, int j, int) const
     {
@@ -254,10 +259,10 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
     u32x4_t r0;
     uint32_t d, qh, c[4], h[4];
     static QMM_DEV int slot(int i) { return nib_perm(i); }
-    static constexpr int LOADS = 3;
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    static constexpr int LOADS = 3, AREA = WORD_AREA + 2 * ROW_AREA;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
-        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, g) * 22;
+        const uint8_t* p = m.w + n * m.row_bytes + block_of(m, u, q) * 22;
         r0 = load16(p + 6);
         qh = load4(p + 2);
         d = load2(p);
@@ -270,15 +275,20 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
     }
     // h[j]: the fifth bits of this lane group's values of block j, the first
     // four in bits 0..3, the last four in bits 16..19
-    QMM_DEV void unpack(const MoeMatrix&, int g)
+    QMM_DEV void unpack(const MoeMatrix& m, uint32_t* area, int lane)
     {
+        put_transposed(area, lane, r0);
+        put_row(area + WORD_AREA, lane, d);
+        put_row(area + WORD_AREA + ROW_AREA, lane, qh);
+        wave_sync();
+        const u32x4_t v = get_word(area, lane);
+        half_scales(get_row(area + WORD_AREA, lane));
+        const u32x4_t f = get_row(area + WORD_AREA + ROW_AREA, lane);
+        wave_sync();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = r0[i];
-        transpose4(c);
-        gather_scales(f16lo(d));
-        gather4(qh, h);
+        for (int i = 0; i < 4; ++i) c[i] = v[i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = (h[j] >> (4 * g)) & 0x000f000fu;
+        for (int j = 0; j < 4; ++j) h[j] = (f[j] >> (4 * (lane >> 4))) & 0x000f000fu;
     }
     QMM_DEV half8_t operand(int, int j, int) const
     {
@@ -335,10 +345,10 @@ struct UnitW4Narrow : Unit32<FMT_W4> {
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
     static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
     static QMM_DEV int place(int k) { return UnitW4::place(k); }
-    static constexpr int LOADS = 3;
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    static constexpr int LOADS = 3, AREA = WORD_AREA + 2 * ROW_AREA;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
-        const int b = block_of(m, u, g);
+        const int b = block_of(m, u, q);
         r0 = *(const u32x4_t*)(m.w + n * m.row_bytes + 16 * b);
         UnitW4::scale_at<S32>(m, n, b, d, z);
     }
@@ -348,16 +358,20 @@ struct UnitW4Narrow : Unit32<FMT_W4> {
         pin_reg(d);
         pin_reg(z);
     }
-    QMM_DEV void unpack(const MoeMatrix& m, int)
+    QMM_DEV void unpack(const MoeMatrix& m, uint32_t* area, int lane)
     {
+        put_transposed(area, lane, r0);
+        put_row(area + WORD_AREA, lane, bits_of(UnitW4::scale_value<S32>(m, d)));
+        put_row(area + WORD_AREA + ROW_AREA, lane, UnitW4::bias_lo(UnitW4::zero_value(m, z)));
+        wave_sync();
+        const u32x4_t v = get_word(area, lane), f = get_row(area + WORD_AREA, lane), o = get_row(area + WORD_AREA + ROW_AREA, lane);
+        wave_sync();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = r0[i];
-        transpose4(c);
-        gather_scales(UnitW4::scale_value<S32>(m, d));
-        uint32_t o[4];
-        gather4(UnitW4::bias_lo(UnitW4::zero_value(m, z)), o);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) bias[j] = half2_of(o[j]);
+        for (int j = 0; j < 4; ++j) {
+            c[j] = v[j];
+            this->s[j] = f32_of(f[j]);
+            bias[j] = half2_of(o[j]);
+        }
     }
     QMM_DEV half8_t operand(int, int j, int) const { return UnitW4::values(c[j], bias[j], UnitW4::bias_hi(bias[j])); }
 };
@@ -384,10 +398,10 @@ struct UnitW4Wide {
     uint32_t c[4];
     float s;
     half2_t lo, hi;
-    static constexpr int LOADS = 3;
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    static constexpr int LOADS = 3, AREA = WORD_AREA + 2 * ROW_AREA;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
-        r0 = *(const u32x4_t*)(m.w + n * m.row_bytes + 64 * u + 16 * g);
+        r0 = *(const u32x4_t*)(m.w + n * m.row_bytes + 64 * u + 16 * q);
         UnitW4::scale_at<S32>(m, n, 4 * u, d, z);
     }
     QMM_DEV void pin()
@@ -396,13 +410,18 @@ struct UnitW4Wide {
         pin_reg(d);
         pin_reg(z);
     }
-    QMM_DEV void unpack(const MoeMatrix& m, int)
+    QMM_DEV void unpack(const MoeMatrix& m, uint32_t* area, int lane)
     {
+        put_transposed(area, lane, r0);
+        put_row(area + WORD_AREA, lane, bits_of(UnitW4::scale_value<S32>(m, d)));
+        put_row(area + WORD_AREA + ROW_AREA, lane, UnitW4::bias_lo(UnitW4::zero_value(m, z)));
+        wave_sync();
+        const u32x4_t v = get_word(area, lane);
+        s = f32_of(area[WORD_AREA + (lane & 15) * 4]);
+        lo = half2_of(area[WORD_AREA + ROW_AREA + (lane & 15) * 4]);
+        wave_sync();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = r0[i];
-        transpose4(c);
-        s = UnitW4::scale_value<S32>(m, d);
-        lo = half2_of(UnitW4::bias_lo(UnitW4::zero_value(m, z)));
+        for (int i = 0; i < 4; ++i) c[i] = v[i];
         hi = UnitW4::bias_hi(lo);
     }
     QMM_DEV half8_t operand(int, int j, int) const { return UnitW4::values(c[j], lo, hi); }
@@ -428,13 +447,13 @@ struct Unit<FMT_Q4_K> {
     u32x4_t hd, r0, r1;
     half2_t sc[2], off[2];  // sub-block scale and -1024 times it; the second's / 16 and -64 times it
     uint32_t mn;            // the two minima, one per byte
-    static constexpr int LOADS = 3;
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    static constexpr int LOADS = 3, AREA = 3 * WORD_AREA;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 144;
         hd = *(const u32x4_t*)p;
-        r0 = *(const u32x4_t*)(p + 16 + 32 * g);
-        r1 = *(const u32x4_t*)(p + 32 + 32 * g);
+        r0 = *(const u32x4_t*)(p + 16 + 32 * q);
+        r1 = *(const u32x4_t*)(p + 32 + 32 * q);
     }
     QMM_DEV void pin()
     {
@@ -442,8 +461,17 @@ struct Unit<FMT_Q4_K> {
         pin_reg(r0);
         pin_reg(r1);
     }
-    QMM_DEV void unpack(const MoeMatrix&, int g)
+    QMM_DEV void unpack(const MoeMatrix& m, uint32_t* area, int lane)
     {
+        put_word(area, lane, hd);
+        put_word(area + WORD_AREA, lane, r0);
+        put_word(area + 2 * WORD_AREA, lane, r1);
+        wave_sync();
+        hd = get_word(area, lane);
+        r0 = get_word(area + WORD_AREA, lane);
+        r1 = get_word(area + 2 * WORD_AREA, lane);
+        wave_sync();
+        const int g = lane >> 4;
         const int sh = 16 * (g & 1);
         const uint32_t a = hd[1] >> sh, b = hd[2] >> sh, e = hd[3] >> sh;
         const uint32_t s2 = g < 2 ? a & 0x3f3fu : (e & 0x0f0fu) | ((a >> 2) & 0x3030u);
@@ -495,15 +523,15 @@ struct Unit<FMT_Q6_K> {
     u32x2_t sc;
     uint32_t d;
     half2_t hi[4], lo[4];  // 16 s1 and s0 of the four quarters' scales
-    static constexpr int LOADS = 5;
-    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int g)
+    static constexpr int LOADS = 5, AREA = 4 * WORD_AREA;
+    QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 210;
-        const uint8_t* q = p + 64 * (g >> 1) + 16 * (g & 1);
-        l0 = load16(q);
-        l1 = load16(q + 32);
-        qh = load16(p + 128 + 32 * (g >> 1) + 16 * (g & 1));
-        __builtin_memcpy(&sc, p + 192 + 8 * (g >> 1), 8);
+        const uint8_t* ql = p + 64 * (q >> 1) + 16 * (q & 1);
+        l0 = load16(ql);
+        l1 = load16(ql + 32);
+        qh = load16(p + 128 + 32 * (q >> 1) + 16 * (q & 1));
+        __builtin_memcpy(&sc, p + 192 + 8 * (q >> 1), 8);
         d = load2(p + 208);
     }
     QMM_DEV void pin()
@@ -514,8 +542,22 @@ struct Unit<FMT_Q6_K> {
         pin_reg(sc);
         pin_reg(d);
     }
-    QMM_DEV void unpack(const MoeMatrix&, int g)
+    QMM_DEV void unpack(const MoeMatrix& m, uint32_t* area, int lane)
     {
+        put_word(area, lane, l0);
+        put_word(area + WORD_AREA, lane, l1);
+        put_word(area + 2 * WORD_AREA, lane, qh);
+        put_word(area + 3 * WORD_AREA, lane, u32x4_t{sc[0], sc[1], d, 0});
+        wave_sync();
+        l0 = get_word(area, lane);
+        l1 = get_word(area + WORD_AREA, lane);
+        qh = get_word(area + 2 * WORD_AREA, lane);
+        const u32x4_t v = get_word(area + 3 * WORD_AREA, lane);
+        wave_sync();
+        sc[0] = v[0];
+        sc[1] = v[1];
+        d = v[2];
+        const int g = lane >> 4;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int v = (int)(int8_t)((sc[t >> 1] >> (16 * (t & 1) + 8 * (g & 1))) & 0xffu);
