@@ -44,30 +44,31 @@ struct MoeArgs {
     int32_t* order;           // [P]
     MoeTile* tiles;           // [max_tiles]
     int max_tiles;
-    // prepared activations (tile path): f16 planes in operand order, the hi
-    // parts and for f32 the lo parts, [Kp/128][rows][128] each (a step of many
-    // rows is one run of memory: rows a power of two apart would share an L2
-    // channel); 1/scale per row; Q4_K: hi and lo of the sub-block sums / 32,
-    // [K/256][rows][16]
+    // prepared activations: f16 planes in operand order, the hi parts and for
+    // f32 the lo parts, for the tile kernel [Kp/128][rows][128], for the rows
+    // kernel [Kp/8][rows][8] (a step of many rows is one run of memory); 1/scale
+    // per row; Q4_K: hi and lo of the sub-block sums / 32, 16 per row and unit
     _Float16* xp;
     int64_t x_rows, Kp;
     float* xinv;
     _Float16* xsum;
 };
 
-// Streaming kernel: up to 16 pairs of an expert per workgroup, weights straight
-// from memory to the matrix cores.  one: a workgroup has one pair (or, for a
-// combine, one token and its slots); waves: waves along K per workgroup.
-hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s);
-// Tile kernel: tile_rows(type) pairs of an expert against 128 weight rows (GLU:
-// 64 of each matrix) per workgroup, prepared activations through LDS.
+// One pair (a combine: one token) per workgroup.
+hipError_t launch_one(const MoeArgs& a, int waves, hipStream_t s);
+// What the kernels below need first (rows: the rows kernel, else the tile kernel).
+hipError_t launch_prep(const MoeArgs& a, bool rows, int tm, hipStream_t s);
+// mt * 16 (mt 1, 2 or 4) pairs of an expert per workgroup, the waves along K.
+hipError_t launch_rows(const MoeArgs& a, int mt, int waves, hipStream_t s);
+// tile_rows(type) pairs of an expert against 256 weight rows (GLU: 128 of each
+// matrix) per workgroup.
 inline int tile_rows(int type) { return type == TYPE_F32 ? 64 : 128; }
-hipError_t launch_prep(const MoeArgs& a, hipStream_t s);
 hipError_t launch_tile(const MoeArgs& a, hipStream_t s);
 
-#define QMM_MOE_DECLARE(F)                                                              \
-    hipError_t launch_stream_##F(const MoeArgs& a, bool one, int waves, hipStream_t s); \
-    hipError_t launch_prep_##F(const MoeArgs& a, hipStream_t s);                        \
+#define QMM_MOE_DECLARE(F)                                                            \
+    hipError_t launch_one_##F(const MoeArgs& a, int waves, hipStream_t s);            \
+    hipError_t launch_prep_##F(const MoeArgs& a, bool rows, int tm, hipStream_t s);   \
+    hipError_t launch_rows_##F(const MoeArgs& a, int mt, int waves, hipStream_t s);   \
     hipError_t launch_tile_##F(const MoeArgs& a, hipStream_t s);
 QMM_MOE_DECLARE(q8_0)
 QMM_MOE_DECLARE(q4_0)

@@ -11,96 +11,47 @@
 namespace qmm {
 namespace {
 
-constexpr int SORT_THREADS = 1024;
-constexpr int MAX_E = 1024;
-
-// Sorts the pairs by expert: order[] holds them expert by expert (those
-// without one last), tiles[] the runs of up to tm pairs of one expert.  One
-// workgroup: a histogram, its prefix sums and a scatter in LDS.  The order of
-// an expert's pairs among themselves comes from atomics and may differ from
-// run to run; every output depends on its own pair alone.
-__global__ __launch_bounds__(SORT_THREADS) void moe_sort(MoeArgs a, int tm)
-{
-    __shared__ int cnt[MAX_E + 1], off[MAX_E + 1], tile0[MAX_E + 2];
-    const int tid = (int)threadIdx.x, E = a.E, B = E + 1, P = (int)(a.T * a.top_k);
-    for (int b = tid; b < B; b += SORT_THREADS) cnt[b] = 0;
-    __syncthreads();
-    for (int p = tid; p < P; p += SORT_THREADS) {
-        const int e = a.ids[p];
-        atomicAdd(&cnt[e >= 0 && e < E ? e : E], 1);
-    }
-    __syncthreads();
-    if (tid < 64) {
-        const int per = (B + 63) / 64, b0 = min(tid * per, B), b1 = min(b0 + per, B);
-        int c = 0, t = 0;
-        for (int b = b0; b < b1; ++b) {
-            c += cnt[b];
-            t += (cnt[b] + tm - 1) / tm;
-        }
-        int ci = c, ti = t;
-        for (int d = 1; d < 64; d *= 2) {
-            const int cu = __shfl_up(ci, d), tu = __shfl_up(ti, d);
-            if (tid >= d) {
-                ci += cu;
-                ti += tu;
-            }
-        }
-        c = ci - c;
-        t = ti - t;
-        for (int b = b0; b < b1; ++b) {
-            off[b] = c;
-            tile0[b] = t;
-            c += cnt[b];
-            t += (cnt[b] + tm - 1) / tm;
-        }
-        if (tid == 63) tile0[B] = ti;
-    }
-    __syncthreads();
-    for (int i = tid; i < a.max_tiles; i += SORT_THREADS) {
-        MoeTile t = {-1, 0, 0, 0};
-        if (i < tile0[B]) {
-            int lo = 0, hi = B;  // the last bucket whose first tile is <= i
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (tile0[mid] <= i) lo = mid;
-                else hi = mid;
-            }
-            const int k = (i - tile0[lo]) * tm;
-            t.e = lo < E ? lo : -1;
-            t.start = off[lo] + k;
-            t.count = min(tm, cnt[lo] - k);
-        }
-        a.tiles[i] = t;
-    }
-    __syncthreads();
-    for (int p = tid; p < P; p += SORT_THREADS) {
-        const int e = a.ids[p];
-        a.order[atomicAdd(&off[e >= 0 && e < E ? e : E], 1)] = p;
-    }
-}
-
-// y[t][n] = sum over the slots with an expert of weights[t][s] * prod[t][s][n]
+// y[t][n] = sum over the slots with an expert of weights[t][s] * prod[t][s][n].
+// V (4 or 1) outputs per thread; rows of outputs along the grid's y.
+template <int V>
 __global__ __launch_bounds__(256) void moe_combine(MoeArgs a, const float* prod)
 {
-    const int64_t outs = a.T * a.N, stride = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < outs; i += stride) {
-        const int64_t t = i / a.N, n = i - t * a.N;
-        float v = 0.0f;
+    typedef float vec_t __attribute__((ext_vector_type(V)));
+    const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+    if (n >= a.N) return;
+    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
+        vec_t v = {};
         for (int s = 0; s < a.top_k; ++s) {
             const int64_t p = t * a.top_k + s;
             const int e = a.ids[p];
-            if (e >= 0 && e < a.E) v = fmaf(a.weights[p], prod[p * a.N + n], v);
+            if (e < 0 || e >= a.E) continue;
+            const vec_t q = *(const vec_t*)(prod + p * a.N + n);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = fmaf(a.weights[p], q[i], v[i]);
         }
-        if (a.y_type == TYPE_F32) store_out<true>(a.y, a.y_type, i, v);
-        else store_out<false>(a.y, a.y_type, i, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (a.y_type == TYPE_F32) store_out<true>(a.y, a.y_type, t * a.N + n + i, v[i]);
+            else store_out<false>(a.y, a.y_type, t * a.N + n + i, v[i]);
+        }
     }
 }
 
-enum { PATH_ONE, PATH_SCAN, PATH_STREAM, PATH_TILE };
+hipError_t launch_combine(const MoeArgs& a, const float* prod, hipStream_t s)
+{
+    const bool four = a.N % 4 == 0;
+    const int64_t per = four ? 1024 : 256;
+    const dim3 grid((unsigned)((a.N + per - 1) / per), (unsigned)std::min<int64_t>(a.T, 65535));
+    if (four) moe_combine<4><<<grid, dim3(256), 0, s>>>(a, prod);
+    else moe_combine<1><<<grid, dim3(256), 0, s>>>(a, prod);
+    return hipGetLastError();
+}
+
+enum { PATH_ONE, PATH_ROWS, PATH_TILE };
 
 // What a call runs and what it needs of the workspace.
 struct MoePlan {
-    int path, waves;
+    int path, waves, mt;
     bool sort;
     int tm, max_tiles;
     int64_t x_rows, Kp;
@@ -114,13 +65,18 @@ MoePlan plan_of(const MoeArgs& a)
     MoePlan p = {};
     const int64_t P = a.T * a.top_k;
     const bool dense = a.fmt >= FMT_W4;
-    if (a.T == 1) p.path = PATH_ONE;
-    else if (P > 24 * (int64_t)(dense ? 4 : a.E)) p.path = PATH_TILE;
-    else p.path = dense || P > 64 ? PATH_STREAM : PATH_SCAN;
-    p.waves = 4;
-    p.tm = p.path == PATH_TILE ? tile_rows(a.type) : 16;
+    const int64_t unit = a.fmt == FMT_Q4_K || a.fmt == FMT_Q6_K ? 256 : 128, units = (a.K + unit - 1) / unit;
+    const int64_t avg = dense ? P : (P + a.E - 1) / a.E;  // pairs of an expert
+    if (a.T <= (dense ? 1 : 2)) p.path = PATH_ONE;
+    else if (avg > 48) p.path = PATH_TILE;
+    else p.path = PATH_ROWS;
+    p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    const int64_t items = units * (p.path == PATH_ONE && a.op == MOE_COMBINE ? a.top_k : 1);
+    p.waves = 1;
+    while (p.waves < (p.path == PATH_ONE ? 16 : 8) && p.waves * 2 <= items) p.waves *= 2;
+    p.tm = p.path == PATH_TILE ? tile_rows(a.type) : 16 * p.mt;
     p.max_tiles = (int)(dense ? (P + p.tm - 1) / p.tm : P / p.tm + std::min<int64_t>(a.E + 1, P));
-    p.sort = !dense && p.path >= PATH_STREAM;
+    p.sort = !dense && p.path != PATH_ONE;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -131,14 +87,15 @@ MoePlan plan_of(const MoeArgs& a)
         p.order = take((size_t)P * 4);
         p.tiles = take((size_t)p.max_tiles * sizeof(MoeTile));
     }
-    if (p.path == PATH_TILE) {
-        p.x_rows = a.per_slot ? P : a.T;
-        p.Kp = (a.K + 255) / 256 * 256;
+    if (p.path != PATH_ONE) {
+        p.x_rows = p.path == PATH_ROWS || a.per_slot ? P : a.T;
+        const int64_t step = p.path == PATH_TILE ? 256 : unit;
+        p.Kp = (a.K + step - 1) / step * step;
         p.xp = take((size_t)p.x_rows * p.Kp * (a.type == TYPE_F32 ? 4 : 2));
         p.xinv = take((size_t)p.x_rows * 4);
         if (a.fmt == FMT_Q4_K) p.xsum = take((size_t)p.x_rows * (p.Kp / 256) * 32);
+        if (a.op == MOE_COMBINE) p.products = take((size_t)P * (size_t)a.N * 4);
     }
-    if (a.op == MOE_COMBINE && p.path != PATH_ONE) p.products = take((size_t)P * (size_t)a.N * 4);
     p.bytes = off;
     return p;
 }
@@ -146,36 +103,29 @@ MoePlan plan_of(const MoeArgs& a)
 hipError_t launch_moe(const MoeArgs& call, const MoePlan& p, char* ws, hipStream_t s)
 {
     MoeArgs a = call;
-    hipError_t e = hipSuccess;
     a.y_type = a.type;
+    if (p.path == PATH_ONE) return launch_one(a, p.waves, s);
+    a.order = (int32_t*)(ws + p.order);
+    a.tiles = (MoeTile*)(ws + p.tiles);
     a.max_tiles = p.max_tiles;
-    if (p.sort) {
-        a.order = (int32_t*)(ws + p.order);
-        a.tiles = (MoeTile*)(ws + p.tiles);
-        moe_sort<<<dim3(1), dim3(SORT_THREADS), 0, s>>>(a, p.tm);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (p.path == PATH_TILE) {
-        a.xp = (_Float16*)(ws + p.xp);
-        a.xinv = (float*)(ws + p.xinv);
-        a.xsum = (_Float16*)(ws + p.xsum);
-        a.x_rows = p.x_rows;
-        a.Kp = p.Kp;
-        if ((e = launch_prep(a, s)) != hipSuccess) return e;
-    }
-    const bool summed = a.op == MOE_COMBINE && p.path != PATH_ONE;
+    a.xp = (_Float16*)(ws + p.xp);
+    a.xinv = (float*)(ws + p.xinv);
+    a.xsum = (_Float16*)(ws + p.xsum);
+    a.x_rows = p.x_rows;
+    a.Kp = p.Kp;
+    hipError_t e = launch_prep(a, p.path == PATH_ROWS, p.tm, s);
+    if (e != hipSuccess) return e;
     float* products = (float*)(ws + p.products);
-    if (summed) {
+    if (call.op == MOE_COMBINE) {
         a.op = MOE_RUN;
         a.y = products;
         a.y_type = TYPE_F32;
     }
-    e = p.path == PATH_TILE ? launch_tile(a, s) : launch_stream(a, p.path == PATH_ONE, p.waves, s);
-    if (e != hipSuccess || !summed) return e;
+    e = p.path == PATH_TILE ? launch_tile(a, s) : launch_rows(a, p.mt, p.waves, s);
+    if (e != hipSuccess || call.op != MOE_COMBINE) return e;
     a = call;
     a.y_type = a.type;
-    moe_combine<<<dim3((unsigned)std::min<int64_t>((a.T * a.N + 255) / 256, 1 << 16)), dim3(256), 0, s>>>(a, products);
-    return hipGetLastError();
+    return launch_combine(a, products, s);
 }
 
 int bad(const char* msg) { return set_error(QMM_EINVAL, msg); }
@@ -249,15 +199,21 @@ bool off16(const void* p) { return (uintptr_t)p % 16 != 0; }
     case FMT_W4_WIDE_S32: return CALL(w4_wide_s32); \
     default: return CALL(w4);                   \
     }
-hipError_t launch_stream(const MoeArgs& a, bool one, int waves, hipStream_t s)
+hipError_t launch_one(const MoeArgs& a, int waves, hipStream_t s)
 {
-#define CALL(F) launch_stream_##F(a, one, waves, s)
+#define CALL(F) launch_one_##F(a, waves, s)
     QMM_MOE_DISPATCH(CALL)
 #undef CALL
 }
-hipError_t launch_prep(const MoeArgs& a, hipStream_t s)
+hipError_t launch_prep(const MoeArgs& a, bool rows, int tm, hipStream_t s)
 {
-#define CALL(F) launch_prep_##F(a, s)
+#define CALL(F) launch_prep_##F(a, rows, tm, s)
+    QMM_MOE_DISPATCH(CALL)
+#undef CALL
+}
+hipError_t launch_rows(const MoeArgs& a, int mt, int waves, hipStream_t s)
+{
+#define CALL(F) launch_rows_##F(a, mt, waves, s)
     QMM_MOE_DISPATCH(CALL)
 #undef CALL
 }

@@ -1,0 +1,238 @@
+// qmm_moe_prep.h -- what the rows and tile kernels need before they start, in
+// one launch: the activations in operand order and the pairs sorted by expert.
+//
+// Block 0 (where there are experts) sorts: a histogram, its prefix sums and a
+// scatter in LDS give tiles[], the runs of up to tm pairs of one expert, those
+// without an expert last.  The other blocks bring rows into operand order, each
+// scaled by a power of two so that its f16 parts (f32: hi + lo) hold it.
+//
+// Tile kernel: rows as the caller has them, [step][row][128]; order[] (the
+// pairs expert by expert) from the scatter.  The order of an expert's pairs
+// among themselves comes from atomics and may differ from run to run: every
+// output depends on its own pair alone.
+// Rows kernel: rows in sorted order, [step][operand piece][row][8], so that an
+// operand's lanes read neighbouring bytes.  A row's place is the number of
+// pairs with a lower expert or the same one and a lower index, counted by the
+// row's own waves, which also write order[].
+#pragma once
+#include "qmm_moe_unit.h"
+
+namespace qmm {
+
+constexpr int MOE_MAX_E = 1024, PREP_THREADS = 1024, PREP_WAVES = PREP_THREADS / 64;
+
+struct SortSpace {
+    int cnt[MOE_MAX_E + 1], off[MOE_MAX_E + 1], tile0[MOE_MAX_E + 2];
+};
+
+QMM_DEV int bucket_of(const MoeArgs& a, int p)
+{
+    const int e = a.ids[p];
+    return e >= 0 && e < a.E ? e : a.E;
+}
+
+template <bool SCATTER>
+QMM_DEV void sort_pairs(const MoeArgs& a, int tm, SortSpace& s)
+{
+    constexpr int KEEP = 16;  // pairs per thread whose place in their bucket stays in registers
+    const int tid = (int)threadIdx.x, E = a.E, B = E + 1, P = (int)(a.T * a.top_k);
+    for (int b = tid; b < B; b += PREP_THREADS) s.cnt[b] = 0;
+    __syncthreads();
+    int bucket[KEEP], rank[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+        const int p = i * PREP_THREADS + tid;
+        bucket[i] = p < P ? bucket_of(a, p) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        if (bucket[i] >= 0) rank[i] = atomicAdd(&s.cnt[bucket[i]], 1);
+    __syncthreads();
+    // the kept pairs come first in their buckets
+    if (SCATTER)
+        for (int b = tid; b < B; b += PREP_THREADS) s.off[b] = s.cnt[b];
+    __syncthreads();
+    for (int p = KEEP * PREP_THREADS + tid; p < P; p += PREP_THREADS) atomicAdd(&s.cnt[bucket_of(a, p)], 1);
+    __syncthreads();
+    if (tid < 64) {
+        const int per = (B + 63) / 64, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+        int c = 0, t = 0;
+        for (int b = b0; b < b1; ++b) {
+            c += s.cnt[b];
+            t += (s.cnt[b] + tm - 1) / tm;
+        }
+        int ci = c, ti = t;
+        for (int d = 1; d < 64; d *= 2) {
+            const int cu = __shfl_up(ci, d), tu = __shfl_up(ti, d);
+            if (tid >= d) {
+                ci += cu;
+                ti += tu;
+            }
+        }
+        c = ci - c;
+        t = ti - t;
+        for (int b = b0; b < b1; ++b) {
+            const int n = s.cnt[b];
+            s.tile0[b] = t;
+            t += (n + tm - 1) / tm;
+            s.cnt[b] = c;  // from here on: the bucket's first place
+            c += n;
+        }
+        if (tid == 63) s.tile0[B] = ti;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.max_tiles; i += PREP_THREADS) {
+        MoeTile t = {-1, 0, 0, 0};
+        if (i < s.tile0[B]) {
+            int lo = 0, hi = B;  // the last bucket whose first tile is <= i
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (s.tile0[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            const int k = (i - s.tile0[lo]) * tm, n = (lo + 1 < B ? s.cnt[lo + 1] : P) - s.cnt[lo];
+            t.e = lo < E ? lo : -1;
+            t.start = s.cnt[lo] + k;
+            t.count = min(tm, n - k);
+        }
+        a.tiles[i] = t;
+    }
+    if constexpr (SCATTER) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            if (bucket[i] >= 0) a.order[s.cnt[bucket[i]] + rank[i]] = i * PREP_THREADS + tid;
+        for (int p = KEEP * PREP_THREADS + tid; p < P; p += PREP_THREADS) {
+            const int b = bucket_of(a, p);
+            a.order[s.cnt[b] + atomicAdd(&s.off[b], 1)] = p;
+        }
+    }
+}
+
+// wr (1, 4 or 16): waves that share a row.  ROWS: for the rows kernel.
+template <int FMT, int PL, bool ROWS>
+__global__ __launch_bounds__(PREP_THREADS) void moe_prep(MoeArgs a, int tm, int wr)
+{
+    using U = Unit<FMT>;
+    __shared__ union {
+        SortSpace sort;
+        struct {
+            float am[PREP_WAVES];
+            int place[PREP_WAVES];
+        } row;
+    } sh;
+    int block = (int)blockIdx.x;
+    if (a.ids) {
+        if (block == 0) {
+            sort_pairs<!ROWS>(a, tm, sh.sort);
+            return;
+        }
+        --block;
+    }
+    const int lane = (int)__lane_id(), wave = (int)threadIdx.x >> 6, sub = wave % wr;
+    const int64_t row = (int64_t)block * (PREP_WAVES / wr) + wave / wr;  // of the output
+    const bool live = row < a.x_rows;
+    // rows kernel with experts: row is a pair
+    const int64_t src = ROWS && a.ids && !a.per_slot ? row / a.top_k : row;
+    float am = 0.0f;
+    int place = 0;
+    if (live) {
+        for (int64_t k = (sub * 64 + lane) * 4; k < a.K; k += wr * 256) {
+            float v[4];
+            Raw4<PL> w;
+            w.load(a.x, src * a.K + k);
+            w.values(a.type, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) am = fmaxf(am, fabsf(v[i]));
+        }
+        if (ROWS && a.ids) {
+            const int mine = bucket_of(a, (int)row), P = (int)a.x_rows;
+            for (int q0 = sub * 64; q0 < P; q0 += wr * 64) {
+                const int q = q0 + lane, b = q < P ? bucket_of(a, q) : a.E + 1;
+                place += __builtin_popcountll(__ballot(b < mine || (b == mine && q < (int)row)));
+            }
+        }
+    }
+    am = wave_max(am);
+    if (wr > 1) {
+        if (lane == 0) {
+            sh.row.am[wave] = am;
+            sh.row.place[wave] = place;
+        }
+        __syncthreads();
+        const int w0 = wave - sub;
+        place = 0;
+        for (int i = 0; i < wr; ++i) {
+            am = fmaxf(am, sh.row.am[w0 + i]);
+            place += sh.row.place[w0 + i];
+        }
+    }
+    if (!live) return;
+    float s, inv;
+    act_scale(am, s, inv);
+    const int64_t dst = ROWS && a.ids ? place : row;
+    if (sub == 0 && lane == 0) {
+        a.xinv[dst] = inv;
+        if (ROWS && a.ids) a.order[dst] = (int)row;
+    }
+    const int64_t plane = a.x_rows * a.Kp;
+    for (int64_t q = sub * 64 + lane; q < a.Kp / 8; q += wr * 64) {  // piece [unit][step][j][g]
+        constexpr int PIECES = U::UNIT / 8;
+        const int64_t u = q / PIECES;
+        const int i = (int)(q % PIECES), h = i >> 4, j = (i >> 2) & 3, g = i & 3;
+        float v[8];
+        half8_t p[PL];
+        float sum = 0.0f;
+        if (u * U::UNIT + U::o0(h, j, g) < a.K) {
+            float e[8];
+            Raw4<PL> w0, w1;
+            w0.load(a.x, src * a.K + u * U::UNIT + U::o0(h, j, g));
+            w1.load(a.x, src * a.K + u * U::UNIT + U::o1(h, j, g));
+            w0.values(a.type, e);
+            w1.values(a.type, e + 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = e[U::slot(k)] * s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        }
+        split8<PL>(v, p);
+        const int64_t at = ROWS ? (q * a.x_rows + dst) * 8 : ((q >> 4) * a.x_rows + dst) * 128 + (q & 15) * 8;
+#pragma unroll
+        for (int k = 0; k < PL; ++k) *(half8_t*)(a.xp + k * plane + at) = p[k];
+        if constexpr (U::MINS) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += v[k];
+            sum += __shfl_xor(sum, 4);
+            sum += __shfl_xor(sum, 8);
+            sum *= 0.03125f;
+            if (j == 0) {
+                // rows kernel: [unit][g][row][4], tile kernel: [unit][row][g][4]
+                _Float16* o = a.xsum + (ROWS ? (u * 4 + g) * a.x_rows + dst : (u * a.x_rows + dst) * 4 + g) * 4 + h;
+                const _Float16 hi = (_Float16)sum;
+                o[0] = hi;
+                o[2] = (_Float16)(sum - (float)hi);
+            }
+        }
+    }
+}
+
+template <int FMT, int PL>
+hipError_t launch_prep_t(const MoeArgs& a, bool rows, int tm, hipStream_t s)
+{
+    // enough waves to fill the chip, each with some work
+    int wr = 1;
+    while (wr < 16 && a.x_rows * wr < 4096 && a.K > wr * 1024) wr *= 4;
+    const int64_t per = PREP_WAVES / wr;
+    const dim3 grid((unsigned)((a.x_rows + per - 1) / per + (a.ids ? 1 : 0))), block(PREP_THREADS);
+    if (rows) moe_prep<FMT, PL, true><<<grid, block, 0, s>>>(a, tm, wr);
+    else moe_prep<FMT, PL, false><<<grid, block, 0, s>>>(a, tm, wr);
+    return hipGetLastError();
+}
+
+#define QMM_MOE_PREP(NAME, FMT)                                                                                     \
+    hipError_t launch_prep_##NAME(const MoeArgs& a, bool rows, int tm, hipStream_t s)                               \
+    {                                                                                                               \
+        return a.type == TYPE_F32 ? launch_prep_t<FMT, 2>(a, rows, tm, s) : launch_prep_t<FMT, 1>(a, rows, tm, s); \
+    }
+
+}  // namespace qmm

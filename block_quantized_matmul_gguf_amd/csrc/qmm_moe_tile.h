@@ -319,67 +319,6 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
     }
 }
 
-// Activations in operand order.  One wave per row: its largest magnitude, then
-// eight values per lane at a time, scaled, as f16 parts.
-template <int FMT, int PL>
-__global__ __launch_bounds__(256) void moe_prep(MoeArgs a)
-{
-    using U = Unit<FMT>;
-    const int lane = (int)__lane_id();
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= a.x_rows) return;
-    float am = 0.0f;
-    for (int64_t k = lane * 4; k < a.K; k += 256) {
-        float v[4];
-        Raw4<PL> w;
-        w.load(a.x, row * a.K + k);
-        w.values(a.type, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) am = fmaxf(am, fabsf(v[i]));
-    }
-    float s, inv;
-    act_scale(wave_max(am), s, inv);
-    if (lane == 0) a.xinv[row] = inv;
-    const int64_t plane = a.x_rows * a.Kp;
-    for (int64_t q = lane; q < a.Kp / 8; q += 64) {  // piece [unit][step][j][g]
-        constexpr int PIECES = U::UNIT / 8;
-        const int64_t u = q / PIECES;
-        const int i = (int)(q % PIECES), h = i >> 4, j = (i >> 2) & 3, g = i & 3;
-        float v[8];
-        half8_t p[PL];
-        float sum = 0.0f;
-        if (u * U::UNIT + U::o0(h, j, g) < a.K) {
-            float e[8];
-            Raw4<PL> w0, w1;
-            w0.load(a.x, row * a.K + u * U::UNIT + U::o0(h, j, g));
-            w1.load(a.x, row * a.K + u * U::UNIT + U::o1(h, j, g));
-            w0.values(a.type, e);
-            w1.values(a.type, e + 4);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = e[U::slot(k)] * s;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-        }
-        split8<PL>(v, p);
-#pragma unroll
-        for (int k = 0; k < PL; ++k) *(half8_t*)(a.xp + k * plane + ((q >> 4) * a.x_rows + row) * 128 + (q & 15) * 8) = p[k];
-        if constexpr (U::MINS) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += v[k];
-            sum += __shfl_xor(sum, 4);
-            sum += __shfl_xor(sum, 8);
-            sum *= 0.03125f;
-            if (j == 0) {
-                _Float16* o = a.xsum + (u * a.x_rows + row) * 16 + g * 4 + h;
-                const _Float16 hi = (_Float16)sum;
-                o[0] = hi;
-                o[2] = (_Float16)(sum - (float)hi);
-            }
-        }
-    }
-}
-
 template <int FMT, int PL, int MT, int NW>
 hipError_t launch_tile_t(const MoeArgs& a, hipStream_t s)
 {
@@ -393,20 +332,10 @@ hipError_t launch_tile_t(const MoeArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <int FMT>
-hipError_t launch_prep_t(const MoeArgs& a, hipStream_t s)
-{
-    const dim3 grid((unsigned)((a.x_rows + 3) / 4)), block(256);
-    if (a.type == TYPE_F32) moe_prep<FMT, 2><<<grid, block, 0, s>>>(a);
-    else moe_prep<FMT, 1><<<grid, block, 0, s>>>(a);
-    return hipGetLastError();
-}
-
-#define QMM_MOE_TILE(NAME, FMT)                                                                        \
-    hipError_t launch_prep_##NAME(const MoeArgs& a, hipStream_t s) { return launch_prep_t<FMT>(a, s); } \
+#define QMM_MOE_TILE(NAME, FMT)                                                                          \
     hipError_t launch_tile_##NAME(const MoeArgs& a, hipStream_t s)                                      \
     {                                                                                                   \
-        return a.type == TYPE_F32 ? launch_tile_t<FMT, 2, 4, 8>(a, s) : launch_tile_t<FMT, 1, 8, 8>(a, s);\
+        return a.type == TYPE_F32 ? launch_tile_t<FMT, 2, 4, 8>(a, s) : launch_tile_t<FMT, 1, 8, 8>(a, s); \
     }
 
 }  // namespace qmm

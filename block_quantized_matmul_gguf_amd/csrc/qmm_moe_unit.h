@@ -121,6 +121,16 @@ struct MoeMatrix {
     uint32_t group_magic;
 };
 
+// Eight neighbours that make one operand, in its order of slots.
+template <class U>
+QMM_DEV void put_operand(_Float16* to, half8_t v)
+{
+    half8_t w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = v[U::slot(i)];
+    *(half8_t*)to = w;
+}
+
 // Per format:
 //   UNIT   values of a unit;  HALVES  steps of 128 values in it
 //   load   of row n: lane quarter q's words;  unpack  the exchange, and scales
@@ -128,7 +138,8 @@ struct MoeMatrix {
 //   CHAIN  products of a step share one scale (and so one accumulator)
 //   PARTS  operands per product;  MINS  Q4_K's minima
 //   o0, o1, slot: the k values of lane group g in product j of step h are
-//     o0 .. o0+3 and o1 .. o1+3; slot i of the operand holds number slot(i)
+//     o0 .. o0+3 and o1 .. o1+3; slot i of the operand holds number slot(i);
+//   put8   the inverse
 template <int FMT>
 struct Unit;
 
@@ -140,11 +151,18 @@ struct Unit32 {
     static constexpr bool CHAIN = false, MINS = false;
     static QMM_DEV int o0(int, int j, int g) { return 32 * j + 4 * g; }
     static QMM_DEV int o1(int, int j, int g) { return 32 * j + 16 + 4 * g; }
-    // position of value k of a unit in operand order [step][j][g][slot]
-    static QMM_DEV int place(int k)
+    // values k .. k+7 (k a multiple of 8) of a unit to their places in operand order [step][j][g][slot]
+    static QMM_DEV void put8(_Float16* x, int k, half8_t v)
     {
-        const int e = k & 31, i = (e & 3) | ((e & 16) >> 2);  // number within the operand's eight
-        return (((k >> 5) * 4 + ((e >> 2) & 3)) << 3) | (FMT == FMT_Q8_0 ? i : nib_perm(i));
+        typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+        _Float16* to = x + ((k >> 5) * 4 + ((k >> 2) & 3)) * 8 + ((k >> 2) & 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            half4_t w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = v[4 * i + (FMT == FMT_Q8_0 ? j : nib_perm(j))];
+            *(half4_t*)(to + 8 * i) = w;
+        }
     }
     // Block 4u + q, or the row's last: past the end activations are zero, and a
     // load that always happens keeps the wave's count of loads in flight known.
@@ -306,7 +324,7 @@ struct UnitW4 {
     static QMM_DEV int o0(int, int j, int g) { return 32 * j + 8 * g; }
     static QMM_DEV int o1(int, int j, int g) { return 32 * j + 8 * g + 4; }
     static QMM_DEV int slot(int i) { return (i >> 1) | ((i & 1) << 2); }
-    static QMM_DEV int place(int k) { return (k & ~7) | ((k & 3) << 1) | ((k >> 2) & 1); }
+    static QMM_DEV void put8(_Float16* x, int k, half8_t v) { put_operand<UnitW4>(x + k, v); }
     // -(1024 + z) and -(64 + z), in both halves of a dword
     static QMM_DEV uint32_t bias_lo(uint32_t z) { return (0xe400u | z) * 0x00010001u; }
     static QMM_DEV half2_t bias_hi(half2_t lo) { return lo + both(960.0f); }
@@ -344,7 +362,7 @@ struct UnitW4Narrow : Unit32<FMT_W4> {
     static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
     static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
-    static QMM_DEV int place(int k) { return UnitW4::place(k); }
+    static QMM_DEV void put8(_Float16* x, int k, half8_t v) { UnitW4::put8(x, k, v); }
     static constexpr int LOADS = 3, AREA = WORD_AREA + 2 * ROW_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
@@ -391,7 +409,7 @@ struct UnitW4Wide {
     static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
     static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
-    static QMM_DEV int place(int k) { return UnitW4::place(k); }
+    static QMM_DEV void put8(_Float16* x, int k, half8_t v) { UnitW4::put8(x, k, v); }
     u32x4_t r0;
     UnitW4::scale_t<S32> d;
     uint8_t z;
@@ -443,7 +461,10 @@ struct Unit<FMT_Q4_K> {
     static QMM_DEV int o0(int h, int j, int g) { return 64 * g + 32 * h + 8 * j; }
     static QMM_DEV int o1(int h, int j, int g) { return o0(h, j, g) + 4; }
     static QMM_DEV int slot(int i) { return nib_perm(i); }
-    static QMM_DEV int place(int k) { return ((((k >> 5) & 1) * 4 + ((k >> 3) & 3)) * 4 + (k >> 6)) * 8 + nib_perm(k & 7); }
+    static QMM_DEV void put8(_Float16* x, int k, half8_t v)
+    {
+        put_operand<Unit<FMT_Q4_K>>(x + ((((k >> 5) & 1) * 4 + ((k >> 3) & 3)) * 4 + (k >> 6)) * 8, v);
+    }
     u32x4_t hd, r0, r1;
     half2_t sc[2], off[2];  // sub-block scale and -1024 times it; the second's / 16 and -64 times it
     uint32_t mn;            // the two minima, one per byte
@@ -514,10 +535,10 @@ struct Unit<FMT_Q6_K> {
     }
     static QMM_DEV int o1(int h, int j, int g) { return o0(h, j, g) + 4; }
     static QMM_DEV int slot(int i) { return i; }
-    static QMM_DEV int place(int k)
+    static QMM_DEV void put8(_Float16* x, int k, half8_t v)
     {
         const int jj = 2 * ((k >> 5) & 3) + ((k >> 3) & 1), g = 2 * (k >> 7) + ((k >> 4) & 1);
-        return (jj * 4 + g) * 8 + (k & 7);
+        put_operand<Unit<FMT_Q6_K>>(x + (jj * 4 + g) * 8, v);
     }
     u32x4_t l0, l1, qh;
     u32x2_t sc;
@@ -657,28 +678,32 @@ QMM_DEV half8_t sums_operand(const float s[2])
 
 QMM_DEV f32x4_t mfma(half8_t a, half8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// One step (128 values) of NT units against 16 activation rows: acc[t] += the
-// step's sums.  A(j, part) gives activation operands.
-template <int FMT, int PL, int NT, class AF>
-QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[NT])
+// One step (128 values) of NT units against MT groups of 16 activation rows:
+// acc[m][t] += the step's sums.  A(m, j, part) gives activation operands.
+template <int FMT, int PL, int MT, int NT, class AF>
+QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[MT][NT])
 {
     using U = Unit<FMT>;
-    f32x4_t d[NT];
+    f32x4_t d[NT][MT];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            if (!U::CHAIN || j == 0) d[t] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int q = 0; q < U::PARTS; ++q) {
                 const half8_t b = un[t].operand(h, j, q);
 #pragma unroll
-                for (int p = 0; p < PL; ++p) d[t] = mfma(A(j, p), b, d[t]);
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int p = 0; p < PL; ++p)
+                        d[t][m] = mfma(A(m, j, p), b, p + q == 0 && (!U::CHAIN || j == 0) ? f32x4_t{0, 0, 0, 0} : d[t][m]);
             }
             if (!U::CHAIN || j == 3) {
                 const float s = un[t].scale(j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(s, d[t][i], acc[t][i]);
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(s, d[t][m][i], acc[m][t][i]);
             }
         }
     }
