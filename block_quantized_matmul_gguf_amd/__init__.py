@@ -19,6 +19,7 @@ module fails loudly if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 Q4_0, Q5_0, Q8_0, Q4_K, Q6_K, Q8_K = 2, 6, 8, 12, 14, 15
@@ -395,14 +396,14 @@ def _tensor(t, dtype, dims, name, device=None):
     ``dtype`` (None: a float type) and ``dims`` dimensions."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if dims is not None and t.dim() not in (dims if isinstance(dims, tuple) else (dims,)):
-        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    if dims is not None and t.dim() not in dims:
+        raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -417,26 +418,42 @@ def _out(t, shape, dtype, device, name):
     return t
 
 
+def _current_stream(torch, index):
+    """The handle of device ``index``'s current stream (torch's own shortcut to
+    it: building a Stream object would cost a fifth of a small call)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _on_device(device, stream, body):
     """Runs body(stream handle) with ``device`` current and ``stream`` (None:
     that device's current stream) as the stream of allocations."""
     torch = _torch()
-    if stream is not None and stream.device != device:
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return body(_current_stream(torch, device.index))
+        with torch.cuda.device(device):
+            return body(_current_stream(torch, device.index))
+    if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    if stream is None and torch.cuda.current_device() == device.index:
-        return body(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
-        if stream is None:
-            return body(torch.cuda.current_stream().cuda_stream)
-        with torch.cuda.stream(stream):
-            return body(stream.cuda_stream)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
-def _scratch(nbytes, device, where):
-    """(pointer, bytes, the tensor that owns them) of a call's workspace."""
-    if nbytes < 0:
-        raise QmmError(EINVAL, where, last_error())
-    if nbytes == 0:
+@functools.lru_cache(maxsize=4096)
+def _experts_workspace(product, fmt, e, n, k, t, top_k, code):
+    return int(lib().qmatmul_experts_workspace_bytes(product, fmt, e, n, k, t, top_k, code))
+
+
+@functools.lru_cache(maxsize=4096)
+def _w4_workspace(n, k, m, group, code):
+    return int(lib().qmatmul_w4_workspace_bytes(n, k, m, group, code))
+
+
+def _scratch(nbytes, device):
+    """(pointer, bytes, the tensor that owns them) of a call's workspace; none
+    for sizes that the call itself will refuse."""
+    if nbytes <= 0:
         return None, 0, None
     ws = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
     return ws.data_ptr(), nbytes, ws
@@ -454,14 +471,14 @@ def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups:
     never chosen; slots left over have id -1 and weight 0.  Weights are the
     scores, divided by their sum if ``renormalize``, times ``scale``."""
     torch = _torch()
-    _tensor(logits, None, 2, "logits")
+    _tensor(logits, None, (2,), "logits")
     code = _type_of(logits, "logits")
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
     dev = logits.device
     t, e = logits.shape
     if bias is not None:
-        _tensor(bias, torch.float32, 1, "bias", dev)
+        _tensor(bias, torch.float32, (1,), "bias", dev)
         if bias.shape[0] != e:
             raise ValueError(f"bias must have shape ({e},), got {tuple(bias.shape)}")
 
@@ -485,7 +502,7 @@ def _expert_args(fmt, w, x, ids, x_dims, name):
     _tensor(x, None, x_dims, name)
     code = _type_of(x, name)
     dev = x.device
-    _tensor(ids, torch.int32, 2, "ids", dev)
+    _tensor(ids, torch.int32, (2,), "ids", dev)
     t, k = ids.shape
     if x.shape[0] != t or (x.dim() == 3 and x.shape[1] != k):
         raise ValueError(f"{name} {tuple(x.shape)} and ids {tuple(ids.shape)} differ in tokens or slots")
@@ -495,7 +512,7 @@ def _expert_args(fmt, w, x, ids, x_dims, name):
         raise ValueError(f"K={kk} is not a multiple of the block size of format {fmt}")
     e = n = None
     for t_w, w_name in w:
-        _tensor(t_w, torch.uint8, 3, w_name, dev)
+        _tensor(t_w, torch.uint8, (3,), w_name, dev)
         if t_w.shape[2] != rb or (e is not None and (t_w.shape[0] != e or t_w.shape[1] != n)):
             raise ValueError(f"{w_name} must be [E, N, {rb}] uint8, got {tuple(t_w.shape)}")
         e, n = t_w.shape[0], t_w.shape[1]
@@ -513,8 +530,8 @@ def experts_matmul(fmt: int, w, x, ids, y=None, stream=None):
 
     def body(s):
         out = _out(y, (t, k, n), x.dtype, dev, "y")
-        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_RUN if x.dim() == 2 else EXPERTS_RUN_SLOTS, fmt,
-                                                                      e, n, kk, t, k, code), dev, "qmatmul_experts_run")
+        ws, nb, keep = _scratch(_experts_workspace(EXPERTS_RUN if x.dim() == 2 else EXPERTS_RUN_SLOTS, fmt, e, n, kk, t, k,
+                                                   code), dev)
         _check(lib().qmatmul_experts_run(fmt, e, n, kk, t, k, code, int(x.dim() == 3), w.data_ptr(), x.data_ptr(),
                                          ids.data_ptr(), out.data_ptr(), ws, nb, s), "qmatmul_experts_run")
         return out
@@ -528,13 +545,12 @@ def experts_glu(fmt: int, w_gate, w_up, x, ids, act: str = "silu", h=None, strea
     "gelu" (the tanh form).  Returns [T, top_k, N] in x's type."""
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-    e, n, kk, t, k, code = _expert_args(fmt, ((w_gate, "w_gate"), (w_up, "w_up")), x, ids, 2, "x")
+    e, n, kk, t, k, code = _expert_args(fmt, ((w_gate, "w_gate"), (w_up, "w_up")), x, ids, (2,), "x")
     dev = x.device
 
     def body(s):
         out = _out(h, (t, k, n), x.dtype, dev, "h")
-        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_GLU, fmt, e, n, kk, t, k, code), dev,
-                                "qmatmul_experts_glu")
+        ws, nb, keep = _scratch(_experts_workspace(EXPERTS_GLU, fmt, e, n, kk, t, k, code), dev)
         _check(lib().qmatmul_experts_glu(fmt, e, n, kk, t, k, code, ACTS[act], w_gate.data_ptr(), w_up.data_ptr(),
                                          x.data_ptr(), ids.data_ptr(), out.data_ptr(), ws, nb, s), "qmatmul_experts_glu")
         return out
@@ -546,16 +562,15 @@ def experts_combine(fmt: int, w, h, ids, weights, y=None, stream=None):
     """y[t] = sum_s weights[t, s] * (h[t, s] . W[ids[t, s]]^T): the experts'
     last product and the weighted sum over a token's slots.  h: [T, top_k, K],
     weights: float32 [T, top_k].  Returns [T, N] in h's type."""
-    e, n, kk, t, k, code = _expert_args(fmt, ((w, "w"),), h, ids, 3, "h")
+    e, n, kk, t, k, code = _expert_args(fmt, ((w, "w"),), h, ids, (3,), "h")
     dev = h.device
-    _tensor(weights, _torch().float32, 2, "weights", dev)
+    _tensor(weights, _torch().float32, (2,), "weights", dev)
     if tuple(weights.shape) != (t, k):
         raise ValueError(f"weights must have shape {(t, k)}, got {tuple(weights.shape)}")
 
     def body(s):
         out = _out(y, (t, n), h.dtype, dev, "y")
-        ws, nb, keep = _scratch(lib().qmatmul_experts_workspace_bytes(EXPERTS_COMBINE, fmt, e, n, kk, t, k, code), dev,
-                                "qmatmul_experts_combine")
+        ws, nb, keep = _scratch(_experts_workspace(EXPERTS_COMBINE, fmt, e, n, kk, t, k, code), dev)
         _check(lib().qmatmul_experts_combine(fmt, e, n, kk, t, k, code, w.data_ptr(), h.data_ptr(), ids.data_ptr(),
                                              weights.data_ptr(), out.data_ptr(), ws, nb, s), "qmatmul_experts_combine")
         return out
@@ -570,28 +585,28 @@ def w4_matmul(q, scales, x, zeros=None, y=None, stream=None):
     G a multiple of 32; zeros: uint8 [N, K/G]; x: float32, float16 or bfloat16
     [M, K].  Returns [M, N] in x's type."""
     torch = _torch()
-    _tensor(x, None, 2, "x")
+    _tensor(x, None, (2,), "x")
     code = _type_of(x, "x")
     dev = x.device
     m, kk = x.shape
-    _tensor(q, torch.uint8, 2, "q", dev)
+    _tensor(q, torch.uint8, (2,), "q", dev)
     n = q.shape[0]
     if q.shape[1] * 2 != kk:
         raise ValueError(f"q must be [N, {kk // 2}] for K={kk}, got {tuple(q.shape)}")
-    _tensor(scales, None, 2, "scales", dev)
+    _tensor(scales, None, (2,), "scales", dev)
     scode = _type_of(scales, "scales")
     ng = scales.shape[1]
     if scales.shape[0] != n or ng == 0 or kk % ng:
         raise ValueError(f"scales must be [{n}, K / group], got {tuple(scales.shape)} for K={kk}")
     if zeros is not None:
-        _tensor(zeros, torch.uint8, 2, "zeros", dev)
+        _tensor(zeros, torch.uint8, (2,), "zeros", dev)
         if zeros.shape != scales.shape:
             raise ValueError(f"zeros must have the scales' shape {tuple(scales.shape)}, got {tuple(zeros.shape)}")
     g = kk // ng
 
     def body(s):
         out = _out(y, (m, n), x.dtype, dev, "y")
-        ws, nb, keep = _scratch(lib().qmatmul_w4_workspace_bytes(n, kk, m, g, code), dev, "qmatmul_w4_run")
+        ws, nb, keep = _scratch(_w4_workspace(n, kk, m, g, code), dev)
         _check(lib().qmatmul_w4_run(n, kk, m, g, code, scode, q.data_ptr(), scales.data_ptr(),
                                     None if zeros is None else zeros.data_ptr(), x.data_ptr(), out.data_ptr(), ws, nb, s),
                "qmatmul_w4_run")

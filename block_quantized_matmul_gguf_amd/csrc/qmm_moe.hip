@@ -63,18 +63,44 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 MoePlan plan_of(const MoeArgs& a)
 {
     MoePlan p = {};
+    p.mt = 1;
     const int64_t P = a.T * a.top_k;
     const bool dense = a.fmt >= FMT_W4;
     const int64_t unit = a.fmt == FMT_Q4_K || a.fmt == FMT_Q6_K ? 256 : 128, units = (a.K + unit - 1) / unit;
     const int64_t avg = dense ? P : (P + a.E - 1) / a.E;  // pairs of an expert
-    if (a.T <= (dense ? 1 : 2)) p.path = PATH_ONE;
-    else if (avg > 48) p.path = PATH_TILE;
-    else p.path = PATH_ROWS;
-    p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    const bool f32 = a.type == TYPE_F32;
+    // Few pairs: each on its own, weights that two of them share read again (from L2) in the one launch
+    // this takes.  glu Q4_K 64 x 1024 x 2048, 8 slots: 4 tokens 20.3 us against 24.7 us of the rows
+    // kernel, 8 tokens the other way; 4-bit 14336 x 4096: 2 rows as fast, 3 rows slower.
+    if (P <= (dense ? 2 : 32)) p.path = PATH_ONE;
+    // Up to 16 pairs of an expert (64 rows of one matrix) the weights' bytes decide and the rows kernel,
+    // which splits K over waves, has more of them in flight: glu at 128 tokens (16 pairs of an expert)
+    // 75 us against 78 us, at 256 tokens 103 us against 87 us; 4-bit at 64 rows 30 us, at 128 rows 49 us
+    // against 46 us.
+    else if (avg <= (dense ? 64 : 16)) p.path = PATH_ROWS;
+    else p.path = PATH_TILE;
+    if (p.path == PATH_ROWS) {
+        // one more row group costs little, decoding the weights again a lot; four groups of the
+        // 256-value formats or of f32's two parts do not fit in registers
+        p.mt = avg <= 16 ? 1 : avg <= 32 || f32 || unit == 256 ? 2 : 4;
+    } else if (p.path == PATH_TILE) {
+        // A row tile costs about 5 + mt (4-bit, 14336 x 4096: 36, 45 and 72 us at 2, 4 and 8): the
+        // smallest that still leaves one round of workgroups; else by the pairs of an expert, as a
+        // tile half empty costs as much as a full one (glu Q4_K at 256, 1024 and 2048 tokens: 87, 223
+        // and 383 us with 2, 97, 173 and 302 us with 4, 132, 213 and 295 us with 8).
+        const int most = f32 ? 4 : 8;
+        const int64_t bn = a.op == MOE_GLU ? 128 : 256, nb = (a.N + bn - 1) / bn;
+        const int64_t half = dense ? 0 : std::min<int64_t>(a.E, P) / 2;
+        p.mt = 2;
+        while (p.mt < most && ((P + 16 * p.mt - 1) / (16 * p.mt) + half) * nb > 256) p.mt *= 2;
+        if (!dense && p.mt > 2) p.mt = std::min(most, avg <= 32 ? 2 : avg <= 160 ? 4 : 8);
+    }
+    // waves along K: more while each keeps two units and the chip has room for them
     const int64_t items = units * (p.path == PATH_ONE && a.op == MOE_COMBINE ? a.top_k : 1);
+    const int64_t cols = (a.N + 15) / 16, groups = p.path == PATH_ONE ? cols * (a.op == MOE_COMBINE ? a.T : P) : cols * std::min<int64_t>(P, a.E) / 2;
     p.waves = 1;
-    while (p.waves < (p.path == PATH_ONE ? 16 : 8) && p.waves * 2 <= items) p.waves *= 2;
-    p.tm = p.path == PATH_TILE ? tile_rows(a.type) : 16 * p.mt;
+    while (p.waves * 2 <= (p.path == PATH_ONE ? 16 : 8) && p.waves * 4 <= items && (p.waves < 4 || groups * p.waves < 2048)) p.waves *= 2;
+    p.tm = 16 * p.mt;
     p.max_tiles = (int)(dense ? (P + p.tm - 1) / p.tm : P / p.tm + std::min<int64_t>(a.E + 1, P));
     p.sort = !dense && p.path != PATH_ONE;
     size_t off = 0;
@@ -121,7 +147,7 @@ hipError_t launch_moe(const MoeArgs& call, const MoePlan& p, char* ws, hipStream
         a.y = products;
         a.y_type = TYPE_F32;
     }
-    e = p.path == PATH_TILE ? launch_tile(a, s) : launch_rows(a, p.mt, p.waves, s);
+    e = p.path == PATH_TILE ? launch_tile(a, p.mt, s) : launch_rows(a, p.mt, p.waves, s);
     if (e != hipSuccess || call.op != MOE_COMBINE) return e;
     a = call;
     a.y_type = a.type;
@@ -217,9 +243,9 @@ hipError_t launch_rows(const MoeArgs& a, int mt, int waves, hipStream_t s)
     QMM_MOE_DISPATCH(CALL)
 #undef CALL
 }
-hipError_t launch_tile(const MoeArgs& a, hipStream_t s)
+hipError_t launch_tile(const MoeArgs& a, int mt, hipStream_t s)
 {
-#define CALL(F) launch_tile_##F(a, s)
+#define CALL(F) launch_tile_##F(a, mt, s)
     QMM_MOE_DISPATCH(CALL)
 #undef CALL
 }

@@ -59,39 +59,39 @@ struct TileUnit<FMT, true> {
 // One step (128 values) of two weight units against MT groups of 16 activation
 // rows in LDS (see moe_tile; at[j] is the lane's offset for product j): acc[m][t] += the step's sums.
 //
-// The step goes in pieces of two operand reads and four products (four pieces
-// per product index j).  With the products of a piece run the reads of the
-// piece after next, the scaling of the piece before and a part of the decoding
-// for the next j, issued between them: a matrix product occupies its unit for
-// four issue slots, three of which are free for vector work.
+// The step goes in pieces of two operand reads and four products (PL * MT / 2
+// pieces per product index j).  With the products of a piece run the reads of
+// the piece after next, the scaling of the piece before and a part of the
+// decoding for the next j, issued between them: a matrix product occupies its
+// unit for four issue slots, three of which are free for vector work.
 constexpr int VALU_PER_PRODUCT = 6;
 template <int FMT, int PL, int MT>
 QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds, const int (&at)[4], f32x4_t (&acc)[MT][2])
 {
     using U = Unit<FMT>;
-    static_assert(PL * MT == 8, "four pieces of two reads per product index");
-    constexpr int GM = 2 / PL;  // row groups of a piece
+    constexpr int GM = 2 / PL;           // row groups of a piece
+    constexpr int PJ = PL * MT / 2;      // pieces per j
     half8_t a[3][GM][PL];
     auto read = [&](int q) {
 #pragma unroll
         for (int m = 0; m < GM; ++m)
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-                a[q % 3][m][p] = *(const half8_t*)(lds + (p * MT + (q & 3) * GM + m) * 2048 + at[q >> 2]);
+                a[q % 3][m][p] = *(const half8_t*)(lds + (p * MT + q % PJ * GM + m) * 2048 + at[q / PJ]);
     };
-    f32x4_t d[U::CHAIN ? 4 : 2][GM][2];
-    constexpr int DM = U::CHAIN ? 3 : 1;
+    constexpr int DN = U::CHAIN ? PJ : 2;  // accumulators: per piece of a j, or in turn
+    f32x4_t d[DN][GM][2];
     half8_t b[2][2][U::PARTS];
     auto scale = [&](int q) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float s = un[t].scale_of(h, q >> 2);
+            const float s = un[t].scale_of(h, q / PJ);
 #pragma unroll
             for (int m = 0; m < GM; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = (q & 3) * GM + m;
-                    acc[r][t][i] = fmaf(s, d[q & DM][m][t][i], acc[r][t][i]);
+                    const int r = q % PJ * GM + m;
+                    acc[r][t][i] = fmaf(s, d[q % DN][m][t][i], acc[r][t][i]);
                 }
         }
     };
@@ -105,9 +105,9 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
     decode(0, 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-        const int j = q >> 2;
-        if (q < 14) read(q + 2);
+    for (int q = 0; q < 4 * PJ; ++q) {
+        const int j = q / PJ;
+        if (q + 2 < 4 * PJ) read(q + 2);
 #pragma unroll
         for (int m = 0; m < GM; ++m)
 #pragma unroll
@@ -117,10 +117,11 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const bool first = p + k == 0 && (!U::CHAIN || j == 0);
-                        d[q & DM][m][t] = mfma(a[q % 3][m][p], b[j & 1][t][k], first ? f32x4_t{0, 0, 0, 0} : d[q & DM][m][t]);
+                        d[q % DN][m][t] = mfma(a[q % 3][m][p], b[j & 1][t][k], first ? f32x4_t{0, 0, 0, 0} : d[q % DN][m][t]);
                     }
-        if (q > (U::CHAIN ? 12 : 0)) scale(q - 1);
-        if (j < 3 && (q & 1) == 0) decode(j + 1, (q >> 1) & 1);
+        if (q > (U::CHAIN ? 3 * PJ : 0)) scale(q - 1);
+        if (j < 3 && q % PJ == 0) decode(j + 1, 0);
+        if (j < 3 && q % PJ == PJ / 2) decode(j + 1, 1);
 #pragma unroll
         for (int i = 0; i < 4 * U::PARTS; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
@@ -129,7 +130,7 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
         }
         __builtin_amdgcn_sched_barrier(0);
     }
-    scale(15);
+    scale(4 * PJ - 1);
 }
 
 template <int FMT, int PL, int MT, int NW, bool GLU, bool WIDE>
@@ -137,9 +138,8 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 {
     using U = Unit<FMT>;
     constexpr int RING = 3;              // steps in LDS: one in use, two on their way
-    constexpr int GW = PL * MT / NW;     // row groups (of one plane) a wave copies,
-    constexpr int COPIES = GW * 4;       // 16 bytes per lane each, in a step
-    static_assert(PL * MT % NW == 0 && MT / 2 <= NW, "waves share the copies evenly");
+    constexpr int COPIES = PL * MT * 4 / NW;  // a wave's copies of a step, of four rows each
+    static_assert(PL * MT * 4 % NW == 0 && MT / 2 <= NW, "waves share the copies evenly");
     // Activations [RING][part * MT + m][row][16 places of 8 values]: value group j * 4 + g of row r is
     // in place (j * 4 + g) ^ r, so that the lanes of an operand read without bank conflicts and those
     // of a copy read 256 neighbouring bytes.  Then (Q4_K) the sums of two units [2][m][2][16][8].
@@ -193,34 +193,31 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
     if (t.e >= 0) {
         const int units = (int)(a.Kp / 256), steps = 2 * units;
         const int64_t plane = a.x_rows * a.Kp;
-        // a copy takes four rows: lane's row lane >> 4 of them, place lane & 15
-        const _Float16* src[GW][4];
+        // copy c: rows 4 (c % 4) .. + 3 of group c / 4 % MT of plane c / 4 / MT, lane's row lane >> 4
+        // of them and place lane & 15
+        const _Float16* src[COPIES];
         const _Float16* ssrc = nullptr;
 #pragma unroll
-        for (int i = 0; i < GW; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int q = wave * GW + i, row = 4 * k + g;  // plane q / MT, rows of group q % MT
-                const int at = t.start + min(q % MT * 16 + row, t.count - 1);
-                src[i][k] = a.xp + (q / MT) * plane + (int64_t)row_of(a.ids ? a.order[at] : at) * 128 + (r ^ row) * 8;
-            }
+        for (int i = 0; i < COPIES; ++i) {
+            const int c = wave * COPIES + i, row = c % 4 * 4 + g;
+            const int at = t.start + min(c / 4 % MT * 16 + row, t.count - 1);
+            src[i] = a.xp + (c / 4 / MT) * plane + (int64_t)row_of(a.ids ? a.order[at] : at) * 128 + (r ^ row) * 8;
+        }
         // sums: 16 halves per row and unit; waves below MT / 2 copy [m][p][r] of m = 2 wave, 2 wave + 1
         if constexpr (U::MINS) {
             const int sm = (wave * 2 + (lane >> 5)) & (MT - 1);
             const int i = t.start + min(sm * 16 + r, t.count - 1);
             ssrc = a.xsum + (int64_t)row_of(a.ids ? a.order[i] : i) * 16 + ((lane >> 4) & 1) * 8;
         }
-        // The walk along K starts at another unit in every workgroup: all of them at one place of
-        // rows a power of two apart would ask the same L2 channel.
-        const int first = (int)((b * 5 + tile) % units);
+        // The walk along K starts at another unit for other weight rows: all of them at one place of
+        // rows a power of two apart would ask the same L2 channel.  It must not depend on the row
+        // tile: which of an expert's tiles a pair is in can differ from run to run, its sums may not.
+        const int first = (int)((b * 5 + t.e) % units);
         auto place_of = [&](int u) { return u + first < units ? u + first : u + first - units; };
         auto stage = [&](int s, int buf) {  // step s of the walk
             const int64_t su = place_of(s >> 1), at = 2 * su + (s & 1);
 #pragma unroll
-            for (int i = 0; i < GW; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    copy_to_lds(src[i][k] + at * a.x_rows * 128, lds + buf * STEP + (wave * GW + i) * 2048 + k * 512);
+            for (int i = 0; i < COPIES; ++i) copy_to_lds(src[i] + at * a.x_rows * 128, lds + buf * STEP + (wave * COPIES + i) * 512);
             if constexpr (U::MINS) {
                 if ((s & 1) == 0 && wave < MT / 2) copy_to_lds(ssrc + su * a.x_rows * 16, lds + RING * STEP + ((s >> 1) & 1) * SUMS + wave * 512);
             }
@@ -332,10 +329,18 @@ hipError_t launch_tile_t(const MoeArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-#define QMM_MOE_TILE(NAME, FMT)                                                                          \
-    hipError_t launch_tile_##NAME(const MoeArgs& a, hipStream_t s)                                      \
-    {                                                                                                   \
-        return a.type == TYPE_F32 ? launch_tile_t<FMT, 2, 4, 8>(a, s) : launch_tile_t<FMT, 1, 8, 8>(a, s); \
+template <int FMT, int PL>
+hipError_t launch_tile_p(const MoeArgs& a, int mt, hipStream_t s)
+{
+    if constexpr (PL == 1)
+        if (mt == 8) return launch_tile_t<FMT, PL, 8, 8>(a, s);
+    return mt == 2 ? launch_tile_t<FMT, PL, 2, 8>(a, s) : launch_tile_t<FMT, PL, 4, 8>(a, s);
+}
+
+#define QMM_MOE_TILE(NAME, FMT)                                                                    \
+    hipError_t launch_tile_##NAME(const MoeArgs& a, int mt, hipStream_t s)                        \
+    {                                                                                             \
+        return a.type == TYPE_F32 ? launch_tile_p<FMT, 2>(a, mt, s) : launch_tile_p<FMT, 1>(a, mt, s); \
     }
 
 }  // namespace qmm
