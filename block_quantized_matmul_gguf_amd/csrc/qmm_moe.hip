@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/qmatmul.h"
 #include "qmm_moe_unit.h"
@@ -69,10 +70,16 @@ MoePlan plan_of(const MoeArgs& a)
     const int64_t unit = a.fmt == FMT_Q4_K || a.fmt == FMT_Q6_K ? 256 : 128, units = (a.K + unit - 1) / unit;
     const int64_t avg = dense ? P : (P + a.E - 1) / a.E;  // pairs of an expert
     const bool f32 = a.type == TYPE_F32;
-    // Few pairs: each on its own, weights that two of them share read again (from L2) in the one launch
-    // this takes.  glu Q4_K 64 x 1024 x 2048, 8 slots: 4 tokens 20.3 us against 24.7 us of the rows
-    // kernel, 8 tokens the other way; 4-bit 14336 x 4096: 2 rows as fast, 3 rows slower.
-    if (P <= (dense ? 2 : 32)) p.path = PATH_ONE;
+    // Few pairs: each on its own, in the one launch this takes; weights that several share are read
+    // again, from L2.  That pays while the reading costs less than the preparation's launch, measured
+    // as 26 MB (4-bit 4096 x 4096: 4 rows 9.8 us against 11.2 us of the rows kernel, 6 rows 13.5 us
+    // against 11.3 us; glu Q4_K 64 x 1024 x 2048, 8 slots: 5 tokens 23.7 us against 26.1 us, 8 tokens
+    // 34.6 us against 29.4 us), half as much for f32's two parts and twice for a combine, which saves
+    // its summing launch too (8 tokens 29.3 us against 37.8 us).
+    const bool combine = a.op == MOE_COMBINE;
+    const double alike = dense ? 1.0 : a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, (double)P));  // experts among P even choices
+    const double again = ((double)P - alike) * (double)a.N * (double)a.row_bytes * (a.op == MOE_GLU ? 2 : 1) * (f32 ? 2 : 1);
+    if (P <= (combine ? 64 : 48) && again <= (combine ? 52e6 : 26e6)) p.path = PATH_ONE;
     // Up to 16 pairs of an expert (64 rows of one matrix) the weights' bytes decide and the rows kernel,
     // which splits K over waves, has more of them in flight: glu at 128 tokens (16 pairs of an expert)
     // 75 us against 78 us, at 256 tokens 103 us against 87 us; 4-bit at 64 rows 30 us, at 128 rows 49 us

@@ -6,9 +6,11 @@
 //
 // Scores are formed in 64 bits: a selection compares sums (score + bias, a
 // group's two best) that can lie next to each other, and 64 bits keep the
-// order the definition gives; at this size they cost nothing that shows (a
-// row is a few hundred values; the call is bound by its launch for few rows
-// and by the top_k argmax rounds, each one pass of lane exchanges, for many).
+// order the definition gives.  A call with few rows is bound by its launch; one
+// with many by instructions, of which the top_k rounds have most.  So a lane
+// sorts its keys once, a round compares the lanes' best only, in two 32-bit
+// halves (a maximum across lanes is one instruction per exchange then), and
+// the winner moves on to its next.
 #include <hip/hip_runtime.h>
 
 #include "../../include/qmatmul.h"
@@ -29,7 +31,7 @@ struct RouteArgs {
     int64_t T;
     int E, k, groups, top_groups, group_top, group_size;
     int type, sigmoid, renorm;
-    float scale;
+    float scale, group_inv;  // 1 / group_size
 };
 
 // Order of doubles as order of unsigned integers; -inf and NaN are mapped to
@@ -54,13 +56,22 @@ QMM_DEV uint64_t readlane_u64(uint64_t v, int l)
     return ((uint64_t)hi << 32) | lo;
 }
 QMM_DEV uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-QMM_DEV uint64_t wave_max_u64(uint64_t v)
+// max(v, v of another lane) as one instruction: the exchanges used reach every
+// lane, so nothing of the old value is kept.
+template <int CTRL>
+QMM_DEV uint32_t max_dpp(uint32_t v)
 {
-    v = max_u64(v, dpp_u64<DPP_X1>(v));
-    v = max_u64(v, dpp_u64<DPP_X2>(v));
-    v = max_u64(v, dpp_u64<DPP_HMIRROR>(v));
-    v = max_u64(v, dpp_u64<DPP_MIRROR>(v));
-    return max_u64(max_u64(readlane_u64(v, 0), readlane_u64(v, 16)), max_u64(readlane_u64(v, 32), readlane_u64(v, 48)));
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true));
+}
+QMM_DEV uint32_t wave_max_u32(uint32_t v)
+{
+    v = max_dpp<DPP_X1>(v);
+    v = max_dpp<DPP_X2>(v);
+    v = max_dpp<DPP_HMIRROR>(v);
+    v = max_dpp<DPP_MIRROR>(v);
+    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0), b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32), d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+    return max(max(a, b), max(c, d));
 }
 template <int CTRL>
 QMM_DEV double dpp_f64(double v)
@@ -96,6 +107,7 @@ template <int J, bool GROUPS>
 __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteArgs a)
 {
     __shared__ uint64_t keys_s[GROUPS ? WAVES : 1][GROUPS ? 64 * J : 1];
+    __shared__ double score_s[WAVES][64 * J];
     __shared__ double gscore_s[GROUPS ? WAVES : 1][GROUPS ? MAX_GROUPS : 1];
     const int lane = (int)__lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -126,8 +138,9 @@ __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteArgs a)
             sum += s[j];
         }
         sum = wave_sum_f64(sum);
+        const double factor = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
-        for (int j = 0; j < J; ++j) s[j] = sum > 0.0 ? s[j] / sum : 0.0;
+        for (int j = 0; j < J; ++j) s[j] *= factor;
     }
     uint64_t key[J];
 #pragma unroll
@@ -175,38 +188,55 @@ __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteArgs a)
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int e = lane * J + j;
-            if (e < a.E && !((stay >> (e / a.group_size)) & 1)) key[j] = 0;
+            // e / group_size: (e + 1/2) times a reciprocal good to 2^-22, e below 2^10
+            const int of = (int)(((float)e + 0.5f) * a.group_inv);
+            if (e < a.E && !((stay >> of) & 1)) key[j] = 0;
         }
     }
 
-    // top_k rounds: the largest key, its lowest lane, that lane's lowest register
-    int my_id = -1;
-    double my_s = 0.0;
-    for (int r = 0; r < a.k; ++r) {
-        uint64_t best = 0;
+    // a lane's keys in descending order, equal ones (only neighbours change places) by index
+    uint32_t hi[J], lo[J];
+    int at[J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) best = max_u64(best, key[j]);
-        const uint64_t m = wave_max_u64(best);
-        if (m == 0) break;  // none left
-        const int owner = (int)__builtin_ctzll(__ballot(best == m));
-        int e = 0;
-        double sv = 0.0;
-        bool open = true;
+    for (int j = 0; j < J; ++j) {
+        score_s[wave][lane * J + j] = s[j];
+        hi[j] = (uint32_t)(key[j] >> 32);
+        lo[j] = (uint32_t)key[j];
+        at[j] = lane * J + j;
+    }
+#pragma unroll
+    for (int n = 0; n < J; ++n)
+#pragma unroll
+        for (int j = n & 1; j + 1 < J; j += 2) {
+            const bool up = (((uint64_t)hi[j + 1] << 32) | lo[j + 1]) > (((uint64_t)hi[j] << 32) | lo[j]);
+            const uint32_t h0 = hi[j], l0 = lo[j];
+            const int a0 = at[j];
+            hi[j] = up ? hi[j + 1] : h0;
+            lo[j] = up ? lo[j + 1] : l0;
+            at[j] = up ? at[j + 1] : a0;
+            hi[j + 1] = up ? h0 : hi[j + 1];
+            lo[j + 1] = up ? l0 : lo[j + 1];
+            at[j + 1] = up ? a0 : at[j + 1];
+        }
+    // top_k rounds: the largest of the lanes' first keys, its lowest lane
+    int my_id = -1;
+    for (int r = 0; r < a.k; ++r) {
+        const uint32_t mh = wave_max_u32(hi[0]);
+        const uint32_t ml = wave_max_u32(hi[0] == mh ? lo[0] : 0);
+        if ((mh | ml) == 0) break;  // none left
+        const int owner = (int)__builtin_ctzll(__ballot(hi[0] == mh && lo[0] == ml));
+        const int id = __builtin_amdgcn_readlane(at[0], owner);
+        my_id = lane == r ? id : my_id;
+        const bool mine = lane == owner;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const bool hit = open && key[j] == m;
-            e = hit ? j : e;
-            sv = hit ? s[j] : sv;
-            key[j] = hit && lane == owner ? 0 : key[j];
-            open = open && !hit;
-        }
-        const int id = owner * J + __builtin_amdgcn_readlane(e, owner);
-        const double sw = readlane_f64(sv, owner);
-        if (lane == r) {
-            my_id = id;
-            my_s = sw;
+            hi[j] = mine ? (j + 1 < J ? hi[(j + 1) % J] : 0) : hi[j];
+            lo[j] = mine ? (j + 1 < J ? lo[(j + 1) % J] : 0) : lo[j];
+            at[j] = mine && j + 1 < J ? at[(j + 1) % J] : at[j];
         }
     }
+    wave_sync();
+    double my_s = my_id >= 0 ? score_s[wave][my_id] : 0.0;
     if (a.renorm) {
         const double sum = wave_sum_f64(my_s);
         my_s = sum > 0.0 ? my_s / sum : 0.0;
@@ -261,6 +291,7 @@ extern "C" int qmatmul_route_experts(const void* logits, int type, int64_t T, in
     a.top_groups = top_groups;
     a.group_top = group_top;
     a.group_size = (int)(E / groups);
+    a.group_inv = 1.0f / (float)a.group_size;
     a.type = type;
     a.sigmoid = score == QMM_SCORE_SIGMOID;
     a.renorm = renormalize != 0;

@@ -477,6 +477,28 @@ def test_a_layer_on_streams_and_in_graphs(t):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("fmt", ["Q8_0", "Q4_K"])
+@pytest.mark.parametrize("t", [3, 40, 420, 2100])
+def test_values_depend_on_their_own_row_alone(fmt, dtype, t):
+    """Runs again, and with the tokens in another order, give the same bits: the order in which the sort's
+    atomics place an expert's pairs, and with it their tile, does not show."""
+    f, e, n, k, kk = FMTS[fmt], 5, 70, 3, 1024
+    b, _, _ = weights_of(f, 140, e * n, kk)
+    wd = torch.from_numpy(b.reshape(e, n, -1)).cuda()
+    x, _ = acts(141, (t, kk), TYPES[dtype])
+    ids = torch.from_numpy(choose(142, t, e, k, "twice")).cuda()
+    g = torch.rand((t, k)).cuda()
+    h = qmm.experts_glu(f, wd, wd, x, ids)
+    y = qmm.experts_combine(f, wd, acts(143, (t, k, kk), TYPES[dtype])[0], ids, g)
+    perm = torch.from_numpy(np.random.default_rng(144).permutation(t)).cuda()
+    for _ in range(3):
+        assert torch.equal(qmm.experts_glu(f, wd, wd, x, ids), h)
+        assert torch.equal(qmm.experts_glu(f, wd, wd, x[perm].contiguous(), ids[perm].contiguous()), h[perm])
+        hh = acts(143, (t, k, kk), TYPES[dtype])[0][perm].contiguous()
+        assert torch.equal(qmm.experts_combine(f, wd, hh, ids[perm].contiguous(), g[perm].contiguous()), y[perm])
+
+
 def test_given_outputs_and_refusals():
     f, e, n, k, t = qmm.Q4_0, 4, 24, 64, 3
     b, w, wa = weights_of(f, 130, e * n, k)
