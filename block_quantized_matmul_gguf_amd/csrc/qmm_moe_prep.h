@@ -20,9 +20,14 @@
 namespace qmm {
 
 constexpr int MOE_MAX_E = 1024, PREP_THREADS = 1024, PREP_WAVES = PREP_THREADS / 64;
+constexpr int SORT_KEEP = 16;  // pairs per thread whose place in their bucket stays in registers
 
+constexpr int SORT_COPIES = 4;  // counters per bucket, by lane: fewer lanes of a wave meet at one
+
+template <bool SCATTER>
 struct SortSpace {
-    int cnt[MOE_MAX_E + 1], off[MOE_MAX_E + 1], tile0[MOE_MAX_E + 2];
+    int cnt[(MOE_MAX_E + 1) * SORT_COPIES], off[SCATTER ? (MOE_MAX_E + 1) * SORT_COPIES : 1], tile0[MOE_MAX_E + 2];
+    uint16_t order[SCATTER ? SORT_KEEP * PREP_THREADS : 1];
 };
 
 QMM_DEV int bucket_of(const MoeArgs& a, int p)
@@ -32,34 +37,44 @@ QMM_DEV int bucket_of(const MoeArgs& a, int p)
 }
 
 template <bool SCATTER>
-QMM_DEV void sort_pairs(const MoeArgs& a, int tm, SortSpace& s)
+QMM_DEV void sort_pairs(const MoeArgs& a, int tm, SortSpace<SCATTER>& s)
 {
-    constexpr int KEEP = 16;  // pairs per thread whose place in their bucket stays in registers
-    const int tid = (int)threadIdx.x, E = a.E, B = E + 1, P = (int)(a.T * a.top_k);
-    for (int b = tid; b < B; b += PREP_THREADS) s.cnt[b] = 0;
-    __syncthreads();
-    int bucket[KEEP], rank[KEEP];
+    constexpr int KEEP = SORT_KEEP, C = SORT_COPIES;
+    const int tid = (int)threadIdx.x, mine = tid % C, E = a.E, B = E + 1, P = (int)(a.T * a.top_k);
+    for (int b = tid; b < B * C; b += PREP_THREADS) s.cnt[b] = 0;
+    int bucket[KEEP], rank[KEEP];  // bucket * C + copy
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) {
         const int p = i * PREP_THREADS + tid;
-        bucket[i] = p < P ? bucket_of(a, p) : -1;
+        bucket[i] = p < P ? bucket_of(a, p) * C + mine : -1;
     }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
         if (bucket[i] >= 0) rank[i] = atomicAdd(&s.cnt[bucket[i]], 1);
     __syncthreads();
-    // the kept pairs come first in their buckets
-    if (SCATTER)
-        for (int b = tid; b < B; b += PREP_THREADS) s.off[b] = s.cnt[b];
-    __syncthreads();
-    for (int p = KEEP * PREP_THREADS + tid; p < P; p += PREP_THREADS) atomicAdd(&s.cnt[bucket_of(a, p)], 1);
-    __syncthreads();
+    if (P > KEEP * PREP_THREADS) {
+        // the kept pairs come first among their counter's
+        if constexpr (SCATTER) {
+            for (int b = tid; b < B * C; b += PREP_THREADS) s.off[b] = s.cnt[b];
+            __syncthreads();
+        }
+        for (int p = KEEP * PREP_THREADS + tid; p < P; p += PREP_THREADS) atomicAdd(&s.cnt[bucket_of(a, p) * C + mine], 1);
+        __syncthreads();
+    }
     if (tid < 64) {
         const int per = (B + 63) / 64, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+        auto size = [&](int b) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) n += s.cnt[b * C + i];
+            return n;
+        };
         int c = 0, t = 0;
         for (int b = b0; b < b1; ++b) {
-            c += s.cnt[b];
-            t += (s.cnt[b] + tm - 1) / tm;
+            const int n = size(b);
+            c += n;
+            t += (n + tm - 1) / tm;
         }
         int ci = c, ti = t;
         for (int d = 1; d < 64; d *= 2) {
@@ -72,11 +87,14 @@ QMM_DEV void sort_pairs(const MoeArgs& a, int tm, SortSpace& s)
         c = ci - c;
         t = ti - t;
         for (int b = b0; b < b1; ++b) {
-            const int n = s.cnt[b];
             s.tile0[b] = t;
-            t += (n + tm - 1) / tm;
-            s.cnt[b] = c;  // from here on: the bucket's first place
-            c += n;
+            t += (size(b) + tm - 1) / tm;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int n = s.cnt[b * C + i];
+                s.cnt[b * C + i] = c;  // from here on: the counter's first place
+                c += n;
+            }
         }
         if (tid == 63) s.tile0[B] = ti;
     }
@@ -90,20 +108,30 @@ QMM_DEV void sort_pairs(const MoeArgs& a, int tm, SortSpace& s)
                 if (s.tile0[mid] <= i) lo = mid;
                 else hi = mid;
             }
-            const int k = (i - s.tile0[lo]) * tm, n = (lo + 1 < B ? s.cnt[lo + 1] : P) - s.cnt[lo];
+            const int at = s.cnt[lo * C], k = (i - s.tile0[lo]) * tm, n = (lo + 1 < B ? s.cnt[(lo + 1) * C] : P) - at;
             t.e = lo < E ? lo : -1;
-            t.start = s.cnt[lo] + k;
+            t.start = at + k;
             t.count = min(tm, n - k);
         }
         a.tiles[i] = t;
     }
     if constexpr (SCATTER) {
+        if (P <= KEEP * PREP_THREADS) {
+            // through LDS, so that the stores are of neighbours: scattered ones go a lane at a time
+            // through one compute unit's address unit
 #pragma unroll
-        for (int i = 0; i < KEEP; ++i)
-            if (bucket[i] >= 0) a.order[s.cnt[bucket[i]] + rank[i]] = i * PREP_THREADS + tid;
-        for (int p = KEEP * PREP_THREADS + tid; p < P; p += PREP_THREADS) {
-            const int b = bucket_of(a, p);
-            a.order[s.cnt[b] + atomicAdd(&s.off[b], 1)] = p;
+            for (int i = 0; i < KEEP; ++i)
+                if (bucket[i] >= 0) s.order[s.cnt[bucket[i]] + rank[i]] = (uint16_t)(i * PREP_THREADS + tid);
+            __syncthreads();
+            for (int p = tid; p < P; p += PREP_THREADS) a.order[p] = s.order[p];
+        } else {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+                if (bucket[i] >= 0) a.order[s.cnt[bucket[i]] + rank[i]] = i * PREP_THREADS + tid;
+            for (int p = KEEP * PREP_THREADS + tid; p < P; p += PREP_THREADS) {
+                const int b = bucket_of(a, p) * C + mine;
+                a.order[s.cnt[b] + atomicAdd(&s.off[b], 1)] = p;
+            }
         }
     }
 }
@@ -114,7 +142,7 @@ __global__ __launch_bounds__(PREP_THREADS) void moe_prep(MoeArgs a, int tm, int 
 {
     using U = Unit<FMT>;
     __shared__ union {
-        SortSpace sort;
+        SortSpace<!ROWS> sort;
         struct {
             float am[PREP_WAVES];
             int place[PREP_WAVES];
@@ -133,16 +161,44 @@ __global__ __launch_bounds__(PREP_THREADS) void moe_prep(MoeArgs a, int tm, int 
     const bool live = row < a.x_rows;
     // rows kernel with experts: row is a pair
     const int64_t src = ROWS && a.ids && !a.per_slot ? row / a.top_k : row;
+    // piece q [unit][step][j][g] of the row: where its two runs of four values are
+    constexpr int PIECES = U::UNIT / 8, KEEP = 4;
+    const int64_t pieces = a.Kp / 8;
+    auto run = [&](int64_t q, int second) {
+        const int i = (int)(q % PIECES), h = i >> 4, j = (i >> 2) & 3, g = i & 3;
+        return q / PIECES * U::UNIT + (second ? U::o1(h, j, g) : U::o0(h, j, g));
+    };
+    auto load = [&](int64_t q, Raw4<PL> (&w)[2]) {
+        w[0].clear();
+        w[1].clear();
+        if (q < pieces && run(q, 0) < a.K) {  // K is a multiple of 32: both runs lie inside or outside
+            w[0].load(a.x, src * a.K + run(q, 0));
+            w[1].load(a.x, src * a.K + run(q, 1));
+        }
+    };
+    // a row that fits is loaded once
+    const bool keep = pieces <= (int64_t)KEEP * wr * 64;
+    Raw4<PL> kept[KEEP][2];
     float am = 0.0f;
     int place = 0;
     if (live) {
-        for (int64_t k = (sub * 64 + lane) * 4; k < a.K; k += wr * 256) {
-            float v[4];
-            Raw4<PL> w;
-            w.load(a.x, src * a.K + k);
-            w.values(a.type, v);
+        auto largest = [&](const Raw4<PL> (&w)[2]) {
+            float v[8];
+            w[0].values(a.type, v);
+            w[1].values(a.type, v + 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) am = fmaxf(am, fabsf(v[i]));
+            for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(v[i]));
+        };
+        if (keep) {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i) load((i * wr + sub) * 64 + lane, kept[i]);
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i) largest(kept[i]);
+        } else {
+            for (int64_t q = sub * 64 + lane; q < pieces; q += wr * 64) {
+                load(q, kept[0]);
+                largest(kept[0]);
+            }
         }
         if (ROWS && a.ids) {
             const int mine = bucket_of(a, (int)row), P = (int)a.x_rows;
@@ -175,31 +231,20 @@ __global__ __launch_bounds__(PREP_THREADS) void moe_prep(MoeArgs a, int tm, int 
         if (ROWS && a.ids) a.order[dst] = (int)row;
     }
     const int64_t plane = a.x_rows * a.Kp;
-    for (int64_t q = sub * 64 + lane; q < a.Kp / 8; q += wr * 64) {  // piece [unit][step][j][g]
-        constexpr int PIECES = U::UNIT / 8;
-        const int64_t u = q / PIECES;
+    auto store = [&](int64_t q, const Raw4<PL> (&w)[2]) {
         const int i = (int)(q % PIECES), h = i >> 4, j = (i >> 2) & 3, g = i & 3;
-        float v[8];
+        float e[8], v[8];
         half8_t p[PL];
-        float sum = 0.0f;
-        if (u * U::UNIT + U::o0(h, j, g) < a.K) {
-            float e[8];
-            Raw4<PL> w0, w1;
-            w0.load(a.x, src * a.K + u * U::UNIT + U::o0(h, j, g));
-            w1.load(a.x, src * a.K + u * U::UNIT + U::o1(h, j, g));
-            w0.values(a.type, e);
-            w1.values(a.type, e + 4);
+        w[0].values(a.type, e);
+        w[1].values(a.type, e + 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = e[U::slot(k)] * s;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-        }
+        for (int k = 0; k < 8; ++k) v[k] = e[U::slot(k)] * s;
         split8<PL>(v, p);
         const int64_t at = ROWS ? (q * a.x_rows + dst) * 8 : ((q >> 4) * a.x_rows + dst) * 128 + (q & 15) * 8;
 #pragma unroll
         for (int k = 0; k < PL; ++k) *(half8_t*)(a.xp + k * plane + at) = p[k];
         if constexpr (U::MINS) {
+            float sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum += v[k];
             sum += __shfl_xor(sum, 4);
@@ -207,11 +252,25 @@ __global__ __launch_bounds__(PREP_THREADS) void moe_prep(MoeArgs a, int tm, int 
             sum *= 0.03125f;
             if (j == 0) {
                 // rows kernel: [unit][g][row][4], tile kernel: [unit][row][g][4]
+                const int64_t u = q / PIECES;
                 _Float16* o = a.xsum + (ROWS ? (u * 4 + g) * a.x_rows + dst : (u * a.x_rows + dst) * 4 + g) * 4 + h;
                 const _Float16 hi = (_Float16)sum;
                 o[0] = hi;
                 o[2] = (_Float16)(sum - (float)hi);
             }
+        }
+    };
+    // (pieces come 16 to a step: the lanes that add a sub-block's sums are all here or all gone)
+    if (keep) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            const int64_t q = (i * wr + sub) * 64 + lane;
+            if (q < pieces) store(q, kept[i]);
+        }
+    } else {
+        for (int64_t q = sub * 64 + lane; q < pieces; q += wr * 64) {
+            load(q, kept[0]);
+            store(q, kept[0]);
         }
     }
 }
@@ -221,7 +280,7 @@ hipError_t launch_prep_t(const MoeArgs& a, bool rows, int tm, hipStream_t s)
 {
     // enough waves to fill the chip, each with some work
     int wr = 1;
-    while (wr < 16 && a.x_rows * wr < 4096 && a.K > wr * 1024) wr *= 4;
+    while (wr < 16 && (a.K > wr * 2048 || (a.x_rows * wr < 4096 && a.K > wr * 1024))) wr *= 4;
     const int64_t per = PREP_WAVES / wr;
     const dim3 grid((unsigned)((a.x_rows + per - 1) / per + (a.ids ? 1 : 0))), block(PREP_THREADS);
     if (rows) moe_prep<FMT, PL, true><<<grid, block, 0, s>>>(a, tm, wr);

@@ -547,3 +547,17 @@ def test_given_outputs_and_refusals():
         qmm.route_experts(torch.zeros((2, 8)).cuda(), 2, score="relu")
     with pytest.raises(ValueError):
         qmm.route_experts(torch.zeros((2, 8)).cuda(), 2, bias=torch.zeros(9).cuda())
+
+
+def test_more_pairs_than_the_sort_keeps_in_registers():
+    """17000 pairs (16384 stay in registers), then 20 times that, some without an expert."""
+    f, e, n, k, kk = qmm.Q8_0, 7, 33, 4, 64
+    b, w, wa = weights_of(f, 150, e * n, kk)
+    wd = torch.from_numpy(b.reshape(e, n, -1)).cuda()
+    for t in (4096, 4250, 85000):
+        ids_h = choose(151 + t, t, e, k, "twice")
+        x, xh = acts(152 + t, (t, kk), torch.bfloat16)
+        y = qmm.experts_matmul(f, wd, x, torch.from_numpy(ids_h).cuda())
+        step = max(1, t // 3000)
+        ref, a = product_ref(w, wa, e, n, ids_h[::step], per_slot(xh[::step], k))
+        close(y[::step], ref, BAR * a, f"{t} tokens")
