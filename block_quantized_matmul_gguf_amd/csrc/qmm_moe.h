@@ -60,15 +60,15 @@ hipError_t launch_one(const MoeArgs& a, int waves, hipStream_t s);
 hipError_t launch_prep(const MoeArgs& a, bool rows, int tm, hipStream_t s);
 // mt * 16 (mt 1, 2 or 4) pairs of an expert per workgroup, the waves along K.
 hipError_t launch_rows(const MoeArgs& a, int mt, int waves, hipStream_t s);
-// mt * 16 (mt 2, 4 or, but for f32, 8) pairs of an expert against 256 weight
-// rows (GLU: 128 of each matrix) per workgroup.
-hipError_t launch_tile(const MoeArgs& a, int mt, hipStream_t s);
+// tm (32, 64 or, but for f32, 128) pairs of an expert against 256 weight rows
+// (GLU: 128 of each matrix) per workgroup.
+hipError_t launch_tile(const MoeArgs& a, int tm, hipStream_t s);
 
 #define QMM_MOE_DECLARE(F)                                                            \
     hipError_t launch_one_##F(const MoeArgs& a, int waves, hipStream_t s);            \
     hipError_t launch_prep_##F(const MoeArgs& a, bool rows, int tm, hipStream_t s);   \
     hipError_t launch_rows_##F(const MoeArgs& a, int mt, int waves, hipStream_t s);   \
-    hipError_t launch_tile_##F(const MoeArgs& a, int mt, hipStream_t s);
+    hipError_t launch_tile_##F(const MoeArgs& a, int tm, hipStream_t s);
 QMM_MOE_DECLARE(q8_0)
 QMM_MOE_DECLARE(q4_0)
 QMM_MOE_DECLARE(q5_0)

@@ -91,16 +91,16 @@ MoePlan plan_of(const MoeArgs& a)
         // 256-value formats or of f32's two parts do not fit in registers
         p.mt = avg <= 16 ? 1 : avg <= 32 || f32 || unit == 256 ? 2 : 4;
     } else if (p.path == PATH_TILE) {
-        // A row tile costs about 5 + mt (4-bit, 14336 x 4096: 36, 45 and 72 us at 2, 4 and 8): the
-        // smallest that still leaves one round of workgroups; else by the pairs of an expert, as a
-        // tile half empty costs as much as a full one (glu Q4_K at 256, 1024 and 2048 tokens: 87, 223
-        // and 383 us with 2, 97, 173 and 302 us with 4, 132, 213 and 295 us with 8).
+        // A row tile of 16 mt rows costs about 5 + mt (4-bit, 14336 x 4096, one round of workgroups: 45,
+        // 54 and 73 us at 2, 4 and 8): the smallest that still leaves one round, else the largest, an
+        // expert's last rows having smaller bodies (glu Q4_K, 64 experts, 8 slots, with tiles of 32, 64
+        // and 128 rows: 256 tokens 90, 87 and 89 us, 1024 tokens 231, 177 and 169 us; Q5_0, 8 experts,
+        // 614 pairs: 40, 48 and 48 us).
         const int most = f32 ? 4 : 8;
         const int64_t bn = a.op == MOE_GLU ? 128 : 256, nb = (a.N + bn - 1) / bn;
         const int64_t half = dense ? 0 : std::min<int64_t>(a.E, P) / 2;
         p.mt = 2;
         while (p.mt < most && ((P + 16 * p.mt - 1) / (16 * p.mt) + half) * nb > 256) p.mt *= 2;
-        if (!dense && p.mt > 2) p.mt = std::min(most, avg <= 32 ? 2 : avg <= 160 ? 4 : 8);
     }
     // waves along K: more while each keeps two units and the chip has room for them
     const int64_t items = units * (p.path == PATH_ONE && a.op == MOE_COMBINE ? a.top_k : 1);
@@ -154,7 +154,7 @@ hipError_t launch_moe(const MoeArgs& call, const MoePlan& p, char* ws, hipStream
         a.y = products;
         a.y_type = TYPE_F32;
     }
-    e = p.path == PATH_TILE ? launch_tile(a, p.mt, s) : launch_rows(a, p.mt, p.waves, s);
+    e = p.path == PATH_TILE ? launch_tile(a, p.tm, s) : launch_rows(a, p.mt, p.waves, s);
     if (e != hipSuccess || call.op != MOE_COMBINE) return e;
     a = call;
     a.y_type = a.type;
@@ -250,9 +250,9 @@ hipError_t launch_rows(const MoeArgs& a, int mt, int waves, hipStream_t s)
     QMM_MOE_DISPATCH(CALL)
 #undef CALL
 }
-hipError_t launch_tile(const MoeArgs& a, int mt, hipStream_t s)
+hipError_t launch_tile(const MoeArgs& a, int tm, hipStream_t s)
 {
-#define CALL(F) launch_tile_##F(a, mt, s)
+#define CALL(F) launch_tile_##F(a, tm, s)
     QMM_MOE_DISPATCH(CALL)
 #undef CALL
 }

@@ -2,8 +2,9 @@
 // one launch: the activations in operand order and the pairs sorted by expert.
 //
 // Block 0 (where there are experts) sorts: a histogram, its prefix sums and a
-// scatter in LDS give tiles[], the runs of up to tm pairs of one expert, those
-// without an expert last.  The other blocks bring rows into operand order, each
+// scatter in LDS give tiles[], the runs of up to tm pairs of one expert: the
+// full ones first, then the ends of runs, those of more than half a tile before
+// the others, so that the longest work starts first.  The other blocks bring rows into operand order, each
 // scaled by a power of two so that its f16 parts (f32: hi + lo) hold it.
 //
 // Tile kernel: rows as the caller has them, [step][row][128]; order[] (the
@@ -27,6 +28,7 @@ constexpr int SORT_COPIES = 4;  // counters per bucket, by lane: fewer lanes of 
 template <bool SCATTER>
 struct SortSpace {
     int cnt[(MOE_MAX_E + 1) * SORT_COPIES], off[SCATTER ? (MOE_MAX_E + 1) * SORT_COPIES : 1], tile0[MOE_MAX_E + 2];
+    uint32_t last[MOE_MAX_E + 1], lasts;
     uint16_t order[SCATTER ? SORT_KEEP * PREP_THREADS : 1];
 };
 
@@ -70,25 +72,36 @@ QMM_DEV void sort_pairs(const MoeArgs& a, int tm, SortSpace<SCATTER>& s)
             for (int i = 0; i < C; ++i) n += s.cnt[b * C + i];
             return n;
         };
+        // a bucket's last tile, if not full, is one of the larger (1) or of the smaller ones (1 << 16)
+        auto last = [&](int n) { return n % tm == 0 ? 0u : n % tm * 2 > tm ? 1u : 1u << 16; };
         int c = 0, t = 0;
+        uint32_t l = 0;
         for (int b = b0; b < b1; ++b) {
             const int n = size(b);
             c += n;
-            t += (n + tm - 1) / tm;
+            t += n / tm;
+            l += last(n);
         }
         int ci = c, ti = t;
+        uint32_t li = l;
         for (int d = 1; d < 64; d *= 2) {
             const int cu = __shfl_up(ci, d), tu = __shfl_up(ti, d);
+            const uint32_t lu = __shfl_up(li, d);
             if (tid >= d) {
                 ci += cu;
                 ti += tu;
+                li += lu;
             }
         }
         c = ci - c;
         t = ti - t;
+        l = li - l;
         for (int b = b0; b < b1; ++b) {
+            const int n = size(b);
             s.tile0[b] = t;
-            t += (size(b) + tm - 1) / tm;
+            s.last[b] = l;
+            t += n / tm;
+            l += last(n);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const int n = s.cnt[b * C + i];
@@ -96,22 +109,32 @@ QMM_DEV void sort_pairs(const MoeArgs& a, int tm, SortSpace<SCATTER>& s)
                 c += n;
             }
         }
-        if (tid == 63) s.tile0[B] = ti;
+        if (tid == 63) {
+            s.tile0[B] = ti;
+            s.lasts = li;
+        }
     }
     __syncthreads();
+    const int full = s.tile0[B], larger = (int)(s.lasts & 0xffff), smaller = (int)(s.lasts >> 16);
+    for (int b = tid; b < B; b += PREP_THREADS) {
+        const int at = s.cnt[b * C], n = (b + 1 < B ? s.cnt[(b + 1) * C] : P) - at, k = n % tm;
+        if (k == 0) continue;
+        const int i = full + (k * 2 > tm ? (int)(s.last[b] & 0xffff) : larger + (int)(s.last[b] >> 16));
+        a.tiles[i] = {b < E ? b : -1, at + n - k, k, 0};
+    }
     for (int i = tid; i < a.max_tiles; i += PREP_THREADS) {
+        if (i >= full && i < full + larger + smaller) continue;
         MoeTile t = {-1, 0, 0, 0};
-        if (i < s.tile0[B]) {
+        if (i < full) {
             int lo = 0, hi = B;  // the last bucket whose first tile is <= i
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
                 if (s.tile0[mid] <= i) lo = mid;
                 else hi = mid;
             }
-            const int at = s.cnt[lo * C], k = (i - s.tile0[lo]) * tm, n = (lo + 1 < B ? s.cnt[(lo + 1) * C] : P) - at;
             t.e = lo < E ? lo : -1;
-            t.start = at + k;
-            t.count = min(tm, n - k);
+            t.start = s.cnt[lo * C] + (i - s.tile0[lo]) * tm;
+            t.count = tm;
         }
         a.tiles[i] = t;
     }

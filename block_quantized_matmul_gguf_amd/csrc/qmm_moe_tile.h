@@ -133,53 +133,37 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
     scale(4 * PJ - 1);
 }
 
-template <int FMT, int PL, int MT, int NW, bool GLU, bool WIDE>
-__global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
+// Dwords of LDS of a tile kernel: activations [RING][part * MT + m][row][16
+// places of 8 values]: value group j * 4 + g of row r is in place (j * 4 + g) ^
+// r, so that the lanes of an operand read without bank conflicts and those of a
+// copy read 256 neighbouring bytes.  Then (Q4_K) the sums of two units
+// [2][m][2][16][8], then the waves' exchange areas.  (One array: beside another
+// one, reads of this would be made to wait for every copy in flight.)  The
+// outputs go through it too, once the products are done.
+constexpr int TILE_WAVES = 8, TILE_RING = 3;  // steps in LDS: one in use, two on their way
+template <int FMT, int PL, int MT>
+struct TileSpace {
+    static constexpr int STEP = PL * MT * 4 * 512, SUMS = Unit<FMT>::MINS ? MT * 256 : 0;  // halves
+    static constexpr int AREAS = TILE_RING * STEP + 2 * SUMS, HALVES = AREAS + TILE_WAVES * Unit<FMT>::AREA * 2;
+};
+
+// A row tile of at most MT * 16 rows against the workgroup's weight rows.
+template <int FMT, int PL, int MT, bool GLU, bool WIDE>
+QMM_DEV void tile_body(const MoeArgs& a, const MoeTile& t, int64_t b, _Float16* lds)
 {
     using U = Unit<FMT>;
-    constexpr int RING = 3;              // steps in LDS: one in use, two on their way
+    using S = TileSpace<FMT, PL, MT>;
+    constexpr int NW = TILE_WAVES, RING = TILE_RING, STEP = S::STEP, SUMS = S::SUMS;
     constexpr int COPIES = PL * MT * 4 / NW;  // a wave's copies of a step, of four rows each
     static_assert(PL * MT * 4 % NW == 0 && MT / 2 <= NW, "waves share the copies evenly");
-    // Activations [RING][part * MT + m][row][16 places of 8 values]: value group j * 4 + g of row r is
-    // in place (j * 4 + g) ^ r, so that the lanes of an operand read without bank conflicts and those
-    // of a copy read 256 neighbouring bytes.  Then (Q4_K) the sums of two units [2][m][2][16][8].
-    constexpr int STEP = PL * MT * 4 * 512, SUMS = U::MINS ? MT * 256 : 0;
-    // Then the waves' exchange areas.  (One array: beside another one, reads of this would be made
-    // to wait for every copy in flight.)
-    __shared__ __align__(16) _Float16 lds[RING * STEP + 2 * SUMS + NW * U::AREA * 2];
-
+    constexpr int BN = NW * (GLU ? 16 : 32);
     const int lane = (int)__lane_id(), r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    constexpr int BN = NW * (GLU ? 16 : 32);
-    const int nb = (int)((a.N + BN - 1) / BN);
-
-    // Workgroups go to the eight XCDs in turn.  Experts: an XCD takes all
-    // weight tiles of its row tiles, so a row tile's activations enter one L2.
-    // One matrix: an XCD takes all row tiles of its weight tiles.
-    const int64_t id = blockIdx.x, seq = id >> 3;
-    int64_t b, tile;
-    if (a.ids) {
-        tile = seq / nb * 8 + (id & 7);
-        b = seq % nb;
-    } else {
-        b = seq / a.max_tiles * 8 + (id & 7);
-        tile = seq % a.max_tiles;
-    }
-    if (b >= nb || tile >= a.max_tiles) return;
-    MoeTile t;
-    if (a.ids) {
-        t = a.tiles[tile];
-    } else {
-        t.e = 0;
-        t.start = (int)tile * MT * 16;
-        t.count = (int)min((int64_t)MT * 16, a.T - t.start);
-    }
-    if (t.count <= 0) return;
     const int64_t n0 = b * BN;
 
-    // the pair of row 16 m + r, and where its activations are
-    auto pair_of = [&](int m) {
-        const int i = t.start + min(m * 16 + r, t.count - 1);
+    // the pair of a row, and where its activations are
+    auto pair_of = [&](int row) {
+        const int i = t.start + min(row, t.count - 1);
         return a.ids ? a.order[i] : i;
     };
     auto row_of = [&](int pair) { return a.per_slot ? pair : pair / a.top_k; };
@@ -200,14 +184,12 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
             const int c = wave * COPIES + i, row = c % 4 * 4 + g;
-            const int at = t.start + min(c / 4 % MT * 16 + row, t.count - 1);
-            src[i] = a.xp + (c / 4 / MT) * plane + (int64_t)row_of(a.ids ? a.order[at] : at) * 128 + (r ^ row) * 8;
+            src[i] = a.xp + (c / 4 / MT) * plane + (int64_t)row_of(pair_of(c / 4 % MT * 16 + row)) * 128 + (r ^ row) * 8;
         }
         // sums: 16 halves per row and unit; waves below MT / 2 copy [m][p][r] of m = 2 wave, 2 wave + 1
         if constexpr (U::MINS) {
             const int sm = (wave * 2 + (lane >> 5)) & (MT - 1);
-            const int i = t.start + min(sm * 16 + r, t.count - 1);
-            ssrc = a.xsum + (int64_t)row_of(a.ids ? a.order[i] : i) * 16 + ((lane >> 4) & 1) * 8;
+            ssrc = a.xsum + (int64_t)row_of(pair_of(sm * 16 + r)) * 16 + ((lane >> 4) & 1) * 8;
         }
         // The walk along K starts at another unit for other weight rows: all of them at one place of
         // rows a power of two apart would ask the same L2 channel.  It must not depend on the row
@@ -264,7 +246,7 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
                     fetch(min(u + 1, units - 1), next);
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) cur[c].unpack_step(mat, (uint32_t*)(lds + RING * STEP + 2 * SUMS) + wave * U::AREA, lane, h);
+                for (int c = 0; c < 2; ++c) cur[c].unpack_step(mat, (uint32_t*)(lds + S::AREAS) + wave * U::AREA, lane, h);
                 stage(min(s + 2, steps - 1), buf == 0 ? 2 : buf - 1);
                 tile_step<FMT, PL, MT>(cur, h, lds + buf * STEP, operand_at, acc);
                 if constexpr (U::MINS) {
@@ -289,58 +271,109 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_tile(MoeArgs a)
 
     vm_wait<0>();  // copies past the last step: none may land in LDS that is no longer this workgroup's
 
-    // sums 4g + i of row group m are those of rows 16 m + 4 g + i
+    // Sums 4g + i of row group m are those of rows 16 m + 4 g + i.  Outputs go
+    // out through LDS, MP row groups at a time, so that neighbouring lanes store
+    // neighbouring bytes.
+    typedef std::conditional_t<WIDE, float, uint16_t> out_t;
+    constexpr int VEC = 16 / (int)sizeof(out_t), GROUP = 16 * BN * (int)sizeof(out_t);
+    constexpr int MP = MT * GROUP <= S::HALVES * 2 ? MT : MT / 2;
+    static_assert(MP * GROUP <= S::HALVES * 2, "the outputs fit where the activations were");
+    out_t* const out = (out_t*)lds;
+    const bool vec = a.N % VEC == 0 && (uintptr_t)a.y % 16 == 0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (m * 16 >= t.count) break;
-        const int pair = pair_of(m);
-        const float inv = t.e >= 0 ? a.xinv[row_of(pair)] : 0.0f;
+    for (int m0 = 0; m0 < MT; m0 += MP) {
+        if (m0 * 16 >= t.count) break;
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 4 * g + i;
-            const int64_t p = __shfl(pair, row);
-            const float f = __shfl(inv, row);
-            if (m * 16 + row >= t.count) continue;
-            if constexpr (GLU) {
-                const int64_t n = n0 + wave * 16 + r;
-                const float v = t.e < 0 ? 0.0f : activate(acc[m][0][i] * f, a.act) * (acc[m][1][i] * f);
-                if (n < a.N) store_out<WIDE>(a.y, a.y_type, p * a.N + n, v);
-            } else {
+        for (int m = m0; m < m0 + MP; ++m) {
+            const float inv = t.e >= 0 ? a.xinv[row_of(pair_of(m * 16 + r))] : 0.0f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int64_t n = n0 + wave * 32 + c * 16 + r;
-                    if (n < a.N) store_out<WIDE>(a.y, a.y_type, p * a.N + n, acc[m][c][i] * f);
+            for (int i = 0; i < 4; ++i) {
+                const float f = __shfl(inv, 4 * g + i);
+                out_t* o = out + ((m - m0) * 16 + 4 * g + i) * BN + r;
+                if constexpr (GLU) {
+                    const float v = t.e < 0 ? 0.0f : activate(acc[m][0][i] * f, a.act) * (acc[m][1][i] * f);
+                    o[wave * 16] = rounded<WIDE>(a.y_type, v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) o[wave * 32 + c * 16] = rounded<WIDE>(a.y_type, acc[m][c][i] * f);
                 }
+            }
+        }
+        __syncthreads();
+        const int rows = min(MP * 16, t.count - m0 * 16);
+        if (vec) {
+            for (int q = (int)threadIdx.x; q < rows * (BN / VEC); q += 64 * NW) {
+                const int row = q / (BN / VEC), n = q % (BN / VEC) * VEC;
+                if (n0 + n < a.N) *(u32x4_t*)((out_t*)a.y + (int64_t)pair_of(m0 * 16 + row) * a.N + n0 + n) = *(const u32x4_t*)(out + row * BN + n);
+            }
+        } else {
+            for (int q = (int)threadIdx.x; q < rows * BN; q += 64 * NW) {
+                const int row = q / BN, n = q % BN;
+                if (n0 + n < a.N) ((out_t*)a.y)[(int64_t)pair_of(m0 * 16 + row) * a.N + n0 + n] = out[q];
             }
         }
     }
 }
 
-template <int FMT, int PL, int MT, int NW>
-hipError_t launch_tile_t(const MoeArgs& a, hipStream_t s)
+// tm (at most MT * 16): rows of a tile; the smallest body that holds a tile's
+// rows works on it, an expert's last ones often being few.
+template <int FMT, int PL, bool GLU, bool WIDE>
+__global__ __launch_bounds__(64 * TILE_WAVES, 2) void moe_tile(MoeArgs a, int tm)
 {
-    constexpr bool experts = FMT < FMT_W4;
-    const int64_t bn = NW * (a.op == MOE_GLU ? 16 : 32), nb = (a.N + bn - 1) / bn;
-    const int64_t grid = a.ids ? (a.max_tiles + 7) / 8 * 8 * nb : (nb + 7) / 8 * 8 * a.max_tiles;
-    const dim3 g((unsigned)grid), block(64 * NW);
-    if (experts && a.op == MOE_GLU) moe_tile<FMT, PL, MT, NW, experts, PL == 2><<<g, block, 0, s>>>(a);
-    else if (PL == 2 || a.y_type != TYPE_F32) moe_tile<FMT, PL, MT, NW, false, PL == 2><<<g, block, 0, s>>>(a);
-    else moe_tile<FMT, PL, MT, NW, false, PL == 2 || experts><<<g, block, 0, s>>>(a);  // a combine's products
-    return hipGetLastError();
+    constexpr int MT = 8 / PL;
+    __shared__ __align__(16) _Float16 lds[TileSpace<FMT, PL, MT>::HALVES];
+    constexpr int BN = TILE_WAVES * (GLU ? 16 : 32);
+    const int nb = (int)((a.N + BN - 1) / BN);
+
+    // Workgroups go to the eight XCDs in turn.  Experts: an XCD takes all
+    // weight tiles of its row tiles, so a row tile's activations enter one L2.
+    // One matrix: an XCD takes all row tiles of its weight tiles.
+    const int64_t id = blockIdx.x, seq = id >> 3;
+    int64_t b, tile;
+    if (a.ids) {
+        tile = seq / nb * 8 + (id & 7);
+        b = seq % nb;
+    } else {
+        b = seq / a.max_tiles * 8 + (id & 7);
+        tile = seq % a.max_tiles;
+    }
+    if (b >= nb || tile >= a.max_tiles) return;
+    MoeTile t;
+    if (a.ids) {
+        t = a.tiles[tile];
+    } else {
+        t.e = 0;
+        t.start = (int)tile * tm;
+        t.count = (int)min((int64_t)tm, a.T - t.start);
+    }
+    if (t.count <= 0) return;
+    if (t.count <= 32) {
+        tile_body<FMT, PL, 2, GLU, WIDE>(a, t, b, lds);
+    } else if (MT == 4 || t.count <= 64) {
+        tile_body<FMT, PL, 4, GLU, WIDE>(a, t, b, lds);
+    } else {
+        tile_body<FMT, PL, MT, GLU, WIDE>(a, t, b, lds);
+    }
 }
 
 template <int FMT, int PL>
-hipError_t launch_tile_p(const MoeArgs& a, int mt, hipStream_t s)
+hipError_t launch_tile_t(const MoeArgs& a, int tm, hipStream_t s)
 {
-    if constexpr (PL == 1)
-        if (mt == 8) return launch_tile_t<FMT, PL, 8, 8>(a, s);
-    return mt == 2 ? launch_tile_t<FMT, PL, 2, 8>(a, s) : launch_tile_t<FMT, PL, 4, 8>(a, s);
+    constexpr bool experts = FMT < FMT_W4;
+    const int64_t bn = TILE_WAVES * (a.op == MOE_GLU ? 16 : 32), nb = (a.N + bn - 1) / bn;
+    const int64_t grid = a.ids ? (a.max_tiles + 7) / 8 * 8 * nb : (nb + 7) / 8 * 8 * a.max_tiles;
+    const dim3 g((unsigned)grid), block(64 * TILE_WAVES);
+    if (experts && a.op == MOE_GLU) moe_tile<FMT, PL, experts, PL == 2><<<g, block, 0, s>>>(a, tm);
+    else if (PL == 2 || a.y_type != TYPE_F32) moe_tile<FMT, PL, false, PL == 2><<<g, block, 0, s>>>(a, tm);
+    else moe_tile<FMT, PL, false, PL == 2 || experts><<<g, block, 0, s>>>(a, tm);  // a combine's products
+    return hipGetLastError();
 }
 
-#define QMM_MOE_TILE(NAME, FMT)                                                                    \
-    hipError_t launch_tile_##NAME(const MoeArgs& a, int mt, hipStream_t s)                        \
-    {                                                                                             \
-        return a.type == TYPE_F32 ? launch_tile_p<FMT, 2>(a, mt, s) : launch_tile_p<FMT, 1>(a, mt, s); \
+#define QMM_MOE_TILE(NAME, FMT)                                                                      \
+    hipError_t launch_tile_##NAME(const MoeArgs& a, int tm, hipStream_t s)                          \
+    {                                                                                               \
+        return a.type == TYPE_F32 ? launch_tile_t<FMT, 2>(a, tm, s) : launch_tile_t<FMT, 1>(a, tm, s); \
     }
 
 }  // namespace qmm

@@ -709,16 +709,21 @@ QMM_DEV void step(const Unit<FMT> (&un)[NT], int h, AF A, f32x4_t (&acc)[MT][NT]
     }
 }
 
-// Rounds v to the output type: WIDE f32, else f16 or bf16.
+// v in the output type: WIDE f32, else the bits of f16 or bf16.
+template <bool WIDE>
+QMM_DEV std::conditional_t<WIDE, float, uint16_t> rounded(int type, float v)
+{
+    if constexpr (WIDE) {
+        return v;
+    } else {
+        const uint16_t h = f16bits(v), b = __builtin_bit_cast(uint16_t, (__bf16)v);
+        return type == TYPE_F16 ? h : b;
+    }
+}
 template <bool WIDE>
 QMM_DEV void store_out(void* y, int type, int64_t i, float v)
 {
-    if constexpr (WIDE) {
-        ((float*)y)[i] = v;
-    } else {
-        const uint16_t h = f16bits(v), b = __builtin_bit_cast(uint16_t, (__bf16)v);
-        ((uint16_t*)y)[i] = type == TYPE_F16 ? h : b;
-    }
+    ((std::conditional_t<WIDE, float, uint16_t>*)y)[i] = rounded<WIDE>(type, v);
 }
 
 // act 0: v / (1 + e^-v); 1: 0.5 v (1 + tanh t) = v / (1 + e^-2t), t = sqrt(2/pi) (v + 0.044715 v^3)
