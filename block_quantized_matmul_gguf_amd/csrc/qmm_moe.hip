@@ -79,13 +79,21 @@ MoePlan plan_of(const MoeArgs& a)
     const bool combine = a.op == MOE_COMBINE;
     const double alike = dense ? 1.0 : a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, (double)P));  // experts among P even choices
     const double again = ((double)P - alike) * (double)a.N * (double)a.row_bytes * (a.op == MOE_GLU ? 2 : 1) * (f32 ? 2 : 1);
-    if (P <= (combine ? 64 : 48) && again <= (combine ? 52e6 : 26e6)) p.path = PATH_ONE;
-    // Up to 16 pairs of an expert (64 rows of one matrix) the weights' bytes decide and the rows kernel,
-    // which splits K over waves, has more of them in flight: glu at 128 tokens (16 pairs of an expert)
-    // 75 us against 78 us, at 256 tokens 103 us against 87 us; 4-bit at 64 rows 30 us, at 128 rows 49 us
-    // against 46 us.
-    else if (avg <= (dense ? 64 : 16)) p.path = PATH_ROWS;
-    else p.path = PATH_TILE;
+    p.path = P <= (combine ? 64 : 48) && again <= (combine ? 52e6 : 26e6) ? PATH_ONE : PATH_ROWS;
+    // Few pairs of an expert: the weights' bytes decide, and the rows kernel, which splits K over waves,
+    // has more of them in flight (glu Q4_K, 64 experts, bf16: 8 pairs of an expert 59 us against 64 us,
+    // 12 pairs 68 us against 71 us, 16 pairs 78 us against 75 us; f32: 78 us against 75 us, 105 us
+    // against 88 us at 8 and 16).  Few tiles: the tile kernel leaves compute units idle.  That is
+    // counted in tiles of 32 rows times weight rows, 40000 being half of what fills the chip (Q5_0, 8
+    // experts, N 1536: 400 pairs 28 us against 38 us, 800 pairs 39 us against 40 us; 4-bit, N 8192: 128
+    // rows 21 us against 25 us, 192 rows 29 us against 26 us), less with the 256-value formats, which
+    // the tile kernel decodes in fewer instructions (Q4_K, N 1536: 200 pairs 18 us against 23 us, 400
+    // pairs 26 us against 24 us).  Every row counts its place among the pairs, so there may not be many
+    // of them (256 experts: 512 pairs 30 us against 34 us, 1024 36 us against 35 us, 2048 49 us against 40 us).
+    const int64_t half = dense ? 0 : std::min<int64_t>(a.E, P) / 2;  // tiles that are not full
+    const int64_t columns = a.N * (a.op == MOE_GLU ? 2 : 1);
+    const bool few = avg <= (dense ? 16 : 11) || ((P + 31) / 32 + half) * columns <= (unit == 256 ? 22000 : 40000);
+    if (p.path != PATH_ONE) p.path = few && (dense || P <= 1024) ? PATH_ROWS : PATH_TILE;
     if (p.path == PATH_ROWS) {
         // one more row group costs little, decoding the weights again a lot; four groups of the
         // 256-value formats or of f32's two parts do not fit in registers
@@ -98,7 +106,6 @@ MoePlan plan_of(const MoeArgs& a)
         // 614 pairs: 40, 48 and 48 us).
         const int most = f32 ? 4 : 8;
         const int64_t bn = a.op == MOE_GLU ? 128 : 256, nb = (a.N + bn - 1) / bn;
-        const int64_t half = dense ? 0 : std::min<int64_t>(a.E, P) / 2;
         p.mt = 2;
         while (p.mt < most && ((P + 16 * p.mt - 1) / (16 * p.mt) + half) * nb > 256) p.mt *= 2;
     }
