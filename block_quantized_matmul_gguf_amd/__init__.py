@@ -370,8 +370,10 @@ def dequantize_weights(fmt: int, w, n: int, k: int, out=None, stream=None):
 #
 # These calls take no plan.  A call's scratch tensor and, unless the caller
 # gives them, its outputs come from torch's allocator on the stream of the
-# call, so calls may overlap on different streams and be captured in graphs
-# that run side by side.
+# call (``stream``, a torch.cuda.Stream, or the current one), so calls may
+# overlap on different streams and be captured in graphs that run side by side.
+# As with torch's own work on a second stream, the caller has that stream wait
+# for inputs made on another, and keeps them until it is done with them.
 
 F32, F16, BF16 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}

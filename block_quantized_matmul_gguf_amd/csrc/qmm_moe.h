@@ -54,6 +54,25 @@ struct MoeArgs {
     _Float16* xsum;
 };
 
+// Waves of the preparation that share an activation row: enough to fill the
+// chip, each with some work.
+inline int prep_waves(int64_t K, int64_t rows)
+{
+    int wr = 1;
+    while (wr < 16 && (K > wr * 2048 || (rows * wr < 4096 && K > wr * 1024))) wr *= 4;
+    return wr;
+}
+// Workgroups of the preparation (1024 threads each), and of the tile kernel (512).
+inline int64_t prep_blocks(const MoeArgs& a, int64_t rows)
+{
+    const int64_t per = 16 / prep_waves(a.K, rows);
+    return (rows + per - 1) / per + (a.fmt < FMT_W4 ? 1 : 0);
+}
+inline int64_t tile_blocks(const MoeArgs& a, int64_t tiles)
+{
+    const int64_t bn = a.op == MOE_GLU ? 128 : 256, nb = (a.N + bn - 1) / bn;
+    return a.fmt < FMT_W4 ? (tiles + 7) / 8 * 8 * nb : (nb + 7) / 8 * 8 * tiles;
+}
 // One pair (a combine: one token) per workgroup.
 hipError_t launch_one(const MoeArgs& a, int waves, hipStream_t s);
 // What the kernels below need first (rows: the rows kernel, else the tile kernel).

@@ -53,7 +53,7 @@ enum { PATH_ONE, PATH_ROWS, PATH_TILE };
 // What a call runs and what it needs of the workspace.
 struct MoePlan {
     int path, waves, mt;
-    bool sort;
+    bool sort, launchable;
     int tm, max_tiles;
     int64_t x_rows, Kp;
     size_t order, tiles, products, xp, xinv, xsum, bytes;  // offsets
@@ -137,6 +137,10 @@ MoePlan plan_of(const MoeArgs& a)
         if (a.op == MOE_COMBINE) p.products = take((size_t)P * (size_t)a.N * 4);
     }
     p.bytes = off;
+    // a grid has fewer than 2^32 threads (the other kernels' grids stay below that at any size that
+    // the checks let through)
+    p.launchable = (p.path == PATH_ONE || prep_blocks(a, p.x_rows) < (1ll << 22)) &&
+                   (p.path != PATH_TILE || tile_blocks(a, p.max_tiles) < (1ll << 23));
     return p;
 }
 
@@ -213,11 +217,18 @@ MoeArgs experts_args(int op, int format, int64_t E, int64_t N, int64_t K, int64_
     return a;
 }
 
-int64_t workspace_bytes(const MoeArgs& a) { return a.T == 0 ? 0 : (int64_t)plan_of(a).bytes; }
+int64_t workspace_bytes(const MoeArgs& a)
+{
+    if (a.T == 0) return 0;
+    const MoePlan p = plan_of(a);
+    if (!p.launchable) return bad("shape too large"), -1;
+    return (int64_t)p.bytes;
+}
 
 int run(const MoeArgs& a, void* ws, size_t ws_bytes, void* stream)
 {
     const MoePlan p = plan_of(a);
+    if (!p.launchable) return bad("shape too large");
     if (p.bytes > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < p.bytes)) return bad("ws must be 16-byte aligned and hold the call's workspace bytes");
     const hipError_t e = launch_moe(a, p, (char*)ws, (hipStream_t)stream);
     return e == hipSuccess ? QMM_OK : set_error(QMM_EHIP, hipGetErrorString(e));

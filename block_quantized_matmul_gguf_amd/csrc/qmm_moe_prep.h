@@ -301,11 +301,8 @@ __global__ __launch_bounds__(PREP_THREADS) void moe_prep(MoeArgs a, int tm, int 
 template <int FMT, int PL>
 hipError_t launch_prep_t(const MoeArgs& a, bool rows, int tm, hipStream_t s)
 {
-    // enough waves to fill the chip, each with some work
-    int wr = 1;
-    while (wr < 16 && (a.K > wr * 2048 || (a.x_rows * wr < 4096 && a.K > wr * 1024))) wr *= 4;
-    const int64_t per = PREP_WAVES / wr;
-    const dim3 grid((unsigned)((a.x_rows + per - 1) / per + (a.ids ? 1 : 0))), block(PREP_THREADS);
+    const int wr = prep_waves(a.K, a.x_rows);
+    const dim3 grid((unsigned)prep_blocks(a, a.x_rows)), block(PREP_THREADS);
     if (rows) moe_prep<FMT, PL, true><<<grid, block, 0, s>>>(a, tm, wr);
     else moe_prep<FMT, PL, false><<<grid, block, 0, s>>>(a, tm, wr);
     return hipGetLastError();

@@ -361,9 +361,7 @@ template <int FMT, int PL>
 hipError_t launch_tile_t(const MoeArgs& a, int tm, hipStream_t s)
 {
     constexpr bool experts = FMT < FMT_W4;
-    const int64_t bn = TILE_WAVES * (a.op == MOE_GLU ? 16 : 32), nb = (a.N + bn - 1) / bn;
-    const int64_t grid = a.ids ? (a.max_tiles + 7) / 8 * 8 * nb : (nb + 7) / 8 * 8 * a.max_tiles;
-    const dim3 g((unsigned)grid), block(64 * TILE_WAVES);
+    const dim3 g((unsigned)tile_blocks(a, a.max_tiles)), block(64 * TILE_WAVES);
     if (experts && a.op == MOE_GLU) moe_tile<FMT, PL, experts, PL == 2><<<g, block, 0, s>>>(a, tm);
     else if (PL == 2 || a.y_type != TYPE_F32) moe_tile<FMT, PL, false, PL == 2><<<g, block, 0, s>>>(a, tm);
     else moe_tile<FMT, PL, false, PL == 2 || experts><<<g, block, 0, s>>>(a, tm);  // a combine's products

@@ -32,20 +32,6 @@
 
 namespace qmm {
 
-// dw with the upper half-wave of a and the lower half-wave of b exchanged
-QMM_DEV void swap32(uint32_t& a, uint32_t& b)
-{
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-// odd 16-lane rows of a exchanged with even rows of b
-QMM_DEV void swap16(uint32_t& a, uint32_t& b)
-{
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
 // The exchange through a wave's LDS.  A word area holds 16 bytes per (row,
 // quarter), the quarters of a row permuted so that neither side has bank
 // conflicts; a row area holds a dword per (row, quarter).

@@ -323,8 +323,10 @@ int qmatmul_route_experts(const void* logits, int type, int64_t T, int64_t E, co
  * qmatmul_row_bytes(format, K) bytes, 16-byte aligned); ids: device int32
  * [T x top_k]; an id outside 0..E-1 means no expert; the same id may come
  * twice in a row.  x, h and y have the type `type`; x and h 16-byte aligned.
- * Activations are not quantized (mode (a)), products are summed in f32 and
- * each output is rounded once, to `type`.
+ * Activations are not quantized (mode (a)): f16 ones enter as they are, bf16
+ * and f32 ones to 2^-22 of themselves or 2^-40 of the largest magnitude in
+ * their row, whichever is more.  Products are summed in f32 and each output is
+ * rounded once, to `type`.
  *
  * qmatmul_experts_run: y[t][s] = x[t] . W[ids[t][s]]^T, y [T x top_k x N];
  *   per_slot = 0: x [T x K], one row for a token's slots; per_slot = 1:
@@ -336,11 +338,12 @@ int qmatmul_route_experts(const void* logits, int type, int64_t T, int64_t E, co
  *   [T x top_k]; slots without an expert add nothing, whatever their h and
  *   weight hold.
  *
- * A row of x with an infinity or NaN makes the outputs computed from it
- * non-finite (NaN where the sum holds inf - inf or 0 * inf) and no others.
+ * A row of x with an infinity or NaN makes all the outputs computed from it
+ * non-finite (infinite or NaN) and no others.
  * Limits: E <= 1024, top_k <= 64, T * top_k <= 2^24, N <= 2^24, and
- * qmatmul_create's limit on K.  T == 0 enqueues nothing.  Outputs must not overlap
- * inputs.
+ * qmatmul_create's limit on K; QMM_EINVAL ("shape too large") also where a
+ * launch would need 2^32 threads (2^22 rows with K > 8192, or 2^23 tiles of
+ * outputs).  T == 0 enqueues nothing.  Outputs must not overlap inputs.
  */
 int64_t qmatmul_experts_workspace_bytes(int product, int format, int64_t E, int64_t N, int64_t K, int64_t T,
                                         int64_t top_k, int type); /* -1 if invalid */
@@ -363,8 +366,10 @@ int qmatmul_experts_combine(int format, int64_t E, int64_t N, int64_t K, int64_t
  * in its high nibble, 16-byte aligned.  scales: device [N x K/group] of
  * scale_type (QMM_F32, QMM_F16 or QMM_BF16).  zeros: device uint8 [N x
  * K/group], 0..15 (other values are used as they are).  group: a multiple of
- * 32 that divides K; N and M at most 2^24.  x (16-byte aligned) and y have the type `type`.  M >= 0;
- * M == 0 enqueues nothing.  Sums and rounding as qmatmul_experts_run.
+ * 32 that divides K; N and M at most 2^24, K at most 2^20, N * K / 2 at most
+ * 2^40.  x (16-byte aligned) and y have the type `type`.  M >= 0; M == 0
+ * enqueues nothing.  Sums, rounding, non-finite rows and the limit on a launch as
+ * with qmatmul_experts_run.
  */
 int64_t qmatmul_w4_workspace_bytes(int64_t N, int64_t K, int64_t M, int64_t group, int type); /* -1 if invalid */
 int qmatmul_w4_run(int64_t N, int64_t K, int64_t M, int64_t group, int type, int scale_type, const void* q,

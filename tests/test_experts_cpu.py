@@ -134,3 +134,32 @@ def test_bindings_refuse_wrong_tensors():
                            torch.zeros((2, 1), dtype=torch.int32))
     with pytest.raises(ValueError, match="act"):
         qmm.experts_glu(qmm.Q8_0, None, None, None, None, act="relu")
+
+
+@pytest.mark.parametrize("n,k,m,group,fits", [
+    (8, 16384, 1 << 22, 128, False), (8, 16384, (1 << 22) - 1, 128, True), (8, 4096, 1 << 24, 32, False),
+    (8, 4096, (1 << 24) - 4, 32, True), (1 << 24, 64, 1 << 24, 64, False), (1 << 24, 64, 1 << 13, 64, True),
+])
+def test_launches_of_2_to_the_32_threads_are_refused_w4(n, k, m, group, fits):
+    need = qmm.lib().qmatmul_w4_workspace_bytes(n, k, m, group, qmm.BF16)
+    assert (need > 0) == fits
+    if not fits:
+        assert need == -1 and "large" in qmm.last_error()
+        assert w4(N=n, K=k, M=m, group=group, type=qmm.BF16, ws=0x40000, ws_bytes=1 << 60) == qmm.EINVAL
+        assert "large" in qmm.last_error()
+
+
+@pytest.mark.parametrize("product,code", [("run", qmm.EXPERTS_RUN), ("glu", qmm.EXPERTS_GLU), ("combine", qmm.EXPERTS_COMBINE)])
+@pytest.mark.parametrize("e,n,k,t,top_k,fits", [
+    (1024, 1 << 21, 32, 2048, 1, False), (1024, 1 << 20, 32, 1024, 1, True), (4, 64, 16384, 1 << 22, 1, False),
+    (4, 64, 8192, 1 << 21, 8, None), (4, 64, 2048, 1 << 23, 2, True),
+])
+def test_launches_of_2_to_the_32_threads_are_refused_experts(product, code, e, n, k, t, top_k, fits):
+    if fits is None:  # a row per token fits (2^21), a row per pair (2^24) does not
+        fits = product != "combine"
+    need = qmm.lib().qmatmul_experts_workspace_bytes(code, qmm.Q8_0, e, n, k, t, top_k, qmm.F16)
+    assert (need > 0) == fits
+    if not fits:
+        assert need == -1 and "large" in qmm.last_error()
+        assert experts(product, E=e, N=n, K=k, T=t, top_k=top_k, type=qmm.F16, ws=0x40000, ws_bytes=1 << 60) == qmm.EINVAL
+        assert "large" in qmm.last_error()

@@ -561,3 +561,181 @@ def test_more_pairs_than_the_sort_keeps_in_registers():
         step = max(1, t // 3000)
         ref, a = product_ref(w, wa, e, n, ids_h[::step], per_slot(xh[::step], k))
         close(y[::step], ref, BAR * a, f"{t} tokens")
+
+
+# ------------------------------------------- the kernels of larger calls --
+#
+# Which kernel runs depends on the number of pairs, the pairs per expert and
+# the tiles of outputs: one pair per workgroup up to 48 pairs; 16, 32 or 64
+# rows per workgroup up to 1024 pairs where there are few tiles; else tiles of
+# 32, 64 or 128 rows.
+
+def skewed(seed, t, e, k):
+    """Experts with very different numbers of pairs, the last one without any."""
+    g = np.random.default_rng(seed)
+    return np.minimum((g.random((t, k)) ** 2 * (e - 1)).astype(np.int32), e - 2)
+
+
+def products_case(fmt, dtype, t, e, k, n, kk, ids_h, ops, seed):
+    f, dt = FMTS[fmt], TYPES[dtype]
+    b, w, wa = weights_of(f, seed, e * n, kk)
+    wd = torch.from_numpy(b.reshape(e, n, -1)).cuda()
+    ids = torch.from_numpy(ids_h).cuda()
+    x, xh = acts(seed + 1, (t, kk), dt)
+    y, a = product_ref(w, wa, e, n, ids_h, per_slot(xh, k))
+    if "run" in ops:
+        close(qmm.experts_matmul(f, wd, x, ids), y, BAR * a, "experts_matmul")
+    if "glu" in ops:  # the same matrix as gate and up
+        ag = act_ref(y, "silu")
+        slack = 1.13 * BAR * a * (np.abs(y) + BAR * a) + np.abs(y) * BAR * a + 2.0**-20 * np.abs(ag * y)
+        close(qmm.experts_glu(f, wd, wd, x, ids), ag * y, slack, "experts_glu")
+    if "combine" in ops:
+        h, hh = acts(seed + 2, (t, k, kk), dt)
+        y, a = product_ref(w, wa, e, n, ids_h, hh)
+        g = np.random.default_rng(seed + 3).random((t, k)).astype(np.float32)
+        gd = g.astype(np.float64)[:, :, None]
+        close(qmm.experts_combine(f, wd, h, ids, torch.from_numpy(g).cuda()), (y * gd).sum(1), BAR * (a * gd).sum(1), "combine")
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("t,e,k,n,mult,ops", [
+    (1100, 6, 1, 70, 3, ("run", "glu", "combine")), (1400, 5, 1, 1300, 1, ("run", "glu")), (750, 9, 4, 1290, 2, ("run",)),
+    (520, 40, 3, 136, 5, ("run", "combine")), (1025, 2, 1, 33, 6, ("glu", "combine")),
+])
+def test_tiles_of_every_size(fmt, dtype, t, e, k, n, mult, ops):
+    print(f"tiles {fmt} {dtype} T={t} E={e} k={k} N={n} mult={mult}", flush=True)
+    products_case(fmt, dtype, t, e, k, n, k_of(FMTS[fmt], mult), skewed(160 + t, t, e, k), ops, 161 + t)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("t,e,k,n,mult", [(60, 16, 4, 50, 2), (100, 8, 2, 33, 5), (70, 1, 1, 97, 3), (256, 4, 4, 40, 1), (49, 64, 1, 130, 6)])
+def test_rows_of_every_count(fmt, dtype, t, e, k, n, mult):
+    print(f"rows {fmt} {dtype} T={t} E={e} k={k} N={n} mult={mult}", flush=True)
+    ids = choose(170 + t, t, e, k, "twice" if t != 256 else "any")
+    products_case(fmt, dtype, t, e, k, n, k_of(FMTS[fmt], mult), ids, ("run", "glu", "combine"), 171 + t)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("m,n,k,group,zeros,sdtype", [
+    (49, 33, 96, 32, True, "f16"), (50, 130, 384, 128, False, "f32"), (64, 61, 1056, 96, True, "bf16"), (65, 40, 640, 64, False, "f16"),
+    (16, 1200, 4096, 128, True, "f16"), (31, 1200, 4096, 64, False, "f32"), (48, 1300, 4096, 32, True, "bf16"),
+    (1100, 1300, 96, 32, True, "f16"), (1500, 1300, 384, 128, False, "bf16"), (3000, 1290, 160, 32, False, "f32"),
+    (3001, 1300, 256, 256, True, "f32"), (1537, 1030, 288, 96, True, "f16"),
+])
+def test_w4_rows_and_tiles(dtype, m, n, k, group, zeros, sdtype):
+    print(f"w4 {dtype} M={m} N={n} K={k} G={group} zeros={zeros} {sdtype}", flush=True)
+    q, s, z, w = w4_case(180 + m, n, k, group, zeros, TYPES[sdtype])
+    x, xh = acts(181 + m, (m, k), TYPES[dtype])
+    close(qmm.w4_matmul(q, s, x, zeros=z), xh @ w.T, BAR * (np.abs(xh) @ np.abs(w).T), "w4")
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("fmt", list(FMTS) + ["W4"])
+@pytest.mark.parametrize("m", [1, 20, 60, 1100])
+def test_long_rows(fmt, dtype, m):
+    """K = 33024: more than the preparation keeps in registers, several parts of a wave's share of a row.
+    A chain of f32 additions has one per 32 products (inside which a matrix product adds 32 in at most 32
+    steps) and 32 more at most to join waves and parts: each is off by at most 2^-24 of A."""
+    k, n = 33024, 9
+    x, xh = acts(190 + m, (m, k), TYPES[dtype])
+    if fmt == "W4":
+        q, s, z, w = w4_case(191, n, k, 128, True, torch.float16)
+        got, wa = qmm.w4_matmul(q, s, x, zeros=z), np.abs(w)
+    else:
+        b, w, wa = weights_of(FMTS[fmt], 192, n, k)
+        got = qmm.experts_matmul(FMTS[fmt], torch.from_numpy(b.reshape(1, n, -1)).cuda(), x,
+                                 torch.zeros((m, 1), dtype=torch.int32).cuda())[:, 0]
+    close(got, xh @ w.T, (k / 32 + 64) * 2.0**-24 * (np.abs(xh) @ wa.T), "long rows")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_wide_ranges_and_non_finite_rows_in_tiles(fmt, dtype):
+    k, n, m = 512, 40, 1200
+    x = torch.from_numpy(np.tile(value_rows(k), (m // 24, 1))).to(TYPES[dtype])
+    bad = {25: float("nan"), 500: float("inf"), m - 1: float("-inf")}
+    for r, v in bad.items():
+        x[r, (37 * r) % k] = v
+    b, w, wa = weights_of(FMTS[fmt], 200, n, k)
+    y = qmm.experts_matmul(FMTS[fmt], torch.from_numpy(b.reshape(1, n, -1)).cuda(), x.cuda(),
+                           torch.zeros((m, 1), dtype=torch.int32).cuda())[:, 0]
+    for r in bad:
+        assert not torch.isfinite(y[r]).any()
+    good = [r for r in range(m) if r not in bad]
+    xh = x.double().numpy()[good]
+    with np.errstate(over="ignore"):
+        close(y[good], xh @ w.T, BAR * (np.abs(xh) @ wa.T) + 2.0**-126 * k * wa.max(), "finite rows")
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("m", [1, 60, 1500])
+def test_an_outlier_whose_weights_are_zero(dtype, m):
+    """Values far below their row's largest: off by 2^-22 of themselves or 2^-40 of that one, as documented."""
+    k, n = 256, 1024
+    q, s, z, w = w4_case(210, n, k, 64, False, torch.float32)
+    q[:, 50] = 0x88  # elements 100 and 101: zero weights
+    w = w.copy()
+    w[:, 100:102] = 0
+    x, _ = acts(211, (m, k), TYPES[dtype])
+    big = 60000.0 if dtype == "f16" else 2.0**24
+    x[:, 100] = big
+    x[:, 7] *= 2.0**-12
+    xh = f64(x)
+    aw = np.abs(w)
+    lost = np.maximum(2.0**-22 * np.abs(xh), 2.0**-40 * big) if dtype != "f16" else 0 * xh
+    close(qmm.w4_matmul(q, s, x), xh @ w.T, BAR * (np.abs(xh) @ aw.T) + lost @ aw.T, "outlier")
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("m", [2, 60, 1100])
+def test_half_precision_below_its_normal_range(fmt, m):
+    k, n = 256, 30
+    x, xh = acts(215, (m, k), torch.float16, 2.0**-17)  # most values below 2^-14, kept exactly
+    b, w, wa = weights_of(FMTS[fmt], 216, n, k)
+    ids = torch.zeros((m, 1), dtype=torch.int32).cuda()
+    got = qmm.experts_matmul(FMTS[fmt], torch.from_numpy(b.reshape(1, n, -1)).cuda(), x, ids)[:, 0]
+    close(got, xh @ w.T, BAR * (np.abs(xh) @ wa.T), "subnormal rows")
+
+
+@pytest.mark.parametrize("fmt", ["Q8_0", "Q4_K", "Q6_K"])
+@pytest.mark.parametrize("t", [1, 60, 500])
+def test_a_huge_slot_of_weight_zero_leaves_the_others(fmt, t):
+    f, e, n, k, kk = FMTS[fmt], 4, 48, 3, 512
+    b, w, wa = weights_of(f, 220, e * n, kk)
+    h, _ = acts(221, (t, k, kk), torch.float32)
+    h[:, 1] *= 1e25
+    g = np.random.default_rng(222).random((t, k)).astype(np.float32)
+    g[:, 1] = 0
+    ids_h = choose(223, t, e, k, "any")
+    y, a = product_ref(w, wa, e, n, ids_h, f64(h))
+    gd = g.astype(np.float64)[:, :, None]
+    got = qmm.experts_combine(f, torch.from_numpy(b.reshape(e, n, -1)).cuda(), h, torch.from_numpy(ids_h).cuda(), torch.from_numpy(g).cuda())
+    close(got, (y * gd).sum(1), BAR * (a * gd).sum(1), "combine")
+
+
+@pytest.mark.parametrize("m", [1, 60, 1500])
+def test_w4_in_graphs_replayed_side_by_side(m):
+    k, n = 512, 1030
+    q, s, z, _ = w4_case(230, n, k, 128, True, torch.float16)
+    xs = [acts(231 + i, (m, k), torch.bfloat16)[0] for i in range(2)]
+    want = [qmm.w4_matmul(q, s, x, zeros=z) for x in xs]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for x, st in zip(xs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            outs.append(qmm.w4_matmul(q, s, x, zeros=z))
+        graphs.append(g)
+    for i in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        eager = qmm.w4_matmul(q, s, xs[i % 2], zeros=z)
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[i % 2])
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
