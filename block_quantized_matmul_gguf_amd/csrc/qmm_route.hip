@@ -222,9 +222,13 @@ __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteArgs a)
     int my_id = -1;
     for (int r = 0; r < a.k; ++r) {
         const uint32_t mh = wave_max_u32(hi[0]);
-        const uint32_t ml = wave_max_u32(hi[0] == mh ? lo[0] : 0);
-        if ((mh | ml) == 0) break;  // none left
-        const int owner = (int)__builtin_ctzll(__ballot(hi[0] == mh && lo[0] == ml));
+        uint64_t best = __ballot(hi[0] == mh);
+        if (best & (best - 1)) {  // several lanes share the upper half
+            const uint32_t ml = wave_max_u32(hi[0] == mh ? lo[0] : 0);
+            if ((mh | ml) == 0) break;  // none left
+            best = __ballot(hi[0] == mh && lo[0] == ml);
+        }
+        const int owner = (int)__builtin_ctzll(best);
         const int id = __builtin_amdgcn_readlane(at[0], owner);
         my_id = lane == r ? id : my_id;
         const bool mine = lane == owner;
