@@ -13,7 +13,8 @@ namespace qmm {
 namespace {
 
 // y[t][n] = sum over the slots with an expert of weights[t][s] * prod[t][s][n].
-// V (4 or 1) outputs per thread; rows of outputs along the grid's y.
+// V (4 or 1) outputs per thread; rows of outputs along the grid's y.  Bound by
+// the products' bytes: 98 MB (12000 x 2048) 17 us, 5.8 TB/s.
 template <int V>
 __global__ __launch_bounds__(256) void moe_combine(MoeArgs a, const float* prod)
 {

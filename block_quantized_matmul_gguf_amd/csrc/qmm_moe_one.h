@@ -9,6 +9,11 @@
 // lo) of values scaled by one power of two, with the first weights already on
 // their way; every operand row then holds that one row.  Without barriers in
 // the loop the waves of a compute unit drift apart and keep its loads going.
+//
+// Measured: 4-bit 14336 x 4096, one row: 9.4 us (3.2 TB/s, launch included);
+// GLU of Q4_K, one token on 8 experts of 2 x 1024 x 2048: 8.4 us; combine of
+// Q6_K, one token on 8 experts of 2048 x 1024: 9.9 us, of which the launch and
+// the chain id - weights - sums are more than the bytes (2.9 us).
 #pragma once
 #include "qmm_moe_unit.h"
 

@@ -8,6 +8,14 @@
 // is read and decoded once per workgroup and goes from memory to registers to
 // the matrix cores; the activations, prepared once per call so that an
 // operand's lanes read neighbouring bytes, come from L2.
+//
+// Measured: Q8_0, 76 pairs on 32 experts of 1536 x 576, f32: 11.9 us after 5.8
+// us of preparation; Q5_0, 614 pairs on 8 experts of 1536 x 1536, f32: 28 us,
+// bound by decoding each weight for 32 rows at a time; 4-bit, 64 rows of 14336
+// x 4096, bf16: 29 us in all.  Waves that bring raw rows into operand order
+// themselves save the preparation's launch and lose more to its repetition
+// (those 76 pairs 17.1 us against 17.2 us; GLU of Q4_K, 64 tokens: 105 us
+// against 59 us).
 #pragma once
 #include "qmm_moe_unit.h"
 

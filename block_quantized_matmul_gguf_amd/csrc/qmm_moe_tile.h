@@ -8,6 +8,13 @@
 // into LDS, one step (128 values of K) being 32 KB, two steps ahead of their
 // use, and read by every wave; the next unit's weights are loaded while one is
 // multiplied.
+//
+// Measured: 4-bit 512 x 14336 x 4096 bf16 78 us (770 TF/s); GLU of Q4_K, 16384
+// pairs on 64 experts, 2 x 1024 x 2048, 270 us (510 TF/s).  A step of 128 rows
+// costs a compute unit about 2400 cycles of LDS reads, 2300 of matrix cores and
+// 2400 of vector issue (decoding, scaling, addresses), which overlap by half.
+// Four waves of 64 weight rows, one per SIMD, halve the LDS reads and leave
+// nothing to fill a wave's waits: 107 and 403 us.
 #pragma once
 #include "qmm_moe_unit.h"
 

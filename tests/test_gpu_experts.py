@@ -739,3 +739,31 @@ def test_w4_in_graphs_replayed_side_by_side(m):
         torch.cuda.synchronize()
         assert torch.equal(eager, want[i % 2])
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("m,n", [(540000, 2), (540000, 16), (70000, 3)])
+def test_w4_past_32_bit_offsets(m, n):
+    """540000 x 4096 activations: more than 2^31 values and 2^32 bytes, in x and in the workspace."""
+    k = 4096 if m > 500000 else 64
+    q, s, z, w = w4_case(240, n, k, k, True, torch.float16)
+    x = torch.empty((m, k), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(241))
+    y = qmm.w4_matmul(q, s, x, zeros=z)
+    at = torch.tensor([0, 1, 63, 64, m // 2 - 1, m // 2, m - 65, m - 2, m - 1])
+    xh = f64(x[at.cuda()])
+    close(y[at.cuda()], xh @ w.T, BAR * (np.abs(xh) @ np.abs(w).T), "w4")
+
+
+@pytest.mark.parametrize("t", [1, 30, 100, 1100])
+def test_experts_past_32_bit_offsets(t):
+    """64 x 33000 x 2048 in Q8_0: 4.6e9 bytes, the last expert's last rows past 2^32; few of them not zero."""
+    f, e, n, k = qmm.Q8_0, 64, 33000, 2048
+    b, w, wa = weights_of(f, 250, 40, k)
+    wd = torch.zeros((e, n, b.shape[1]), dtype=torch.uint8, device="cuda")
+    wd[-1, -40:] = torch.from_numpy(b).cuda()
+    x, xh = acts(251, (t, k), torch.float16)
+    ids = torch.full((t, 1), e - 1, dtype=torch.int32).cuda()
+    y = qmm.experts_matmul(f, wd, x, ids)[:, 0]
+    close(y[:, -40:], xh @ w.T, BAR * (np.abs(xh) @ wa.T), "last rows")
+    assert (y[:, :-40] == 0).all()
+    h = qmm.experts_glu(f, wd, wd, x, ids)[:, 0]
+    assert (h[:, :-40] == 0).all() and (h[:, -40:] != 0).any()
