@@ -10,11 +10,14 @@
 // multiplied.
 //
 // Measured: 4-bit 512 x 14336 x 4096 bf16 78 us (770 TF/s); GLU of Q4_K, 16384
-// pairs on 64 experts, 2 x 1024 x 2048, 270 us (510 TF/s).  A step of 128 rows
-// costs a compute unit about 2400 cycles of LDS reads, 2300 of matrix cores and
-// 2400 of vector issue (decoding, scaling, addresses), which overlap by half.
-// Four waves of 64 weight rows, one per SIMD, halve the LDS reads and leave
-// nothing to fill a wave's waits: 107 and 403 us.
+// pairs on 64 experts, 2 x 1024 x 2048, 270 us (510 TF/s).  Of the 4-bit call's
+// time the matrix cores are busy 37%, vector issue 36%, LDS 28%, and a wave
+// spends a third of its life issuing, a third waiting for a unit and the rest
+// waiting for data: two waves per SIMD, all that the registers allow, do not
+// cover each other's chains.  Measured without gain: one barrier per two steps,
+// the weights' exchange a step ahead, operands read further ahead.  Four waves
+// of 64 weight rows, one per SIMD, halve the LDS reads and leave nothing to
+// fill a wave's waits: 107 and 403 us.
 #pragma once
 #include "qmm_moe_unit.h"
 
@@ -68,7 +71,7 @@ struct TileUnit<FMT, true> {
 //
 // The step goes in pieces of two operand reads and four products (PL * MT / 2
 // pieces per product index j).  With the products of a piece run the reads of
-// the piece after next, the scaling of the piece before and a part of the
+// a later piece, the scaling of the piece before and a part of the
 // decoding for the next j, issued between them: a matrix product occupies its
 // unit for four issue slots, three of which are free for vector work.
 constexpr int VALU_PER_PRODUCT = 6;
@@ -78,13 +81,14 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
     using U = Unit<FMT>;
     constexpr int GM = 2 / PL;           // row groups of a piece
     constexpr int PJ = PL * MT / 2;      // pieces per j
-    half8_t a[3][GM][PL];
+    constexpr int AHEAD = U::MINS ? 1 : 2;  // pieces; Q4_K has no registers left for two
+    half8_t a[AHEAD + 1][GM][PL];
     auto read = [&](int q) {
 #pragma unroll
         for (int m = 0; m < GM; ++m)
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-                a[q % 3][m][p] = *(const half8_t*)(lds + (p * MT + q % PJ * GM + m) * 2048 + at[q / PJ]);
+                a[q % (AHEAD + 1)][m][p] = *(const half8_t*)(lds + (p * MT + q % PJ * GM + m) * 2048 + at[q / PJ]);
     };
     constexpr int DN = U::CHAIN ? PJ : 2;  // accumulators: per piece of a j, or in turn
     f32x4_t d[DN][GM][2];
@@ -106,15 +110,15 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
 #pragma unroll
         for (int k = 0; k < U::PARTS; ++k) b[j & 1][t][k] = un[t].operand_of(h, j, k);
     };
-    read(0);
-    read(1);
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) read(q);
     decode(0, 0);
     decode(0, 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < 4 * PJ; ++q) {
         const int j = q / PJ;
-        if (q + 2 < 4 * PJ) read(q + 2);
+        if (q + AHEAD < 4 * PJ) read(q + AHEAD);
 #pragma unroll
         for (int m = 0; m < GM; ++m)
 #pragma unroll
@@ -124,18 +128,23 @@ QMM_DEV void tile_step(const TileUnit<FMT> (&un)[2], int h, const _Float16* lds,
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const bool first = p + k == 0 && (!U::CHAIN || j == 0);
-                        d[q % DN][m][t] = mfma(a[q % 3][m][p], b[j & 1][t][k], first ? f32x4_t{0, 0, 0, 0} : d[q % DN][m][t]);
+                        d[q % DN][m][t] = mfma(a[q % (AHEAD + 1)][m][p], b[j & 1][t][k], first ? f32x4_t{0, 0, 0, 0} : d[q % DN][m][t]);
                     }
         if (q > (U::CHAIN ? 3 * PJ : 0)) scale(q - 1);
         if (j < 3 && q % PJ == 0) decode(j + 1, 0);
         if (j < 3 && q % PJ == PJ / 2) decode(j + 1, 1);
+        // With one scale per step there are few enough sums in flight for this order to fit in
+        // registers and to gain (Q4_K 270 us against 318 us without it); where every product's sums are
+        // scaled the compiler's own order is as good or better (Q8_0 354 us against 361 us).
+        if constexpr (U::CHAIN) {
 #pragma unroll
-        for (int i = 0; i < 4 * U::PARTS; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read
-            __builtin_amdgcn_sched_group_barrier(0x002, VALU_PER_PRODUCT, 0);
+            for (int i = 0; i < 4; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read
+                __builtin_amdgcn_sched_group_barrier(0x002, VALU_PER_PRODUCT, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
     }
     scale(4 * PJ - 1);
 }
