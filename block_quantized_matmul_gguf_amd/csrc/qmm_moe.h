@@ -77,7 +77,8 @@ inline int64_t tile_blocks(const MoeArgs& a, int64_t tiles)
 hipError_t launch_one(const MoeArgs& a, int waves, hipStream_t s);
 // What the kernels below need first (rows: the rows kernel, else the tile kernel).
 hipError_t launch_prep(const MoeArgs& a, bool rows, int tm, hipStream_t s);
-// mt * 16 (mt 1, 2 or 4) pairs of an expert per workgroup, the waves along K.
+// mt * 16 (mt 1, 2 or, 16-bit activations and 32-value blocks, 4) pairs of an
+// expert per workgroup, the waves along K.
 hipError_t launch_rows(const MoeArgs& a, int mt, int waves, hipStream_t s);
 // tm (32, 64 or, but for f32, 128) pairs of an expert against 256 weight rows
 // (GLU: 128 of each matrix) per workgroup.

@@ -9,8 +9,8 @@
 // the matrix cores; the activations, prepared once per call so that an
 // operand's lanes read neighbouring bytes, come from L2.
 //
-// Measured: Q8_0, 76 pairs on 32 experts of 1536 x 576, f32: 11.9 us after 5.8
-// us of preparation; Q5_0, 614 pairs on 8 experts of 1536 x 1536, f32: 28 us,
+// Measured: Q8_0, 76 pairs on 32 experts of 1536 x 576, f32: 11.5 us after 5.8
+// us of preparation; Q5_0, 614 pairs on 8 experts of 1536 x 1536, f32: 26 us,
 // bound by decoding each weight for 32 rows at a time; 4-bit, 64 rows of 14336
 // x 4096, bf16: 29 us in all.  Waves that bring raw rows into operand order
 // themselves save the preparation's launch and lose more to its repetition
@@ -153,7 +153,10 @@ hipError_t launch_rows_t(const MoeArgs& a, int waves, hipStream_t s)
 template <int FMT, int PL>
 hipError_t launch_rows_p(const MoeArgs& a, int mt, int waves, hipStream_t s)
 {
-    return mt == 1 ? launch_rows_t<FMT, PL, 1>(a, waves, s) : mt == 2 ? launch_rows_t<FMT, PL, 2>(a, waves, s) : launch_rows_t<FMT, PL, 4>(a, waves, s);
+    if (mt == 1) return launch_rows_t<FMT, PL, 1>(a, waves, s);
+    if constexpr (PL == 1 && Unit<FMT>::UNIT == 128)
+        if (mt == 4) return launch_rows_t<FMT, PL, 4>(a, waves, s);
+    return launch_rows_t<FMT, PL, 2>(a, waves, s);
 }
 
 #define QMM_MOE_ROWS(NAME, FMT)                                                                                   \

@@ -9,8 +9,8 @@
 // use, and read by every wave; the next unit's weights are loaded while one is
 // multiplied.
 //
-// Measured: 4-bit 512 x 14336 x 4096 bf16 78 us (770 TF/s); GLU of Q4_K, 16384
-// pairs on 64 experts, 2 x 1024 x 2048, 270 us (510 TF/s).  Of the 4-bit call's
+// Measured: 4-bit 512 x 14336 x 4096 bf16 76 us (790 TF/s); GLU of Q4_K, 16384
+// pairs on 64 experts, 2 x 1024 x 2048, 260 us (530 TF/s).  Of the 4-bit call's
 // time the matrix cores are busy 37%, vector issue 36%, LDS 28%, and a wave
 // spends a third of its life issuing, a third waiting for a unit and the rest
 // waiting for data: two waves per SIMD, all that the registers allow, do not
