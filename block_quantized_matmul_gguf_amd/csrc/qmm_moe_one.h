@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * MAXW) void moe_one(MoeArgs a)
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    acc[t] = fmaf(weight, inv * d[0][t][0], acc[t]);
+                    acc[t] = fmaf(weight, unscaled<U::SHIFT>(d[0][t][0], inv), acc[t]);
                     cur[t] = next[t];
                 }
             }

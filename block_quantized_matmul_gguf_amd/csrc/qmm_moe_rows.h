@@ -130,8 +130,8 @@ __global__ __launch_bounds__(64 * ROWS_MAX_WAVES) void moe_rows(MoeArgs a)
             if constexpr (GLU) w += red[k][(m * NT + 1) * 256 + i];
         }
         const float inv = t.e < 0 ? 0.0f : a.xinv[t.start + at];
-        v *= inv;
-        if constexpr (GLU) v = t.e < 0 ? 0.0f : activate(v, a.act) * (w * inv);
+        v = unscaled<U::SHIFT>(v, inv);
+        if constexpr (GLU) v = t.e < 0 ? 0.0f : activate(v, a.act) * unscaled<U::SHIFT>(w, inv);
         const int64_t pair = a.ids ? a.order[t.start + at] : t.start + at;
         store_out<WIDE>(a.y, a.y_type, pair * a.N + nn, v);
     }

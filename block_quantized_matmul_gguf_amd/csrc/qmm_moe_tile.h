@@ -305,11 +305,11 @@ QMM_DEV void tile_body(const MoeArgs& a, const MoeTile& t, int64_t b, _Float16* 
                 const float f = __shfl(inv, 4 * g + i);
                 out_t* o = out + ((m - m0) * 16 + 4 * g + i) * BN + r;
                 if constexpr (GLU) {
-                    const float v = t.e < 0 ? 0.0f : activate(acc[m][0][i] * f, a.act) * (acc[m][1][i] * f);
+                    const float v = t.e < 0 ? 0.0f : activate(unscaled<U::SHIFT>(acc[m][0][i], f), a.act) * unscaled<U::SHIFT>(acc[m][1][i], f);
                     o[wave * 16] = rounded<WIDE>(a.y_type, v);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) o[wave * 32 + c * 16] = rounded<WIDE>(a.y_type, acc[m][c][i] * f);
+                    for (int c = 0; c < 2; ++c) o[wave * 32 + c * 16] = rounded<WIDE>(a.y_type, unscaled<U::SHIFT>(acc[m][c][i], f));
                 }
             }
         }

@@ -154,6 +154,7 @@ QMM_DEV void put_operand(_Float16* to, half8_t v)
 //   LOADS  load instructions of a unit, at least;  AREA  dwords of LDS to exchange in
 //   CHAIN  products of a step share one scale (and so one accumulator)
 //   PARTS  operands per product;  MINS  Q4_K's minima
+//   SHIFT  sums are 2^-SHIFT of what the row's factor makes outputs of
 //   o0, o1, slot: the k values of lane group g in product j of step h are
 //     o0 .. o0+3 and o1 .. o1+3; slot i of the operand holds number slot(i);
 //   put8   the inverse
@@ -164,7 +165,7 @@ struct Unit;
 
 template <int FMT>
 struct Unit32 {
-    static constexpr int UNIT = 128, HALVES = 1, PARTS = 1;
+    static constexpr int UNIT = 128, HALVES = 1, PARTS = 1, SHIFT = 0;
     static constexpr bool CHAIN = false, MINS = false;
     static QMM_DEV int o0(int, int j, int g) { return 32 * j + 4 * g; }
     static QMM_DEV int o1(int, int j, int g) { return 32 * j + 16 + 4 * g; }
@@ -355,7 +356,15 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
 };
 
 // Codes of W4 rows: eight neighbours per dword, lowest nibble first.
+//
+// Scales, of f32's range where they are f32 or bf16, multiply sums of
+// activations not yet scaled back: below 2^15 255 K, so below 2^43.  They enter
+// times 2^-43, which keeps sums of finite ones finite, and the outputs make up
+// for it (unscaled).  That is exact but for scales below 2^-83, which lose what
+// is under 2^-107.
 struct UnitW4 {
+    static constexpr int SHIFT = 43;
+    static constexpr float DOWN = 0x1p-43f;
     static QMM_DEV int o0(int, int j, int g) { return 32 * j + 8 * g; }
     static QMM_DEV int o1(int, int j, int g) { return 32 * j + 8 * g + 4; }
     static QMM_DEV int slot(int i) { return (i >> 1) | ((i & 1) << 2); }
@@ -382,8 +391,8 @@ struct UnitW4 {
     template <bool S32>
     static QMM_DEV float scale_value(const MoeMatrix& m, scale_t<S32> d)
     {
-        if constexpr (S32) return f32_of(d);
-        return m.scale_type == TYPE_F16 ? f16lo(d) : f32_of((uint32_t)d << 16);
+        if constexpr (S32) return f32_of(d) * DOWN;
+        return (m.scale_type == TYPE_F16 ? f16lo(d) : f32_of((uint32_t)d << 16)) * DOWN;
     }
 };
 
@@ -394,6 +403,7 @@ struct UnitW4Narrow : Unit32<FMT_W4> {
     uint8_t z;
     uint32_t c[4];
     half2_t bias[4];
+    static constexpr int SHIFT = UnitW4::SHIFT;
     static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
     static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
@@ -439,7 +449,7 @@ struct Unit<FMT_W4_S32> : UnitW4Narrow<true> {};
 // multiply-adds) and nothing is gathered.
 template <bool S32>
 struct UnitW4Wide {
-    static constexpr int UNIT = 128, HALVES = 1, PARTS = 1;
+    static constexpr int UNIT = 128, HALVES = 1, PARTS = 1, SHIFT = UnitW4::SHIFT;
     static constexpr bool CHAIN = true, MINS = false;
     static QMM_DEV int o0(int h, int j, int g) { return UnitW4::o0(h, j, g); }
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
@@ -490,7 +500,7 @@ struct Unit<FMT_W4_WIDE_S32> : UnitW4Wide<true> {};
 
 template <>
 struct Unit<FMT_Q4_K> {
-    static constexpr int UNIT = 256, HALVES = 2, PARTS = 1;
+    static constexpr int UNIT = 256, HALVES = 2, PARTS = 1, SHIFT = 0;
     static constexpr bool CHAIN = true, MINS = true;
     // lane group g: sub-blocks 2g (low nibbles, step 0) and 2g + 1 (high, step 1)
     static QMM_DEV int o0(int h, int j, int g) { return 64 * g + 32 * h + 8 * j; }
@@ -557,7 +567,7 @@ struct Unit<FMT_Q4_K> {
 
 template <>
 struct Unit<FMT_Q6_K> {
-    static constexpr int UNIT = 256, HALVES = 2, PARTS = 2;
+    static constexpr int UNIT = 256, HALVES = 2, PARTS = 2, SHIFT = 0;
     // its sums could share an accumulator over a step, but that takes more registers than there are
     static constexpr bool CHAIN = false, MINS = false;
     // lane group g: of half g >> 1 of the super-block, in each of its four
@@ -691,6 +701,16 @@ QMM_DEV void act_scale(float amax, float& s, float& inv)
     const int sb = min(268 - eb, 253);
     s = f32_of((uint32_t)sb << 23);
     inv = f32_of((uint32_t)(254 - sb) << 23);
+}
+
+// A sum as the outputs have it: scaled back by the row's factor inv (a power of
+// two), and by 2^SHIFT.  Together they may be past f32's range: one instruction
+// that adds to the exponent and rounds once.
+template <int SHIFT>
+QMM_DEV float unscaled(float sum, float inv)
+{
+    if constexpr (SHIFT == 0) return sum * inv;
+    return __builtin_ldexpf(sum, (int)(bits_of(inv) >> 23) - 127 + SHIFT);
 }
 
 // Eight scaled values (in operand order) as f16 parts.

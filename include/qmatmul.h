@@ -365,7 +365,8 @@ int qmatmul_experts_combine(int format, int64_t E, int64_t N, int64_t K, int64_t
  * q: device, N x K/2 bytes, element 2i in the low nibble of byte i and 2i + 1
  * in its high nibble, 16-byte aligned.  scales: device [N x K/group] of
  * scale_type (QMM_F32, QMM_F16 or QMM_BF16).  zeros: device uint8 [N x
- * K/group], 0..15 (other values are used as they are).  group: a multiple of
+ * K/group], 0..15 (other values are used as they are).  Scales may have any
+ * finite size; those below 2^-83 enter to 2^-107.  group: a multiple of
  * 32 that divides K; N and M at most 2^24, K at most 2^20, N * K / 2 at most
  * 2^40.  x (16-byte aligned) and y have the type `type`.  M >= 0; M == 0
  * enqueues nothing.  Sums, rounding, non-finite rows and the limit on a launch as
