@@ -108,7 +108,7 @@ __global__ __launch_bounds__(64 * MAXW) void moe_one(MoeArgs a)
                 for (int k = 0; k < 8; ++k) am = fmaxf(am, fabsf(v[c][k]));
             }
             float s, inv;
-            act_scale(wave_max(am), s, inv);
+            act_scale(wave_max(am), a.type, s, inv);
 #pragma unroll
             for (int c = 0; c < GROUPS; ++c) {
                 float sum = 0.0f;

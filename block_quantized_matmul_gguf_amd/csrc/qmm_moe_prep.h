@@ -251,7 +251,7 @@ __global__ __launch_bounds__(PREP_THREADS) void moe_prep(MoeArgs a, int tm, int 
     }
     if (!live) return;
     float s, inv;
-    act_scale(am, s, inv);
+    act_scale(am, a.type, s, inv);
     const int64_t dst = ROWS && a.ids ? place : row;
     if (sub == 0 && lane == 0) {
         a.xinv[dst] = inv;

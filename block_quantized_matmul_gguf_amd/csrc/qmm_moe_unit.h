@@ -690,15 +690,16 @@ struct Raw4 {
 };
 
 // The power of two that brings values of magnitude up to amax into f16's
-// range, the largest to [2^14, 2^15) (less where that would need a factor
-// above 2^126), and its inverse.  Scaled f16 parts then hold bf16 values
-// exactly and f32 values, as hi + lo, to 2^-22, but for values 2^-29 and more
-// below the largest, which are off by at most 2^-40 of it.  (An infinite amax
-// only has to leave its row non-finite.)
-QMM_DEV void act_scale(float amax, float& s, float& inv)
+// range, the largest to [2^14, 2^15), and its inverse; at most 2^126, and for
+// f16 values at least 1, which 65504 needs and their smallest do not survive
+// less of.  Scaled f16 parts then hold f16 values exactly, bf16 values as one
+// part and f32 values as hi + lo to 2^-22 of themselves or 2^-25, half of f16's
+// smallest step: 2^-39 of the largest (2^-151 at the factor 2^126).  (An
+// infinite amax only has to leave its row non-finite.)
+QMM_DEV void act_scale(float amax, int type, float& s, float& inv)
 {
     const int eb = (int)(bits_of(amax) >> 23);
-    const int sb = min(268 - eb, 253);
+    const int sb = max(min(268 - eb, 253), type == TYPE_F16 ? 127 : 14);
     s = f32_of((uint32_t)sb << 23);
     inv = f32_of((uint32_t)(254 - sb) << 23);
 }

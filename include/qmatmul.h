@@ -324,8 +324,8 @@ int qmatmul_route_experts(const void* logits, int type, int64_t T, int64_t E, co
  * [T x top_k]; an id outside 0..E-1 means no expert; the same id may come
  * twice in a row.  x, h and y have the type `type`; x and h 16-byte aligned.
  * Activations are not quantized (mode (a)): f16 ones enter as they are, bf16
- * and f32 ones to 2^-22 of themselves or 2^-40 of the largest magnitude in
- * their row, whichever is more.  Products are summed in f32 and each output is
+ * and f32 ones to 2^-22 of themselves, 2^-39 of the largest magnitude in their
+ * row or 2^-151, whichever is most.  Products are summed in f32 and each output is
  * rounded once, to `type`.
  *
  * qmatmul_experts_run: y[t][s] = x[t] . W[ids[t][s]]^T, y [T x top_k x N];

@@ -6,6 +6,7 @@ the output's type, and what the header states that activations and scales lose o
 import numpy as np
 import pytest
 
+import oracle
 import synth
 
 torch = pytest.importorskip("torch")
@@ -13,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 import block_quantized_matmul_gguf_amd as qmm  # noqa: E402
 
-from test_gpu_experts import BAR, TYPES, close, f64, w4_case  # noqa: E402
+from test_gpu_experts import BAR, FMTS, TYPES, close, f64, w4_case, weights_of  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -77,3 +78,101 @@ def test_w4_largest_scales_in_long_rows(m):
     want = -(f64(small).sum(1, keepdims=True) * 255.0 * f64(s)[0, 0]) * np.ones((1, n))
     assert (np.abs(want) < 3.0e38).all()
     close(qmm.w4_matmul(q, s, small.cuda(), zeros=z), want, (k / 32 + 64) * 2.0**-24 * np.abs(want), "long rows")
+
+
+def few_values(dtype, m, k, at, outlier, values):
+    """Rows that are zero but for an outlier at `at` and values[i % len] at element 7."""
+    x = torch.zeros((m, k), dtype=torch.float64)
+    x[:, at] = outlier
+    x[:, 7] = torch.tensor([values[i % len(values)] for i in range(m)], dtype=torch.float64)
+    t = x.to(TYPES[dtype])
+    assert torch.equal(t.double(), x)
+    return t.cuda(), x.numpy()
+
+
+def hollow(fmt, seed, n, k, at):
+    """Blocks of weights up to about 2^16 in which element `at` of every row is exactly zero."""
+    w = synth.weights_f32(seed, n, k) * np.float32(2.0**19)
+    w[:, at] = 0
+    b = oracle.quantize(fmt, w)
+    if fmt == qmm.Q4_K:  # without minima, and the code itself zero
+        b = b.reshape(n, -1, 144).copy()
+        b[:, :, 2:4] = 0
+        sub, i = at % 256 // 32, at % 32
+        b[:, at // 256, 16 + sub // 2 * 32 + i] &= 0x0F if sub % 2 else 0xF0
+        b = b.reshape(n, -1)
+    v = oracle.dequantize(fmt, b, k)
+    assert (v[:, at] == 0).all() and (v[:, 7] != 0).any()
+    return b, v
+
+
+def product(fmt, b, n, x, how):
+    """x . W^T through experts_matmul, or (combine) through experts_combine with weight 1."""
+    wd = torch.from_numpy(b.reshape(1, n, -1)).cuda()
+    ids = torch.zeros((len(x), 1), dtype=torch.int32).cuda()
+    if how == "combine":
+        return qmm.experts_combine(fmt, wd, x[:, None].contiguous(), ids, torch.ones((len(x), 1)).cuda())
+    return qmm.experts_matmul(fmt, wd, x, ids)[:, 0]
+
+
+SMALL = {
+    # what is lost of element 7 beside an outlier: nothing of an f16 value, else 2^-22 of it or 2^-39 of the outlier
+    "f16": [(60000.0, [2.0**-24, 3 * 2.0**-24, 5 * 2.0**-24, 1023 * 2.0**-24, 2.0**-14, 2047 * 2.0**-13]),
+            (65504.0, [2.0**-24, 7 * 2.0**-24]), (32768.0, [2.0**-24, 1025 * 2.0**-23]), (2.0**-14, [2.0**-24, 3 * 2.0**-24])],
+    "bf16": [(1.0, [2.0**-39, 2.0**-38, 255 * 2.0**-46, 129 * 2.0**-40, 171 * 2.0**-30]), (2.0**100, [2.0**61, 2.0**62, 2.0**70]),
+             (2.0**-110, [2.0**-126, 2.0**-130, 2.0**-133])],
+    "f32": [(1.0, [2.0**-39, 2.0**-38, 255 * 2.0**-46, 16777215 * 2.0**-50, 2.0**-20 + 2.0**-43]), (2.0**100, [2.0**61, 2.0**62 + 2.0**40]),
+            (1.9999998807907104, [2.0**-38, 3 * 2.0**-40]), (2.0**-115, [2.0**-126, 2.0**-140, 2.0**-149])],
+}
+
+
+@pytest.mark.parametrize("how", ["run", "combine"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("fmt", list(FMTS) + ["W4"])
+@pytest.mark.parametrize("m", [1, 60, 1500])
+def test_a_small_value_beside_an_outlier_of_weight_zero(fmt, dtype, m, how):
+    """Each value by itself: f16 activations enter as they are, others to 2^-22 of themselves, 2^-39 of
+    their row's largest or 2^-151."""
+    k, n, at = 256, 1030 if how == "run" else 40, 100
+    if fmt == "W4":
+        if how == "combine":
+            pytest.skip("4-bit groups have no combine")
+        q, s, z, _ = w4_case(320, n, k, 64, False, torch.float32)
+        s = s * 2.0**20
+        q[:, 50] = 0x88
+        qh = q.cpu().numpy()
+        w = (np.stack([qh & 15, qh >> 4], -1).reshape(n, k).astype(np.float64) - 8) * np.repeat(f64(s), 64, 1)
+    else:
+        b, w = hollow(FMTS[fmt], 321, n, k, at)
+    for outlier, values in SMALL[dtype]:
+        x, xh = few_values(dtype, m, k, at, outlier, values)
+        y = qmm.w4_matmul(q, s, x) if fmt == "W4" else product(FMTS[fmt], b, n, x, how)
+        v = np.abs(xh[:, 7:8])
+        lost = 0 * v if dtype == "f16" else np.maximum(np.maximum(2.0**-22 * v, 2.0**-39 * outlier), 2.0**-151)
+        close(y, xh[:, 7:8] * w[None, :, 7], (lost + BAR * v) * np.abs(w[None, :, 7]), f"{outlier} {values}")
+
+
+@pytest.mark.parametrize("fmt", list(FMTS) + ["W4"])
+@pytest.mark.parametrize("m", [1, 60, 1500])
+def test_rows_of_the_largest_half(fmt, m):
+    """Rows of 65504 throughout, of either sign, in every sub-block sum the largest there is."""
+    k, n = 512, 1030
+    x = torch.full((m, k), 65504.0, dtype=torch.float16)
+    x[1::3] *= -1
+    x[2::3, ::2] *= -1
+    xh = x.double().numpy()
+    if fmt == "W4":
+        q, s, z, _ = w4_case(330, n, k, 64, True, torch.float16)
+        s, qh = s.float() * 2.0**-10, q.cpu().numpy()
+        codes = np.stack([qh & 15, qh >> 4], -1).reshape(n, k).astype(np.float64) - np.repeat(f64(z), 64, 1)
+        w = codes * np.repeat(f64(s), 64, 1)
+        y, wa = qmm.w4_matmul(q, s, x.cuda(), zeros=z), np.abs(w)
+    else:
+        b, w, wa = weights_of(FMTS[fmt], 331, n, k)
+        y = product(FMTS[fmt], b, n, x.cuda(), "run")
+    want, a = xh @ w.T, np.abs(xh) @ wa.T
+    fits = np.abs(want) + BAR * a < 65504
+    assert fits.any()
+    got = f64(y)
+    assert np.isfinite(got[fits]).all()
+    assert (np.abs(got - want) <= BAR * a + 2.0**-11 * (np.abs(want) + BAR * a) + 2.0**-25)[fits].all()
