@@ -469,9 +469,10 @@ def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups:
     Scores are softmax or sigmoid of the logits; the choice is by score + bias
     (float32 [E]), within the ``top_groups`` best of ``groups`` groups of
     neighbouring experts (a group's score: the sum of its ``group_top`` best
-    choices), ties to the lower index.  Experts with a -inf or NaN logit are
-    never chosen; slots left over have id -1 and weight 0.  Weights are the
-    scores, divided by their sum if ``renormalize``, times ``scale``."""
+    choices), ties to the lower index.  Experts with a -inf or NaN logit or bias
+    are never chosen; slots left over have id -1 and weight 0.  Weights are the
+    scores, divided by their sum if ``renormalize``, times ``scale``; a bias
+    does not change the scores, softmax's sum included."""
     torch = _torch()
     _tensor(logits, None, (2,), "logits")
     code = _type_of(logits, "logits")

@@ -299,8 +299,10 @@ int qmatmul_run_block_sums(const qmm_plan* plan, const void* w_blocks, const flo
  * Choose experts: per row of logits [T x E] (type QMM_F32, QMM_F16 or
  * QMM_BF16; any alignment of that type), the top_k experts and their weights.
  *   s = softmax(logits) or sigmoid(logits); choice c = s + bias (bias: device
- *   f32 [E] or NULL).  An expert whose logit or c is NaN or -inf is masked: it
- *   has no score and is never chosen.
+ *   f32 [E] or NULL).  An expert whose logit is NaN or -inf has no score (0,
+ *   softmax's sum is without it); one whose c is NaN or -inf, by its logit or
+ *   its bias, is masked: never chosen, and no part of a group's score.  A bias
+ *   takes part in the choice alone: s is the same whatever it holds.
  *   groups > 1 (a divisor of E, at most 64): experts form that many groups of
  *   neighbours; a group's score is the sum of its group_top (1 or 2) largest
  *   c; only the top_groups best groups (ties: the lower index) stay.

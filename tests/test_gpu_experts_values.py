@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 import block_quantized_matmul_gguf_amd as qmm  # noqa: E402
 
-from test_gpu_experts import BAR, FMTS, TYPES, close, f64, w4_case, weights_of  # noqa: E402
+from test_gpu_experts import BAR, FMTS, TYPES, close, f64, route_ref, w4_case, weights_of  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -176,3 +176,34 @@ def test_rows_of_the_largest_half(fmt, m):
     got = f64(y)
     assert np.isfinite(got[fits]).all()
     assert (np.abs(got - want) <= BAR * a + 2.0**-11 * (np.abs(want) + BAR * a) + 2.0**-25)[fits].all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("t,e,k,groups,tg,gt", [
+    (1, 8, 3, 1, 1, 1), (9, 64, 64, 1, 1, 1), (33, 160, 6, 8, 3, 2), (5, 96, 20, 32, 5, 1), (4, 1024, 64, 64, 10, 2), (3, 7, 7, 7, 3, 2),
+])
+def test_route_with_biases_that_are_not_finite(dtype, score, renorm, t, e, k, groups, tg, gt):
+    """A bias of -inf or NaN takes its expert out of the choice and out of its group's score; one of +inf
+    puts it first.  The scores, softmax's sum among them, are of the logits alone."""
+    print(f"route {dtype} {score} renorm={renorm} T={t} E={e} k={k} groups={groups}/{tg}/{gt}", flush=True)
+    g = np.random.default_rng(340 + e)
+    l = g.standard_normal((t, e)) * 2
+    l[:, 3] = 9.0  # most of the weight, and out of the choice
+    l[-1, 1::3] = -np.inf
+    x = torch.from_numpy(l.astype(np.float32)).to(TYPES[dtype])
+    b = (0.1 * g.standard_normal(e)).astype(np.float32)
+    b[g.random(e) < 0.2] = -np.inf
+    b[g.random(e) < 0.1] = np.nan
+    b[3] = -np.inf
+    b[5] = np.inf
+    if groups > 1:
+        b[:e // groups] = np.nan  # a group of which nothing is left
+    for bias in (b, np.full(e, -np.inf, np.float32), np.full(e, np.nan, np.float32)):
+        ids, w = qmm.route_experts(x.cuda(), k, score, torch.from_numpy(bias).cuda(), groups, tg, gt, renorm, 1.5)
+        ri, rw = route_ref(x.double().numpy(), k, score, bias, groups, tg, gt, renorm, 1.5)
+        assert np.array_equal(ids.cpu().numpy(), ri)
+        assert np.all(np.abs(f64(w) - rw) <= 2.0**-24 * (1 + 2.0**-20) * np.abs(rw) + 2.0**-150)
+        if not np.isfinite(bias).any():
+            assert (ids == -1).all() and (w == 0).all()
