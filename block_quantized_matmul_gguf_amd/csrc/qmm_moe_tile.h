@@ -231,7 +231,9 @@ QMM_DEV void tile_body(const MoeArgs& a, const MoeTile& t, int64_t b, _Float16* 
         };
         // Loads and copies are issued in every step, past the last one again for it, so that their
         // number in flight is known, and both two steps before their use.  Operations retire in order:
-        // once no more are outstanding than the step before issued, all earlier ones have landed.
+        // once no more are outstanding than the step before issued, all earlier ones have landed.  So a
+        // wait's count may be less than that number (a longer wait) and never more: LOADS is what no
+        // compiler gets below, and tests/test_tile_waits_cpu.py counts both in the built kernels.
         int operand_at[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) operand_at[j] = r * 128 + ((j * 4 + g) ^ r) * 8;

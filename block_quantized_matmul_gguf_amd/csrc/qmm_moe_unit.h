@@ -125,6 +125,11 @@ QMM_DEV half8_t join8(half2_t a, half2_t b, half2_t c, half2_t d)
     return r;
 }
 
+// The fewest instructions that load this many neighbouring bytes per lane,
+// however the compiler joins or cuts the loads that ask for them: one brings 16
+// bytes at most.
+constexpr int loads_of(int bytes) { return (bytes + 15) / 16; }
+
 // A weight matrix as a wave reads it: what is common to its rows.
 struct MoeMatrix {
     const uint8_t* w;
@@ -151,7 +156,8 @@ QMM_DEV void put_operand(_Float16* to, half8_t v)
 // Per format:
 //   UNIT   values of a unit;  HALVES  steps of 128 values in it
 //   load   of row n: lane quarter q's words;  unpack  the exchange, and scales
-//   LOADS  load instructions of a unit, at least;  AREA  dwords of LDS to exchange in
+//   LOADS  load instructions of a unit, at least (loads_of): the tile kernel counts on them
+//   AREA   dwords of LDS to exchange in
 //   CHAIN  products of a step share one scale (and so one accumulator)
 //   PARTS  operands per product;  MINS  Q4_K's minima
 //   SHIFT  sums are 2^-SHIFT of what the row's factor makes outputs of
@@ -217,7 +223,7 @@ struct Unit<FMT_Q8_0> : Unit32<FMT_Q8_0> {
     uint32_t d, c[8];
     Aligned at;
     static QMM_DEV int slot(int i) { return i; }
-    static constexpr int LOADS = 3, AREA = 2 * WORD_AREA + ROW_AREA;
+    static constexpr int LOADS = loads_of(36), AREA = 2 * WORD_AREA + ROW_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const uint8_t* p = at.start(m.w + n * m.row_bytes + block_of(m, u, q) * 34);
@@ -268,7 +274,7 @@ struct Unit<FMT_Q4_0> : Unit32<FMT_Q4_0> {
     uint32_t d, c[4];
     Aligned at;
     static QMM_DEV int slot(int i) { return nib_perm(i); }
-    static constexpr int LOADS = 2, AREA = WORD_AREA + ROW_AREA;
+    static constexpr int LOADS = loads_of(20), AREA = WORD_AREA + ROW_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const uint8_t* p = at.start(m.w + n * m.row_bytes + block_of(m, u, q) * 18);
@@ -310,7 +316,7 @@ struct Unit<FMT_Q5_0> : Unit32<FMT_Q5_0> {
     uint32_t c[4], h[4];
     Aligned at;
     static QMM_DEV int slot(int i) { return nib_perm(i); }
-    static constexpr int LOADS = 2, AREA = WORD_AREA + 2 * ROW_AREA;
+    static constexpr int LOADS = loads_of(24), AREA = WORD_AREA + 2 * ROW_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const uint8_t* p = at.start(m.w + n * m.row_bytes + block_of(m, u, q) * 22);
@@ -408,7 +414,8 @@ struct UnitW4Narrow : Unit32<FMT_W4> {
     static QMM_DEV int o1(int h, int j, int g) { return UnitW4::o1(h, j, g); }
     static QMM_DEV int slot(int i) { return UnitW4::slot(i); }
     static QMM_DEV void put8(_Float16* x, int k, half8_t v) { UnitW4::put8(x, k, v); }
-    static constexpr int LOADS = 3, AREA = WORD_AREA + 2 * ROW_AREA;
+    // codes, scale and zero point come from three arrays
+    static constexpr int LOADS = loads_of(16) + 2, AREA = WORD_AREA + 2 * ROW_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const int b = block_of(m, u, q);
@@ -461,7 +468,7 @@ struct UnitW4Wide {
     uint32_t c[4];
     float s;
     half2_t lo, hi;
-    static constexpr int LOADS = 3, AREA = WORD_AREA + 2 * ROW_AREA;
+    static constexpr int LOADS = loads_of(16) + 2, AREA = WORD_AREA + 2 * ROW_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         r0 = *(const u32x4_t*)(m.w + n * m.row_bytes + 64 * u + 16 * q);
@@ -513,7 +520,7 @@ struct Unit<FMT_Q4_K> {
     u32x4_t hd, r0, r1;
     half2_t sc[2], off[2];  // sub-block scale and -1024 times it; the second's / 16 and -64 times it
     uint32_t mn;            // the two minima, one per byte
-    static constexpr int LOADS = 3, AREA = 3 * WORD_AREA;
+    static constexpr int LOADS = loads_of(48), AREA = 3 * WORD_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 144;
@@ -589,7 +596,8 @@ struct Unit<FMT_Q6_K> {
     u32x2_t sc;
     uint32_t d;
     half2_t hi[4], lo[4];  // 16 s1 and s0 of the four quarters' scales
-    static constexpr int LOADS = 5, AREA = 4 * WORD_AREA;
+    // three words of 16 bytes, scales and d, no two of them at a fixed distance of 16 bytes or less
+    static constexpr int LOADS = 3 * loads_of(16) + 2, AREA = 4 * WORD_AREA;
     QMM_DEV void load(const MoeMatrix& m, int64_t n, int u, int q)
     {
         const uint8_t* p = m.w + n * m.row_bytes + (int64_t)u * 210;
