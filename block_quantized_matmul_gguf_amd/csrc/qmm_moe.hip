@@ -14,7 +14,7 @@ namespace {
 
 // y[t][n] = sum over the slots with an expert of weights[t][s] * prod[t][s][n].
 // V (4 or 1) outputs per thread; rows of outputs along the grid's y.  Bound by
-// the products' bytes: 98 MB (12000 x 2048) 17 us, 5.8 TB/s.
+// the products' bytes: 98 MB (12000 x 2048) 16 us, 6.1 TB/s.
 template <int V>
 __global__ __launch_bounds__(256) void moe_combine(MoeArgs a, const float* prod)
 {
@@ -85,19 +85,22 @@ MoePlan plan_of(const MoeArgs& a)
     // has more of them in flight (glu Q4_K, 64 experts, bf16: 8 pairs of an expert 59 us against 64 us,
     // 12 pairs 68 us against 71 us, 16 pairs 78 us against 75 us; f32: 78 us against 75 us, 105 us
     // against 88 us at 8 and 16).  Few tiles: the tile kernel leaves compute units idle.  That is
-    // counted in tiles of 32 rows times weight rows, 40000 being half of what fills the chip (Q5_0, 8
-    // experts, N 1536: 400 pairs 28 us against 38 us, 800 pairs 39 us against 40 us; 4-bit, N 8192: 128
-    // rows 21 us against 25 us, 192 rows 29 us against 26 us), less with the 256-value formats, which
-    // the tile kernel decodes in fewer instructions (Q4_K, N 1536: 200 pairs 18 us against 23 us, 400
-    // pairs 26 us against 24 us).  Every row counts its place among the pairs, so there may not be many
-    // of them (256 experts: 512 pairs 30 us against 34 us, 1024 36 us against 35 us, 2048 49 us against 40 us).
+    // counted in tiles of 32 rows times weight rows, of which 256 x 256 would give every compute unit a
+    // workgroup; 40000 is where the two kernels meet (Q5_0, 8 experts, N 1536: 400 pairs 28 us against
+    // 38 us, 800 pairs 39 us against 40 us; 4-bit, N 8192: 128 rows 21 us against 25 us, 192 rows 29 us
+    // against 26 us), less with the 256-value formats, which the tile kernel decodes in fewer
+    // instructions (Q4_K, N 1536: 200 pairs 18 us against 23 us, 400 pairs 26 us against 24 us).  Neither
+    // K nor f32's two parts enter, and other formats were not measured for it.  Every row counts its
+    // place among the pairs, so there may not be many of them (256 experts: 512 pairs 30 us against 34
+    // us, 1024 36 us against 35 us, 2048 49 us against 40 us).
     const int64_t half = dense ? 0 : std::min<int64_t>(a.E, P) / 2;  // tiles that are not full
     const int64_t columns = a.N * (a.op == MOE_GLU ? 2 : 1);
     const bool few = avg <= (dense ? 16 : 11) || ((P + 31) / 32 + half) * columns <= (unit == 256 ? 22000 : 40000);
     if (p.path != PATH_ONE) p.path = few && (dense || P <= 1024) ? PATH_ROWS : PATH_TILE;
     if (p.path == PATH_ROWS) {
         // one more row group costs little, decoding the weights again a lot; four groups of the
-        // 256-value formats or of f32's two parts do not fit in registers
+        // 256-value formats or of f32's two parts do not fit in registers (nor, by 36, which are then
+        // loaded again in every unit, do two of Q6_K's with f32's)
         p.mt = avg <= 16 ? 1 : avg <= 32 || f32 || unit == 256 ? 2 : 4;
     } else if (p.path == PATH_TILE) {
         // A row tile of 16 mt rows costs about 5 + mt (4-bit, 14336 x 4096, one round of workgroups: 45,

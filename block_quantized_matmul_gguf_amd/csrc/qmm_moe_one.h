@@ -10,10 +10,12 @@
 // their way; every operand row then holds that one row.  Without barriers in
 // the loop the waves of a compute unit drift apart and keep its loads going.
 //
-// Measured: 4-bit 14336 x 4096, one row: 9.4 us (3.2 TB/s, launch included);
-// GLU of Q4_K, one token on 8 experts of 2 x 1024 x 2048: 8.4 us; combine of
-// Q6_K, one token on 8 experts of 2048 x 1024: 9.9 us, of which the launch and
-// the chain id - weights - sums are more than the bytes (2.9 us).
+// Measured (a replayed graph; weights in the last-level cache, in brackets from
+// HBM): 4-bit 14336 x 4096, one row: 9.9 us (11.8; 3.1 and 2.6 TB/s, launch
+// included); GLU of Q4_K, one token on 8 experts of 2 x 1024 x 2048: 6.6 us
+// (8.4); combine of Q6_K, one token on 8 experts of 2048 x 1024: 8.7 us (9.6), of
+// which the launch and the chain id - weights - sums are more than the bytes
+// (2.9 us).
 #pragma once
 #include "qmm_moe_unit.h"
 

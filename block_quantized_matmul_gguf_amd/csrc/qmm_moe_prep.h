@@ -16,9 +16,9 @@
 // pairs with a lower expert or the same one and a lower index, counted by the
 // row's own waves, which also write order[].
 //
-// Measured: 512 rows of 4096 bf16 8 us, of which the launch is 3; 16384 pairs
-// and 2048 rows of 2048 17 us, the sort being the longest block (the rows alone
-// 8 us): a chain of one compute unit's loads, atomics, sums and stores.
+// Measured: 512 rows of 4096 bf16 7 us, of which the launch is 3; 16384 pairs
+// and 2048 rows of 2048 12.5 us (16 after a pause), the sort being the longest
+// block (the rows alone 8 us): a chain of one compute unit's loads, atomics, sums and stores.
 #pragma once
 #include "qmm_moe_unit.h"
 

@@ -9,8 +9,9 @@
 // the matrix cores; the activations, prepared once per call so that an
 // operand's lanes read neighbouring bytes, come from L2.
 //
-// Measured: Q8_0, 76 pairs on 32 experts of 1536 x 576, f32: 11.5 us after 5.8
-// us of preparation; Q5_0, 614 pairs on 8 experts of 1536 x 1536, f32: 26 us,
+// Measured: Q8_0, 76 pairs on 32 experts of 1536 x 576, f32: 10.6 us after 5.2
+// us of preparation, two waves a workgroup each waiting for its own loads; Q5_0,
+// 614 pairs on 8 experts of 1536 x 1536, f32: 25 us,
 // bound by decoding each weight for 32 rows at a time; 4-bit, 64 rows of 14336
 // x 4096, bf16: 29 us in all.  Waves that bring raw rows into operand order
 // themselves save the preparation's launch and lose more to its repetition

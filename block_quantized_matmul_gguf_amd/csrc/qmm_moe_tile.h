@@ -9,12 +9,15 @@
 // use, and read by every wave; the next unit's weights are loaded while one is
 // multiplied.
 //
-// Measured: 4-bit 512 x 14336 x 4096 bf16 76 us (790 TF/s); GLU of Q4_K, 16384
-// pairs on 64 experts, 2 x 1024 x 2048, 260 us (530 TF/s).  Of the 4-bit call's
-// time the matrix cores are busy 37%, vector issue 36%, LDS 28%, and a wave
-// spends a third of its life issuing, a third waiting for a unit and the rest
-// waiting for data: two waves per SIMD, all that the registers allow, do not
-// cover each other's chains.  Measured without gain: one barrier per two steps,
+// Measured (traced, 300 calls in a row, weights in the last-level cache): 4-bit
+// 512 x 14336 x 4096 bf16 69 us (875 TF/s; the first calls after a pause 73 to
+// 78), GLU of Q4_K, 16384 pairs on 64 experts, 2 x 1024 x 2048, 222 us (620 TF/s;
+// the first 245).  On the 224 compute units that the 4-bit call keeps, matrix
+// cores are busy 38% of the time, vector issue 41%, LDS 28%, and a wave spends a
+// third of its life issuing, a third waiting for a unit and the rest waiting for
+// data: two waves per SIMD, all that the registers allow, do not cover each
+// other's chains.  (The 16-bit Q4_K kernels keep two or three registers in
+// memory, outside the loop.)  Measured without gain: one barrier per two steps,
 // the weights' exchange a step ahead, operands read further ahead.  Four waves
 // of 64 weight rows, one per SIMD, halve the LDS reads and leave nothing to
 // fill a wave's waits: 107 and 403 us.

@@ -11,9 +11,9 @@
 // sorts its keys once, a round compares the lanes' best only, in two 32-bit
 // halves (a maximum across lanes is one instruction per exchange then), the
 // lower ones only where several lanes share the upper, and the winner moves on
-// to its next.  Measured: 1 x 64 2.9 us (an empty launch is as long), 333 x 160
-// in groups 6.9 us, 8192 x 256 with bias and groups 18 to 19 us, of which 9 MB
-// at the rate of a copy would be 2.
+// to its next.  Measured (a replayed graph): 1 x 64 2.9 us (an empty launch is
+// as long), 333 x 160 in groups 5.9 us, 8192 x 256 with bias and groups 17 to 18
+// us, of which 9 MB at the rate of a copy would be 2.
 #include <hip/hip_runtime.h>
 
 #include "../../include/qmatmul.h"
