@@ -374,6 +374,7 @@ def dequantize_weights(fmt: int, w, n: int, k: int, out=None, stream=None):
 # overlap on different streams and be captured in graphs that run side by side.
 # As with torch's own work on a second stream, the caller has that stream wait
 # for inputs made on another, and keeps them until it is done with them.
+# An output that the caller gives must not overlap an input (QmmError).
 
 F32, F16, BF16 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}

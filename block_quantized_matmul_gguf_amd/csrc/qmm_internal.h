@@ -159,4 +159,15 @@ int run_on_scratch(int format, int64_t N, int64_t K, int64_t M, int mode, const 
                    void* scratch, size_t scratch_bytes, void* stream, bool dry_run);
 int set_error(int code, const char* msg);
 
+// An argument's memory (null: none), and whether two of them share a byte.
+struct MemRange {
+    const void* p;
+    int64_t bytes;
+};
+inline bool overlap(const MemRange& a, const MemRange& b)
+{
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x <= y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes);
+}
+
 }  // namespace qmm

@@ -229,11 +229,26 @@ int64_t workspace_bytes(const MoeArgs& a)
     return (int64_t)p.bytes;
 }
 
+// Whether what the call writes (y, and its part of ws) lies apart from what it
+// reads and from each other: workgroups write while others still read.
+bool outputs_apart(const MoeArgs& a, const void* ws, size_t ws_bytes)
+{
+    const int64_t P = a.T * a.top_k, matrix = a.E * a.N * a.row_bytes, size = type_bytes(a.type);
+    const int64_t groups = a.group_blocks ? a.N * (a.K / 32 / a.group_blocks) : 0;
+    const MemRange y = {a.y, (a.op == MOE_COMBINE ? a.T : P) * a.N * size}, w = {ws, (int64_t)ws_bytes};
+    const MemRange reads[] = {{a.w0, matrix}, {a.w1, matrix}, {a.scales, groups * type_bytes(a.scale_type)}, {a.zeros, groups},
+                              {a.x, (a.per_slot ? P : a.T) * a.K * size}, {a.ids, P * 4}, {a.weights, P * 4}};
+    for (const MemRange& r : reads)
+        if (overlap(y, r) || overlap(w, r)) return false;
+    return !overlap(y, w);
+}
+
 int run(const MoeArgs& a, void* ws, size_t ws_bytes, void* stream)
 {
     const MoePlan p = plan_of(a);
     if (!p.launchable) return bad("shape too large");
     if (p.bytes > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < p.bytes)) return bad("ws must be 16-byte aligned and hold the call's workspace bytes");
+    if (!outputs_apart(a, ws, p.bytes)) return bad("outputs and ws must not overlap inputs or each other");
     const hipError_t e = launch_moe(a, p, (char*)ws, (hipStream_t)stream);
     return e == hipSuccess ? QMM_OK : set_error(QMM_EHIP, hipGetErrorString(e));
 }

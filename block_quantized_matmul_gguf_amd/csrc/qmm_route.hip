@@ -286,6 +286,10 @@ extern "C" int qmatmul_route_experts(const void* logits, int type, int64_t T, in
     if (!logits || !ids || !weights) return bad("null pointer");
     if ((uintptr_t)logits % (type == QMM_F32 ? 4 : 2) || (uintptr_t)bias % 4 || (uintptr_t)ids % 4 || (uintptr_t)weights % 4)
         return bad("misaligned pointer");
+    const MemRange out[] = {{ids, T * top_k * 4}, {weights, T * top_k * 4}};
+    const MemRange in[] = {{logits, T * E * (type == QMM_F32 ? 4 : 2)}, {bias, E * 4}, out[0]};
+    if (overlap(out[0], in[0]) || overlap(out[0], in[1]) || overlap(out[1], in[0]) || overlap(out[1], in[1]) || overlap(out[1], in[2]))
+        return bad("ids and weights must not overlap the inputs or each other");
     RouteArgs a;
     a.logits = logits;
     a.bias = bias;

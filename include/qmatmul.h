@@ -313,7 +313,8 @@ int qmatmul_run_block_sums(const qmm_plan* plan, const void* w_blocks, const flo
  *   id is -1.
  * Scores, sums and comparisons are carried in 64 bits; weights are rounded
  * once, to f32.  1 <= top_k <= 64, top_k <= E <= 1024, 0 <= T <= 2^24.  A +inf logit
- * gives softmax its limit: the +inf experts share the whole weight.
+ * gives softmax its limit: the +inf experts share the whole weight.  ids and
+ * weights must not overlap the inputs or each other (QMM_EINVAL).
  */
 int qmatmul_route_experts(const void* logits, int type, int64_t T, int64_t E, const float* bias, int score,
                           int top_k, int groups, int top_groups, int group_top, int renormalize, float scale,
@@ -345,7 +346,8 @@ int qmatmul_route_experts(const void* logits, int type, int64_t T, int64_t E, co
  * Limits: E <= 1024, top_k <= 64, T * top_k <= 2^24, N <= 2^24, and
  * qmatmul_create's limit on K; QMM_EINVAL ("shape too large") also where a
  * launch would need 2^32 threads (2^22 rows with K > 8192, or 2^23 tiles of
- * outputs).  T == 0 enqueues nothing.  Outputs must not overlap inputs.
+ * outputs).  T == 0 enqueues nothing.  Outputs and ws must not overlap inputs or
+ * each other (QMM_EINVAL).
  */
 int64_t qmatmul_experts_workspace_bytes(int product, int format, int64_t E, int64_t N, int64_t K, int64_t T,
                                         int64_t top_k, int type); /* -1 if invalid */
@@ -371,8 +373,8 @@ int qmatmul_experts_combine(int format, int64_t E, int64_t N, int64_t K, int64_t
  * finite size; those below 2^-83 enter to 2^-107.  group: a multiple of
  * 32 that divides K; N and M at most 2^24, K at most 2^20, N * K / 2 at most
  * 2^40.  x (16-byte aligned) and y have the type `type`.  M >= 0; M == 0
- * enqueues nothing.  Sums, rounding, non-finite rows and the limit on a launch as
- * with qmatmul_experts_run.
+ * enqueues nothing.  Sums, rounding, non-finite rows, the limit on a launch and
+ * overlaps as with qmatmul_experts_run.
  */
 int64_t qmatmul_w4_workspace_bytes(int64_t N, int64_t K, int64_t M, int64_t group, int type); /* -1 if invalid */
 int qmatmul_w4_run(int64_t N, int64_t K, int64_t M, int64_t group, int type, int scale_type, const void* q,
