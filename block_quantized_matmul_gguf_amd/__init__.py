@@ -36,6 +36,15 @@ LIB_PATH = os.path.join(_HERE, "libqmatmul.so")
 
 _p, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 
+class CacheStruct(ctypes.Structure):
+    """``qmm_cache`` of the header."""
+    _fields_ = [("format_k", _int), ("format_v", _int), ("pages", _i64), ("page_size", _i64), ("heads", _i64), ("dim", _i64),
+                ("k", _p), ("v", _p), ("batch", _i64), ("table_width", _i64), ("table", _p), ("starts", _p),
+                ("lengths", _p)]
+
+
+_cache_p = ctypes.POINTER(CacheStruct)
+
 # name: (restype, argtypes) for every symbol the header declares
 SIGNATURES = {
     "qmatmul_create": (_int, [ctypes.POINTER(_p), _int, _i64, _i64, _i64, _int]),
@@ -57,6 +66,11 @@ SIGNATURES = {
     "qmatmul_experts_combine": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
     "qmatmul_w4_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64, _int]),
     "qmatmul_w4_run": (_int, [_i64, _i64, _i64, _i64, _int, _int, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
+    "qmatmul_cache_store": (_int, [_cache_p, _i64, _int, _p, _i64, _p, _i64, _p]),
+    "qmatmul_cache_load": (_int, [_cache_p, _i64, _int, _p, _p, _p]),
+    "qmatmul_cache_attention_workspace_bytes": (_i64, [_cache_p, _i64, _i64, _int, _int, _i64, _i64]),
+    "qmatmul_cache_attention": (_int, [_cache_p, _i64, _i64, _int, _p, _i64, ctypes.c_float, _int, _i64, ctypes.c_float,
+                                       _i64, _p, _p, _p, ctypes.c_size_t, _p]),
     "qmatmul_check": (_int, [_int, _i64, _i64, _i64, _int]),
     "qmatmul_row_bytes": (_i64, [_int, _i64]),
     "qmatmul_block_sums_per_row": (_i64, [_int, _i64]),
@@ -615,5 +629,139 @@ def w4_matmul(q, scales, x, zeros=None, y=None, stream=None):
                                     None if zeros is None else zeros.data_ptr(), x.data_ptr(), out.data_ptr(), ws, nb, s),
                "qmatmul_w4_run")
         return out
+
+    return _on_device(dev, stream, body)
+
+
+# ------------------------------------------- quantized cache, attention ----
+#
+# Streams, scratch and outputs as with the experts' calls above.
+
+def _cache_args(fmt_k, fmt_v, k_cache, v_cache, table, starts, lengths):
+    """Checks a cache and a batch; their ``qmm_cache``."""
+    torch = _torch()
+    _tensor(k_cache, torch.uint8, (4,), "k_cache")
+    dev = k_cache.device
+    _tensor(v_cache, torch.uint8, (4,), "v_cache", dev)
+    for t, dims, name in ((table, (2,), "table"), (starts, (1,), "starts"), (lengths, (1,), "lengths")):
+        _tensor(t, torch.int32, dims, name, dev)
+    pages, heads, page_size, rk = k_cache.shape
+    block = BLOCK_BYTES.get(fmt_k)
+    if fmt_k not in (Q8_0, Q4_0) or fmt_v not in (Q8_0, Q4_0):
+        raise ValueError(f"cache formats are Q8_0 and Q4_0, got {fmt_k} and {fmt_v}")
+    if rk == 0 or rk % block:
+        raise ValueError(f"k_cache must be [pages, heads, page size, row bytes], got {tuple(k_cache.shape)}")
+    dim = rk // block * 32
+    want = (pages, heads, page_size, dim // 32 * BLOCK_BYTES[fmt_v])
+    if tuple(v_cache.shape) != want:
+        raise ValueError(f"v_cache must have shape {want}, got {tuple(v_cache.shape)}")
+    batch, width = table.shape
+    if starts.shape[0] != batch + 1 or lengths.shape[0] != batch:
+        raise ValueError(f"for {batch} sequences starts must be [{batch + 1}] and lengths [{batch}], got "
+                         f"{tuple(starts.shape)} and {tuple(lengths.shape)}")
+    return CacheStruct(fmt_k, fmt_v, pages, page_size, heads, dim, k_cache.data_ptr(), v_cache.data_ptr(), batch, width,
+                       table.data_ptr(), starts.data_ptr(), lengths.data_ptr())
+
+
+def _token_rows(t, heads, dim, name, device):
+    """Checks a tensor of tokens [T, heads (None: any), dim], contiguous but for
+    the step from token to token; (T, heads, that step, type)."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the GPU of the cache, {device}, got {t.device}")
+    code = _type_of(t, name)
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}], got {tuple(t.shape)}")
+    n, h, _ = t.shape
+    step, across, along = t.stride()
+    if n == 0:
+        return n, h, h * dim, code
+    if along != 1 or (h > 1 and across != dim):
+        raise ValueError(f"{name} must be contiguous within a token, got strides {t.stride()}")
+    return n, h, h * dim if n == 1 else step, code
+
+
+def cache_store(fmt_k: int, fmt_v: int, k_cache, v_cache, k, v, table, starts, lengths, stream=None):
+    """Quantizes the tokens' keys and values k, v (float32, float16 or bfloat16
+    [T, heads, dim], of one type; the step from token to token is free) into the
+    pages of their sequences, in place.
+
+    k_cache, v_cache: uint8 [pages, heads, page_size, row_bytes(fmt, dim)], fmt
+    Q8_0 or Q4_0, page_size a multiple of 64, dim 64, 96, 128 or 256 (the bytes
+    of 64 tokens are in the library's own order: ``cache_load`` reads them).
+    table int32 [B, W]: the pages of each sequence; starts int32 [B + 1]: where
+    its rows of k and v begin; lengths int32 [B]: its tokens in the cache, these
+    rows included as the last ones.  Rows of no sequence and positions without a
+    page are left out."""
+    c = _cache_args(fmt_k, fmt_v, k_cache, v_cache, table, starts, lengths)
+    dev = k_cache.device
+    t, _, k_step, code = _token_rows(k, c.heads, c.dim, "k", dev)
+    tv, _, v_step, code_v = _token_rows(v, c.heads, c.dim, "v", dev)
+    if tv != t or code_v != code:
+        raise ValueError(f"k and v must have one shape and type, got {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype}")
+
+    def body(s):
+        _check(lib().qmatmul_cache_store(c, t, code, k.data_ptr(), k_step, v.data_ptr(), v_step, s), "qmatmul_cache_store")
+
+    _on_device(dev, stream, body)
+
+
+def cache_load(fmt_k: int, fmt_v: int, k_cache, v_cache, table, starts, lengths, tokens: int, dtype=None, k=None, v=None,
+               stream=None):
+    """The keys and values of the batch's rows read back: (k, v), each [tokens,
+    heads, dim] of ``dtype`` (float32 unless given).  Cache, table, starts and
+    lengths as in ``cache_store``; tokens: rows of the outputs (starts[B]; rows
+    of no sequence are not written).  With starts the running sum of lengths
+    these are the whole sequences.  Positions without a page give zeros."""
+    torch = _torch()
+    c = _cache_args(fmt_k, fmt_v, k_cache, v_cache, table, starts, lengths)
+    dev = k_cache.device
+    if tokens < 0:
+        raise ValueError(f"tokens must not be negative, got {tokens}")
+    dtype = dtype or (torch.float32 if k is None else k.dtype)
+    shape = (tokens, c.heads, c.dim)
+
+    def body(s):
+        ko, vo = _out(k, shape, dtype, dev, "k"), _out(v, shape, dtype, dev, "v")
+        _check(lib().qmatmul_cache_load(c, tokens, _type_of(ko, "k"), ko.data_ptr(), vo.data_ptr(), s), "qmatmul_cache_load")
+        return ko, vo
+
+    return _on_device(dev, stream, body)
+
+
+def cache_attention(fmt_k: int, fmt_v: int, k_cache, v_cache, q, table, starts, lengths, scale: float | None = None,
+                    causal: bool = True, window: int = 0, softcap: float = 0.0, max_length: int = 0, out=None, lse=None,
+                    stream=None):
+    """Attention of the batch's rows over the cache: out[n, h] = sum_j p_j v_j
+    with p the softmax of scale * q[n, h] . k_j over the positions that the row
+    sees (causal: up to its own; window: its last ``window``), capped first as
+    softcap * tanh(x / softcap) if softcap > 0.
+
+    q: float32, float16 or bfloat16 [T, q_heads, dim] (the step from token to
+    token is free), q_heads a multiple of the cache's heads; scale: 1 /
+    sqrt(dim) unless given.  Cache, table, starts and lengths as in
+    ``cache_store``: one new token per sequence, many, or both side by side.
+    max_length: a bound on lengths if known (0: what the table can hold), by which
+    the work is split.  Returns [T, q_heads, dim] in q's type; rows that see
+    nothing are zeros, rows of no sequence are not written.  lse: float32 [T,
+    q_heads] to be filled with ln sum exp(score)."""
+    torch = _torch()
+    c = _cache_args(fmt_k, fmt_v, k_cache, v_cache, table, starts, lengths)
+    dev = k_cache.device
+    t, heads, step, code = _token_rows(q, None, c.dim, "q", dev)
+    if lse is not None:
+        _out(lse, (t, heads), torch.float32, dev, "lse")
+    if scale is None:
+        scale = c.dim ** -0.5
+
+    def body(s):
+        o = _out(out, (t, heads, c.dim), q.dtype, dev, "out")
+        need = int(lib().qmatmul_cache_attention_workspace_bytes(c, t, heads, code, int(causal), window, max_length))
+        ws, nb, keep = _scratch(need, dev)
+        _check(lib().qmatmul_cache_attention(c, t, heads, code, q.data_ptr(), step, scale, int(causal), window, softcap,
+                                             max_length, o.data_ptr(), None if lse is None else lse.data_ptr(), ws, nb, s),
+               "qmatmul_cache_attention")
+        return o
 
     return _on_device(dev, stream, body)

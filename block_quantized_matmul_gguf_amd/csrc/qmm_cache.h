@@ -1,0 +1,99 @@
+// qmm_cache.h -- the quantized paged cache of keys and values: its layout,
+// and the arguments that its kernels and the attention over it share.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qmm_internal.h"
+
+namespace qmm {
+
+constexpr int CACHE_GROUP = 64;  // tokens whose bytes lie together
+
+// One batch of sequences over one cache; see qmm_cache in the public header.
+struct CacheArgs {
+    uint8_t* k;
+    uint8_t* v;
+    const int32_t* table;    // [batch][width]
+    const int32_t* starts;   // [batch + 1]
+    const int32_t* lengths;  // [batch]
+    int64_t T;               // rows of the tokens' tensors
+    int64_t pages;
+    int batch, width;
+    int heads, dim;
+    int page_size;
+    int page_groups;         // groups of a page,
+    uint32_t page_magic;     // and ceil(2^32 / page_groups), 0 when that is 1
+    int64_t group_k, group_v;  // bytes of a group of one head
+    int fmt_k, fmt_v, type;
+};
+
+struct StoreArgs {
+    CacheArgs c;
+    const void* k;
+    const void* v;
+    int64_t k_stride, v_stride;  // values from token to token
+};
+struct LoadArgs {
+    CacheArgs c;
+    void* k;
+    void* v;
+};
+struct AttnArgs {
+    CacheArgs c;
+    const void* q;
+    int64_t q_stride;
+    int q_heads, per;   // query heads, and of them to one head of the cache
+    float scale;        // of the scores, times log2(e) where there is no cap
+    float cap, cap_inv; // cap * log2(e), scale / cap; 0: none
+    int causal, window;
+    void* out;
+    float* lse;
+};
+
+hipError_t launch_cache_store(const StoreArgs& a, hipStream_t s);
+hipError_t launch_cache_load(const LoadArgs& a, hipStream_t s);
+
+#if defined(__HIPCC__)
+// The page index of a group (position / 64).
+__device__ __forceinline__ uint32_t cache_page_of(const CacheArgs& c, uint32_t group)
+{
+    return c.page_magic ? __umulhi(group, c.page_magic) : group;
+}
+
+// Sequence s of token row n: the last whose start is at or before n; -1 if n
+// lies before the first or behind the last.
+__device__ __forceinline__ int cache_sequence_of(const CacheArgs& c, int64_t n)
+{
+    int lo = 0, hi = c.batch;  // starts[lo] <= n < starts[hi] wanted
+    if (n < c.starts[0] || n >= c.starts[c.batch]) return -1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (c.starts[mid] <= n) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// The page of a position of sequence s, or -1: before the sequence, past the
+// table, or an entry that names no page.
+__device__ __forceinline__ int64_t cache_page(const CacheArgs& c, int s, int64_t pos)
+{
+    if (pos < 0) return -1;
+    const int64_t group = pos / CACHE_GROUP;
+    if (group >= (int64_t)c.width * c.page_groups) return -1;
+    const int32_t id = c.table[(int64_t)s * c.width + cache_page_of(c, (uint32_t)group)];
+    return id < 0 || id >= c.pages ? -1 : id;
+}
+
+// Place of token t (0..63 of its group) in the order of scales and values:
+// t = 32 s + 16 h + 4 g + i lies at 16 g + 8 s + 4 h + i, so that the sixteen
+// tokens that one lane group g of the matrix instructions meets in a group
+// (rows 4 g + i of four 16-row tiles) are neighbours.
+__device__ __forceinline__ int cache_place(int t)
+{
+    return ((t >> 2) & 3) * 16 + (t >> 5) * 8 + ((t >> 4) & 1) * 4 + (t & 3);
+}
+#endif
+
+}  // namespace qmm

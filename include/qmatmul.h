@@ -381,6 +381,96 @@ int qmatmul_w4_run(int64_t N, int64_t K, int64_t M, int64_t group, int type, int
                    const void* scales, const uint8_t* zeros, const void* x, void* y, void* ws, size_t ws_bytes,
                    void* stream);
 
+/*
+ * Keys and values in a quantized paged cache, and attention over it: what lies
+ * between a layer's q/k/v products and its output product in a server.  Like
+ * the experts' calls these need no plan, allocate nothing and only enqueue
+ * kernels.
+ *
+ * A cache is `pages` pages of page_size tokens; a page holds, for each of
+ * `heads` heads, page_size rows of `dim` values in Q8_0 or Q4_0 blocks (32
+ * values of a token and head): pages * heads * page_size *
+ * qmatmul_row_bytes(format, dim) bytes for the keys (k, format_k) and as much
+ * in format_v for the values (v).  Codes and scales are those that
+ * qmatmul_quantize_act (Q8_0) and qmatmul_quantize_weights (Q4_0) give for the
+ * row, with two exceptions: a block whose scale rounds to 0 has the codes of 0,
+ * and a block that holds an infinity or a NaN, or whose scale is beyond f16,
+ * reads back as NaN throughout.  Their order within a page is the one in which
+ * the kernels read them; for 64 neighbouring tokens t (t = 32 s + 16 h + 4 g + i
+ * = 16 u + r) of a head, together 64 * row bytes:
+ *   keys: four tiles u of 64 lanes 16 c + r; a lane holds, for each block b, the
+ *     codes of dimensions 32 b + 8 c + (0..7), cut into pieces of 16 bytes and a
+ *     rest, each piece stored for the 64 lanes in turn;
+ *   values: for each block b 64 lanes 16 g + n; a lane holds the codes of
+ *     dimensions 32 b + n and 32 b + 16 + n (p = 0, 1) of 16 tokens in the order
+ *     8 s + 4 h + i; Q8_0 [p][lane][16 bytes], Q4_0 [lane][p][8 bytes];
+ *   codes: Q8_0 a byte q + 128; Q4_0 the 4 bits of q + 8, of eight in order
+ *     number e in nibble e / 2 + 4 * (e % 2) of a 32-bit word;
+ *   then f16 scales [dim / 32][64], token t at place 16 g + 8 s + 4 h + i.
+ *
+ * A batch names its sequences' tokens: sequence s has lengths[s] tokens in the
+ * cache, the last starts[s + 1] - starts[s] of which are the call's; row
+ * starts[s] + i of the call's tensors is its token at position lengths[s] -
+ * (starts[s + 1] - starts[s]) + i.  starts must not decrease; rows before
+ * starts[0] and from starts[batch] on belong to no sequence and are neither
+ * read nor written.  Position p lies in page table[s][p / page_size].  A
+ * position without a page (negative, past the table, or where the entry is not
+ * in 0..pages - 1) holds nothing: it is not stored, reads back as zeros, and
+ * attention does not see it.
+ */
+typedef struct qmm_cache {
+    int format_k, format_v;    /* QMM_Q8_0 or QMM_Q4_0 each */
+    int64_t pages, page_size;  /* page_size: a multiple of 64, at most 8192 */
+    int64_t heads, dim;        /* dim: 64, 96, 128 or 256 */
+    void* k;                   /* device, 16-byte aligned */
+    void* v;
+    int64_t batch, table_width;
+    const int32_t* table;      /* device [batch][table_width] */
+    const int32_t* starts;     /* device [batch + 1] */
+    const int32_t* lengths;    /* device [batch] */
+} qmm_cache;
+
+/*
+ * qmatmul_cache_store: the call's T rows of keys and values (device, `type`
+ * QMM_F32, QMM_F16 or QMM_BF16, [T][heads][dim] with k_stride and v_stride
+ * values from token to token) into the cache.  Bytes of other tokens keep their
+ * values.  Where two rows of a call have the same place (two sequences that
+ * share a page and both write it), the place holds codes of either.
+ * qmatmul_cache_load: the rows read back, contiguous [T][heads][dim] of `type`,
+ * each value rounded once; with lengths = starts[s + 1] - starts[s] these are
+ * whole sequences.
+ */
+int qmatmul_cache_store(const qmm_cache* cache, int64_t T, int type, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, void* stream);
+int qmatmul_cache_load(const qmm_cache* cache, int64_t T, int type, void* k, void* v, void* stream);
+
+/*
+ * qmatmul_cache_attention: out[n][h] = sum_j p_j v_j, p = softmax over the
+ * positions j that row n sees of c(scale * q[n][h] . k_j); query heads h to one
+ * head of the cache: h / (q_heads / heads).  Row n at position p sees 0 <= j <
+ * lengths[s]; causal: j <= p; window > 0 (causal only): j > p - window.  c is
+ * the identity, or softcap * tanh(x / softcap) where softcap > 0.  q: device
+ * `type` [T][q_heads][dim], q_stride values from token to token; out: the same
+ * type, contiguous.  lse: device f32 [T][q_heads] or NULL: ln of the sum of
+ * exp(score), by which results over parts of a sequence can be joined.  A row
+ * that sees nothing has out 0 and lse -inf.
+ * Scores and sums are f32; q enters as f16 parts (f32 as two: 2^-22 of the
+ * row's largest), probabilities times value scales as f16 (f32: as two parts).
+ * A NaN or infinity in q, or a NaN in a key that a row sees, makes that row NaN;
+ * a NaN in a value that a row sees makes the dimensions of its block NaN; what
+ * a row does not see does not touch it.
+ * max_length: at least the largest of lengths where the caller knows it (0:
+ * table_width * page_size); it goes into how the work is split and the size of
+ * the workspace; results are right also for longer sequences.
+ * Limits: q_heads a multiple of heads, at most 1024; T <= 2^24, T * q_heads <=
+ * 2^25.  Outputs and ws must not overlap inputs or each other (QMM_EINVAL).
+ */
+int64_t qmatmul_cache_attention_workspace_bytes(const qmm_cache* cache, int64_t T, int64_t q_heads, int type, int causal,
+                                                int64_t window, int64_t max_length); /* reads no pointer; -1 if invalid */
+int qmatmul_cache_attention(const qmm_cache* cache, int64_t T, int64_t q_heads, int type, const void* q, int64_t q_stride,
+                            float scale, int causal, int64_t window, float softcap, int64_t max_length, void* out,
+                            float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Host-only helpers (no HIP calls; safe without a GPU). */
 int qmatmul_check(int format, int64_t N, int64_t K, int64_t M_max, int mode); /* what create validates */
 int64_t qmatmul_row_bytes(int format, int64_t K);           /* bytes of one row of blocks, -1 if invalid */
