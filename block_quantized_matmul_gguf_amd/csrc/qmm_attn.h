@@ -1,0 +1,101 @@
+// qmm_attn.h -- attention over the quantized cache: what its kernels share.
+#pragma once
+#include "qmm_cache.h"
+
+namespace qmm {
+
+// One call.  Work is cut along the rows (a tile: tile_rows neighbouring rows of
+// one sequence and head of the cache, row r = token r / per, query head r % per)
+// and along the positions (pieces of piece_groups groups of 64 tokens, counted
+// from the first group that a tile sees; the last piece takes the rest).
+struct AttnArgs {
+    CacheArgs c;
+    const void* q;
+    int64_t q_stride;
+    int q_heads, per;  // query heads, and of them to one head of the cache
+    float scale;       // of the scores times log2(e); with a cap: 1 / cap of them
+    float cap;         // cap * log2(e), or 0
+    int causal, window;
+    void* out;
+    float* lse;
+    int tile_rows, tiles;  // tiles: upper bound over the batch
+    int pieces, piece_groups;
+    float* part;           // [pieces][T * q_heads][dim] sums of a piece,
+    float* part_ml;        // [pieces][T * q_heads][2] its maximum and sum of exponentials
+};
+
+#define QMM_ATTN_DECLARE(P)                                                                        \
+    hipError_t launch_attn_rows_##P(const AttnArgs& a, bool two_parts, int rt, hipStream_t s);
+QMM_ATTN_DECLARE(q8q8)
+QMM_ATTN_DECLARE(q8q4)
+QMM_ATTN_DECLARE(q4q8)
+QMM_ATTN_DECLARE(q4q4)
+#undef QMM_ATTN_DECLARE
+
+// How a call is cut into tiles and pieces (fields of a); the bytes of workspace.
+int64_t plan_attention(AttnArgs& a, int64_t max_length);
+hipError_t launch_attention(AttnArgs& a, void* ws, hipStream_t s);
+
+#if defined(__HIPCC__)
+// The rows and positions of one tile.
+struct AttnTile {
+    int s;                // sequence
+    int64_t n0;           // its first token row
+    int rows;             // rows of the sequence
+    int r0;               // first row of the tile
+    int64_t first;        // position of the sequence's token row 0
+    int64_t len;          // positions that can be seen: min(length, what the table holds)
+    // positions that row r sees: [lo, hi)
+    __device__ int64_t pos(const AttnArgs& a, int r) const { return first + r / a.per; }
+    __device__ int64_t hi(const AttnArgs& a, int r) const
+    {
+        const int64_t h = a.causal ? (pos(a, r) + 1 < len ? pos(a, r) + 1 : len) : len;
+        return h > 0 ? h : 0;
+    }
+    __device__ int64_t lo(const AttnArgs& a, int r) const
+    {
+        const int64_t l = a.window ? pos(a, r) - a.window + 1 : 0;
+        return l > 0 ? l : 0;
+    }
+};
+
+// Tile ids: sequence s takes those from floor((starts[s] - starts[0]) * per /
+// tile_rows) + s on; a sequence of m rows needs ceil(m / tile_rows) of them,
+// which is what lies up to the next one's first or less.  False: no such tile.
+__device__ __forceinline__ bool attn_tile(const AttnArgs& a, int id, AttnTile& t)
+{
+    const CacheArgs& c = a.c;
+    const int64_t base = c.starts[0];
+    auto first_id = [&](int s) { return ((int64_t)c.starts[s] - base) * a.per / a.tile_rows + s; };
+    int lo = 0, hi = c.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_id(mid) <= id) lo = mid;
+        else hi = mid;
+    }
+    const int64_t n0 = c.starts[lo], n1 = c.starts[lo + 1];
+    if (n0 < 0 || n1 > c.T || n1 <= n0) return false;  // no rows, or starts that name rows that are not there
+    const int64_t rows = (n1 - n0) * a.per, r0 = (id - first_id(lo)) * a.tile_rows;
+    if (r0 < 0 || r0 >= rows) return false;
+    t.s = lo;
+    t.n0 = n0;
+    t.rows = (int)rows;
+    t.r0 = (int)r0;
+    t.first = (int64_t)c.lengths[lo] - (n1 - n0);
+    const int64_t held = (int64_t)c.width * c.page_size, len = c.lengths[lo];
+    t.len = len < held ? len : held;
+    return true;
+}
+
+// Groups [g0, g1) that rows r0..r1 see, and the pieces they are cut into.
+__device__ __forceinline__ int attn_pieces(const AttnArgs& a, const AttnTile& t, int r0, int r1, int& g0, int& g1)
+{
+    g0 = (int)(t.lo(a, r0) / CACHE_GROUP);
+    g1 = (int)((t.hi(a, r1) + CACHE_GROUP - 1) / CACHE_GROUP);
+    if (g1 <= g0) return g1 = g0, 1;
+    const int n = (g1 - g0 + a.piece_groups - 1) / a.piece_groups;
+    return n < a.pieces ? n : a.pieces;
+}
+#endif
+
+}  // namespace qmm

@@ -1,0 +1,133 @@
+// qmm_attn.hip -- attention over the quantized cache: how a call is cut, and
+// the join of its pieces.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/qmatmul.h"
+#include "qmm_attn.h"
+#include "qmm_attn_rows.h"
+
+namespace qmm {
+namespace {
+
+// out = sum_z o_z 2^(m_z - m) / sum_z l_z 2^(m_z - m) over the pieces of a row.
+// `lanes` neighbouring threads hold a row's dimensions, four each; `share` such
+// sets take the pieces in turn.
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int lanes, int share)
+{
+    __shared__ float acc[256][5];
+    const CacheArgs& c = a.c;
+    const int tid = (int)threadIdx.x, per_row = lanes * share, slot = tid / per_row;
+    const int d = 4 * (tid % lanes), part = tid / lanes % share;
+    const int64_t all = c.T * a.q_heads, row = (int64_t)blockIdx.x * (256 / per_row) + slot;
+    float top = -3.402823466e38f, sum = 0.0f;
+    f32x4_t v = f32x4_t{0, 0, 0, 0};
+    int pieces = 0;
+    if (row < all && d < c.dim) {
+        const int64_t n = row / a.q_heads;
+        const int s = cache_sequence_of(c, n), h = (int)(row - n * a.q_heads) % a.per;
+        AttnTile t;
+        if (s >= 0) {
+            const int64_t n0 = c.starts[s], n1 = c.starts[s + 1], held = (int64_t)c.width * c.page_size;
+            t.s = s;
+            t.n0 = n0;
+            t.rows = n0 >= 0 && n1 <= c.T ? (int)((n1 - n0) * a.per) : 0;
+            t.first = (int64_t)c.lengths[s] - (n1 - n0);
+            t.len = c.lengths[s] < held ? c.lengths[s] : held;
+            const int r = (int)(n - n0) * a.per + h;
+            t.r0 = r / a.tile_rows * a.tile_rows;
+            int g0, g1;
+            if (r < t.rows) pieces = attn_pieces(a, t, t.r0, min(t.r0 + a.tile_rows, t.rows) - 1, g0, g1);
+        }
+        if (pieces > 1) {
+            for (int z = part; z < pieces; z += share) top = fmaxf(top, a.part_ml[2 * (z * all + row)]);
+            for (int z = part; z < pieces; z += share) {
+                const int64_t p = z * all + row;
+                const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - top);
+                const f32x4_t x = *(const f32x4_t*)(a.part + p * c.dim + d);
+                sum += f * a.part_ml[2 * p + 1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = fmaf(f, x[k], v[k]);
+            }
+        }
+    }
+    if (share > 1) {
+        acc[tid][0] = top;
+        acc[tid][1] = sum;
+        __syncthreads();
+        const float mine = top;
+        sum = 0.0f;
+        for (int w = 0; w < share; ++w) top = fmaxf(top, acc[slot * per_row + w * lanes + tid % lanes][0]);
+        for (int w = 0; w < share; ++w) {
+            const float* x = acc[slot * per_row + w * lanes + tid % lanes];
+            sum += x[1] * __builtin_amdgcn_exp2f(x[0] - top);
+        }
+        const float f = __builtin_amdgcn_exp2f(mine - top);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[tid][k] = v[k] *= f;
+        __syncthreads();
+        if (part == 0) {
+            for (int w = 1; w < share; ++w)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] += acc[tid + w * lanes][k];
+        }
+    }
+    if (part != 0 || pieces <= 1) return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float y[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    store4(a.out, c.type, row * c.dim + d, y);
+    if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+int64_t plan_attention(AttnArgs& a, int64_t max_length)
+{
+    const CacheArgs& c = a.c;
+    const int64_t rows = (c.T * a.per + c.batch - 1) / c.batch, most = c.dim > 128 ? 64 : 128;
+    a.tile_rows = 16;
+    while (a.tile_rows < most && a.tile_rows < rows) a.tile_rows *= 2;
+    a.tiles = (int)(c.T * a.per / a.tile_rows + c.batch);
+    int64_t span = (int64_t)c.width * c.page_size;
+    if (max_length > 0) span = std::min(span, max_length);
+    if (a.window) span = std::min(span, (int64_t)a.window + a.tile_rows + 126);
+    const int64_t groups = std::max<int64_t>(1, (span + CACHE_GROUP - 1) / CACHE_GROUP);
+    const int64_t base = (int64_t)a.tiles * c.heads;
+    const int64_t want = std::min((2048 + base - 1) / base, (groups + 15) / 16);
+    a.piece_groups = (int)((groups + want - 1) / want);
+    a.pieces = (int)((groups + a.piece_groups - 1) / a.piece_groups);
+    if (a.pieces <= 1) {
+        a.pieces = 1;
+        return 0;
+    }
+    const int64_t all = c.T * a.q_heads;
+    return align256(a.pieces * all * c.dim * 4) + align256(a.pieces * all * 8);
+}
+
+hipError_t launch_attention(AttnArgs& a, void* ws, hipStream_t s)
+{
+    const CacheArgs& c = a.c;
+    const int64_t all = c.T * a.q_heads;
+    if (a.pieces > 1) {
+        a.part = (float*)ws;
+        a.part_ml = (float*)((char*)ws + align256(a.pieces * all * c.dim * 4));
+    }
+    const bool two = c.type == QMM_F32;
+    const int rt = a.tile_rows > 16 && c.dim <= 128 ? 2 : 1;
+    hipError_t e;
+    if (c.fmt_k == FMT_Q8_0) e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q8q8(a, two, rt, s) : launch_attn_rows_q8q4(a, two, rt, s);
+    else e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q4q8(a, two, rt, s) : launch_attn_rows_q4q4(a, two, rt, s);
+    if (e != hipSuccess || a.pieces == 1) return e;
+    const int lanes = c.dim <= 64 ? 16 : c.dim <= 128 ? 32 : 64;
+    int share = 1;
+    while (share * 2 * lanes <= 256 && share * 2 <= a.pieces) share *= 2;
+    const int64_t per_block = 256 / (lanes * share);
+    hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)((all + per_block - 1) / per_block)), dim3(256), 0, s, a, lanes, share);
+    return hipGetLastError();
+}
+
+}  // namespace qmm

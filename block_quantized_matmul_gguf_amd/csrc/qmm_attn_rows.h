@@ -1,0 +1,530 @@
+// qmm_attn_rows.h -- attention over the quantized cache, keys and values from
+// memory to the matrix cores by each wave for itself.
+//
+// For a group of 64 tokens and 16 rows of queries a wave forms
+//   S^T = K Q^T     four tiles of 16 tokens, one v_mfma_f32_16x16x32_f16 per
+//                   quantized block: the codes enter as exact integers, so S is
+//                   sum_b d_b (codes . q) with the scales in f32;
+//   p = exp2(S - m) with the running maximum m and sum of each row;
+//   O^T += V^T P^T  the codes again as integers, P times the tokens' scales of
+//                   the block as the other operand.
+// S^T has a row's scores in a lane's registers and the four lane groups, which
+// is how the second product wants P^T: with the cache's order of tokens nothing
+// moves between lanes.  Scales go through the wave's LDS as f32, those of the
+// values times 2^-E: E follows the largest scale met, so that P d 2^-E uses
+// f16's range whatever the values' size (2^14 at most; below 2^-14, 2^-28 of the
+// largest, it loses bits).  A token that no row of the wave sees gets scale 0,
+// and so does one whose values are not finite; the rows that see it get NaN
+// directly.
+//
+// The waves of a workgroup take row tiles of 16 RT rows, and where there are
+// fewer of these than waves they share the tokens and join in LDS.
+#pragma once
+#include "../../include/qmatmul.h"
+#include "qmm_act.h"
+#include "qmm_attn.h"
+
+namespace qmm {
+
+constexpr int ATTN_WAVES = 4;
+
+QMM_DEV half8_t codes8_q8(uint32_t w0, uint32_t w1)
+{
+    const half2_t bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};  // 1024 + 128
+    const uint32_t d[4] = {__builtin_amdgcn_perm(0x64646464u, w0, 0x05010400u), __builtin_amdgcn_perm(0x64646464u, w0, 0x07030602u),
+                           __builtin_amdgcn_perm(0x64646464u, w1, 0x05010400u), __builtin_amdgcn_perm(0x64646464u, w1, 0x07030602u)};
+    half8_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const half2_t h = __builtin_bit_cast(half2_t, d[i]) + bias;
+        r[2 * i] = h[0];
+        r[2 * i + 1] = h[1];
+    }
+    return r;
+}
+// nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7: f16 1024 + n with the nibble in
+// bits 0..3, 64 + n with it in bits 4..7
+QMM_DEV half8_t codes8_q4(uint32_t w)
+{
+    const half2_t b0 = {(_Float16)-1032.0f, (_Float16)-1032.0f}, b1 = {(_Float16)-72.0f, (_Float16)-72.0f};
+    const uint32_t v = w >> 8;
+    const half2_t h[4] = {__builtin_bit_cast(half2_t, (w & 0x000f000fu) | 0x64006400u) + b0,
+                          __builtin_bit_cast(half2_t, (w & 0x00f000f0u) | 0x54005400u) + b1,
+                          __builtin_bit_cast(half2_t, (v & 0x000f000fu) | 0x64006400u) + b0,
+                          __builtin_bit_cast(half2_t, (v & 0x00f000f0u) | 0x54005400u) + b1};
+    half8_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = h[i][0];
+        r[2 * i + 1] = h[i][1];
+    }
+    return r;
+}
+
+// max and sum over the four lanes that hold one row (l, l + 16, l + 32, l + 48)
+QMM_DEV float rows_max(float v)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    v = fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+    const uint32_t w = __builtin_bit_cast(uint32_t, v);
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+}
+QMM_DEV float rows_sum(float v)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    v = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+    const uint32_t w = __builtin_bit_cast(uint32_t, v);
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
+}
+
+QMM_DEV uint16_t attn_bf16(float f)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, f);
+    return f != f ? (uint16_t)0x7fc0 : (uint16_t)((u + 0x7fffu + ((u >> 16) & 1)) >> 16);
+}
+
+// p s for two neighbours as f16, hi and (TWO) what hi lacks: hi + lo = p s to
+// 2^-22.  hi is fixed before lo is formed: the compiler may round p s to f16
+// once in one place and by way of f32 in another, and a lo of the other hi would
+// be a whole f16 step off.
+template <bool TWO>
+QMM_DEV void split_products(float p0, float s0, float p1, float s1, uint32_t& hi, uint32_t& lo)
+{
+    const float v0 = p0 * s0, v1 = p1 * s1;
+    const half2_t h = {(_Float16)v0, (_Float16)v1};
+    hi = __builtin_bit_cast(uint32_t, h);
+    if constexpr (TWO) {
+        asm volatile("" : "+v"(hi));
+        const half2_t r = {(_Float16)(v0 - f16lo(hi)), (_Float16)(v1 - f16hi(hi))};
+        lo = __builtin_bit_cast(uint32_t, r);
+    }
+}
+
+// Eight values of a query row as f32.
+QMM_DEV void load8(const void* p, int type, int64_t at, float x[8])
+{
+    if (type == QMM_F32) {
+        const float4* v = (const float4*)((const float*)p + at);
+        const float4 a = v[0], b = v[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const u32x4_t w = *(const u32x4_t*)((const uint16_t*)p + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (type == QMM_F16) {
+                x[2 * i] = f16lo(w[i]);
+                x[2 * i + 1] = f16hi(w[i]);
+            } else {
+                x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+                x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+            }
+        }
+    }
+}
+// Four neighbouring values of an output row.
+QMM_DEV void store4(void* p, int type, int64_t at, const float x[4])
+{
+    if (type == QMM_F32) {
+        *(float4*)((float*)p + at) = float4{x[0], x[1], x[2], x[3]};
+    } else {
+        u32x2_t w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint16_t a = type == QMM_F16 ? f16bits(x[2 * i]) : attn_bf16(x[2 * i]);
+            const uint16_t b = type == QMM_F16 ? f16bits(x[2 * i + 1]) : attn_bf16(x[2 * i + 1]);
+            w[i] = (uint32_t)a | ((uint32_t)b << 16);
+        }
+        *(u32x2_t*)((uint16_t*)p + at) = w;
+    }
+}
+
+// Entry i of a sequence's row of the table, as a scalar load.
+QMM_DEV int32_t table_entry(const int32_t* row, uint32_t i)
+{
+    return ((const __attribute__((address_space(4))) int32_t*)row)[i];
+}
+
+// `N` dwords of a lane from a piece of memory where the wave's lanes lie side
+// by side in pieces of 16 bytes and a rest.
+template <int N>
+QMM_DEV void load_pieces(const uint8_t* p, int lane, uint32_t r[N])
+{
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+        const u32x4_t w = *(const u32x4_t*)(p + j * 1024 + lane * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[4 * j + i] = w[i];
+    }
+    if constexpr (N % 4 != 0) {
+        const uint32_t* w = (const uint32_t*)(p + N / 4 * 1024 + lane * (N % 4) * 4);
+#pragma unroll
+        for (int i = 0; i < N % 4; ++i) r[N / 4 * 4 + i] = w[i];
+    }
+}
+
+template <int FK, int FV, int DB, int NP, int RT>
+__global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
+{
+    constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a lane per key tile
+    constexpr int VN = FV == FMT_Q8_0 ? 8 : 4;                     // and per block of values
+    constexpr int SN = (DB + 1) / 2;                               // of scales per lane
+    constexpr int SCALES = 2 * DB * 64;                            // f32 of a wave
+    constexpr int ROWS = 16 * RT;
+    extern __shared__ __align__(16) float lds[];
+    const CacheArgs& c = a.c;
+    const int lane = (int)__lane_id(), g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+
+    // head fastest: the tiles of one head follow each other in steps of `heads` workgroups
+    const int head = (int)(blockIdx.x % (uint32_t)c.heads);
+    const uint32_t rest = blockIdx.x / (uint32_t)c.heads;
+    const int id = (int)(rest % (uint32_t)a.tiles), piece = (int)(rest / (uint32_t)a.tiles);
+    AttnTile t;
+    if (!attn_tile(a, id, t)) return;
+    const int last = min(t.r0 + a.tile_rows, t.rows) - 1;
+    int g0, g1;
+    const int pieces = attn_pieces(a, t, t.r0, last, g0, g1);
+    if (piece >= pieces) return;
+    if (piece > 0) g0 += piece * a.piece_groups;
+    if (piece + 1 < pieces) g1 = min(g1, g0 + a.piece_groups);
+
+    // waves: `along` of them share the tokens of a row tile
+    const int tiles = (last - t.r0) / ROWS + 1;
+    const int along = tiles == 1 ? ATTN_WAVES : tiles == 2 ? ATTN_WAVES / 2 : 1;
+    const int wr = wave / along, wt = wave % along;
+    const int w0 = t.r0 + wr * ROWS, w1 = min(w0 + ROWS - 1, last);
+    const bool work = w0 <= last;
+    const int64_t wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
+    // every row of the wave sees [flo, fhi)
+    const int64_t flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
+
+    // rows of this lane: their queries as f16 parts, what they see
+    half8_t q[RT][DB][NP];
+    float factor[RT], m[RT], l[RT];
+    int hi[RT], lo[RT];
+    int64_t at[RT];  // output row (token, query head), or -1
+    f32x4_t o[RT][2 * DB];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = w0 + 16 * rt + (lane & 15);
+        const bool live = r <= last;
+        const int token = live ? r / a.per : 0, h = live ? r - token * a.per : 0;
+        at[rt] = live ? (t.n0 + token) * a.q_heads + head * a.per + h : -1;
+        hi[rt] = live ? (int)t.hi(a, r) : 0;
+        lo[rt] = live ? (int)t.lo(a, r) : 0;
+        const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + h) * D;
+        float x[DB][8], top = 0.0f;
+        bool fine = true;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[b][e] = 0.0f;
+            if (live) load8(a.q, c.type, from + 32 * b + 8 * g4, x[b]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                top = fmaxf(top, fabsf(x[b][e]));
+                fine = fine && fabsf(x[b][e]) <= 3.402823466e38f;
+            }
+        }
+        top = rows_max(top);
+        fine = rows_max(fine ? 0.0f : 1.0f) == 0.0f;
+        // f16 rows enter as they are, others scaled by a power of two (exact)
+        const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
+        const float up = ldexpf(1.0f, e2);
+        factor[rt] = a.scale * ldexpf(1.0f, -e2);
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                _Float16 hi16, lo16;
+                float xs;
+                split_one(fine ? x[b][e] : __builtin_nanf(""), up, hi16, lo16, xs);
+                q[rt][b][0][e] = hi16;
+                if constexpr (NP == 2) q[rt][b][1][e] = lo16;
+            }
+        m[rt] = -3.402823466e38f;
+        l[rt] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * DB; ++i) o[rt][i] = f32x4_t{0, 0, 0, 0};
+    }
+
+    // scales of the wave: keys [DB][64], values [DB][64]
+    float* ks = lds + wave * SCALES;
+    float* vs = ks + DB * 64;
+    const int32_t* row = c.table + (int64_t)t.s * c.width;
+    const int64_t head_k = (int64_t)c.page_groups * c.group_k, head_v = (int64_t)c.page_groups * c.group_v;
+    int expo = -1000;  // E
+
+    // the wave's groups, and those of them that have a page
+    const int wg0 = max(g0, (int)(wlo / CACHE_GROUP)), wg1 = work ? min(g1, (int)((whi + CACHE_GROUP - 1) / CACHE_GROUP)) : 0;
+    auto page_at = [&](int g) { return table_entry(row, cache_page_of(c, (uint32_t)g)); };
+    for (int g = g0 + (wg0 - g0 + along - 1 - wt) / along * along + wt; g < wg1; g += along) {
+        const int32_t page = page_at(g);
+        if (page < 0 || page >= c.pages) continue;
+        const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
+        const uint8_t* kp = c.k + ((int64_t)page * c.heads + head) * head_k + in_page * c.group_k;
+        const uint8_t* vp = c.v + ((int64_t)page * c.heads + head) * head_v + in_page * c.group_v;
+        uint32_t kr[4][KN], vr[DB][VN], sk[SN], sv[SN];
+#pragma unroll
+        for (int i = 0; i < SN; ++i) {
+            const int w = lane + 64 * i;
+            const bool in = DB % 2 == 0 || w < 32 * DB;
+            sk[i] = in ? *(const uint32_t*)(kp + 256 * KN * 4 + 4 * w) : 0u;
+            sv[i] = in ? *(const uint32_t*)(vp + 256 * VN * DB + 4 * w) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load_pieces<KN>(kp + u * 256 * KN, lane, kr[u]);
+#pragma unroll
+        for (int b = 0; b < DB; ++b) load_pieces<VN>(vp + b * 256 * VN, lane, vr[b]);
+
+        // scales to LDS: word w holds places 2 (w % 32), + 1 of block w / 32
+        const bool whole = (int64_t)g * 64 >= wlo && (int64_t)g * 64 + 64 <= whi;
+        float top = 0.0f;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < SN; ++i) {
+            const int w = lane + 64 * i, pl = 2 * (w & 31);
+            if (DB % 2 != 0 && w >= 32 * DB) continue;
+            float s0 = f16lo(sv[i]), s1 = f16hi(sv[i]);
+            if (!whole) {  // of tokens that nobody sees anything may lie there
+                const int64_t p = (int64_t)g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+                s0 = p >= wlo && p < whi ? s0 : 0.0f;
+                s1 = p + 1 >= wlo && p + 1 < whi ? s1 : 0.0f;
+            }
+            const bool f0 = fabsf(s0) <= 65504.0f, f1 = fabsf(s1) <= 65504.0f;
+            odd = odd || !f0 || !f1;
+            s0 = f0 ? s0 : 0.0f;
+            s1 = f1 ? s1 : 0.0f;
+            top = fmaxf(top, fmaxf(fabsf(s0), fabsf(s1)));
+            sv[i] = (uint32_t)f16bits(s0) | ((uint32_t)f16bits(s1) << 16);
+            ks[2 * w] = f16lo(sk[i]);
+            ks[2 * w + 1] = f16hi(sk[i]);
+        }
+        top = wave_max(top);
+        // E: the largest scale times 2^-E lies in [2^13, 2^14)
+        const int was = expo;
+        if (top > 0.0f) expo = max(expo, ilogbf(top) - 13);
+        expo = __builtin_amdgcn_readfirstlane(expo);
+        const float down = ldexpf(1.0f, -expo);
+#pragma unroll
+        for (int i = 0; i < SN; ++i) {
+            const int w = lane + 64 * i;
+            if (DB % 2 != 0 && w >= 32 * DB) continue;
+            vs[2 * w] = top > 0.0f ? f16lo(sv[i]) * down : 0.0f;
+            vs[2 * w + 1] = top > 0.0f ? f16hi(sv[i]) * down : 0.0f;
+        }
+        wave_sync();
+        const bool rescale = was != expo;
+        const float shift = rescale ? ldexpf(1.0f, was - expo) : 1.0f;  // 0 the first time
+
+        float p[RT][16];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[rt][i] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                half8_t k;
+                if constexpr (FK == FMT_Q8_0) k = codes8_q8(kr[u][2 * b], kr[u][2 * b + 1]);
+                else k = codes8_q4(kr[u][b]);
+                const f32x4_t s = *(const f32x4_t*)(ks + 64 * b + 16 * g4 + 4 * u);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    f32x4_t x = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[rt][b][0], f32x4_t{0, 0, 0, 0}, 0, 0, 0);
+                    if constexpr (NP == 2) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[rt][b][1], x, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[rt][4 * u + i] = fmaf(s[i], x[i], p[rt][4 * u + i]);
+                }
+            }
+
+        const bool masked = (int64_t)g * 64 < flo || (int64_t)g * 64 + 64 > fhi;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float best = -3.402823466e38f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float x = p[rt][i] * factor[rt];
+                if (a.cap != 0.0f) {
+                    if constexpr (NP == 2) x = a.cap * tanhf(x);
+                    else x = a.cap * (1.0f - 2.0f / (1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * x)));
+                }
+                if (masked) {
+                    const int j = g * 64 + 16 * (i >> 2) + 4 * g4 + (i & 3);
+                    x = j >= lo[rt] && j < hi[rt] ? x : -__builtin_inff();
+                }
+                p[rt][i] = x;
+                best = fmaxf(best, x);
+            }
+            best = rows_max(best);
+            const float now = fmaxf(m[rt], best), keep = __builtin_amdgcn_exp2f(m[rt] - now);
+            if (__any(now > m[rt]) || rescale) {
+                const float both = keep * shift;
+                l[rt] *= keep;
+#pragma unroll
+                for (int i = 0; i < 2 * DB; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[rt][i][k] *= both;
+                m[rt] = now;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[rt][i] = __builtin_amdgcn_exp2f(p[rt][i] - m[rt]);
+                l[rt] += p[rt][i];
+            }
+        }
+
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                const f32x4_t s0 = *(const f32x4_t*)(vs + 64 * b + 16 * g4 + 8 * s);
+                const f32x4_t s1 = *(const f32x4_t*)(vs + 64 * b + 16 * g4 + 8 * s + 4);
+                half8_t pv[RT][NP];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    u32x4_t part[2];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        uint32_t h, r = 0;
+                        split_products<NP == 2>(p[rt][8 * s + e], e < 4 ? s0[e & 3] : s1[e & 3], p[rt][8 * s + e + 1],
+                                                e < 4 ? s0[(e & 3) + 1] : s1[(e & 3) + 1], h, r);
+                        part[0][e >> 1] = h;
+                        part[1][e >> 1] = r;
+                    }
+#pragma unroll
+                    for (int np = 0; np < NP; ++np) pv[rt][np] = __builtin_bit_cast(half8_t, part[np]);
+                }
+#pragma unroll
+                for (int par = 0; par < 2; ++par) {
+                    half8_t v;
+                    if constexpr (FV == FMT_Q8_0) v = codes8_q8(vr[b][4 * par + 2 * s], vr[b][4 * par + 2 * s + 1]);
+                    else v = codes8_q4(vr[b][2 * par + s]);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int np = 0; np < NP; ++np)
+                            o[rt][2 * b + par] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pv[rt][np], o[rt][2 * b + par], 0, 0, 0);
+                }
+            }
+
+        if (__any(odd)) {  // values that are not finite: NaN to the rows that see them
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+                for (int pl = 0; pl < 64; ++pl) {
+                    const float s = f16lo(*(const uint16_t*)(vp + 256 * VN * DB + 2 * (64 * b + pl)));
+                    if (fabsf(s) <= 65504.0f) continue;
+                    const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float add = j >= lo[rt] && j < hi[rt] ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[rt][2 * b + (k >> 2)][k & 3] += add;
+                    }
+                }
+        }
+    }
+
+    // join: every wave's sums as one with the maximum over the waves that share its rows
+    float* all = lds + ATTN_WAVES * SCALES;                  // [waves][ROWS][2] maximum, sum
+    float* sums = lds + ATTN_WAVES * (SCALES + 2 * ROWS);    // [waves][ROWS][D]
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        l[rt] = rows_sum(l[rt]);
+        if (g4 == 0) {
+            all[(wave * ROWS + 16 * rt + lane) * 2] = m[rt];
+            all[(wave * ROWS + 16 * rt + lane) * 2 + 1] = l[rt];
+        }
+    }
+    __syncthreads();
+    const float unit = expo > -1000 ? ldexpf(1.0f, expo) : 0.0f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = 16 * rt + (lane & 15);
+        float top = m[rt];
+        for (int w = 0; w < along; ++w) top = fmaxf(top, all[((wr * along + w) * ROWS + r) * 2]);
+        const float f = __builtin_amdgcn_exp2f(m[rt] - top) * unit;
+#pragma unroll
+        for (int i = 0; i < 2 * DB; ++i) {
+            f32x4_t v = o[rt][i];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] *= f;
+            *(f32x4_t*)(sums + (wave * ROWS + r) * D + 16 * i + 4 * g4) = v;
+        }
+    }
+    __syncthreads();
+    const int rows = last - t.r0 + 1;
+    for (int i = (int)threadIdx.x; i < rows * (D / 4); i += 64 * ATTN_WAVES) {
+        const int r = i / (D / 4), d = 4 * (i - r * (D / 4)), first = r / ROWS * along, rr = r % ROWS;
+        float top = -3.402823466e38f, sum = 0.0f;
+        for (int w = first; w < first + along; ++w) top = fmaxf(top, all[(w * ROWS + rr) * 2]);
+        f32x4_t v = f32x4_t{0, 0, 0, 0};
+        for (int w = first; w < first + along; ++w) {
+            sum += all[(w * ROWS + rr) * 2 + 1] * __builtin_amdgcn_exp2f(all[(w * ROWS + rr) * 2] - top);
+            const f32x4_t x = *(const f32x4_t*)(sums + (w * ROWS + rr) * D + d);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] += x[k];
+        }
+        const int token = (t.r0 + r) / a.per, h = t.r0 + r - token * a.per;
+        const int64_t to = (t.n0 + token) * a.q_heads + head * a.per + h;
+        if (pieces == 1) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float y[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+            store4(a.out, c.type, to * D + d, y);
+            if (a.lse && d == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+        } else {
+            const int64_t p = piece * (c.T * a.q_heads) + to;
+            *(f32x4_t*)(a.part + p * D + d) = v;
+            if (d == 0) {
+                a.part_ml[2 * p] = top;
+                a.part_ml[2 * p + 1] = sum;
+            }
+        }
+    }
+}
+
+template <int FK, int FV, int DB, int NP, int RT>
+hipError_t launch_attn_rows(const AttnArgs& a, hipStream_t s)
+{
+    constexpr int lds = ATTN_WAVES * (2 * DB * 64 + 2 * 16 * RT + 16 * RT * 32 * DB) * 4;
+    static bool done[64] = {};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    if (lds > 65536 && (dev >= 64 || !done[dev])) {
+        e = hipFuncSetAttribute((const void*)attn_rows_kernel<FK, FV, DB, NP, RT>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        if (dev < 64) done[dev] = true;
+    }
+    const int64_t blocks = (int64_t)a.tiles * a.c.heads * a.pieces;
+    hipLaunchKernelGGL((attn_rows_kernel<FK, FV, DB, NP, RT>), dim3((uint32_t)blocks), dim3(64 * ATTN_WAVES), lds, s, a);
+    return hipGetLastError();
+}
+
+template <int FK, int FV, int DB>
+hipError_t launch_attn_rows_db(const AttnArgs& a, bool two_parts, int rt, hipStream_t s)
+{
+    if constexpr (DB <= 4) {
+        if (rt == 2) return two_parts ? launch_attn_rows<FK, FV, DB, 2, 2>(a, s) : launch_attn_rows<FK, FV, DB, 1, 2>(a, s);
+    }
+    return two_parts ? launch_attn_rows<FK, FV, DB, 2, 1>(a, s) : launch_attn_rows<FK, FV, DB, 1, 1>(a, s);
+}
+
+#define QMM_ATTN_ROWS(P, FK, FV)                                                            \
+    hipError_t launch_attn_rows_##P(const AttnArgs& a, bool two_parts, int rt, hipStream_t s) \
+    {                                                                                       \
+        switch (a.c.dim) {                                                                  \
+        case 64: return launch_attn_rows_db<FK, FV, 2>(a, two_parts, rt, s);                \
+        case 96: return launch_attn_rows_db<FK, FV, 3>(a, two_parts, rt, s);                \
+        case 128: return launch_attn_rows_db<FK, FV, 4>(a, two_parts, rt, s);               \
+        default: return launch_attn_rows_db<FK, FV, 8>(a, two_parts, rt, s);                \
+        }                                                                                   \
+    }
+
+}  // namespace qmm

@@ -39,17 +39,6 @@ struct LoadArgs {
     void* k;
     void* v;
 };
-struct AttnArgs {
-    CacheArgs c;
-    const void* q;
-    int64_t q_stride;
-    int q_heads, per;   // query heads, and of them to one head of the cache
-    float scale;        // of the scores, times log2(e) where there is no cap
-    float cap, cap_inv; // cap * log2(e), scale / cap; 0: none
-    int causal, window;
-    void* out;
-    float* lse;
-};
 
 hipError_t launch_cache_store(const StoreArgs& a, hipStream_t s);
 hipError_t launch_cache_load(const LoadArgs& a, hipStream_t s);

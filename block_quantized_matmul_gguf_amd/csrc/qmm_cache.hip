@@ -7,7 +7,7 @@
 
 #include "../../include/qmatmul.h"
 #include "qmm_act.h"
-#include "qmm_cache.h"
+#include "qmm_attn.h"
 
 namespace qmm {
 namespace {
@@ -151,69 +151,6 @@ __global__ __launch_bounds__(256) void load_kernel(LoadArgs a)
     const CacheArgs& c = a.c;
     const int64_t per = 2ll * c.heads * c.dim;
     for (int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x; item < c.T * per; item += (int64_t)gridDim.x * 256) load_item(a, item, per);
-}
-
-// A wave per row (token and query head): a lane per position for the scores,
-// a lane per dimension (and 64 further on) for the sums.
-__global__ __launch_bounds__(64) void attn_simple_kernel(AttnArgs a)
-{
-    const CacheArgs& c = a.c;
-    __shared__ float q[256];
-    const int lane = threadIdx.x;
-    const int64_t n = blockIdx.x / a.q_heads;
-    const int head = blockIdx.x % a.q_heads, kv = head / a.per, dim = c.dim;
-    const int s = cache_sequence_of(c, n);
-    if (s < 0) return;
-    for (int d = lane; d < dim; d += 64) q[d] = load_value(a.q, c.type, n * a.q_stride + (int64_t)head * dim + d);
-    __syncthreads();
-    const int64_t len = min((int64_t)c.lengths[s], (int64_t)c.width * c.page_size);
-    const int64_t pos = (int64_t)c.lengths[s] - (c.starts[s + 1] - n);
-    const int64_t hi = a.causal ? min(len, pos + 1) : len;
-    const int64_t lo = a.window ? max((int64_t)0, pos - a.window + 1) : 0;
-    float m = -__builtin_inff(), l = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int64_t j0 = lo / 64 * 64; j0 < hi; j0 += 64) {
-        const int64_t page = cache_page(c, s, j0);
-        if (page < 0) continue;
-        const uint32_t g = (uint32_t)(j0 / CACHE_GROUP);
-        const int64_t at = (page * c.heads + kv) * c.page_groups + (g - cache_page_of(c, g) * c.page_groups);
-        const uint8_t *kp = c.k + at * c.group_k, *vp = c.v + at * c.group_v;
-        float sum = 0.0f;
-        int shift;
-        for (int b = 0; b < dim / 32; ++b) {
-            float part = 0.0f;
-            for (int d = 32 * b; d < 32 * b + 32; ++d) {
-                const int code = kp[code_byte(c.fmt_k, false, dim, lane, d, shift)];
-                part += q[d] * (float)(c.fmt_k == QMM_Q8_0 ? code - 128 : ((code >> shift) & 15) - 8);
-            }
-            sum += part * f16lo(*(const uint16_t*)(kp + scale_byte(c.fmt_k, dim, lane, b)));
-        }
-        float x = a.cap != 0.0f ? a.cap * tanhf(sum * a.cap_inv) : sum * a.scale;
-        const bool seen = j0 + lane >= lo && j0 + lane < hi;
-        if (!seen) x = -__builtin_inff();
-        const float top = fmaxf(m, wave_max(x));
-        if (top == -__builtin_inff() && !__any(x != x)) continue;
-        const float keep = exp2f(m - top), p = seen ? exp2f(x - top) : 0.0f;
-        l *= keep;
-        for (int i = 0; i < 4; ++i) o[i] *= keep;
-        m = top;
-        for (int t = 0; t < 64; ++t) {
-            const float pt = __shfl(p, t);
-            l += pt;
-            if (pt == 0.0f) continue;
-            for (int i = 0; i < 4; ++i) {
-                const int d = lane + 64 * i;
-                if (d >= dim) break;
-                const int code = vp[code_byte(c.fmt_v, true, dim, t, d, shift)];
-                o[i] += pt * (f16lo(*(const uint16_t*)(vp + scale_byte(c.fmt_v, dim, t, d >> 5))) *
-                              (float)(c.fmt_v == QMM_Q8_0 ? code - 128 : ((code >> shift) & 15) - 8));
-            }
-        }
-    }
-    for (int i = 0; i < 4; ++i) {
-        const int d = lane + 64 * i;
-        if (d < dim) store_value(a.out, c.type, (n * a.q_heads + head) * dim + d, l == 0.0f ? 0.0f : o[i] / l);
-    }
-    if (a.lse && lane == 0) a.lse[n * a.q_heads + head] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.69314718f;
 }
 
 int bad(const char* msg) { return set_error(QMM_EINVAL, msg); }
@@ -364,7 +301,18 @@ static int check_attention(const qmm_cache* cache, int64_t T, int64_t q_heads, i
     if (window < 0 || window > 0x7fffffff) return bad("window must be in 0..2^31 - 1");
     if (window && !causal) return bad("a window needs a causal mask");
     if (max_length < 0) return bad("max_length must not be negative");
+    if (cache->batch * cache->heads > (1 << 22)) return bad("batch * heads must be at most 2^22");
     return QMM_OK;
+}
+static AttnArgs attention_args(const qmm_cache* cache, int64_t T, int64_t q_heads, int type, int causal, int64_t window)
+{
+    AttnArgs a = {};
+    a.c = cache_args(cache, T, type);
+    a.q_heads = (int)q_heads;
+    a.per = (int)(q_heads / cache->heads);
+    a.causal = causal != 0;
+    a.window = (int)window;
+    return a;
 }
 
 extern "C" int64_t qmatmul_cache_attention_workspace_bytes(const qmm_cache* cache, int64_t T, int64_t q_heads, int type,
@@ -372,7 +320,9 @@ extern "C" int64_t qmatmul_cache_attention_workspace_bytes(const qmm_cache* cach
 {
     set_error(QMM_OK, "");
     if (check_attention(cache, T, q_heads, type, causal, window, max_length) != QMM_OK) return -1;
-    return 0;
+    if (T == 0 || cache->batch == 0) return 0;
+    AttnArgs a = attention_args(cache, T, q_heads, type, causal, window);
+    return plan_attention(a, max_length);
 }
 
 extern "C" int qmatmul_cache_attention(const qmm_cache* cache, int64_t T, int64_t q_heads, int type, const void* q,
@@ -390,23 +340,19 @@ extern "C" int qmatmul_cache_attention(const qmm_cache* cache, int64_t T, int64_
     if ((st = check_rows(q, q_stride, q_heads, cache->dim, type)) != QMM_OK) return st;
     if ((st = check_rows(out, row, q_heads, cache->dim, type)) != QMM_OK) return st;
     if ((uintptr_t)lse % 4) return bad("lse must be 4-byte aligned");
-    AttnArgs a = {};
-    a.c = cache_args(cache, T, type);
+    AttnArgs a = attention_args(cache, T, q_heads, type, causal, window);
     a.q = q;
     a.q_stride = q_stride;
-    a.q_heads = (int)q_heads;
-    a.per = (int)(q_heads / cache->heads);
-    a.scale = scale * 1.4426950408889634f;
-    a.cap = softcap * 1.4426950408889634f;
-    a.cap_inv = softcap > 0.0f ? scale / softcap : 0.0f;
-    a.causal = causal != 0;
-    a.window = (int)window;
+    const float log2e = 1.4426950408889634f;
+    a.scale = softcap > 0.0f ? scale / softcap : scale * log2e;
+    a.cap = softcap * log2e;
     a.out = out;
     a.lse = lse;
+    const int64_t need = plan_attention(a, max_length);
+    if (need > 0 && (!ws || off16(ws) || ws_bytes < (size_t)need)) return bad("ws must be 16-byte aligned and hold the call's workspace bytes");
     const Ranges r = ranges_of(a.c);
-    const MemRange writes[] = {{out, span(T, row, row, type)}, {lse, 4 * T * q_heads}};
+    const MemRange writes[] = {{out, span(T, row, row, type)}, {lse, 4 * T * q_heads}, {need ? ws : nullptr, need}};
     const MemRange reads[] = {r.k, r.v, r.table, r.starts, r.lengths, {q, span(T, q_stride, row, type)}};
     if (!apart(writes, reads)) return bad("outputs and ws must not overlap inputs or each other");
-    hipLaunchKernelGGL(attn_simple_kernel, dim3((uint32_t)(T * q_heads)), dim3(64), 0, (hipStream_t)stream, a);
-    return status(hipGetLastError());
+    return status(launch_attention(a, ws, (hipStream_t)stream));
 }

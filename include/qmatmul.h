@@ -455,7 +455,8 @@ int qmatmul_cache_load(const qmm_cache* cache, int64_t T, int type, void* k, voi
  * exp(score), by which results over parts of a sequence can be joined.  A row
  * that sees nothing has out 0 and lse -inf.
  * Scores and sums are f32; q enters as f16 parts (f32 as two: 2^-22 of the
- * row's largest), probabilities times value scales as f16 (f32: as two parts).
+ * row's largest), probabilities times value scales as f16 (f32: as two parts),
+ * which leaves at most 2^-37 of the largest value in the cache per position.
  * A NaN or infinity in q, or a NaN in a key that a row sees, makes that row NaN;
  * a NaN in a value that a row sees makes the dimensions of its block NaN; what
  * a row does not see does not touch it.

@@ -68,7 +68,7 @@ def test_load_refusals(kw):
                                 dict(window=5, causal=0), dict(max_length=-1), dict(scale=float("nan")), dict(scale=float("inf")),
                                 dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(out=None),
                                 dict(out=OUT + 8), dict(lse=Y + 2), dict(xs=255), dict(xs=258), dict(out=X), dict(out=K),
-                                dict(lse=X), dict(lse=OUT), dict(out=V + 256), dict(lse=LENGTHS), dict(T=1 << 18, q_heads=1024)], ids=str)
+                                dict(lse=X), dict(lse=OUT), dict(out=V + 256), dict(lse=LENGTHS), dict(T=1 << 18, q_heads=1024), dict(batch=1 << 20, heads=8, q_heads=8)], ids=str)
 def test_attention_refusals(kw):
     assert call("attention", **kw) == qmm.EINVAL and qmm.last_error()
 

@@ -14,6 +14,12 @@ of the positions that a row sees:
     too), and the output's error that times A;
   * a probability (times the value's scale) is rounded to f16: 2^-11 (f32: two
     parts, 2^-21), values to f16 for bf16: 2^-11;
+  * that operand is P d 2^-E in f16, E such that the largest scale d met is
+    below 2^(E + 14) and at least 2^(E + 13): below 2^-14 it is off by up to half
+    f16's smallest step, 2^-25, which times a code (at most 128) and 2^E is at
+    most 2^-38 128 d, or 2^-37 of the largest |v| of the sequence (a block has a
+    code of 127 or 8 at least).  Each position can be off by that, and the
+    probabilities' sum that divides it is at least 1: L 2^-37 max|v|;
   * sums over L positions in f32: at most L / 16 + 16 roundings of partial sums
     (sixteen or more products enter an accumulator at once), 2^-24 each;
   * one rounding to the output's type.
@@ -52,9 +58,13 @@ def starts_of(counts):
     return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
 
 
-def slack(dt, dim, length, big, top, softcap=0.0):
+def largest(v):
+    return float(np.nan_to_num(np.abs(v)).max(initial=0.0))
+
+
+def slack(dt, dim, length, big, top, most, softcap=0.0):
     s = top * (LOSS_S[dt] + (dim + 8) * 2.0**-24) + 2.0**-22 * (top + 4) + 2.0**-22 + softcap * 2.0**-21
-    return big * (2 * np.expm1(2 * s)[..., None] / 2 + LOSS_P[dt] + (length / 16 + 16) * 2.0**-24), s
+    return big * (2 * np.expm1(2 * s)[..., None] / 2 + LOSS_P[dt] + (length / 16 + 16) * 2.0**-24) + length * 2.0**-37 * most, s
 
 
 def check(got, want, tol, what):
@@ -85,7 +95,7 @@ def run_case(seed, fk, fv, dtype, heads, per, dim, page, lengths, new, causal=Tr
         rows = slice(st[s], st[s + 1])
         pos = np.arange(n - new[s], n)
         o, l, big, top = ref.attention(qh[rows], c.kq[s], c.vq[s], pos, dim ** -0.5 if scale is None else scale, causal, window, softcap)
-        tol, e = slack(dt, dim, n, big, top, softcap)
+        tol, e = slack(dt, dim, n, big, top, largest(c.vq[s]), softcap)
         check(out[rows], o, tol, f"out of sequence {s}")
         check(lse[rows], l, np.where(np.isfinite(l), 2 * e + (n / 16 + 16) * 2.0**-24 + LOSS_P[dt], 0.0), f"lse of sequence {s}")
     return out, lse
@@ -153,7 +163,7 @@ def test_rows_that_see_nothing():
             rows = slice(st[s], st[s + 1])
             seen = np.arange(n) >= 64 if s == 3 else None
             o, l, big, top = ref.attention(qh[rows], c.kq[s], c.vq[s], np.arange(n - new[s], n), dim ** -0.5, seen=seen)
-            tol, e = slack(dt, dim, n, big, top)
+            tol, e = slack(dt, dim, n, big, top, largest(c.vq[s]))
             check(out[rows], o, tol, f"out of sequence {s}")
             check(lse[rows], l, np.where(np.isfinite(l), 2 * e + 2.0**-19 + LOSS_P[dt], 0.0), f"lse of sequence {s}")
 
