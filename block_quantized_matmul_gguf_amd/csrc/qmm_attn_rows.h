@@ -81,12 +81,6 @@ QMM_DEV float rows_sum(float v)
     return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
 }
 
-QMM_DEV uint16_t attn_bf16(float f)
-{
-    const uint32_t u = __builtin_bit_cast(uint32_t, f);
-    return f != f ? (uint16_t)0x7fc0 : (uint16_t)((u + 0x7fffu + ((u >> 16) & 1)) >> 16);
-}
-
 // p s for two neighbours as f16, hi and (TWO) what hi lacks: hi + lo = p s to
 // 2^-22.  hi is fixed before lo is formed: the compiler may round p s to f16
 // once in one place and by way of f32 in another, and a lo of the other hi would
@@ -101,45 +95,6 @@ QMM_DEV void split_products(float p0, float s0, float p1, float s1, uint32_t& hi
         asm volatile("" : "+v"(hi));
         const half2_t r = {(_Float16)(v0 - f16lo(hi)), (_Float16)(v1 - f16hi(hi))};
         lo = __builtin_bit_cast(uint32_t, r);
-    }
-}
-
-// Eight values of a query row as f32.
-QMM_DEV void load8(const void* p, int type, int64_t at, float x[8])
-{
-    if (type == QMM_F32) {
-        const float4* v = (const float4*)((const float*)p + at);
-        const float4 a = v[0], b = v[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const u32x4_t w = *(const u32x4_t*)((const uint16_t*)p + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (type == QMM_F16) {
-                x[2 * i] = f16lo(w[i]);
-                x[2 * i + 1] = f16hi(w[i]);
-            } else {
-                x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
-                x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
-            }
-        }
-    }
-}
-// Four neighbouring values of an output row.
-QMM_DEV void store4(void* p, int type, int64_t at, const float x[4])
-{
-    if (type == QMM_F32) {
-        *(float4*)((float*)p + at) = float4{x[0], x[1], x[2], x[3]};
-    } else {
-        u32x2_t w;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint16_t a = type == QMM_F16 ? f16bits(x[2 * i]) : attn_bf16(x[2 * i]);
-            const uint16_t b = type == QMM_F16 ? f16bits(x[2 * i + 1]) : attn_bf16(x[2 * i + 1]);
-            w[i] = (uint32_t)a | ((uint32_t)b << 16);
-        }
-        *(u32x2_t*)((uint16_t*)p + at) = w;
     }
 }
 

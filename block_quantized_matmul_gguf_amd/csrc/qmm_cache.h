@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/qmatmul.h"
+#include "qmm_device.h"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -44,6 +46,68 @@ hipError_t launch_cache_store(const StoreArgs& a, hipStream_t s);
 hipError_t launch_cache_load(const LoadArgs& a, hipStream_t s);
 
 #if defined(__HIPCC__)
+QMM_DEV uint16_t cache_bf16(float f)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, f);
+    return f != f ? (uint16_t)0x7fc0 : (uint16_t)((u + 0x7fffu + ((u >> 16) & 1)) >> 16);
+}
+
+// Eight neighbouring values of a token's row as f32.
+QMM_DEV void load8(const void* p, int type, int64_t at, float x[8])
+{
+    if (type == QMM_F32) {
+        const float4* v = (const float4*)((const float*)p + at);
+        const float4 a = v[0], b = v[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const u32x4_t w = *(const u32x4_t*)((const uint16_t*)p + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (type == QMM_F16) {
+                x[2 * i] = f16lo(w[i]);
+                x[2 * i + 1] = f16hi(w[i]);
+            } else {
+                x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+                x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+            }
+        }
+    }
+}
+// Four, and eight, of an output row.
+QMM_DEV void store4(void* p, int type, int64_t at, const float x[4])
+{
+    if (type == QMM_F32) {
+        *(float4*)((float*)p + at) = float4{x[0], x[1], x[2], x[3]};
+    } else {
+        u32x2_t w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint16_t a = type == QMM_F16 ? f16bits(x[2 * i]) : cache_bf16(x[2 * i]);
+            const uint16_t b = type == QMM_F16 ? f16bits(x[2 * i + 1]) : cache_bf16(x[2 * i + 1]);
+            w[i] = (uint32_t)a | ((uint32_t)b << 16);
+        }
+        *(u32x2_t*)((uint16_t*)p + at) = w;
+    }
+}
+
+QMM_DEV void store8(void* p, int type, int64_t at, const float x[8])
+{
+    if (type == QMM_F32) {
+        ((float4*)((float*)p + at))[0] = float4{x[0], x[1], x[2], x[3]};
+        ((float4*)((float*)p + at))[1] = float4{x[4], x[5], x[6], x[7]};
+    } else {
+        u32x4_t w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint16_t a = type == QMM_F16 ? f16bits(x[2 * i]) : cache_bf16(x[2 * i]);
+            const uint16_t b = type == QMM_F16 ? f16bits(x[2 * i + 1]) : cache_bf16(x[2 * i + 1]);
+            w[i] = (uint32_t)a | ((uint32_t)b << 16);
+        }
+        *(u32x4_t*)((uint16_t*)p + at) = w;
+    }
+}
+
 // The page index of a group (position / 64).
 __device__ __forceinline__ uint32_t cache_page_of(const CacheArgs& c, uint32_t group)
 {

@@ -12,145 +12,267 @@
 namespace qmm {
 namespace {
 
-QMM_DEV float load_value(const void* p, int type, int64_t i)
+// One group of 64 tokens of one head, keys or values, per workgroup.  Its bytes
+// pass through LDS in the cache's own order, where a thread deals with eight
+// neighbouring dimensions (an octet) of a token, so that memory sees whole rows
+// of tokens on one side and whole pieces of 16 bytes on the other.  Both calls
+// are bound by those bytes: 16 bytes of padding after every 128 let the octets
+// of a token (128 bytes or a multiple apart) lie in different LDS banks.
+QMM_DEV int padded(int byte) { return byte + (byte >> 7) * 16; }
+
+// The rows of a call that lie in one group: tile ids of sequence s begin at
+// floor(starts[s] / 64) + 2 s, which leaves it the floor(m / 64) + 2 that m rows
+// can touch.
+struct CacheTile {
+    int ta, tb;      // tokens [ta, tb) of the group
+    int64_t n;       // row of token ta
+    int64_t page;    // -1: none
+    int in_page;     // group in the page
+};
+QMM_DEV bool cache_tile(const CacheArgs& c, int id, CacheTile& t)
 {
-    if (type == QMM_F32) return ((const float*)p)[i];
-    if (type == QMM_F16) return (float)((const _Float16*)p)[i];
-    return __builtin_bit_cast(float, (uint32_t)((const uint16_t*)p)[i] << 16);
+    const int64_t base = c.starts[0];
+    auto first_id = [&](int s) { return ((int64_t)c.starts[s] - base) / CACHE_GROUP + 2 * (int64_t)s; };
+    int lo = 0, hi = c.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_id(mid) <= id) lo = mid;
+        else hi = mid;
+    }
+    const int64_t n0 = c.starts[lo], n1 = c.starts[lo + 1];
+    if (n0 < 0 || n1 > c.T || n1 <= n0) return false;  // no rows, or starts that name rows that are not there
+    const int64_t p0 = (int64_t)c.lengths[lo] - (n1 - n0);
+    // groups counted from the one of p0, which may lie before the sequence
+    const int64_t group = (p0 >> 6) + (id - first_id(lo)), from = group * CACHE_GROUP;
+    const int64_t a = p0 > from ? p0 : from, b = p0 + (n1 - n0) < from + CACHE_GROUP ? p0 + (n1 - n0) : from + CACHE_GROUP;
+    if (a >= b) return false;
+    t.ta = (int)(a - from);
+    t.tb = (int)(b - from);
+    t.n = n0 + (a - p0);
+    t.page = cache_page(c, lo, from);
+    t.in_page = t.page < 0 ? 0 : (int)(group - (int64_t)cache_page_of(c, (uint32_t)group) * c.page_groups);
+    return true;
 }
-QMM_DEV uint16_t bf16_bits(float f)
+// blockIdx: keys or values fastest, then the head, then the tile
+struct CacheBlock {
+    bool values;
+    int head, fmt;
+    uint8_t* at;  // the group's bytes
+};
+QMM_DEV bool cache_block(const CacheArgs& c, CacheTile& t, CacheBlock& b)
 {
-    if (f != f) return 0x7fc0;
-    const uint32_t u = __builtin_bit_cast(uint32_t, f);
-    return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1)) >> 16);
-}
-QMM_DEV void store_value(void* p, int type, int64_t i, float f)
-{
-    if (type == QMM_F32) ((float*)p)[i] = f;
-    else if (type == QMM_F16) ((_Float16*)p)[i] = (_Float16)f;
-    else ((uint16_t*)p)[i] = bf16_bits(f);
+    b.values = blockIdx.x & 1;
+    const uint32_t rest = blockIdx.x >> 1;
+    b.head = (int)(rest % (uint32_t)c.heads);
+    if (!cache_tile(c, (int)(rest / (uint32_t)c.heads), t)) return false;
+    b.fmt = b.values ? c.fmt_v : c.fmt_k;
+    b.at = (b.values ? c.v : c.k) + ((t.page * c.heads + b.head) * c.page_groups + t.in_page) * (b.values ? c.group_v : c.group_k);
+    return true;
 }
 
-// Byte (and nibble) of the code of token t, dimension d in a group.
-QMM_DEV int code_byte(int fmt, bool values, int dim, int t, int d, int& shift)
+// First byte of an octet o = 4 b + c of token t among the keys (8 bytes of Q8_0,
+// 4 of Q4_0).
+template <int DB>
+QMM_DEV int key_byte(int fmt, int t, int o)
 {
-    const int b = d >> 5, place = cache_place(t);
-    shift = 0;
-    if (values) {
-        const int lane = (place >> 4) * 16 + (d & 15), p = (d >> 4) & 1, e = place & 15;
-        if (fmt == QMM_Q8_0) return b * 2048 + p * 1024 + lane * 16 + e;
-        const int nib = ((e & 7) >> 1) + 4 * (e & 1);
-        shift = 4 * (nib & 1);
-        return b * 1024 + lane * 16 + p * 8 + (e >> 3) * 4 + (nib >> 1);
-    }
-    const int lane = ((d >> 3) & 3) * 16 + (t & 15), e = d & 7;
-    int held = dim / 4, at = 8 * b + e;
-    if (fmt != QMM_Q8_0) {
-        const int nib = (e >> 1) + 4 * (e & 1);
-        shift = 4 * (nib & 1);
-        held = dim / 8;
-        at = 4 * b + (nib >> 1);
-    }
-    const int piece = at >> 4, size = min(16, held - 16 * piece);
+    const int b = o >> 2, held = fmt == QMM_Q8_0 ? 8 * DB : 4 * DB, at = fmt == QMM_Q8_0 ? 8 * b : 4 * b, piece = at >> 4;
+    const int size = min(16, held - 16 * piece), lane = (o & 3) * 16 + (t & 15);
     return (t >> 4) * 64 * held + piece * 1024 + lane * size + (at & 15);
 }
-QMM_DEV int scale_byte(int fmt, int dim, int t, int b)
+// First byte of what four tokens from t (a multiple of 4) have of dimension d:
+// Q8_0 the four codes; Q4_0 the word of eight, whose bits from 8 h on hold the
+// four in nibbles 0, 4, 1, 5.
+QMM_DEV int value_byte(int fmt, int t, int d)
 {
-    return (fmt == QMM_Q8_0 ? 64 * dim : 32 * dim) + 2 * (64 * b + cache_place(t));
+    const int b = d >> 5, p = (d >> 4) & 1, lane = ((t >> 2) & 3) * 16 + (d & 15), s = t >> 5, h = (t >> 4) & 1;
+    return fmt == QMM_Q8_0 ? b * 2048 + p * 1024 + lane * 16 + 8 * s + 4 * h : b * 1024 + lane * 16 + p * 8 + 4 * s;
 }
+// Bit of token i (0..3) of a quad in that word.
+QMM_DEV int nibble_bit(int i) { return 16 * (i & 1) + 4 * (i >> 1); }
 
-QMM_DEV void store_item(const StoreArgs& a, int64_t item, int nb)
+constexpr int CACHE_THREADS = 256;
+
+template <int DB>
+__global__ __launch_bounds__(CACHE_THREADS) void store_kernel(StoreArgs a)
 {
 #pragma clang fp contract(off)
+    constexpr int D = 32 * DB, OCT = D / 8;
+    __shared__ __align__(16) uint8_t codes[64 * D / 8 * 9];
+    __shared__ uint16_t scales[DB * 64];
     const CacheArgs& c = a.c;
-    const int64_t n = item / (2 * c.heads * nb);
-    const int r = (int)(item - n * (2 * c.heads * nb)), b = r % nb, head = r / nb % c.heads;
-    const bool values = r >= c.heads * nb;
-    const int s = cache_sequence_of(c, n);
-    if (s < 0) return;
-    const int64_t pos = (int64_t)c.lengths[s] - (c.starts[s + 1] - n);
-    const int64_t page = cache_page(c, s, pos);
-    if (page < 0) return;
-    const int fmt = values ? c.fmt_v : c.fmt_k;
-    const uint32_t g = (uint32_t)(pos / CACHE_GROUP);
-    const int64_t gbytes = values ? c.group_v : c.group_k;
-    uint8_t* to = (values ? c.v : c.k) + ((page * c.heads + head) * c.page_groups + (g - cache_page_of(c, g) * c.page_groups)) * gbytes;
-    const int64_t from = n * (values ? a.v_stride : a.k_stride) + (int64_t)head * c.dim + 32 * b;
-    const int t = (int)(pos % CACHE_GROUP);
-    float x[32], top = 0.0f, first = 0.0f;
-    bool fine = true;
-    for (int j = 0; j < 32; ++j) {
-        x[j] = load_value(values ? a.v : a.k, c.type, from + j);
-        fine = fine && fabsf(x[j]) <= 3.402823466e38f;
-        if (fabsf(x[j]) > top) { top = fabsf(x[j]); first = x[j]; }
+    CacheTile t;
+    CacheBlock k;
+    if (!cache_block(c, t, k) || t.page < 0) return;
+    const int fmt = k.fmt, tid = (int)threadIdx.x;
+    const bool q8 = fmt == QMM_Q8_0;
+    const void* src = k.values ? a.v : a.k;
+    const int64_t stride = k.values ? a.v_stride : a.k_stride;
+
+    // where a word is shared by tokens that are not all here it starts as it is in memory
+    const int size = q8 ? 64 * D : 32 * D;
+    const bool whole = t.ta == 0 && t.tb == 64;
+    if (!q8 && k.values) {
+        for (int w = 4 * tid; w < size; w += 4 * CACHE_THREADS)
+            *(uint32_t*)(codes + padded(w)) = whole ? 0u : *(const uint32_t*)(k.at + w);
+        __syncthreads();
     }
-    const float d = fmt == QMM_Q8_0 ? top / 127.0f : first / -8.0f;
-    uint16_t bits = f16bits(d);
-    fine = fine && (bits & 0x7fff) < 0x7c00;
-    const bool none = !fine || (bits & 0x7fff) == 0;
-    const float id = none ? 0.0f : 1.0f / d;
-    if (!fine) bits = 0x7e00;
-    *(uint16_t*)(to + scale_byte(fmt, c.dim, t, b)) = bits;
-    for (int j = 0; j < 32; j += 2) {
-        int sh0, sh1;
-        const int at0 = code_byte(fmt, values, c.dim, t, 32 * b + j, sh0);
-        if (fmt == QMM_Q8_0) {
-            const int at1 = code_byte(fmt, values, c.dim, t, 32 * b + j + 1, sh1);
-            to[at0] = (uint8_t)(none ? 128 : q8_0_q(x[j], id) + 128);
-            to[at1] = (uint8_t)(none ? 128 : q8_0_q(x[j + 1], id) + 128);
+    const int rows = t.tb - t.ta;
+    for (int i = tid; i < (rows * OCT + 3) / 4 * 4; i += CACHE_THREADS) {  // the four lanes of a block stay together
+        const int r = i / OCT, o = i - r * OCT, tok = t.ta + r;
+        float x[8];
+        load8(src, c.type, (t.n + r) * stride + (int64_t)k.head * D + 8 * o, x);
+        float top = 0.0f, first = 0.0f;
+        bool fine = true;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float m = fabsf(x[e]);
+            fine = fine && m <= 3.402823466e38f;
+            if (m > top) {
+                top = m;
+                first = x[e];
+            }
+        }
+        // over the block's four lanes: the largest, and the first lane that has it
+        float best = fmaxf(top, dpp_f<DPP_X1>(top));
+        best = fmaxf(best, dpp_f<DPP_X2>(best));
+        float bad = fine ? 0.0f : 1.0f;
+        bad = fmaxf(bad, dpp_f<DPP_X1>(bad));
+        bad = fmaxf(bad, dpp_f<DPP_X2>(bad));
+        const int lane = (int)__lane_id();
+        const uint32_t have = (uint32_t)(__ballot(top == best) >> (lane & 60)) & 15u;
+        const float mx = __shfl(first, (lane & 60) + (have ? __builtin_ctz(have) : 0));
+        const float d = q8 ? best / 127.0f : mx / -8.0f;
+        uint16_t bits = f16bits(d);
+        const bool dead = bad != 0.0f || (bits & 0x7fff) >= 0x7c00, none = dead || (bits & 0x7fff) == 0;
+        const float id = none ? 0.0f : 1.0f / d;
+        if (dead) bits = 0x7e00;
+        uint32_t q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (q8) q[e] = none ? 128u : (uint32_t)(q8_0_q(x[e], id) + 128) & 255u;
+            else q[e] = none ? 8u : (uint32_t)min(15, (int)(x[e] * id + 8.5f));
+        }
+        if ((o & 3) == 0) scales[(o >> 2) * 64 + cache_place(tok)] = bits;
+        if (!k.values) {
+            uint8_t* to = codes + padded(key_byte<DB>(fmt, tok, o));
+            if (q8) {
+                *(uint32_t*)to = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
+                *(uint32_t*)(to + 4) = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
+            } else {
+                *(uint32_t*)to = q[0] | q[2] << 4 | q[4] << 8 | q[6] << 12 | q[1] << 16 | q[3] << 20 | q[5] << 24 | q[7] << 28;
+            }
         } else {
-            // the nibbles of a byte: keys, two dimensions; values, two tokens
-            for (int u = 0; u < 2; ++u) {
-                const int at = code_byte(fmt, values, c.dim, t, 32 * b + j + u, sh1);
-                const float y = x[j + u] * id + 8.5f;
-                const uint32_t q = none ? 8u : (uint32_t)min(15, (int)y);
-                uint32_t* w = (uint32_t*)(to + (at & ~3));
-                const int up = 8 * (at & 3) + sh1;
-                atomicAnd(w, ~(15u << up));
-                atomicOr(w, q << up);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int w = padded(value_byte(fmt, tok & ~3, 8 * o + e));
+                if (q8) {
+                    codes[w + (tok & 3)] = (uint8_t)q[e];
+                } else {
+                    const int bit = 8 * ((tok >> 4) & 1) + nibble_bit(tok & 3);
+                    if (!whole) atomicAnd((uint32_t*)(codes + w), ~(15u << bit));
+                    atomicOr((uint32_t*)(codes + w), q[e] << bit);
+                }
             }
         }
     }
-}
-
-// A thread per token, head and eight dimensions of every block pair would be
-// faster; one thread per token, head and block is the plain form.
-__global__ __launch_bounds__(256) void store_kernel(StoreArgs a)
-{
-    const CacheArgs& c = a.c;
-    const int nb = c.dim / 32;
-    for (int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x; item < c.T * 2 * c.heads * nb; item += (int64_t)gridDim.x * 256) store_item(a, item, nb);
-}
-
-QMM_DEV void load_item(const LoadArgs& a, int64_t item, int64_t per)
-{
-    const CacheArgs& c = a.c;
-    const int64_t n = item / per;
-    const int r = (int)(item - n * per), d = r % c.dim, head = r / c.dim % c.heads;
-    const bool values = r >= c.heads * c.dim;
-    const int s = cache_sequence_of(c, n);
-    if (s < 0) return;
-    const int64_t pos = (int64_t)c.lengths[s] - (c.starts[s + 1] - n);
-    const int64_t page = cache_page(c, s, pos);
-    float v = 0.0f;
-    if (page >= 0) {
-        const int fmt = values ? c.fmt_v : c.fmt_k, t = (int)(pos % CACHE_GROUP);
-        const uint32_t g = (uint32_t)(pos / CACHE_GROUP);
-        const int64_t gbytes = values ? c.group_v : c.group_k;
-        const uint8_t* at = (values ? c.v : c.k) + ((page * c.heads + head) * c.page_groups + (g - cache_page_of(c, g) * c.page_groups)) * gbytes;
-        int shift;
-        const int code = at[code_byte(fmt, values, c.dim, t, d, shift)];
-        const float scale = f16lo(*(const uint16_t*)(at + scale_byte(fmt, c.dim, t, d >> 5)));
-        v = scale * (float)(fmt == QMM_Q8_0 ? code - 128 : ((code >> shift) & 15) - 8);
+    __syncthreads();
+    // out: pieces that hold tokens of the call alone as a whole
+    if (whole) {
+        for (int w = 16 * tid; w < size; w += 16 * CACHE_THREADS) *(u32x4_t*)(k.at + w) = *(const u32x4_t*)(codes + padded(w));
+    } else if (!k.values) {
+        for (int i = tid; i < rows * OCT; i += CACHE_THREADS) {
+            const int r = i / OCT, at = key_byte<DB>(fmt, t.ta + r, i - r * OCT);
+            *(uint32_t*)(k.at + at) = *(const uint32_t*)(codes + padded(at));
+            if (q8) *(uint32_t*)(k.at + at + 4) = *(const uint32_t*)(codes + padded(at) + 4);
+        }
+    } else if (q8) {
+        for (int i = tid; i < rows * D; i += CACHE_THREADS) {
+            const int r = i / D, tok = t.ta + r, at = value_byte(fmt, tok & ~3, i - r * D) + (tok & 3);
+            k.at[at] = codes[padded(at)];
+        }
+    } else {
+        for (int w = 4 * tid; w < size; w += 4 * CACHE_THREADS) {  // a word has tokens 32 s + 4 g + (0..3) and 16 on
+            const int tok = ((w >> 2) & 1) * 32 + ((w & 1023) >> 8) * 4;
+            if ((tok < t.tb && tok + 4 > t.ta) || (tok + 16 < t.tb && tok + 20 > t.ta)) *(uint32_t*)(k.at + w) = *(const uint32_t*)(codes + padded(w));
+        }
     }
-    store_value(values ? a.v : a.k, c.type, (n * c.heads + head) * c.dim + d, v);
+    for (int i = tid; i < DB * 64; i += CACHE_THREADS) {
+        const int pl = i & 63, tok = ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+        if (tok >= t.ta && tok < t.tb) *(uint16_t*)(k.at + size + 2 * i) = scales[i];
+    }
 }
 
-__global__ __launch_bounds__(256) void load_kernel(LoadArgs a)
+template <int DB>
+__global__ __launch_bounds__(CACHE_THREADS) void load_kernel(LoadArgs a)
 {
+    constexpr int D = 32 * DB, OCT = D / 8;
+    __shared__ __align__(16) uint8_t codes[64 * D / 8 * 9];
+    __shared__ __align__(16) uint16_t scales[DB * 64];
     const CacheArgs& c = a.c;
-    const int64_t per = 2ll * c.heads * c.dim;
-    for (int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x; item < c.T * per; item += (int64_t)gridDim.x * 256) load_item(a, item, per);
+    CacheTile t;
+    CacheBlock k;
+    if (!cache_block(c, t, k)) return;
+    const int fmt = k.fmt, tid = (int)threadIdx.x;
+    const bool q8 = fmt == QMM_Q8_0;
+    void* dst = k.values ? a.v : a.k;
+    auto row = [&](int tok, int o) { return ((t.n + tok - t.ta) * c.heads + k.head) * D + 8 * o; };
+    const int rows = t.tb - t.ta;
+    if (t.page < 0) {
+        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = tid; i < rows * OCT; i += CACHE_THREADS) {
+            const int r = i / OCT, o = i - r * OCT;
+            store4(dst, c.type, row(t.ta + r, o), zero);
+            store4(dst, c.type, row(t.ta + r, o) + 4, zero);
+        }
+        return;
+    }
+    const int size = q8 ? 64 * D : 32 * D;
+    if (rows >= 16) {
+        for (int w = 16 * tid; w < size; w += 16 * CACHE_THREADS) *(u32x4_t*)(codes + padded(w)) = *(const u32x4_t*)(k.at + w);
+        if (tid < DB * 8) *(u32x4_t*)(scales + 8 * tid) = *(const u32x4_t*)(k.at + size + 16 * tid);
+        __syncthreads();
+    }
+    // few rows: straight from memory
+    auto word = [&](int at) { return rows >= 16 ? *(const uint32_t*)(codes + padded(at)) : *(const uint32_t*)(k.at + at); };
+    auto scale = [&](int b, int tok) {
+        const int i = b * 64 + cache_place(tok);
+        return f16lo(rows >= 16 ? scales[i] : *(const uint16_t*)(k.at + size + 2 * i));
+    };
+    const int quads = ((t.tb + 3) >> 2) - (t.ta >> 2);
+    for (int i = tid; i < quads * OCT; i += CACHE_THREADS) {
+        const int r = i / OCT, o = i - r * OCT, t0 = (t.ta & ~3) + 4 * r;
+        float x[4][8];  // [token][dimension] codes
+        if (!k.values) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = key_byte<DB>(fmt, t0 + j, o);
+                const uint32_t w = word(at), w1 = q8 ? word(at + 4) : 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (q8) x[j][e] = (float)(int)(((e < 4 ? w : w1) >> (8 * (e & 3))) & 255u) - 128.0f;
+                    else x[j][e] = (float)(int)((w >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u) - 8.0f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t w = word(value_byte(fmt, t0, 8 * o + e)) >> (q8 ? 0 : 8 * ((t0 >> 4) & 1));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (q8) x[j][e] = (float)(int)((w >> (8 * j)) & 255u) - 128.0f;
+                    else x[j][e] = (float)(int)((w >> nibble_bit(j)) & 15u) - 8.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (t0 + j < t.ta || t0 + j >= t.tb) continue;
+            const float s = scale(o >> 2, t0 + j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] *= s;
+            store8(dst, c.type, row(t0 + j, o), x[j]);
+        }
+    }
 }
 
 int bad(const char* msg) { return set_error(QMM_EINVAL, msg); }
@@ -172,6 +294,7 @@ int check_cache(const qmm_cache* c, int64_t T, int type)
     if (c->batch < 0 || c->batch > (1 << 20)) return bad("batch must be in 0..2^20");
     if (c->table_width < 0 || c->table_width > 0x7fffffff / c->page_size) return bad("table_width must not be negative, nor table_width * page_size 2^31 or more");
     if (T < 0 || T > (1ll << 24) || T * c->heads > (1ll << 27)) return bad("T must be in 0..2^24 and T * heads at most 2^27");
+    if (c->batch * c->heads > (1 << 21)) return bad("batch * heads must be at most 2^21");
     return QMM_OK;
 }
 int check_pointers(const qmm_cache* c)
@@ -239,18 +362,19 @@ int status(hipError_t e) { return e == hipSuccess ? QMM_OK : set_error(QMM_EHIP,
 
 }  // namespace
 
-hipError_t launch_cache_store(const StoreArgs& a, hipStream_t s)
-{
-    const int64_t items = a.c.T * 2 * a.c.heads * (a.c.dim / 32);
-    hipLaunchKernelGGL(store_kernel, dim3((uint32_t)std::min<int64_t>((items + 255) / 256, 1 << 20)), dim3(256), 0, s, a);
+// Grids stay below 2^32 threads: T * heads <= 2^27 and batch * heads <= 2^21.
+#define QMM_CACHE_LAUNCH(KERNEL)                                                                              \
+    const int64_t blocks = 2 * (a.c.T / CACHE_GROUP + 2ll * a.c.batch) * a.c.heads;                           \
+    const dim3 grid((uint32_t)blocks), block(CACHE_THREADS);                                                  \
+    switch (a.c.dim) {                                                                                        \
+    case 64: hipLaunchKernelGGL(KERNEL<2>, grid, block, 0, s, a); break;                                      \
+    case 96: hipLaunchKernelGGL(KERNEL<3>, grid, block, 0, s, a); break;                                      \
+    case 128: hipLaunchKernelGGL(KERNEL<4>, grid, block, 0, s, a); break;                                     \
+    default: hipLaunchKernelGGL(KERNEL<8>, grid, block, 0, s, a); break;                                      \
+    }                                                                                                         \
     return hipGetLastError();
-}
-hipError_t launch_cache_load(const LoadArgs& a, hipStream_t s)
-{
-    const int64_t items = a.c.T * 2 * a.c.heads * a.c.dim;
-    hipLaunchKernelGGL(load_kernel, dim3((uint32_t)std::min<int64_t>((items + 255) / 256, 1 << 20)), dim3(256), 0, s, a);
-    return hipGetLastError();
-}
+hipError_t launch_cache_store(const StoreArgs& a, hipStream_t s) { QMM_CACHE_LAUNCH(store_kernel) }
+hipError_t launch_cache_load(const LoadArgs& a, hipStream_t s) { QMM_CACHE_LAUNCH(load_kernel) }
 
 }  // namespace qmm
 
@@ -301,7 +425,6 @@ static int check_attention(const qmm_cache* cache, int64_t T, int64_t q_heads, i
     if (window < 0 || window > 0x7fffffff) return bad("window must be in 0..2^31 - 1");
     if (window && !causal) return bad("a window needs a causal mask");
     if (max_length < 0) return bad("max_length must not be negative");
-    if (cache->batch * cache->heads > (1 << 22)) return bad("batch * heads must be at most 2^22");
     return QMM_OK;
 }
 static AttnArgs attention_args(const qmm_cache* cache, int64_t T, int64_t q_heads, int type, int causal, int64_t window)

@@ -424,7 +424,7 @@ typedef struct qmm_cache {
     int64_t heads, dim;        /* dim: 64, 96, 128 or 256 */
     void* k;                   /* device, 16-byte aligned */
     void* v;
-    int64_t batch, table_width;
+    int64_t batch, table_width; /* batch <= 2^20, batch * heads <= 2^21, table_width * page_size < 2^31 */
     const int32_t* table;      /* device [batch][table_width] */
     const int32_t* starts;     /* device [batch + 1] */
     const int32_t* lengths;    /* device [batch] */

@@ -35,7 +35,7 @@ SHARED = [
     (dict(heads=0), qmm.EINVAL), (dict(heads=1025), qmm.EINVAL), (dict(page_size=0), qmm.EINVAL), (dict(page_size=32), qmm.EINVAL),
     (dict(page_size=100), qmm.EINVAL), (dict(page_size=8256), qmm.EINVAL), (dict(page_size=-64), qmm.EINVAL),
     (dict(pages=-1), qmm.EINVAL), (dict(pages=1 << 31), qmm.EINVAL), (dict(batch=-1), qmm.EINVAL),
-    (dict(batch=(1 << 20) + 1), qmm.EINVAL), (dict(table_width=-1), qmm.EINVAL), (dict(table_width=1 << 25), qmm.EINVAL),
+    (dict(batch=(1 << 20) + 1), qmm.EINVAL), (dict(batch=1 << 20, heads=4), qmm.EINVAL), (dict(table_width=-1), qmm.EINVAL), (dict(table_width=1 << 25), qmm.EINVAL),
     (dict(T=-1), qmm.EINVAL), (dict(T=(1 << 24) + 1), qmm.EINVAL), (dict(T=1 << 24, heads=16, q_heads=16), qmm.EINVAL),
     (dict(k=None), qmm.EINVAL), (dict(v=None), qmm.EINVAL), (dict(table=None), qmm.EINVAL), (dict(starts=None), qmm.EINVAL),
     (dict(lengths=None), qmm.EINVAL), (dict(k=K + 8), qmm.EINVAL), (dict(v=V + 4), qmm.EINVAL), (dict(table=TABLE + 2), qmm.EINVAL),
@@ -68,7 +68,7 @@ def test_load_refusals(kw):
                                 dict(window=5, causal=0), dict(max_length=-1), dict(scale=float("nan")), dict(scale=float("inf")),
                                 dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(out=None),
                                 dict(out=OUT + 8), dict(lse=Y + 2), dict(xs=255), dict(xs=258), dict(out=X), dict(out=K),
-                                dict(lse=X), dict(lse=OUT), dict(out=V + 256), dict(lse=LENGTHS), dict(T=1 << 18, q_heads=1024), dict(batch=1 << 20, heads=8, q_heads=8)], ids=str)
+                                dict(lse=X), dict(lse=OUT), dict(out=V + 256), dict(lse=LENGTHS), dict(T=1 << 18, q_heads=1024)], ids=str)
 def test_attention_refusals(kw):
     assert call("attention", **kw) == qmm.EINVAL and qmm.last_error()
 
