@@ -18,6 +18,7 @@ struct AttnArgs {
     int causal, window;
     void* out;
     float* lse;
+    int many;              // the kernel for many rows
     int tile_rows, tiles;  // tiles: upper bound over the batch
     int pieces, piece_groups;
     float* part;           // [pieces][T * q_heads][dim] sums of a piece,
@@ -25,7 +26,8 @@ struct AttnArgs {
 };
 
 #define QMM_ATTN_DECLARE(P)                                                                        \
-    hipError_t launch_attn_rows_##P(const AttnArgs& a, bool two_parts, int rt, hipStream_t s);
+    hipError_t launch_attn_rows_##P(const AttnArgs& a, bool two_parts, int rt, hipStream_t s);  \
+    hipError_t launch_attn_tile_##P(const AttnArgs& a, hipStream_t s);
 QMM_ATTN_DECLARE(q8q8)
 QMM_ATTN_DECLARE(q8q4)
 QMM_ATTN_DECLARE(q4q8)

@@ -90,7 +90,10 @@ int64_t plan_attention(AttnArgs& a, int64_t max_length)
     const CacheArgs& c = a.c;
     const int64_t rows = (c.T * a.per + c.batch - 1) / c.batch, most = c.dim > 128 ? 64 : 128;
     a.tile_rows = 16;
-    while (a.tile_rows < most && a.tile_rows < rows) a.tile_rows *= 2;
+    a.many = c.type != QMM_F32 && rows >= 128 && !(c.type == QMM_F16 && c.dim > 128);
+    if (a.many) a.tile_rows = 256;
+    else
+        while (a.tile_rows < most && a.tile_rows < rows) a.tile_rows *= 2;
     a.tiles = (int)(c.T * a.per / a.tile_rows + c.batch);
     int64_t span = (int64_t)c.width * c.page_size;
     if (max_length > 0) span = std::min(span, max_length);
@@ -119,7 +122,10 @@ hipError_t launch_attention(AttnArgs& a, void* ws, hipStream_t s)
     const bool two = c.type == QMM_F32;
     const int rt = a.tile_rows > 16 && c.dim <= 128 ? 2 : 1;
     hipError_t e;
-    if (c.fmt_k == FMT_Q8_0) e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q8q8(a, two, rt, s) : launch_attn_rows_q8q4(a, two, rt, s);
+    if (a.many) {
+        if (c.fmt_k == FMT_Q8_0) e = c.fmt_v == FMT_Q8_0 ? launch_attn_tile_q8q8(a, s) : launch_attn_tile_q8q4(a, s);
+        else e = c.fmt_v == FMT_Q8_0 ? launch_attn_tile_q4q8(a, s) : launch_attn_tile_q4q4(a, s);
+    } else if (c.fmt_k == FMT_Q8_0) e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q8q8(a, two, rt, s) : launch_attn_rows_q8q4(a, two, rt, s);
     else e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q4q8(a, two, rt, s) : launch_attn_rows_q4q4(a, two, rt, s);
     if (e != hipSuccess || a.pieces == 1) return e;
     const int lanes = c.dim <= 64 ? 16 : c.dim <= 128 ? 32 : 64;

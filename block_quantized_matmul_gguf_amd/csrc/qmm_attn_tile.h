@@ -1,0 +1,451 @@
+// qmm_attn_tile.h -- attention over the quantized cache for many rows.
+//
+// A workgroup of NW waves takes NW * 32 RT rows of one sequence and head of the
+// cache; 64 tokens at a time are decoded to f16 once for all of them, into LDS
+// in operand order, while the matrix cores work on the 64 before:
+//   S^T = K Q^T     v_mfma_f32_32x32x16_f16, 32 tokens by 32 rows
+//   p = exp2(S f - m), the running maximum m raised only where a score passes it
+//                   by 2^8 (p is at most 2^14 then, and sums are the same)
+//   O^T += V^T P^T  P^T straight from the registers that S^T left it in: row r of
+//                   an S^T tile is the token whose place in the values' order of
+//                   tokens fits the operand
+// Keys are code * d rounded to f16 once (NK == 1: bf16 queries, whose own
+// rounding is eight times that) or hi + lo, which is exact (f16 queries); values
+// code * d rounded to f16; both times a power of two per 64 tokens, so that
+// neither end of f16's range is met.
+#pragma once
+#include "qmm_attn_rows.h"
+
+namespace qmm {
+
+// Place in a 32-row S^T tile of token t (0..31): quad 4 a + 2 s + j of tokens (a,
+// s, j of 0, 1) is quad 4 s + 2 a + j of rows.
+QMM_DEV int tile_row(int t)
+{
+    const int quad = t >> 2;
+    return (((quad >> 1) & 1) * 4 + (quad >> 2) * 2 + (quad & 1)) * 4 + (t & 3);
+}
+
+QMM_DEV half8_t mul8(half8_t a, half2_t s)
+{
+    half8_t r;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const half2_t x = half2_t{a[i], a[i + 1]} * s;
+        r[i] = x[0];
+        r[i + 1] = x[1];
+    }
+    return r;
+}
+
+template <int FK, int FV, int DB, int NK, int RT, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
+{
+    constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a thread's keys
+    constexpr int VN = FV == FMT_Q8_0 ? 8 : 4, VU = (DB * 64 + 255) / 256;  // of a unit of values; units of a thread
+    constexpr int SN = (DB + 1) / 2, KB = 64 * D * 2, STAGE = KB * (NK + 1), SCALE = 2 * DB * 64;
+    constexpr int ROWS = 32 * RT;
+    constexpr float RAISE = 8.0f, LIFT = 6.0f;  // powers of two: what m may lag behind, and p at m
+    extern __shared__ __align__(16) uint8_t smem[];
+    const CacheArgs& c = a.c;
+    const int tid = (int)threadIdx.x, lane = (int)__lane_id(), h = lane >> 5, col = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    _Float16* const my_scales = (_Float16*)(smem + 2 * STAGE) + wave * SCALE;  // keys [DB][64], values [DB][64]
+
+    const int head = (int)(blockIdx.x % (uint32_t)c.heads);
+    const uint32_t rest = blockIdx.x / (uint32_t)c.heads;
+    const int id = (int)(rest % (uint32_t)a.tiles), piece = (int)(rest / (uint32_t)a.tiles);
+    AttnTile t;
+    if (!attn_tile(a, id, t)) return;
+    const int last = min(t.r0 + a.tile_rows, t.rows) - 1;
+    int g0, g1;
+    const int pieces = attn_pieces(a, t, t.r0, last, g0, g1);
+    if (piece >= pieces) return;
+    if (piece > 0) g0 += piece * a.piece_groups;
+    if (piece + 1 < pieces) g1 = min(g1, g0 + a.piece_groups);
+    const int64_t glo = t.lo(a, t.r0), ghi = t.hi(a, last);  // what any row of the workgroup sees
+
+    const int w0 = t.r0 + wave * ROWS, w1 = min(w0 + ROWS - 1, last);
+    const bool work = w0 <= last;
+    const int64_t wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
+    const int64_t flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
+
+    half8_t q[RT][2 * DB];
+    float factor[RT], m[RT], l[RT];
+    int hi[RT], lo[RT];
+    int64_t at[RT];
+    f32x16_t o[RT][DB];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = w0 + 32 * rt + col;
+        const bool live = r <= last;
+        const int token = live ? r / a.per : 0, qh = live ? r - token * a.per : 0;
+        at[rt] = live ? (t.n0 + token) * a.q_heads + head * a.per + qh : -1;
+        hi[rt] = live ? (int)t.hi(a, r) : 0;
+        lo[rt] = live ? (int)t.lo(a, r) : 0;
+        const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + qh) * D;
+        const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+        float top = 0.0f;
+        bool fine = true;
+        // twice over the row (it is in the caches): its largest value, then the operands
+#pragma unroll
+        for (int ks = 0; ks < 2 * DB; ++ks) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+            if (live) load8(a.q, c.type, from + 16 * ks + 8 * h, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                top = fmaxf(top, fabsf(x[e]));
+                fine = fine && fabsf(x[e]) <= 3.402823466e38f;
+            }
+        }
+        {
+            const uint32_t u = __builtin_bit_cast(uint32_t, top), f = fine ? 0u : 1u;
+            const auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(f, f, false, false);
+            top = fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
+            fine = ((uint32_t)y[0] | (uint32_t)y[1]) == 0;
+        }
+        const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
+        const float up = sign * ldexpf(1.0f, e2);
+        factor[rt] = fabsf(a.scale) * ldexpf(1.0f, -e2);
+#pragma unroll
+        for (int ks = 0; ks < 2 * DB; ++ks) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+            if (live) load8(a.q, c.type, from + 16 * ks + 8 * h, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[rt][ks][e] = (_Float16)(fine ? x[e] * up : __builtin_nanf(""));
+        }
+        m[rt] = -3.0e38f;
+        l[rt] = 0.0f;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[rt][b][i] = 0.0f;
+    }
+
+    const int32_t* row = c.table + (int64_t)t.s * c.width;
+    const int64_t head_k = (int64_t)c.page_groups * c.group_k, head_v = (int64_t)c.page_groups * c.group_v;
+    // the next group at or after g that has a page
+    auto next = [&](int g, int32_t& page) {
+        for (; g < g1; ++g) {
+            page = table_entry(row, cache_page_of(c, (uint32_t)g));
+            if (page >= 0 && page < c.pages) break;
+        }
+        return g;
+    };
+    const bool do_k = NW == 4 || wave < 4, do_v = NW == 4 || wave >= 4;
+    const int unit = tid & 255;
+    uint32_t kr[KN], vr[VU][VN], sk[SN], sv[SN];
+    auto fetch = [&](int g, int32_t page) {
+        const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
+        const uint8_t* kp = c.k + ((int64_t)page * c.heads + head) * head_k + in_page * c.group_k;
+        const uint8_t* vp = c.v + ((int64_t)page * c.heads + head) * head_v + in_page * c.group_v;
+#pragma unroll
+        for (int i = 0; i < SN; ++i) {
+            const int w = lane + 64 * i;
+            const bool in = DB % 2 == 0 || w < 32 * DB;
+            sk[i] = in ? *(const uint32_t*)(kp + 1024 * KN + 4 * w) : 0u;
+            sv[i] = in ? *(const uint32_t*)(vp + 256 * VN * DB + 4 * w) : 0u;
+        }
+        if (do_k) load_pieces<KN>(kp + (unit >> 6) * 256 * KN, unit & 63, kr);
+        if (do_v) {
+#pragma unroll
+            for (int i = 0; i < VU; ++i) {
+                const int v = unit + 256 * i;
+                if (DB % 4 == 0 || v < 64 * DB) load_pieces<VN>(vp + (v >> 6) * 256 * VN, v & 63, vr[i]);
+            }
+        }
+    };
+    // of the 64 tokens that are decoded next, and of those in LDS: exponents taken off keys and values, and
+    // whether a value is not finite
+    int k_expo = 0, v_expo = -1000, new_expo = -1000;
+    bool odd = false;
+    auto decode = [&](int g, uint8_t* stage) {
+        const bool whole = (int64_t)g * 64 >= glo && (int64_t)g * 64 + 64 <= ghi;
+        float kt = 0.0f, vt = 0.0f;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < SN; ++i) {
+            const int w = lane + 64 * i, pl = 2 * (w & 31);
+            float s[4] = {f16lo(sk[i]), f16hi(sk[i]), f16lo(sv[i]), f16hi(sv[i])};
+            if (!whole) {  // of tokens that nobody sees anything may lie there
+                const int64_t p = (int64_t)g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+                if (p < glo || p >= ghi) s[0] = s[2] = 0.0f;
+                if (p + 1 < glo || p + 1 >= ghi) s[1] = s[3] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (fabsf(s[e]) <= 65504.0f) kt = fmaxf(kt, fabsf(s[e]));
+                const bool f = fabsf(s[2 + e]) <= 65504.0f;
+                bad = bad || !f;
+                s[2 + e] = f ? s[2 + e] : 0.0f;
+                vt = fmaxf(vt, fabsf(s[2 + e]));
+            }
+            const half2_t x = {(_Float16)s[0], (_Float16)s[1]}, y = {(_Float16)s[2], (_Float16)s[3]};
+            sk[i] = __builtin_bit_cast(uint32_t, x);
+            sv[i] = __builtin_bit_cast(uint32_t, y);
+        }
+        odd = __any(bad);
+        kt = wave_max(kt);
+        vt = wave_max(vt);
+        // the largest scale in [2^7, 2^8): a value of at most 2^15
+        k_expo = __builtin_amdgcn_readfirstlane(kt > 0.0f ? ilogbf(kt) - 7 : 0);
+        new_expo = __builtin_amdgcn_readfirstlane(vt > 0.0f ? max(v_expo, ilogbf(vt) - 7) : v_expo);
+        const float kd = ldexpf(1.0f, -k_expo), vd = vt > 0.0f ? ldexpf(1.0f, -new_expo) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < SN; ++i) {
+            const int w = lane + 64 * i;
+            if (DB % 2 != 0 && w >= 32 * DB) continue;
+            const half2_t x = {(_Float16)(f16lo(sk[i]) * kd), (_Float16)(f16hi(sk[i]) * kd)};
+            const half2_t y = {(_Float16)(f16lo(sv[i]) * vd), (_Float16)(f16hi(sv[i]) * vd)};
+            ((half2_t*)my_scales)[w] = x;
+            ((half2_t*)my_scales)[DB * 32 + w] = y;
+        }
+        wave_sync();
+        if (do_k) {  // one token's octet c of every block
+            const int u = unit >> 6, tok = 16 * u + (unit & 15), cc = (unit >> 4) & 3;
+            const int to = (tok & 32) + tile_row(tok & 31);
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                half8_t k;
+                if constexpr (FK == FMT_Q8_0) k = codes8_q8(kr[2 * b], kr[2 * b + 1]);
+                else k = codes8_q4(kr[b]);
+                const _Float16 s = my_scales[64 * b + cache_place(tok)];
+                const half8_t x = mul8(k, half2_t{s, s});
+                *(half8_t*)(stage + ((4 * b + cc) * 64 + to) * 16) = x;
+                if constexpr (NK == 2) {  // what the rounding took off, exactly
+                    half8_t y;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const half2_t z = __builtin_elementwise_fma(half2_t{k[e], k[e + 1]}, half2_t{s, s}, -half2_t{x[e], x[e + 1]});
+                        y[e] = z[0];
+                        y[e + 1] = z[1];
+                    }
+                    *(half8_t*)(stage + KB + ((4 * b + cc) * 64 + to) * 16) = y;
+                }
+            }
+        }
+        if (do_v) {  // sixteen tokens of dimensions n and n + 16 of a block
+#pragma unroll
+            for (int i = 0; i < VU; ++i) {
+                const int v = unit + 256 * i, b = v >> 6, g4 = (v >> 4) & 3, n = v & 15;
+                if (DB % 4 != 0 && v >= 64 * DB) continue;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const half8_t sc = *(const half8_t*)(my_scales + DB * 64 + 64 * b + 16 * g4 + 8 * s);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        half8_t x;
+                        if constexpr (FV == FMT_Q8_0) x = codes8_q8(vr[i][4 * p + 2 * s], vr[i][4 * p + 2 * s + 1]);
+                        else x = codes8_q4(vr[i][2 * p + s]);
+                        *(half8_t*)(stage + KB * NK + ((4 * s + g4) * D + 32 * b + 16 * p + n) * 16) = x * sc;
+                    }
+                }
+            }
+        }
+    };
+
+    int32_t page = -1;
+    int g = next(g0, page), cur = 0;
+    if (g < g1) {
+        fetch(g, page);
+        decode(g, smem);
+        int32_t ahead_page = -1;
+        int ahead = next(g + 1, ahead_page);
+        if (ahead < g1) fetch(ahead, ahead_page);
+        while (true) {
+            __syncthreads();
+            const uint8_t* stage = smem + cur * STAGE;
+            const float shift = new_expo != v_expo ? ldexpf(1.0f, v_expo - new_expo) : 1.0f;  // 0 the first time
+            const bool rescale = new_expo != v_expo, was_odd = odd;
+            const float unit_k = ldexpf(1.0f, k_expo);
+            v_expo = new_expo;
+            if (rescale) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int b = 0; b < DB; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
+            }
+            if ((int64_t)g * 64 + 64 > wlo && (int64_t)g * 64 < whi) {
+                f32x16_t s[RT][2];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[rt][half][i] = 0.0f;
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int ks = 0; ks < 2 * DB; ++ks)
+#pragma unroll
+                        for (int nk = 0; nk < NK; ++nk) {
+                            const half8_t k = *(const half8_t*)(stage + nk * KB + ((2 * ks + h) * 64 + 32 * half + col) * 16);
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) s[rt][half] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[rt][ks], s[rt][half], 0, 0, 0);
+                        }
+                half8_t p[RT][2][2];
+                const bool masked = (int64_t)g * 64 < flo || (int64_t)g * 64 + 64 > fhi;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    float f = fmaxf(factor[rt] * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
+                    if (a.cap != 0.0f) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                s[rt][half][i] = 1.0f - 2.0f / (1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * (s[rt][half][i] * f)));
+                        f = a.cap;
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                // row 8 (i / 4) + 4 h + i % 4 of the tile: quad 2 (i / 4) + h
+                                const int quad = ((i >> 2) & 1) * 4 + (i >> 3) * 2, j = g * 64 + 32 * half + 4 * (quad + h) + (i & 3);
+                                s[rt][half][i] = j >= lo[rt] && j < hi[rt] ? s[rt][half][i] : -__builtin_inff();
+                            }
+                    }
+                    float best = s[rt][0][0];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) best = fmaxf(best, s[rt][half][i]);
+                    const uint32_t u = __builtin_bit_cast(uint32_t, best);
+                    const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+                    best = f * fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
+                    if (__any(best > m[rt] + RAISE)) {
+                        const float now = fmaxf(m[rt], best), keep = __builtin_amdgcn_exp2f(m[rt] - now);
+                        l[rt] *= keep;
+#pragma unroll
+                        for (int b = 0; b < DB; ++b)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[rt][b][i] *= keep;
+                        m[rt] = now;
+                    }
+                    const float off = LIFT - m[rt];
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][half][i], f, off));
+                            sum += e;
+                            p[rt][half][i >> 3][i & 7] = (_Float16)e;
+                        }
+                    l[rt] += sum;
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                        for (int b = 0; b < DB; ++b) {
+                            const half8_t v = *(const half8_t*)(stage + KB * NK + ((4 * half + 2 * ks + h) * D + 32 * b + col) * 16);
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) o[rt][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[rt][half][ks], o[rt][b], 0, 0, 0);
+                        }
+                if (was_odd) {  // values that are not finite: NaN to the rows that see them
+                    const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
+                    const uint8_t* vp = c.v + ((int64_t)page * c.heads + head) * head_v + in_page * c.group_v;
+#pragma unroll
+                    for (int b = 0; b < DB; ++b)
+                        for (int pl = 0; pl < 64; ++pl) {
+                            const float x = f16lo(*(const uint16_t*)(vp + 256 * VN * DB + 2 * (64 * b + pl)));
+                            if (fabsf(x) <= 65504.0f) continue;
+                            const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                const float add = j >= lo[rt] && j < hi[rt] ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[rt][b][i] += add;
+                            }
+                        }
+                }
+            }
+            if (ahead >= g1) break;
+            cur ^= 1;
+            decode(ahead, smem + cur * STAGE);
+            g = ahead;
+            page = ahead_page;
+            ahead = next(g + 1, ahead_page);
+            if (ahead < g1) fetch(ahead, ahead_page);
+        }
+    }
+
+    const float unit_v = v_expo > -1000 ? ldexpf(1.0f, v_expo) : 0.0f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, l[rt]);
+        const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        const float sum = __builtin_bit_cast(float, (uint32_t)both[0]) + __builtin_bit_cast(float, (uint32_t)both[1]);
+        if (at[rt] < 0) continue;
+        const float f = pieces > 1 ? unit_v : sum == 0.0f ? 0.0f : unit_v / sum;
+        const int64_t p = piece * (c.T * a.q_heads) + at[rt];
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int d = 32 * b + 2 * i + 4 * h;
+                const float y[4] = {o[rt][b][i] * f, o[rt][b][i + 1] * f, o[rt][b][i + 2] * f, o[rt][b][i + 3] * f};
+                if (pieces == 1) store4(a.out, c.type, at[rt] * D + d, y);
+                else *(f32x4_t*)(a.part + p * D + d) = f32x4_t{y[0], y[1], y[2], y[3]};
+            }
+        if (h == 0) {
+            if (pieces > 1) {
+                a.part_ml[2 * p] = m[rt] - LIFT;
+                a.part_ml[2 * p + 1] = sum;
+            } else if (a.lse) {
+                a.lse[at[rt]] = sum == 0.0f ? -__builtin_inff() : (m[rt] - LIFT + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+            }
+        }
+    }
+}
+
+template <int FK, int FV, int DB, int NK, int RT, int NW>
+hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
+{
+    constexpr int lds = 2 * 64 * 32 * DB * 2 * (NK + 1) + NW * 2 * DB * 64 * 2;
+    static_assert(lds <= 160 * 1024, "LDS of a compute unit");
+    static bool done[64] = {};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    if (dev >= 64 || !done[dev]) {
+        e = hipFuncSetAttribute((const void*)attn_tile_kernel<FK, FV, DB, NK, RT, NW>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        if (dev < 64) done[dev] = true;
+    }
+    const int64_t blocks = (int64_t)a.tiles * a.c.heads * a.pieces;
+    hipLaunchKernelGGL((attn_tile_kernel<FK, FV, DB, NK, RT, NW>), dim3((uint32_t)blocks), dim3(64 * NW), lds, s, a);
+    return hipGetLastError();
+}
+
+template <int FK, int FV, int DB>
+hipError_t launch_attn_tile_db(const AttnArgs& a, hipStream_t s)
+{
+    if (a.c.type == QMM_F16) {
+        if constexpr (DB <= 4) return launch_attn_tile<FK, FV, DB, 2, 1, 8>(a, s);
+    }
+    return launch_attn_tile<FK, FV, DB, 1, 1, 8>(a, s);
+}
+
+#define QMM_ATTN_TILE(P, FK, FV)                                         \
+    hipError_t launch_attn_tile_##P(const AttnArgs& a, hipStream_t s)    \
+    {                                                                    \
+        switch (a.c.dim) {                                               \
+        case 64: return launch_attn_tile_db<FK, FV, 2>(a, s);            \
+        case 96: return launch_attn_tile_db<FK, FV, 3>(a, s);            \
+        case 128: return launch_attn_tile_db<FK, FV, 4>(a, s);           \
+        default: return launch_attn_tile_db<FK, FV, 8>(a, s);            \
+        }                                                                \
+    }
+
+}  // namespace qmm

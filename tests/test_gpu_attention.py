@@ -12,8 +12,9 @@ of the positions that a row sees:
   * softcap: |tanh'| <= 1, tanh in f32: 2^-21 of the cap;
   * a probability's relative error is twice the score's (the sum of them has it
     too), and the output's error that times A;
-  * a probability (times the value's scale) is rounded to f16: 2^-11 (f32: two
-    parts, 2^-21), values to f16 for bf16: 2^-11;
+  * a probability is rounded to f16, 2^-11, and so is a value (a code times its
+    scale) where many rows share it, 2^-11; f32: the code is exact, the
+    probability times the scale in two parts, 2^-21;
   * that operand is P d 2^-E in f16, E such that the largest scale d met is
     below 2^(E + 14) and at least 2^(E + 13): below 2^-14 it is off by up to half
     f16's smallest step, 2^-25, which times a code (at most 128) and 2^E is at
@@ -40,7 +41,7 @@ FMTS = {"q8": qmm.Q8_0, "q4": qmm.Q4_0}
 TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 TINY = {torch.float32: 2.0**-140, torch.float16: 2.0**-24, torch.bfloat16: 2.0**-130}
 LOSS_S = {torch.float32: 2.0**-19, torch.float16: 0.0, torch.bfloat16: 2.0**-11}
-LOSS_P = {torch.float32: 2.0**-21, torch.float16: 2.0**-11, torch.bfloat16: 2.0**-10}
+LOSS_P = {torch.float32: 2.0**-21, torch.float16: 2.0**-10, torch.bfloat16: 2.0**-10}
 
 
 @pytest.fixture(scope="module", autouse=True)
