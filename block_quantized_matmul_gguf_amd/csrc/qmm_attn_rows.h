@@ -308,7 +308,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
                 float x = p[rt][i] * factor[rt];
                 if (a.cap != 0.0f) {
                     if constexpr (NP == 2) x = a.cap * tanhf(x);
-                    else x = a.cap * (1.0f - 2.0f / (1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * x)));
+                    else x = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * x)));
                 }
                 if (masked) {
                     const int j = g * 64 + 16 * (i >> 2) + 4 * g4 + (i & 3);

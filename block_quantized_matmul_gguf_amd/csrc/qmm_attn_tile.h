@@ -26,6 +26,30 @@ QMM_DEV int tile_row(int t)
     return (((quad >> 1) & 1) * 4 + (quad >> 2) * 2 + (quad & 1)) * 4 + (t & 3);
 }
 
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+// Both halves' maxima over the wave, the same in every lane.
+template <int CTRL>
+QMM_DEV u16x2_t max_dpp_u16x2(u16x2_t v)
+{
+    return __builtin_elementwise_max(v, __builtin_bit_cast(u16x2_t, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true)));
+}
+QMM_DEV uint32_t wave_max_u16x2(u16x2_t v)
+{
+    v = max_dpp_u16x2<DPP_X1>(v);
+    v = max_dpp_u16x2<DPP_X2>(v);
+    v = max_dpp_u16x2<DPP_HMIRROR>(v);
+    v = max_dpp_u16x2<DPP_MIRROR>(v);
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int l = 0; l < 64; l += 16) {
+        const uint32_t x = (uint32_t)__builtin_amdgcn_readlane((int)u, l);
+        lo = max(lo, x & 0xffffu);
+        hi = max(hi, x >> 16);
+    }
+    return lo | (hi << 16);
+}
+
 QMM_DEV half8_t mul8(half8_t a, half2_t s)
 {
     half8_t r;
@@ -45,6 +69,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
     constexpr int VN = FV == FMT_Q8_0 ? 8 : 4, VU = (DB * 64 + 255) / 256;  // of a unit of values; units of a thread
     constexpr int SN = (DB + 1) / 2, KB = 64 * D * 2, STAGE = KB * (NK + 1), SCALE = 2 * DB * 64;
     constexpr int ROWS = 32 * RT;
+    constexpr int NONE = -1000;  // no exponent yet
     constexpr float RAISE = 8.0f, LIFT = 6.0f;  // powers of two: what m may lag behind, and p at m
     extern __shared__ __align__(16) uint8_t smem[];
     const CacheArgs& c = a.c;
@@ -162,48 +187,58 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
     };
     // of the 64 tokens that are decoded next, and of those in LDS: exponents taken off keys and values, and
     // whether a value is not finite
-    int k_expo = 0, v_expo = -1000, new_expo = -1000;
+    int k_expo = 0, v_expo = NONE, new_expo = NONE;
     bool odd = false;
     auto decode = [&](int g, uint8_t* stage) {
         const bool whole = (int64_t)g * 64 >= glo && (int64_t)g * 64 + 64 <= ghi;
-        float kt = 0.0f, vt = 0.0f;
-        bool bad = false;
+        if (!whole) {  // of tokens that nobody sees anything may lie there
+#pragma unroll
+            for (int i = 0; i < SN; ++i) {
+                const int pl = 2 * (lane & 31);
+                const int64_t p = (int64_t)g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+                const uint32_t keep = (p >= glo && p < ghi ? 0xffffu : 0u) | (p + 1 >= glo && p + 1 < ghi ? 0xffff0000u : 0u);
+                sk[i] &= keep;
+                sv[i] &= keep;
+            }
+        }
+        // the largest magnitude of each, as f16 bits (keys low, values high), over lane and wave
+        u16x2_t kt = {0, 0}, vt = {0, 0};
 #pragma unroll
         for (int i = 0; i < SN; ++i) {
-            const int w = lane + 64 * i, pl = 2 * (w & 31);
-            float s[4] = {f16lo(sk[i]), f16hi(sk[i]), f16lo(sv[i]), f16hi(sv[i])};
-            if (!whole) {  // of tokens that nobody sees anything may lie there
-                const int64_t p = (int64_t)g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
-                if (p < glo || p >= ghi) s[0] = s[2] = 0.0f;
-                if (p + 1 < glo || p + 1 >= ghi) s[1] = s[3] = 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (fabsf(s[e]) <= 65504.0f) kt = fmaxf(kt, fabsf(s[e]));
-                const bool f = fabsf(s[2 + e]) <= 65504.0f;
-                bad = bad || !f;
-                s[2 + e] = f ? s[2 + e] : 0.0f;
-                vt = fmaxf(vt, fabsf(s[2 + e]));
-            }
-            const half2_t x = {(_Float16)s[0], (_Float16)s[1]}, y = {(_Float16)s[2], (_Float16)s[3]};
-            sk[i] = __builtin_bit_cast(uint32_t, x);
-            sv[i] = __builtin_bit_cast(uint32_t, y);
+            kt = __builtin_elementwise_max(kt, __builtin_bit_cast(u16x2_t, sk[i] & 0x7fff7fffu));
+            vt = __builtin_elementwise_max(vt, __builtin_bit_cast(u16x2_t, sv[i] & 0x7fff7fffu));
         }
-        odd = __any(bad);
-        kt = wave_max(kt);
-        vt = wave_max(vt);
-        // the largest scale in [2^7, 2^8): a value of at most 2^15
-        k_expo = __builtin_amdgcn_readfirstlane(kt > 0.0f ? ilogbf(kt) - 7 : 0);
-        new_expo = __builtin_amdgcn_readfirstlane(vt > 0.0f ? max(v_expo, ilogbf(vt) - 7) : v_expo);
-        const float kd = ldexpf(1.0f, -k_expo), vd = vt > 0.0f ? ldexpf(1.0f, -new_expo) : 0.0f;
+        uint32_t top = wave_max_u16x2(__builtin_elementwise_max(u16x2_t{kt[0], vt[0]}, u16x2_t{kt[1], vt[1]}));
+        odd = (top >> 16) >= 0x7c00u;
+        if (odd || (top & 0xffffu) >= 0x7c00u) {  // again without what is not finite; values there count as 0
+            u16x2_t t2 = {0, 0};
+#pragma unroll
+            for (int i = 0; i < SN; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t k = (sk[i] >> (16 * e)) & 0x7fffu;
+                    uint32_t v = (sv[i] >> (16 * e)) & 0x7fffu;
+                    if (v >= 0x7c00u) {
+                        sv[i] &= e ? 0xffffu : 0xffff0000u;
+                        v = 0;
+                    }
+                    t2 = __builtin_elementwise_max(t2, u16x2_t{(uint16_t)(k >= 0x7c00u ? 0u : k), (uint16_t)v});
+                }
+            top = wave_max_u16x2(t2);
+        }
+        // exponents such that the largest scale comes to [2^7, 2^8), a value to at most 2^15; the factor is a
+        // power of two that f16 holds (2^15 at most: the smallest scales become normal with it too)
+        const int ke = (int)((top & 0xffffu) >> 10), ve = (int)(top >> 26);
+        k_expo = max(ke - 22, -15);
+        new_expo = top >> 16 ? max(v_expo, max(ve - 22, -15)) : v_expo;
+        const _Float16 kd = __builtin_bit_cast(_Float16, (uint16_t)((15 - k_expo) << 10));
+        const _Float16 vd = __builtin_bit_cast(_Float16, (uint16_t)(new_expo == NONE ? 0 : (15 - new_expo) << 10));
 #pragma unroll
         for (int i = 0; i < SN; ++i) {
             const int w = lane + 64 * i;
             if (DB % 2 != 0 && w >= 32 * DB) continue;
-            const half2_t x = {(_Float16)(f16lo(sk[i]) * kd), (_Float16)(f16hi(sk[i]) * kd)};
-            const half2_t y = {(_Float16)(f16lo(sv[i]) * vd), (_Float16)(f16hi(sv[i]) * vd)};
-            ((half2_t*)my_scales)[w] = x;
-            ((half2_t*)my_scales)[DB * 32 + w] = y;
+            ((half2_t*)my_scales)[w] = __builtin_bit_cast(half2_t, sk[i]) * half2_t{kd, kd};
+            ((half2_t*)my_scales)[DB * 32 + w] = __builtin_bit_cast(half2_t, sv[i]) * half2_t{vd, vd};
         }
         wave_sync();
         if (do_k) {  // one token's octet c of every block
@@ -300,7 +335,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
                         for (int half = 0; half < 2; ++half)
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                s[rt][half][i] = 1.0f - 2.0f / (1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * (s[rt][half][i] * f)));
+                                s[rt][half][i] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[rt][half][i] * (2.8853900817779268f * f)));
                         f = a.cap;
                     }
                     if (masked) {
@@ -380,7 +415,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
         }
     }
 
-    const float unit_v = v_expo > -1000 ? ldexpf(1.0f, v_expo) : 0.0f;
+    const float unit_v = v_expo != NONE ? ldexpf(1.0f, v_expo) : 0.0f;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const uint32_t u = __builtin_bit_cast(uint32_t, l[rt]);

@@ -46,11 +46,9 @@ hipError_t launch_cache_store(const StoreArgs& a, hipStream_t s);
 hipError_t launch_cache_load(const LoadArgs& a, hipStream_t s);
 
 #if defined(__HIPCC__)
-QMM_DEV uint16_t cache_bf16(float f)
-{
-    const uint32_t u = __builtin_bit_cast(uint32_t, f);
-    return f != f ? (uint16_t)0x7fc0 : (uint16_t)((u + 0x7fffu + ((u >> 16) & 1)) >> 16);
-}
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+QMM_DEV uint32_t pack_f16(float a, float b) { return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b}); }
+QMM_DEV uint32_t pack_bf16(float a, float b) { return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b}); }
 
 // Eight neighbouring values of a token's row as f32.
 QMM_DEV void load8(const void* p, int type, int64_t at, float x[8])
@@ -60,51 +58,39 @@ QMM_DEV void load8(const void* p, int type, int64_t at, float x[8])
         const float4 a = v[0], b = v[1];
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const u32x4_t w = *(const u32x4_t*)((const uint16_t*)p + at);
+        return;
+    }
+    const u32x4_t w = *(const u32x4_t*)((const uint16_t*)p + at);
+    if (type == QMM_F16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (type == QMM_F16) {
-                x[2 * i] = f16lo(w[i]);
-                x[2 * i + 1] = f16hi(w[i]);
-            } else {
-                x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
-                x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
-            }
+            x[2 * i] = f16lo(w[i]);
+            x[2 * i + 1] = f16hi(w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+            x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
         }
     }
 }
 // Four, and eight, of an output row.
 QMM_DEV void store4(void* p, int type, int64_t at, const float x[4])
 {
-    if (type == QMM_F32) {
-        *(float4*)((float*)p + at) = float4{x[0], x[1], x[2], x[3]};
-    } else {
-        u32x2_t w;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint16_t a = type == QMM_F16 ? f16bits(x[2 * i]) : cache_bf16(x[2 * i]);
-            const uint16_t b = type == QMM_F16 ? f16bits(x[2 * i + 1]) : cache_bf16(x[2 * i + 1]);
-            w[i] = (uint32_t)a | ((uint32_t)b << 16);
-        }
-        *(u32x2_t*)((uint16_t*)p + at) = w;
-    }
+    if (type == QMM_F32) *(float4*)((float*)p + at) = float4{x[0], x[1], x[2], x[3]};
+    else if (type == QMM_F16) *(u32x2_t*)((uint16_t*)p + at) = u32x2_t{pack_f16(x[0], x[1]), pack_f16(x[2], x[3])};
+    else *(u32x2_t*)((uint16_t*)p + at) = u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
 }
-
 QMM_DEV void store8(void* p, int type, int64_t at, const float x[8])
 {
     if (type == QMM_F32) {
         ((float4*)((float*)p + at))[0] = float4{x[0], x[1], x[2], x[3]};
         ((float4*)((float*)p + at))[1] = float4{x[4], x[5], x[6], x[7]};
+    } else if (type == QMM_F16) {
+        *(u32x4_t*)((uint16_t*)p + at) = u32x4_t{pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7])};
     } else {
-        u32x4_t w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint16_t a = type == QMM_F16 ? f16bits(x[2 * i]) : cache_bf16(x[2 * i]);
-            const uint16_t b = type == QMM_F16 ? f16bits(x[2 * i + 1]) : cache_bf16(x[2 * i + 1]);
-            w[i] = (uint32_t)a | ((uint32_t)b << 16);
-        }
-        *(u32x4_t*)((uint16_t*)p + at) = w;
+        *(u32x4_t*)((uint16_t*)p + at) = u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
     }
 }
 
