@@ -49,15 +49,16 @@ struct AttnTile {
     int64_t len;          // positions that can be seen: min(length, what the table holds)
     // positions that row r sees: [lo, hi)
     __device__ int64_t pos(const AttnArgs& a, int r) const { return first + r / a.per; }
-    __device__ int64_t hi(const AttnArgs& a, int r) const
+    // (below 2^31, as lengths and what a table holds)
+    __device__ int hi(const AttnArgs& a, int r) const
     {
         const int64_t h = a.causal ? (pos(a, r) + 1 < len ? pos(a, r) + 1 : len) : len;
-        return h > 0 ? h : 0;
+        return h > 0 ? (int)h : 0;
     }
-    __device__ int64_t lo(const AttnArgs& a, int r) const
+    __device__ int lo(const AttnArgs& a, int r) const
     {
         const int64_t l = a.window ? pos(a, r) - a.window + 1 : 0;
-        return l > 0 ? l : 0;
+        return l > 0 ? (int)l : 0;
     }
 };
 
@@ -92,11 +93,19 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int id, AttnTile& t
 // Groups [g0, g1) that rows r0..r1 see, and the pieces they are cut into.
 __device__ __forceinline__ int attn_pieces(const AttnArgs& a, const AttnTile& t, int r0, int r1, int& g0, int& g1)
 {
-    g0 = (int)(t.lo(a, r0) / CACHE_GROUP);
-    g1 = (int)((t.hi(a, r1) + CACHE_GROUP - 1) / CACHE_GROUP);
+    g0 = t.lo(a, r0) >> 6;
+    g1 = (int)(((int64_t)t.hi(a, r1) + 63) >> 6);
     if (g1 <= g0) return g1 = g0, 1;
     const int n = (g1 - g0 + a.piece_groups - 1) / a.piece_groups;
     return n < a.pieces ? n : a.pieces;
+}
+
+// The bytes of a group of one head as a buffer: its base in scalar registers, a
+// lane's offset in one, and nothing read past it (bytes == 0: nothing at all).
+__device__ __forceinline__ rsrc_t attn_group(const uint8_t* base, const CacheArgs& c, int32_t page, int head, int g, int64_t bytes, bool any = true)
+{
+    const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
+    return make_rsrc(base + (((int64_t)page * c.heads + head) * c.page_groups + in_page) * bytes, any ? (uint32_t)bytes : 0u);
 }
 #endif
 

@@ -100,7 +100,7 @@ int64_t plan_attention(AttnArgs& a, int64_t max_length)
     if (a.window) span = std::min(span, (int64_t)a.window + a.tile_rows + 126);
     const int64_t groups = std::max<int64_t>(1, (span + CACHE_GROUP - 1) / CACHE_GROUP);
     const int64_t base = (int64_t)a.tiles * c.heads;
-    const int64_t want = std::min(((a.many ? 256 : 2048) + base - 1) / base, (groups + 15) / 16);
+    const int64_t want = std::min(((a.many ? 256 : 512) + base - 1) / base, (groups + 7) / 8);
     a.piece_groups = (int)((groups + want - 1) / want);
     a.pieces = (int)((groups + a.piece_groups - 1) / a.piece_groups);
     if (a.pieces <= 1) {

@@ -104,26 +104,30 @@ QMM_DEV int32_t table_entry(const int32_t* row, uint32_t i)
     return ((const __attribute__((address_space(4))) int32_t*)row)[i];
 }
 
-// `N` dwords of a lane from a piece of memory where the wave's lanes lie side
-// by side in pieces of 16 bytes and a rest.
+// `N` dwords of a lane, from byte `at` on, where the 64 lanes lie side by side in
+// pieces of 16 bytes and a rest.
 template <int N>
-QMM_DEV void load_pieces(const uint8_t* p, int lane, uint32_t r[N])
+QMM_DEV void load_pieces(rsrc_t p, uint32_t at, uint32_t lane, uint32_t r[N])
 {
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
-        const u32x4_t w = *(const u32x4_t*)(p + j * 1024 + lane * 16);
+        const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(p, lane * 16 + j * 1024, at, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[4 * j + i] = w[i];
     }
-    if constexpr (N % 4 != 0) {
-        const uint32_t* w = (const uint32_t*)(p + N / 4 * 1024 + lane * (N % 4) * 4);
+    if constexpr (N % 4 == 2) {
+        const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(p, lane * 8 + N / 4 * 1024, at, 0);
+        r[N - 2] = w[0];
+        r[N - 1] = w[1];
+    } else if constexpr (N % 4 == 3) {
 #pragma unroll
-        for (int i = 0; i < N % 4; ++i) r[N / 4 * 4 + i] = w[i];
+        for (int i = 0; i < 3; ++i) r[N / 4 * 4 + i] = __builtin_amdgcn_raw_buffer_load_b32(p, lane * 12 + N / 4 * 1024 + 4 * i, at, 0);
     }
+    static_assert(N % 4 != 1, "no such piece");
 }
 
 template <int FK, int FV, int DB, int NP, int RT>
-__global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void attn_rows_kernel(AttnArgs a)
 {
     constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a lane per key tile
     constexpr int VN = FV == FMT_Q8_0 ? 8 : 4;                     // and per block of values
@@ -154,9 +158,9 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
     const int wr = wave / along, wt = wave % along;
     const int w0 = t.r0 + wr * ROWS, w1 = min(w0 + ROWS - 1, last);
     const bool work = w0 <= last;
-    const int64_t wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
+    const int wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
     // every row of the wave sees [flo, fhi)
-    const int64_t flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
+    const int flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
 
     // rows of this lane: their queries as f16 parts, what they see
     half8_t q[RT][DB][NP];
@@ -170,8 +174,8 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
         const bool live = r <= last;
         const int token = live ? r / a.per : 0, h = live ? r - token * a.per : 0;
         at[rt] = live ? (t.n0 + token) * a.q_heads + head * a.per + h : -1;
-        hi[rt] = live ? (int)t.hi(a, r) : 0;
-        lo[rt] = live ? (int)t.lo(a, r) : 0;
+        hi[rt] = live ? t.hi(a, r) : 0;
+        lo[rt] = live ? t.lo(a, r) : 0;
         const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + h) * D;
         float x[DB][8], top = 0.0f;
         bool fine = true;
@@ -212,33 +216,47 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
     float* ks = lds + wave * SCALES;
     float* vs = ks + DB * 64;
     const int32_t* row = c.table + (int64_t)t.s * c.width;
-    const int64_t head_k = (int64_t)c.page_groups * c.group_k, head_v = (int64_t)c.page_groups * c.group_v;
     int expo = -1000;  // E
 
     // the wave's groups, and those of them that have a page
     const int wg0 = max(g0, (int)(wlo / CACHE_GROUP)), wg1 = work ? min(g1, (int)((whi + CACHE_GROUP - 1) / CACHE_GROUP)) : 0;
-    auto page_at = [&](int g) { return table_entry(row, cache_page_of(c, (uint32_t)g)); };
-    for (int g = g0 + (wg0 - g0 + along - 1 - wt) / along * along + wt; g < wg1; g += along) {
-        const int32_t page = page_at(g);
-        if (page < 0 || page >= c.pages) continue;
-        const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
-        const uint8_t* kp = c.k + ((int64_t)page * c.heads + head) * head_k + in_page * c.group_k;
-        const uint8_t* vp = c.v + ((int64_t)page * c.heads + head) * head_v + in_page * c.group_v;
-        uint32_t kr[4][KN], vr[DB][VN], sk[SN], sv[SN];
+    auto next = [&](int g, int32_t& page) {
+        for (; g < wg1; g += along) {
+            page = table_entry(row, cache_page_of(c, (uint32_t)g));
+            if (page >= 0 && page < c.pages) break;
+        }
+        return g;
+    };
+    // A group's codes and scales are loaded as soon as those of the one before are used up: keys while its
+    // probabilities and sums are formed, values during the next one's scores.  Behind the last group the loads
+    // are of nothing: a branch round them would keep the scores' parts in registers until after it.
+    uint32_t kr[4][KN], vr[DB][VN], sk[SN], sv[SN];
+    auto fetch_keys = [&](int g, int32_t page, bool any) {
+        const rsrc_t kp = attn_group(c.k, c, page, head, g, c.group_k, any), vp = attn_group(c.v, c, page, head, g, c.group_v, any);
 #pragma unroll
-        for (int i = 0; i < SN; ++i) {
-            const int w = lane + 64 * i;
-            const bool in = DB % 2 == 0 || w < 32 * DB;
-            sk[i] = in ? *(const uint32_t*)(kp + 256 * KN * 4 + 4 * w) : 0u;
-            sv[i] = in ? *(const uint32_t*)(vp + 256 * VN * DB + 4 * w) : 0u;
+        for (int i = 0; i < SN; ++i) {  // an odd number of blocks: past the end, and zero
+            sk[i] = __builtin_amdgcn_raw_buffer_load_b32(kp, (uint32_t)lane * 4 + 256 * i, 1024 * KN, 0);
+            sv[i] = __builtin_amdgcn_raw_buffer_load_b32(vp, (uint32_t)lane * 4 + 256 * i, 256 * VN * DB, 0);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) load_pieces<KN>(kp + u * 256 * KN, lane, kr[u]);
+        for (int u = 0; u < 4; ++u) load_pieces<KN>(kp, u * 256 * KN, (uint32_t)lane, kr[u]);
+    };
+    auto fetch_values = [&](int g, int32_t page, bool any) {
+        const rsrc_t vp = attn_group(c.v, c, page, head, g, c.group_v, any);
 #pragma unroll
-        for (int b = 0; b < DB; ++b) load_pieces<VN>(vp + b * 256 * VN, lane, vr[b]);
+        for (int b = 0; b < DB; ++b) load_pieces<VN>(vp, b * 256 * VN, (uint32_t)lane, vr[b]);
+    };
+    int32_t page = -1, ahead_page = -1;
+    int ahead = next(g0 + (wg0 - g0 + along - 1 - wt) / along * along + wt, ahead_page);
+    fetch_keys(ahead, ahead_page, ahead < wg1);
+    fetch_values(ahead, ahead_page, ahead < wg1);
+    while (ahead < wg1) {
+        const int g = ahead;
+        page = ahead_page;
+        ahead = next(g + along, ahead_page);
 
         // scales to LDS: word w holds places 2 (w % 32), + 1 of block w / 32
-        const bool whole = (int64_t)g * 64 >= wlo && (int64_t)g * 64 + 64 <= whi;
+        const bool whole = g * 64 >= wlo && g * 64 + 64 <= whi;
         float top = 0.0f;
         bool odd = false;
 #pragma unroll
@@ -247,7 +265,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
             if (DB % 2 != 0 && w >= 32 * DB) continue;
             float s0 = f16lo(sv[i]), s1 = f16hi(sv[i]);
             if (!whole) {  // of tokens that nobody sees anything may lie there
-                const int64_t p = (int64_t)g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+                const int p = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
                 s0 = p >= wlo && p < whi ? s0 : 0.0f;
                 s1 = p + 1 >= wlo && p + 1 < whi ? s1 : 0.0f;
             }
@@ -283,7 +301,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[rt][i] = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u) {
 #pragma unroll
             for (int b = 0; b < DB; ++b) {
                 half8_t k;
@@ -298,25 +316,32 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
                     for (int i = 0; i < 4; ++i) p[rt][4 * u + i] = fmaf(s[i], x[i], p[rt][4 * u + i]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);  // the scales of one tile at a time in registers
+        }
 
-        const bool masked = (int64_t)g * 64 < flo || (int64_t)g * 64 + 64 > fhi;
+        fetch_keys(ahead, ahead_page, ahead < wg1);
+        const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[rt][i] *= factor[rt];
+            if (a.cap != 0.0f) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if constexpr (NP == 2) p[rt][i] = a.cap * tanhf(p[rt][i]);
+                    else p[rt][i] = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * p[rt][i])));
+                }
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int j = g * 64 + 16 * (i >> 2) + 4 * g4 + (i & 3);
+                    p[rt][i] = j >= lo[rt] && j < hi[rt] ? p[rt][i] : -__builtin_inff();
+                }
+            }
             float best = -3.402823466e38f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float x = p[rt][i] * factor[rt];
-                if (a.cap != 0.0f) {
-                    if constexpr (NP == 2) x = a.cap * tanhf(x);
-                    else x = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * x)));
-                }
-                if (masked) {
-                    const int j = g * 64 + 16 * (i >> 2) + 4 * g4 + (i & 3);
-                    x = j >= lo[rt] && j < hi[rt] ? x : -__builtin_inff();
-                }
-                p[rt][i] = x;
-                best = fmaxf(best, x);
-            }
+            for (int i = 0; i < 16; ++i) best = fmaxf(best, p[rt][i]);
             best = rows_max(best);
             const float now = fmaxf(m[rt], best), keep = __builtin_amdgcn_exp2f(m[rt] - now);
             if (__any(now > m[rt]) || rescale) {
@@ -367,13 +392,16 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_rows_kernel(AttnArgs a)
                         for (int np = 0; np < NP; ++np)
                             o[rt][2 * b + par] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pv[rt][np], o[rt][2 * b + par], 0, 0, 0);
                 }
+                if (b % 2) __builtin_amdgcn_sched_barrier(0);
             }
 
+        fetch_values(ahead, ahead_page, ahead < wg1);
         if (__any(odd)) {  // values that are not finite: NaN to the rows that see them
+            const rsrc_t vp = attn_group(c.v, c, page, head, g, c.group_v);
 #pragma unroll
             for (int b = 0; b < DB; ++b)
                 for (int pl = 0; pl < 64; ++pl) {
-                    const float s = f16lo(*(const uint16_t*)(vp + 256 * VN * DB + 2 * (64 * b + pl)));
+                    const float s = f16lo(__builtin_amdgcn_raw_buffer_load_b16(vp, 0, 256 * VN * DB + 2 * (64 * b + pl), 0));
                     if (fabsf(s) <= 65504.0f) continue;
                     const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
 #pragma unroll

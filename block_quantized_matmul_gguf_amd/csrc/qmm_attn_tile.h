@@ -88,12 +88,12 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
     if (piece >= pieces) return;
     if (piece > 0) g0 += piece * a.piece_groups;
     if (piece + 1 < pieces) g1 = min(g1, g0 + a.piece_groups);
-    const int64_t glo = t.lo(a, t.r0), ghi = t.hi(a, last);  // what any row of the workgroup sees
+    const int glo = t.lo(a, t.r0), ghi = t.hi(a, last);  // what any row of the workgroup sees
 
     const int w0 = t.r0 + wave * ROWS, w1 = min(w0 + ROWS - 1, last);
     const bool work = w0 <= last;
-    const int64_t wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
-    const int64_t flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
+    const int wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
+    const int flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
 
     half8_t q[RT][2 * DB];
     float factor[RT], m[RT], l[RT];
@@ -106,8 +106,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
         const bool live = r <= last;
         const int token = live ? r / a.per : 0, qh = live ? r - token * a.per : 0;
         at[rt] = live ? (t.n0 + token) * a.q_heads + head * a.per + qh : -1;
-        hi[rt] = live ? (int)t.hi(a, r) : 0;
-        lo[rt] = live ? (int)t.lo(a, r) : 0;
+        hi[rt] = live ? t.hi(a, r) : 0;
+        lo[rt] = live ? t.lo(a, r) : 0;
         const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + qh) * D;
         const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
         float top = 0.0f;
@@ -153,7 +153,6 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
     }
 
     const int32_t* row = c.table + (int64_t)t.s * c.width;
-    const int64_t head_k = (int64_t)c.page_groups * c.group_k, head_v = (int64_t)c.page_groups * c.group_v;
     // the next group at or after g that has a page
     auto next = [&](int g, int32_t& page) {
         for (; g < g1; ++g) {
@@ -163,26 +162,20 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
         return g;
     };
     const bool do_k = NW == 4 || wave < 4, do_v = NW == 4 || wave >= 4;
-    const int unit = tid & 255;
+    const int unit = tid & 255, unit_wave = wave & 3;  // tiles of keys, blocks of values to a wave
     uint32_t kr[KN], vr[VU][VN], sk[SN], sv[SN];
     auto fetch = [&](int g, int32_t page) {
-        const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
-        const uint8_t* kp = c.k + ((int64_t)page * c.heads + head) * head_k + in_page * c.group_k;
-        const uint8_t* vp = c.v + ((int64_t)page * c.heads + head) * head_v + in_page * c.group_v;
+        const rsrc_t kp = attn_group(c.k, c, page, head, g, c.group_k), vp = attn_group(c.v, c, page, head, g, c.group_v);
 #pragma unroll
-        for (int i = 0; i < SN; ++i) {
-            const int w = lane + 64 * i;
-            const bool in = DB % 2 == 0 || w < 32 * DB;
-            sk[i] = in ? *(const uint32_t*)(kp + 1024 * KN + 4 * w) : 0u;
-            sv[i] = in ? *(const uint32_t*)(vp + 256 * VN * DB + 4 * w) : 0u;
+        for (int i = 0; i < SN; ++i) {  // an odd number of blocks: past the end, and zero
+            sk[i] = __builtin_amdgcn_raw_buffer_load_b32(kp, (uint32_t)lane * 4 + 256 * i, 1024 * KN, 0);
+            sv[i] = __builtin_amdgcn_raw_buffer_load_b32(vp, (uint32_t)lane * 4 + 256 * i, 256 * VN * DB, 0);
         }
-        if (do_k) load_pieces<KN>(kp + (unit >> 6) * 256 * KN, unit & 63, kr);
+        if (do_k) load_pieces<KN>(kp, (uint32_t)(unit_wave * 256 * KN), (uint32_t)lane, kr);
         if (do_v) {
 #pragma unroll
-            for (int i = 0; i < VU; ++i) {
-                const int v = unit + 256 * i;
-                if (DB % 4 == 0 || v < 64 * DB) load_pieces<VN>(vp + (v >> 6) * 256 * VN, v & 63, vr[i]);
-            }
+            for (int i = 0; i < VU; ++i)
+                if (DB % 4 == 0 || unit_wave + 4 * i < DB) load_pieces<VN>(vp, (uint32_t)((unit_wave + 4 * i) * 256 * VN), (uint32_t)lane, vr[i]);
         }
     };
     // of the 64 tokens that are decoded next, and of those in LDS: exponents taken off keys and values, and
@@ -190,12 +183,12 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
     int k_expo = 0, v_expo = NONE, new_expo = NONE;
     bool odd = false;
     auto decode = [&](int g, uint8_t* stage) {
-        const bool whole = (int64_t)g * 64 >= glo && (int64_t)g * 64 + 64 <= ghi;
+        const bool whole = g * 64 >= glo && g * 64 + 64 <= ghi;
         if (!whole) {  // of tokens that nobody sees anything may lie there
 #pragma unroll
             for (int i = 0; i < SN; ++i) {
                 const int pl = 2 * (lane & 31);
-                const int64_t p = (int64_t)g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+                const int p = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
                 const uint32_t keep = (p >= glo && p < ghi ? 0xffffu : 0u) | (p + 1 >= glo && p + 1 < ghi ? 0xffff0000u : 0u);
                 sk[i] &= keep;
                 sv[i] &= keep;
@@ -307,7 +300,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
             }
-            if ((int64_t)g * 64 + 64 > wlo && (int64_t)g * 64 < whi) {
+            if (g * 64 + 64 > wlo && g * 64 < whi) {
                 f32x16_t s[RT][2];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
@@ -326,7 +319,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
                             for (int rt = 0; rt < RT; ++rt) s[rt][half] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[rt][ks], s[rt][half], 0, 0, 0);
                         }
                 half8_t p[RT][2][2];
-                const bool masked = (int64_t)g * 64 < flo || (int64_t)g * 64 + 64 > fhi;
+                const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     float f = fmaxf(factor[rt] * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
@@ -388,12 +381,11 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
                             for (int rt = 0; rt < RT; ++rt) o[rt][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[rt][half][ks], o[rt][b], 0, 0, 0);
                         }
                 if (was_odd) {  // values that are not finite: NaN to the rows that see them
-                    const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
-                    const uint8_t* vp = c.v + ((int64_t)page * c.heads + head) * head_v + in_page * c.group_v;
+                    const rsrc_t vp = attn_group(c.v, c, page, head, g, c.group_v);
 #pragma unroll
                     for (int b = 0; b < DB; ++b)
                         for (int pl = 0; pl < 64; ++pl) {
-                            const float x = f16lo(*(const uint16_t*)(vp + 256 * VN * DB + 2 * (64 * b + pl)));
+                            const float x = f16lo(__builtin_amdgcn_raw_buffer_load_b16(vp, 0, 256 * VN * DB + 2 * (64 * b + pl), 0));
                             if (fabsf(x) <= 65504.0f) continue;
                             const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
 #pragma unroll
