@@ -637,30 +637,43 @@ def w4_matmul(q, scales, x, zeros=None, y=None, stream=None):
 #
 # Streams, scratch and outputs as with the experts' calls above.
 
+def _is(t, dtype, dims, index):
+    """Whether ``_tensor`` would accept t, in the few steps that a good argument needs."""
+    return (isinstance(t, _torch().Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == dims and t.get_device() == index
+            and t.is_contiguous())
+
+
 def _cache_args(fmt_k, fmt_v, k_cache, v_cache, table, starts, lengths):
     """Checks a cache and a batch; their ``qmm_cache``."""
     torch = _torch()
-    _tensor(k_cache, torch.uint8, (4,), "k_cache")
-    dev = k_cache.device
-    _tensor(v_cache, torch.uint8, (4,), "v_cache", dev)
-    for t, dims, name in ((table, (2,), "table"), (starts, (1,), "starts"), (lengths, (1,), "lengths")):
-        _tensor(t, torch.int32, dims, name, dev)
-    pages, heads, page_size, rk = k_cache.shape
-    block = BLOCK_BYTES.get(fmt_k)
-    if fmt_k not in (Q8_0, Q4_0) or fmt_v not in (Q8_0, Q4_0):
+    if not isinstance(k_cache, torch.Tensor) or not _is(k_cache, torch.uint8, 4, k_cache.get_device()):
+        _tensor(k_cache, torch.uint8, (4,), "k_cache")
+    index = k_cache.get_device()
+    for t, dtype, dims, name in ((v_cache, torch.uint8, 4, "v_cache"), (table, torch.int32, 2, "table"),
+                                 (starts, torch.int32, 1, "starts"), (lengths, torch.int32, 1, "lengths")):
+        if not _is(t, dtype, dims, index):
+            _tensor(t, dtype, (dims,), name, k_cache.device)
+    if (fmt_k != Q8_0 and fmt_k != Q4_0) or (fmt_v != Q8_0 and fmt_v != Q4_0):
         raise ValueError(f"cache formats are Q8_0 and Q4_0, got {fmt_k} and {fmt_v}")
-    if rk == 0 or rk % block:
+    pages, heads, page_size, rk = k_cache.shape
+    blocks, rest = divmod(rk, BLOCK_BYTES[fmt_k])
+    if rk == 0 or rest:
         raise ValueError(f"k_cache must be [pages, heads, page size, row bytes], got {tuple(k_cache.shape)}")
-    dim = rk // block * 32
-    want = (pages, heads, page_size, dim // 32 * BLOCK_BYTES[fmt_v])
-    if tuple(v_cache.shape) != want:
+    want = (pages, heads, page_size, blocks * BLOCK_BYTES[fmt_v])
+    if v_cache.shape != want:
         raise ValueError(f"v_cache must have shape {want}, got {tuple(v_cache.shape)}")
     batch, width = table.shape
     if starts.shape[0] != batch + 1 or lengths.shape[0] != batch:
         raise ValueError(f"for {batch} sequences starts must be [{batch + 1}] and lengths [{batch}], got "
                          f"{tuple(starts.shape)} and {tuple(lengths.shape)}")
-    return CacheStruct(fmt_k, fmt_v, pages, page_size, heads, dim, k_cache.data_ptr(), v_cache.data_ptr(), batch, width,
+    return CacheStruct(fmt_k, fmt_v, pages, page_size, heads, 32 * blocks, k_cache.data_ptr(), v_cache.data_ptr(), batch, width,
                        table.data_ptr(), starts.data_ptr(), lengths.data_ptr())
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(fmt_k, fmt_v, pages, page_size, heads, dim, batch, width, t, q_heads, code, causal, window, max_length):
+    c = CacheStruct(fmt_k, fmt_v, pages, page_size, heads, dim, None, None, batch, width, None, None, None)
+    return int(lib().qmatmul_cache_attention_workspace_bytes(c, t, q_heads, code, causal, window, max_length))
 
 
 def _token_rows(t, heads, dim, name, device):
@@ -669,7 +682,7 @@ def _token_rows(t, heads, dim, name, device):
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
-        raise ValueError(f"{name} must be on the GPU of the cache, {device}, got {t.device}")
+        raise ValueError(f"{name} must be on the cache's GPU, {device}, got {t.device}")
     code = _type_of(t, name)
     if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}], got {tuple(t.shape)}")
@@ -757,8 +770,8 @@ def cache_attention(fmt_k: int, fmt_v: int, k_cache, v_cache, q, table, starts, 
 
     def body(s):
         o = _out(out, (t, heads, c.dim), q.dtype, dev, "out")
-        need = int(lib().qmatmul_cache_attention_workspace_bytes(c, t, heads, code, int(causal), window, max_length))
-        ws, nb, keep = _scratch(need, dev)
+        ws, nb, keep = _scratch(_attention_workspace(c.format_k, c.format_v, c.pages, c.page_size, c.heads, c.dim, c.batch,
+                                                     c.table_width, t, heads, code, int(causal), window, max_length), dev)
         _check(lib().qmatmul_cache_attention(c, t, heads, code, q.data_ptr(), step, scale, int(causal), window, softcap,
                                              max_length, o.data_ptr(), None if lse is None else lse.data_ptr(), ws, nb, s),
                "qmatmul_cache_attention")

@@ -19,10 +19,11 @@ struct AttnArgs {
     void* out;
     float* lse;
     int many;              // the kernel for many rows
-    int tile_rows, tiles;  // tiles: upper bound over the batch
+    int tile_rows, tile_shift, tiles;  // a power of two; tiles: upper bound over the batch
     int pieces, piece_groups;
     float* part;           // [pieces][T * q_heads][dim] sums of a piece,
-    float* part_ml;        // [pieces][T * q_heads][2] its maximum and sum of exponentials
+    float* part_ml;        // [pieces][T * q_heads][2] its maximum and sum of exponentials,
+    int32_t* part_n;       // [T * q_heads] how many pieces the row has
 };
 
 #define QMM_ATTN_DECLARE(P)                                                                        \
@@ -68,24 +69,19 @@ struct AttnTile {
 __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int id, AttnTile& t)
 {
     const CacheArgs& c = a.c;
-    const int64_t base = c.starts[0];
-    auto first_id = [&](int s) { return ((int64_t)c.starts[s] - base) * a.per / a.tile_rows + s; };
-    int lo = 0, hi = c.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_id(mid) <= id) lo = mid;
-        else hi = mid;
-    }
-    const int64_t n0 = c.starts[lo], n1 = c.starts[lo + 1];
+    const int32_t base = c.starts[0];
+    const CacheSequence q = cache_sequence(
+        c, id, [&](int32_t start, int s) { return (int)(((int64_t)start - base) * a.per >> a.tile_shift) + s; });
+    const int64_t n0 = q.n0, n1 = q.n1;
     if (n0 < 0 || n1 > c.T || n1 <= n0) return false;  // no rows, or starts that name rows that are not there
-    const int64_t rows = (n1 - n0) * a.per, r0 = (id - first_id(lo)) * a.tile_rows;
+    const int64_t rows = (n1 - n0) * a.per, r0 = (int64_t)(id - q.first) << a.tile_shift;
     if (r0 < 0 || r0 >= rows) return false;
-    t.s = lo;
+    t.s = q.s;
     t.n0 = n0;
     t.rows = (int)rows;
     t.r0 = (int)r0;
-    t.first = (int64_t)c.lengths[lo] - (n1 - n0);
-    const int64_t held = (int64_t)c.width * c.page_size, len = c.lengths[lo];
+    t.first = q.length - (n1 - n0);
+    const int64_t held = (int64_t)c.width * c.page_size, len = q.length;
     t.len = len < held ? len : held;
     return true;
 }
@@ -96,7 +92,7 @@ __device__ __forceinline__ int attn_pieces(const AttnArgs& a, const AttnTile& t,
     g0 = t.lo(a, r0) >> 6;
     g1 = (int)(((int64_t)t.hi(a, r1) + 63) >> 6);
     if (g1 <= g0) return g1 = g0, 1;
-    const int n = (g1 - g0 + a.piece_groups - 1) / a.piece_groups;
+    const int n = (int)((uint32_t)(g1 - g0 + a.piece_groups - 1) / (uint32_t)a.piece_groups);
     return n < a.pieces ? n : a.pieces;
 }
 

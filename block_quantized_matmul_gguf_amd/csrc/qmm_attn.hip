@@ -13,7 +13,9 @@ namespace {
 
 // out = sum_z o_z 2^(m_z - m) / sum_z l_z 2^(m_z - m) over the pieces of a row.
 // `lanes` neighbouring threads hold a row's dimensions, four each; `share` such
-// sets take the pieces in turn.
+// sets take the pieces in turn.  Few bytes: the chain of loads is what it costs,
+// so four pieces are loaded at a time, and the number of pieces comes from the
+// kernel before.
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int lanes, int share)
 {
     __shared__ float acc[256][5];
@@ -21,36 +23,41 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int lanes, i
     const int tid = (int)threadIdx.x, per_row = lanes * share, slot = tid / per_row;
     const int d = 4 * (tid % lanes), part = tid / lanes % share;
     const int64_t all = c.T * a.q_heads, row = (int64_t)blockIdx.x * (256 / per_row) + slot;
-    float top = -3.402823466e38f, sum = 0.0f;
+    const float none = -3.402823466e38f;
+    float top = none, sum = 0.0f;
     f32x4_t v = f32x4_t{0, 0, 0, 0};
     int pieces = 0;
-    if (row < all && d < c.dim) {
-        const int64_t n = row / a.q_heads;
-        const int s = cache_sequence_of(c, n), h = (int)(row - n * a.q_heads) % a.per;
-        AttnTile t;
-        if (s >= 0) {
-            const int64_t n0 = c.starts[s], n1 = c.starts[s + 1], held = (int64_t)c.width * c.page_size;
-            t.s = s;
-            t.n0 = n0;
-            t.rows = n0 >= 0 && n1 <= c.T ? (int)((n1 - n0) * a.per) : 0;
-            t.first = (int64_t)c.lengths[s] - (n1 - n0);
-            t.len = c.lengths[s] < held ? c.lengths[s] : held;
-            const int r = (int)(n - n0) * a.per + h;
-            t.r0 = r / a.tile_rows * a.tile_rows;
-            int g0, g1;
-            if (r < t.rows) pieces = attn_pieces(a, t, t.r0, min(t.r0 + a.tile_rows, t.rows) - 1, g0, g1);
-        }
-        if (pieces > 1) {
-            for (int z = part; z < pieces; z += share) top = fmaxf(top, a.part_ml[2 * (z * all + row)]);
-            for (int z = part; z < pieces; z += share) {
-                const int64_t p = z * all + row;
-                const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - top);
-                const f32x4_t x = *(const f32x4_t*)(a.part + p * c.dim + d);
-                sum += f * a.part_ml[2 * p + 1];
+    const int64_t first = (int64_t)c.starts[0] * a.q_heads, behind = (int64_t)c.starts[c.batch] * a.q_heads;
+    if (row < all && d < c.dim && row >= first && row < behind) {  // others belong to no sequence
+        pieces = min(a.part_n[row], a.pieces);
+        if (pieces > 1)
+            for (int z0 = part; z0 < pieces; z0 += 4 * share) {
+                float m[4], l[4];
+                f32x4_t x[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = fmaf(f, x[k], v[k]);
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t p = min(z0 + i * share, pieces - 1) * all + row;
+                    m[i] = a.part_ml[2 * p];
+                    l[i] = a.part_ml[2 * p + 1];
+                    x[i] = *(const f32x4_t*)(a.part + p * c.dim + d);
+                }
+                float now = top;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now = fmaxf(now, m[i]);
+                const float keep = __builtin_amdgcn_exp2f(top - now);
+                top = now;
+                sum *= keep;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] *= keep;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (z0 + i * share >= pieces) continue;
+                    const float f = __builtin_amdgcn_exp2f(m[i] - now);
+                    sum += f * l[i];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = fmaf(f, x[i][k], v[k]);
+                }
             }
-        }
     }
     if (share > 1) {
         acc[tid][0] = top;
@@ -88,19 +95,22 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 int64_t plan_attention(AttnArgs& a, int64_t max_length)
 {
     const CacheArgs& c = a.c;
-    const int64_t rows = (c.T * a.per + c.batch - 1) / c.batch, most = c.dim > 128 ? 64 : 128;
-    a.tile_rows = 16;
+    const int64_t rows = (c.T * a.per + c.batch - 1) / c.batch;
+    auto workgroups = [&](int tile_rows) { return (c.T * a.per / tile_rows + c.batch) * c.heads; };
     a.many = c.type != QMM_F32 && rows >= 128 && !(c.type == QMM_F16 && c.dim > 128);
-    if (a.many) a.tile_rows = 256;
+    a.tile_rows = 16;
+    if (a.many) a.tile_rows = c.dim <= 128 && workgroups(256) < 256 ? 128 : 256;
     else
-        while (a.tile_rows < most && a.tile_rows < rows) a.tile_rows *= 2;
+        while (a.tile_rows < (c.dim > 128 ? 64 : 128) && a.tile_rows < rows && workgroups(a.tile_rows) > 512) a.tile_rows *= 2;
+    a.tile_shift = __builtin_ctz(a.tile_rows);
     a.tiles = (int)(c.T * a.per / a.tile_rows + c.batch);
     int64_t span = (int64_t)c.width * c.page_size;
     if (max_length > 0) span = std::min(span, max_length);
     if (a.window) span = std::min(span, (int64_t)a.window + a.tile_rows + 126);
     const int64_t groups = std::max<int64_t>(1, (span + CACHE_GROUP - 1) / CACHE_GROUP);
     const int64_t base = (int64_t)a.tiles * c.heads;
-    const int64_t want = std::min(((a.many ? 256 : 512) + base - 1) / base, (groups + 7) / 8);
+    const int64_t target = a.tile_rows == 256 ? 256 : a.many ? 1024 : 512, least = a.many ? 4 : 8;
+    const int64_t want = std::min((target + base - 1) / base, (groups + least - 1) / least);
     a.piece_groups = (int)((groups + want - 1) / want);
     a.pieces = (int)((groups + a.piece_groups - 1) / a.piece_groups);
     if (a.pieces <= 1) {
@@ -108,7 +118,7 @@ int64_t plan_attention(AttnArgs& a, int64_t max_length)
         return 0;
     }
     const int64_t all = c.T * a.q_heads;
-    return align256(a.pieces * all * c.dim * 4) + align256(a.pieces * all * 8);
+    return align256(a.pieces * all * c.dim * 4) + align256(a.pieces * all * 8) + align256(all * 4);
 }
 
 hipError_t launch_attention(AttnArgs& a, void* ws, hipStream_t s)
@@ -118,6 +128,7 @@ hipError_t launch_attention(AttnArgs& a, void* ws, hipStream_t s)
     if (a.pieces > 1) {
         a.part = (float*)ws;
         a.part_ml = (float*)((char*)ws + align256(a.pieces * all * c.dim * 4));
+        a.part_n = (int32_t*)((char*)a.part_ml + align256(a.pieces * all * 8));
     }
     const bool two = c.type == QMM_F32;
     const int rt = a.tile_rows > 16 && c.dim <= 128 ? 2 : 1;

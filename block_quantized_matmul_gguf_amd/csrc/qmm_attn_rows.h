@@ -460,6 +460,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const float y[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
             store4(a.out, c.type, to * D + d, y);
+            if (a.pieces > 1 && d == 0) a.part_n[to] = 1;
             if (a.lse && d == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
         } else {
             const int64_t p = piece * (c.T * a.q_heads) + to;
@@ -467,6 +468,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
             if (d == 0) {
                 a.part_ml[2 * p] = top;
                 a.part_ml[2 * p + 1] = sum;
+                if (piece == 0) a.part_n[to] = pieces;
             }
         }
     }

@@ -63,7 +63,7 @@ QMM_DEV half8_t mul8(half8_t a, half2_t s)
 }
 
 template <int FK, int FV, int DB, int NK, int RT, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
 {
     constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a thread's keys
     constexpr int VN = FV == FMT_Q8_0 ? 8 : 4, VU = (DB * 64 + 255) / 256;  // of a unit of values; units of a thread
@@ -426,6 +426,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_tile_kernel(AttnArgs a)
                 else *(f32x4_t*)(a.part + p * D + d) = f32x4_t{y[0], y[1], y[2], y[3]};
             }
         if (h == 0) {
+            if (a.pieces > 1 && piece == 0) a.part_n[at[rt]] = pieces;
             if (pieces > 1) {
                 a.part_ml[2 * p] = m[rt] - LIFT;
                 a.part_ml[2 * p + 1] = sum;
@@ -458,8 +459,9 @@ hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
 template <int FK, int FV, int DB>
 hipError_t launch_attn_tile_db(const AttnArgs& a, hipStream_t s)
 {
-    if (a.c.type == QMM_F16) {
-        if constexpr (DB <= 4) return launch_attn_tile<FK, FV, DB, 2, 1, 8>(a, s);
+    if constexpr (DB <= 4) {
+        if (a.tile_rows == 128) return a.c.type == QMM_F16 ? launch_attn_tile<FK, FV, DB, 2, 1, 4>(a, s) : launch_attn_tile<FK, FV, DB, 1, 1, 4>(a, s);
+        if (a.c.type == QMM_F16) return launch_attn_tile<FK, FV, DB, 2, 1, 8>(a, s);
     }
     return launch_attn_tile<FK, FV, DB, 1, 1, 8>(a, s);
 }

@@ -100,18 +100,33 @@ __device__ __forceinline__ uint32_t cache_page_of(const CacheArgs& c, uint32_t g
     return c.page_magic ? __umulhi(group, c.page_magic) : group;
 }
 
-// Sequence s of token row n: the last whose start is at or before n; -1 if n
-// lies before the first or behind the last.
-__device__ __forceinline__ int cache_sequence_of(const CacheArgs& c, int64_t n)
+// The sequence of tile `id`: the last s whose first(starts[s], s) is at or below
+// it, the same in every lane of the wave.  A step compares 64 sequences, so the
+// chain of dependent loads is one for up to 64 of them.  With it come the bounds
+// of its rows and its length.
+struct CacheSequence {
+    int s, first;  // first(s): id - first counts its tiles
+    int64_t n0, n1, length;
+};
+template <class F>
+__device__ __forceinline__ CacheSequence cache_sequence(const CacheArgs& c, int id, F first)
 {
-    int lo = 0, hi = c.batch;  // starts[lo] <= n < starts[hi] wanted
-    if (n < c.starts[0] || n >= c.starts[c.batch]) return -1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (c.starts[mid] <= n) lo = mid;
-        else hi = mid;
+    const int lane = (int)__lane_id();
+    int lo = 0, hi = c.batch;
+    while (true) {
+        const int step = (hi - lo + 63) >> 6, at = lo + lane * step;
+        const bool in = at < hi;
+        const int s = in ? at : lo;
+        const int32_t n0 = c.starts[s], n1 = c.starts[s + 1], length = c.lengths[s];
+        const int begin = first(n0, s);
+        const uint64_t below = __ballot(in && begin <= id);
+        const int pick = below ? __popcll(below) - 1 : 0;
+        lo += pick * step;
+        hi = lo + step < hi ? lo + step : hi;
+        if (step > 1) continue;
+        return {lo, __builtin_amdgcn_readlane(begin, pick), __builtin_amdgcn_readlane(n0, pick), __builtin_amdgcn_readlane(n1, pick),
+                __builtin_amdgcn_readlane(length, pick)};
     }
-    return lo;
 }
 
 // The page of a position of sequence s, or -1: before the sequence, past the

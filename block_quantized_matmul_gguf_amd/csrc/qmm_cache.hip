@@ -31,25 +31,19 @@ struct CacheTile {
 };
 QMM_DEV bool cache_tile(const CacheArgs& c, int id, CacheTile& t)
 {
-    const int64_t base = c.starts[0];
-    auto first_id = [&](int s) { return ((int64_t)c.starts[s] - base) / CACHE_GROUP + 2 * (int64_t)s; };
-    int lo = 0, hi = c.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_id(mid) <= id) lo = mid;
-        else hi = mid;
-    }
-    const int64_t n0 = c.starts[lo], n1 = c.starts[lo + 1];
+    const int32_t base = c.starts[0];
+    const CacheSequence q = cache_sequence(c, id, [&](int32_t start, int s) { return (int)(((int64_t)start - base) >> 6) + 2 * s; });
+    const int64_t n0 = q.n0, n1 = q.n1;
     if (n0 < 0 || n1 > c.T || n1 <= n0) return false;  // no rows, or starts that name rows that are not there
-    const int64_t p0 = (int64_t)c.lengths[lo] - (n1 - n0);
+    const int64_t p0 = q.length - (n1 - n0);
     // groups counted from the one of p0, which may lie before the sequence
-    const int64_t group = (p0 >> 6) + (id - first_id(lo)), from = group * CACHE_GROUP;
+    const int64_t group = (p0 >> 6) + (id - q.first), from = group * CACHE_GROUP;
     const int64_t a = p0 > from ? p0 : from, b = p0 + (n1 - n0) < from + CACHE_GROUP ? p0 + (n1 - n0) : from + CACHE_GROUP;
     if (a >= b) return false;
     t.ta = (int)(a - from);
     t.tb = (int)(b - from);
     t.n = n0 + (a - p0);
-    t.page = cache_page(c, lo, from);
+    t.page = cache_page(c, q.s, from);
     t.in_page = t.page < 0 ? 0 : (int)(group - (int64_t)cache_page_of(c, (uint32_t)group) * c.page_groups);
     return true;
 }
