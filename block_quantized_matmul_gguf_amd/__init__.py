@@ -637,21 +637,23 @@ def w4_matmul(q, scales, x, zeros=None, y=None, stream=None):
 #
 # Streams, scratch and outputs as with the experts' calls above.
 
-def _is(t, dtype, dims, index):
-    """Whether ``_tensor`` would accept t, in the few steps that a good argument needs."""
-    return (isinstance(t, _torch().Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == dims and t.get_device() == index
-            and t.is_contiguous())
-
-
 def _cache_args(fmt_k, fmt_v, k_cache, v_cache, table, starts, lengths):
     """Checks a cache and a batch; their ``qmm_cache``."""
     torch = _torch()
-    if not isinstance(k_cache, torch.Tensor) or not _is(k_cache, torch.uint8, 4, k_cache.get_device()):
-        _tensor(k_cache, torch.uint8, (4,), "k_cache")
-    index = k_cache.get_device()
-    for t, dtype, dims, name in ((v_cache, torch.uint8, 4, "v_cache"), (table, torch.int32, 2, "table"),
-                                 (starts, torch.int32, 1, "starts"), (lengths, torch.int32, 1, "lengths")):
-        if not _is(t, dtype, dims, index):
+    u8, i32 = torch.uint8, torch.int32
+    try:  # what good arguments need, in few steps; the others are told what is wrong below
+        index = k_cache.get_device()
+        good = (index >= 0 and k_cache.dtype is u8 and k_cache.dim() == 4 and k_cache.is_contiguous()
+                and v_cache.get_device() == index and v_cache.dtype is u8 and v_cache.is_contiguous()
+                and table.get_device() == index and table.dtype is i32 and table.dim() == 2 and table.is_contiguous()
+                and starts.get_device() == index and starts.dtype is i32 and starts.dim() == 1 and starts.is_contiguous()
+                and lengths.get_device() == index and lengths.dtype is i32 and lengths.dim() == 1 and lengths.is_contiguous())
+    except AttributeError:
+        good = False
+    if not good:
+        _tensor(k_cache, u8, (4,), "k_cache")
+        for t, dtype, dims, name in ((v_cache, u8, 4, "v_cache"), (table, i32, 2, "table"), (starts, i32, 1, "starts"),
+                                     (lengths, i32, 1, "lengths")):
             _tensor(t, dtype, (dims,), name, k_cache.device)
     if (fmt_k != Q8_0 and fmt_k != Q4_0) or (fmt_v != Q8_0 and fmt_v != Q4_0):
         raise ValueError(f"cache formats are Q8_0 and Q4_0, got {fmt_k} and {fmt_v}")
@@ -736,7 +738,8 @@ def cache_load(fmt_k: int, fmt_v: int, k_cache, v_cache, table, starts, lengths,
     shape = (tokens, c.heads, c.dim)
 
     def body(s):
-        ko, vo = _out(k, shape, dtype, dev, "k"), _out(v, shape, dtype, dev, "v")
+        ko = _out(k, shape, dtype, dev, "k")
+        vo = torch.empty_like(ko) if v is None else _out(v, shape, dtype, dev, "v")
         _check(lib().qmatmul_cache_load(c, tokens, _type_of(ko, "k"), ko.data_ptr(), vo.data_ptr(), s), "qmatmul_cache_load")
         return ko, vo
 
@@ -762,17 +765,21 @@ def cache_attention(fmt_k: int, fmt_v: int, k_cache, v_cache, q, table, starts, 
     torch = _torch()
     c = _cache_args(fmt_k, fmt_v, k_cache, v_cache, table, starts, lengths)
     dev = k_cache.device
-    t, heads, step, code = _token_rows(q, None, c.dim, "q", dev)
+    dim = c.dim
+    t, heads, step, code = _token_rows(q, None, dim, "q", dev)
     if lse is not None:
         _out(lse, (t, heads), torch.float32, dev, "lse")
     if scale is None:
-        scale = c.dim ** -0.5
+        scale = dim ** -0.5
+    pages, cache_heads, page_size, _ = k_cache.shape
+    batch, width = table.shape
+    causal = 1 if causal else 0
 
     def body(s):
-        o = _out(out, (t, heads, c.dim), q.dtype, dev, "out")
-        ws, nb, keep = _scratch(_attention_workspace(c.format_k, c.format_v, c.pages, c.page_size, c.heads, c.dim, c.batch,
-                                                     c.table_width, t, heads, code, int(causal), window, max_length), dev)
-        _check(lib().qmatmul_cache_attention(c, t, heads, code, q.data_ptr(), step, scale, int(causal), window, softcap,
+        o = torch.empty_like(q) if out is None and q.is_contiguous() else _out(out, (t, heads, dim), q.dtype, dev, "out")
+        ws, nb, keep = _scratch(_attention_workspace(fmt_k, fmt_v, pages, page_size, cache_heads, dim, batch, width, t, heads,
+                                                     code, causal, window, max_length), dev)
+        _check(lib().qmatmul_cache_attention(c, t, heads, code, q.data_ptr(), step, scale, causal, window, softcap,
                                              max_length, o.data_ptr(), None if lse is None else lse.data_ptr(), ws, nb, s),
                "qmatmul_cache_attention")
         return o

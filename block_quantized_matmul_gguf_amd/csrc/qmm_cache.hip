@@ -86,85 +86,126 @@ QMM_DEV int nibble_bit(int i) { return 16 * (i & 1) + 4 * (i >> 1); }
 
 constexpr int CACHE_THREADS = 256;
 
-template <int DB>
-__global__ __launch_bounds__(CACHE_THREADS) void store_kernel(StoreArgs a)
+// round-half-away of |y| < 2^22, as the quantizer's roundf: 0.5 less its last bit
+// takes every half away from zero and nothing below one.
+QMM_DEV int round_away(float y) { return (int)(y + __builtin_copysignf(0x1.fffffep-2f, y)); }
+
+template <int DB, int FMT, bool VALUES>
+QMM_DEV void store_group(const StoreArgs& a, const CacheTile& t, const CacheBlock& k, uint8_t* codes, uint16_t* scales)
 {
 #pragma clang fp contract(off)
-    constexpr int D = 32 * DB, OCT = D / 8;
-    __shared__ __align__(16) uint8_t codes[64 * D / 8 * 9];
-    __shared__ uint16_t scales[DB * 64];
+    constexpr int D = 32 * DB, OCT = D / 8, ITEMS = (16 * OCT + CACHE_THREADS - 1) / CACHE_THREADS, fmt = FMT;
+    constexpr bool q8 = FMT == QMM_Q8_0;
     const CacheArgs& c = a.c;
-    CacheTile t;
-    CacheBlock k;
-    if (!cache_block(c, t, k) || t.page < 0) return;
-    const int fmt = k.fmt, tid = (int)threadIdx.x;
-    const bool q8 = fmt == QMM_Q8_0;
-    const void* src = k.values ? a.v : a.k;
-    const int64_t stride = k.values ? a.v_stride : a.k_stride;
-
-    // where a word is shared by tokens that are not all here it starts as it is in memory
-    const int size = q8 ? 64 * D : 32 * D;
+    const int tid = (int)threadIdx.x, lane = (int)__lane_id();
     const bool whole = t.ta == 0 && t.tb == 64;
-    if (!q8 && k.values) {
-        for (int w = 4 * tid; w < size; w += 4 * CACHE_THREADS)
-            *(uint32_t*)(codes + padded(w)) = whole ? 0u : *(const uint32_t*)(k.at + w);
+    const void* src = VALUES ? a.v : a.k;
+    const int64_t stride = VALUES ? a.v_stride : a.k_stride;
+
+    // Four neighbouring tokens (a quad of the values' order) by an octet per thread (dim 256: two of them); the
+    // four lanes of a block stay together.  Loaded before the page is known: one latency for both.
+    const int rows = t.tb - t.ta, quads = ((t.tb + 3) >> 2) - (t.ta >> 2);
+    float x[ITEMS][4][8];
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+        const int i = tid + it * CACHE_THREADS, r = i / OCT, o = i - r * OCT, t0 = (t.ta & ~3) + 4 * r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (t0 + j >= t.ta && t0 + j < t.tb) {
+                load8(src, c.type, (t.n + t0 + j - t.ta) * stride + (int64_t)k.head * D + 8 * o, x[it][j]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[it][j][e] = 0.0f;
+            }
+        }
+    }
+    if (t.page < 0) return;
+
+    // where a byte is shared by tokens that are not all here it starts as it is in memory
+    const int size = q8 ? 64 * D : 32 * D;
+    if (!q8 && VALUES && !whole) {
+        for (int w = 4 * tid; w < size; w += 4 * CACHE_THREADS) *(uint32_t*)(codes + padded(w)) = *(const uint32_t*)(k.at + w);
         __syncthreads();
     }
-    const int rows = t.tb - t.ta;
-    for (int i = tid; i < (rows * OCT + 3) / 4 * 4; i += CACHE_THREADS) {  // the four lanes of a block stay together
-        const int r = i / OCT, o = i - r * OCT, tok = t.ta + r;
-        float x[8];
-        load8(src, c.type, (t.n + r) * stride + (int64_t)k.head * D + 8 * o, x);
-        float top = 0.0f, first = 0.0f;
-        bool fine = true;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float m = fabsf(x[e]);
-            fine = fine && m <= 3.402823466e38f;
-            if (m > top) {
-                top = m;
-                first = x[e];
-            }
-        }
-        // over the block's four lanes: the largest, and the first lane that has it
-        float best = fmaxf(top, dpp_f<DPP_X1>(top));
-        best = fmaxf(best, dpp_f<DPP_X2>(best));
-        float bad = fine ? 0.0f : 1.0f;
-        bad = fmaxf(bad, dpp_f<DPP_X1>(bad));
-        bad = fmaxf(bad, dpp_f<DPP_X2>(bad));
-        const int lane = (int)__lane_id();
-        const uint32_t have = (uint32_t)(__ballot(top == best) >> (lane & 60)) & 15u;
-        const float mx = __shfl(first, (lane & 60) + (have ? __builtin_ctz(have) : 0));
-        const float d = q8 ? best / 127.0f : mx / -8.0f;
-        uint16_t bits = f16bits(d);
-        const bool dead = bad != 0.0f || (bits & 0x7fff) >= 0x7c00, none = dead || (bits & 0x7fff) == 0;
-        const float id = none ? 0.0f : 1.0f / d;
-        if (dead) bits = 0x7e00;
-        uint32_t q[8];
+    for (int it = 0; it < ITEMS; ++it) {
+        const int i = tid + it * CACHE_THREADS, r = i / OCT, o = i - r * OCT, t0 = (t.ta & ~3) + 4 * r;
+        if (r >= quads) continue;
+        uint32_t w[4][2];  // codes of a token: bytes, or eight nibbles in the first
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (q8) q[e] = none ? 128u : (uint32_t)(q8_0_q(x[e], id) + 128) & 255u;
-            else q[e] = none ? 8u : (uint32_t)min(15, (int)(x[e] * id + 8.5f));
-        }
-        if ((o & 3) == 0) scales[(o >> 2) * 64 + cache_place(tok)] = bits;
-        if (!k.values) {
-            uint8_t* to = codes + padded(key_byte<DB>(fmt, tok, o));
+        for (int j = 0; j < 4; ++j) {
+            // the block's largest magnitude over its four lanes, as bits: above those of the largest number is
+            // what is not finite
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, __builtin_bit_cast(uint32_t, x[it][j][e]) & 0x7fffffffu);
+            const uint32_t mine = top;
+            top = max(top, (uint32_t)dpp_i<DPP_X1>((int)top));
+            top = max(top, (uint32_t)dpp_i<DPP_X2>((int)top));
+            float d = __builtin_bit_cast(float, top);
             if (q8) {
-                *(uint32_t*)to = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
-                *(uint32_t*)(to + 4) = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
-            } else {
-                *(uint32_t*)to = q[0] | q[2] << 4 | q[4] << 8 | q[6] << 12 | q[1] << 16 | q[3] << 20 | q[5] << 24 | q[7] << 28;
+                d = d / 127.0f;
+            } else {  // the first element that has it, with its sign
+                float first = 0.0f;
+#pragma unroll
+                for (int e = 7; e >= 0; --e) first = (__builtin_bit_cast(uint32_t, x[it][j][e]) & 0x7fffffffu) == top ? x[it][j][e] : first;
+                const uint32_t have = (uint32_t)(__ballot(mine == top) >> (lane & 60)) & 15u;
+                d = __shfl(first, (lane & 60) + (have ? __builtin_ctz(have) : 0)) / -8.0f;
             }
-        } else {
+            uint16_t bits = f16bits(d);
+            const bool dead = top >= 0x7f800000u || (bits & 0x7fff) >= 0x7c00, none = dead || (bits & 0x7fff) == 0;
+            const float id = none ? 0.0f : 1.0f / d;
+            if (dead) bits = 0x7e00;
+            int q[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int w = padded(value_byte(fmt, tok & ~3, 8 * o + e));
-                if (q8) {
-                    codes[w + (tok & 3)] = (uint8_t)q[e];
+                const float v = none ? 0.0f : x[it][j][e] * id;  // (0 times an infinity is none)
+                q[e] = q8 ? round_away(v) : min(15, (int)(v + 8.5f));
+            }
+            if (q8) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    w[j][h] = (__builtin_amdgcn_perm((uint32_t)q[4 * h + 1], (uint32_t)q[4 * h], 0x0c0c0400u) |
+                               __builtin_amdgcn_perm((uint32_t)q[4 * h + 3], (uint32_t)q[4 * h + 2], 0x04000c0cu)) ^ 0x80808080u;
+            } else {
+                w[j][0] = (uint32_t)(q[0] | q[2] << 4 | q[4] << 8 | q[6] << 12 | q[1] << 16 | q[3] << 20 | q[5] << 24) | (uint32_t)q[7] << 28;
+            }
+            const bool here = t0 + j >= t.ta && t0 + j < t.tb;
+            if ((o & 3) == 0 && here) scales[(o >> 2) * 64 + cache_place(t0 + j)] = bits;
+            if (!VALUES && here) {
+                uint8_t* to = codes + padded(key_byte<DB>(fmt, t0 + j, o));
+                *(uint32_t*)to = w[j][0];
+                if (q8) *(uint32_t*)(to + 4) = w[j][1];
+            }
+        }
+        if (!VALUES) continue;
+        const bool all = t0 >= t.ta && t0 + 4 <= t.tb;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint8_t* to = codes + padded(value_byte(fmt, t0, 8 * o + e));
+            if (q8) {  // byte e of each token's codes
+                const uint32_t s = 0x04000400u + 0x01010101u * (e & 3);
+                const uint32_t lo = __builtin_amdgcn_perm(w[1][e >> 2], w[0][e >> 2], s), hi = __builtin_amdgcn_perm(w[3][e >> 2], w[2][e >> 2], s);
+                const uint32_t four = (lo & 0xffffu) | (hi << 16);
+                if (all) {
+                    *(uint32_t*)to = four;
                 } else {
-                    const int bit = 8 * ((tok >> 4) & 1) + nibble_bit(tok & 3);
-                    if (!whole) atomicAnd((uint32_t*)(codes + w), ~(15u << bit));
-                    atomicOr((uint32_t*)(codes + w), q[e] << bit);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (t0 + j >= t.ta && t0 + j < t.tb) to[j] = (uint8_t)(four >> (8 * j));
+                }
+            } else {  // tokens 0 and 2 of a quad in one byte, 1 and 3 in another, which no other quad has
+                const int bit = 4 * ((e >> 1) + 4 * (e & 1));
+                to += (t0 >> 4) & 1;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t a0 = (w[y][0] >> bit) & 15u, a2 = (w[y + 2][0] >> bit) & 15u;
+                    uint32_t both = a0 | a2 << 4;
+                    if (!all) {
+                        const uint32_t keep = (t0 + y >= t.ta && t0 + y < t.tb ? 0u : 15u) | (t0 + y + 2 >= t.ta && t0 + y + 2 < t.tb ? 0u : 0xf0u);
+                        both = (both & ~keep) | (to[2 * y] & keep);
+                    }
+                    to[2 * y] = (uint8_t)both;
                 }
             }
         }
@@ -173,7 +214,7 @@ __global__ __launch_bounds__(CACHE_THREADS) void store_kernel(StoreArgs a)
     // out: pieces that hold tokens of the call alone as a whole
     if (whole) {
         for (int w = 16 * tid; w < size; w += 16 * CACHE_THREADS) *(u32x4_t*)(k.at + w) = *(const u32x4_t*)(codes + padded(w));
-    } else if (!k.values) {
+    } else if (!VALUES) {
         for (int i = tid; i < rows * OCT; i += CACHE_THREADS) {
             const int r = i / OCT, at = key_byte<DB>(fmt, t.ta + r, i - r * OCT);
             *(uint32_t*)(k.at + at) = *(const uint32_t*)(codes + padded(at));
@@ -197,18 +238,30 @@ __global__ __launch_bounds__(CACHE_THREADS) void store_kernel(StoreArgs a)
 }
 
 template <int DB>
-__global__ __launch_bounds__(CACHE_THREADS) void load_kernel(LoadArgs a)
+__global__ __launch_bounds__(CACHE_THREADS) void store_kernel(StoreArgs a)
 {
-    constexpr int D = 32 * DB, OCT = D / 8;
-    __shared__ __align__(16) uint8_t codes[64 * D / 8 * 9];
-    __shared__ __align__(16) uint16_t scales[DB * 64];
-    const CacheArgs& c = a.c;
+    __shared__ __align__(16) uint8_t codes[64 * 32 * DB / 8 * 9];
+    __shared__ uint16_t scales[DB * 64];
     CacheTile t;
     CacheBlock k;
-    if (!cache_block(c, t, k)) return;
-    const int fmt = k.fmt, tid = (int)threadIdx.x;
-    const bool q8 = fmt == QMM_Q8_0;
-    void* dst = k.values ? a.v : a.k;
+    if (!cache_block(a.c, t, k)) return;
+    if (k.fmt == QMM_Q8_0) {
+        if (k.values) store_group<DB, QMM_Q8_0, true>(a, t, k, codes, scales);
+        else store_group<DB, QMM_Q8_0, false>(a, t, k, codes, scales);
+    } else {
+        if (k.values) store_group<DB, QMM_Q4_0, true>(a, t, k, codes, scales);
+        else store_group<DB, QMM_Q4_0, false>(a, t, k, codes, scales);
+    }
+}
+
+template <int DB, int FMT, bool VALUES>
+QMM_DEV void load_group(const LoadArgs& a, const CacheTile& t, const CacheBlock& k, uint8_t* codes, uint16_t* scales)
+{
+    constexpr int D = 32 * DB, OCT = D / 8, fmt = FMT;
+    constexpr bool q8 = FMT == QMM_Q8_0;
+    const CacheArgs& c = a.c;
+    const int tid = (int)threadIdx.x;
+    void* dst = VALUES ? a.v : a.k;
     auto row = [&](int tok, int o) { return ((t.n + tok - t.ta) * c.heads + k.head) * D + 8 * o; };
     const int rows = t.tb - t.ta;
     if (t.page < 0) {
@@ -236,7 +289,7 @@ __global__ __launch_bounds__(CACHE_THREADS) void load_kernel(LoadArgs a)
     for (int i = tid; i < quads * OCT; i += CACHE_THREADS) {
         const int r = i / OCT, o = i - r * OCT, t0 = (t.ta & ~3) + 4 * r;
         float x[4][8];  // [token][dimension] codes
-        if (!k.values) {
+        if (!VALUES) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int at = key_byte<DB>(fmt, t0 + j, o);
@@ -266,6 +319,23 @@ __global__ __launch_bounds__(CACHE_THREADS) void load_kernel(LoadArgs a)
             for (int e = 0; e < 8; ++e) x[j][e] *= s;
             store8(dst, c.type, row(t0 + j, o), x[j]);
         }
+    }
+}
+
+template <int DB>
+__global__ __launch_bounds__(CACHE_THREADS) void load_kernel(LoadArgs a)
+{
+    __shared__ __align__(16) uint8_t codes[64 * 32 * DB / 8 * 9];
+    __shared__ __align__(16) uint16_t scales[DB * 64];
+    CacheTile t;
+    CacheBlock k;
+    if (!cache_block(a.c, t, k)) return;
+    if (k.fmt == QMM_Q8_0) {
+        if (k.values) load_group<DB, QMM_Q8_0, true>(a, t, k, codes, scales);
+        else load_group<DB, QMM_Q8_0, false>(a, t, k, codes, scales);
+    } else {
+        if (k.values) load_group<DB, QMM_Q4_0, true>(a, t, k, codes, scales);
+        else load_group<DB, QMM_Q4_0, false>(a, t, k, codes, scales);
     }
 }
 
