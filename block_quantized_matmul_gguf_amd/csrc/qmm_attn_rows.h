@@ -316,7 +316,15 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
                     for (int i = 0; i < 4; ++i) p[rt][4 * u + i] = fmaf(s[i], x[i], p[rt][4 * u + i]);
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);  // the scales of one tile at a time in registers
+            if constexpr (DB > 4) {
+                // sums of one tile at a time: with all four in flight their parts and scales fill the registers (24
+                // to 120 of them were kept in memory).  Up to dim 128 they fit, and a wave that has them in flight
+                // is faster: 142 us against 180 us for 64 sequences.
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    asm volatile("" : "+v"(p[rt][4 * u]), "+v"(p[rt][4 * u + 1]), "+v"(p[rt][4 * u + 2]), "+v"(p[rt][4 * u + 3]));
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
 
         fetch_keys(ahead, ahead_page, ahead < wg1);
