@@ -96,12 +96,29 @@ __device__ __forceinline__ int attn_pieces(const AttnArgs& a, const AttnTile& t,
     return n < a.pieces ? n : a.pieces;
 }
 
-// The bytes of a group of one head as a buffer: its base in scalar registers, a
-// lane's offset in one, and nothing read past it (bytes == 0: nothing at all).
-__device__ __forceinline__ rsrc_t attn_group(const uint8_t* base, const CacheArgs& c, int32_t page, int head, int g, int64_t bytes, bool any = true)
+// The bytes of one head in the pages: of a group a buffer with its base in scalar
+// registers, a lane's offset in one, and nothing read past it (any == false:
+// nothing at all).
+struct AttnHead {
+    const uint8_t *k, *v;   // the head in page 0
+    uint32_t step_k, step_v;  // bytes from page to page (at most 2^10 heads * 2^7 groups * 17408 < 2^32)
+    uint32_t bytes_k, bytes_v;
+};
+__device__ __forceinline__ AttnHead attn_head(const CacheArgs& c, int head)
 {
-    const int in_page = g - (int)cache_page_of(c, (uint32_t)g) * c.page_groups;
-    return make_rsrc(base + (((int64_t)page * c.heads + head) * c.page_groups + in_page) * bytes, any ? (uint32_t)bytes : 0u);
+    const uint32_t k = (uint32_t)c.group_k * (uint32_t)c.page_groups, v = (uint32_t)c.group_v * (uint32_t)c.page_groups;
+    return {c.k + (uint64_t)k * (uint32_t)head, c.v + (uint64_t)v * (uint32_t)head, k * (uint32_t)c.heads, v * (uint32_t)c.heads,
+            (uint32_t)c.group_k, (uint32_t)c.group_v};
+}
+__device__ __forceinline__ rsrc_t attn_keys(const AttnHead& h, const CacheArgs& c, int32_t page, int g, bool any = true)
+{
+    const uint32_t in_page = (uint32_t)g - cache_page_of(c, (uint32_t)g) * (uint32_t)c.page_groups;
+    return make_rsrc(h.k + ((uint64_t)h.step_k * (uint32_t)page + in_page * h.bytes_k), any ? h.bytes_k : 0u);
+}
+__device__ __forceinline__ rsrc_t attn_values(const AttnHead& h, const CacheArgs& c, int32_t page, int g, bool any = true)
+{
+    const uint32_t in_page = (uint32_t)g - cache_page_of(c, (uint32_t)g) * (uint32_t)c.page_groups;
+    return make_rsrc(h.v + ((uint64_t)h.step_v * (uint32_t)page + in_page * h.bytes_v), any ? h.bytes_v : 0u);
 }
 #endif
 

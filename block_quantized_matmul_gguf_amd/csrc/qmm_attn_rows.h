@@ -179,13 +179,12 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
         const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + h) * D;
         float x[DB][8], top = 0.0f;
         bool fine = true;
+        load_octets<DB>(a.q, c.type, from + 8 * g4, 32, x);  // (a row past the last: the sequence's first)
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[b][e] = 0.0f;
-            if (live) load8(a.q, c.type, from + 32 * b + 8 * g4, x[b]);
-#pragma unroll
             for (int e = 0; e < 8; ++e) {
+                x[b][e] = live ? x[b][e] : 0.0f;
                 top = fmaxf(top, fabsf(x[b][e]));
                 fine = fine && fabsf(x[b][e]) <= 3.402823466e38f;
             }
@@ -216,6 +215,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
     float* ks = lds + wave * SCALES;
     float* vs = ks + DB * 64;
     const int32_t* row = c.table + (int64_t)t.s * c.width;
+    const AttnHead mem = attn_head(c, head);
     int expo = -1000;  // E
 
     // the wave's groups, and those of them that have a page
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
     // are of nothing: a branch round them would keep the scores' parts in registers until after it.
     uint32_t kr[4][KN], vr[DB][VN], sk[SN], sv[SN];
     auto fetch_keys = [&](int g, int32_t page, bool any) {
-        const rsrc_t kp = attn_group(c.k, c, page, head, g, c.group_k, any), vp = attn_group(c.v, c, page, head, g, c.group_v, any);
+        const rsrc_t kp = attn_keys(mem, c, page, g, any), vp = attn_values(mem, c, page, g, any);
 #pragma unroll
         for (int i = 0; i < SN; ++i) {  // an odd number of blocks: past the end, and zero
             sk[i] = __builtin_amdgcn_raw_buffer_load_b32(kp, (uint32_t)lane * 4 + 256 * i, 1024 * KN, 0);
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
         for (int u = 0; u < 4; ++u) load_pieces<KN>(kp, u * 256 * KN, (uint32_t)lane, kr[u]);
     };
     auto fetch_values = [&](int g, int32_t page, bool any) {
-        const rsrc_t vp = attn_group(c.v, c, page, head, g, c.group_v, any);
+        const rsrc_t vp = attn_values(mem, c, page, g, any);
 #pragma unroll
         for (int b = 0; b < DB; ++b) load_pieces<VN>(vp, b * 256 * VN, (uint32_t)lane, vr[b]);
     };
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
 
         fetch_values(ahead, ahead_page, ahead < wg1);
         if (__any(odd)) {  // values that are not finite: NaN to the rows that see them
-            const rsrc_t vp = attn_group(c.v, c, page, head, g, c.group_v);
+            const rsrc_t vp = attn_values(mem, c, page, g);
 #pragma unroll
             for (int b = 0; b < DB; ++b)
                 for (int pl = 0; pl < 64; ++pl) {

@@ -39,15 +39,12 @@ QMM_DEV uint32_t wave_max_u16x2(u16x2_t v)
     v = max_dpp_u16x2<DPP_X2>(v);
     v = max_dpp_u16x2<DPP_HMIRROR>(v);
     v = max_dpp_u16x2<DPP_MIRROR>(v);
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    uint32_t lo = 0, hi = 0;
-#pragma unroll
-    for (int l = 0; l < 64; l += 16) {
-        const uint32_t x = (uint32_t)__builtin_amdgcn_readlane((int)u, l);
-        lo = max(lo, x & 0xffffu);
-        hi = max(hi, x >> 16);
-    }
-    return lo | (hi << 16);
+    uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    u = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, (uint32_t)a[0]), __builtin_bit_cast(u16x2_t, (uint32_t)a[1])));
+    const auto b = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    u = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, (uint32_t)b[0]), __builtin_bit_cast(u16x2_t, (uint32_t)b[1])));
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)u);
 }
 
 QMM_DEV half8_t mul8(half8_t a, half2_t s)
@@ -62,7 +59,7 @@ QMM_DEV half8_t mul8(half8_t a, half2_t s)
     return r;
 }
 
-template <int FK, int FV, int DB, int NK, int RT, int NW>
+template <int FK, int FV, int DB, int NK, int RT, int NW, bool SKEW = true>
 __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
 {
     constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a thread's keys
@@ -112,19 +109,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
         const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
         float top = 0.0f;
         bool fine = true;
-        // twice over the row (it is in the caches): its largest value, then the operands
+        float x[2 * DB][8];
+        load_octets<2 * DB>(a.q, c.type, from + 8 * h, 16, x);  // (a row past the last: the sequence's first)
 #pragma unroll
-        for (int ks = 0; ks < 2 * DB; ++ks) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-            if (live) load8(a.q, c.type, from + 16 * ks + 8 * h, x);
+        for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                top = fmaxf(top, fabsf(x[e]));
-                fine = fine && fabsf(x[e]) <= 3.402823466e38f;
+                x[ks][e] = live ? x[ks][e] : 0.0f;
+                top = fmaxf(top, fabsf(x[ks][e]));
+                fine = fine && fabsf(x[ks][e]) <= 3.402823466e38f;
             }
-        }
         {
             const uint32_t u = __builtin_bit_cast(uint32_t, top), f = fine ? 0u : 1u;
             const auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
@@ -136,14 +130,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
         const float up = sign * ldexpf(1.0f, e2);
         factor[rt] = fabsf(a.scale) * ldexpf(1.0f, -e2);
 #pragma unroll
-        for (int ks = 0; ks < 2 * DB; ++ks) {
-            float x[8];
+        for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-            if (live) load8(a.q, c.type, from + 16 * ks + 8 * h, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[rt][ks][e] = (_Float16)(fine ? x[e] * up : __builtin_nanf(""));
-        }
+            for (int e = 0; e < 8; ++e) q[rt][ks][e] = (_Float16)(fine ? x[ks][e] * up : __builtin_nanf(""));
         m[rt] = -3.0e38f;
         l[rt] = 0.0f;
 #pragma unroll
@@ -153,19 +142,19 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
     }
 
     const int32_t* row = c.table + (int64_t)t.s * c.width;
-    // the next group at or after g that has a page
+    const AttnHead mem = attn_head(c, head);
+    // the next group at or after g that has a page; `page`: the entry of g's, loaded before
+    auto entry = [&](int g) { return table_entry(row, cache_page_of(c, (uint32_t)min(g, g1 - 1))); };
     auto next = [&](int g, int32_t& page) {
-        for (; g < g1; ++g) {
-            page = table_entry(row, cache_page_of(c, (uint32_t)g));
-            if (page >= 0 && page < c.pages) break;
-        }
+        while (g < g1 && (page < 0 || page >= c.pages))
+            if (++g < g1) page = entry(g);
         return g;
     };
     const bool do_k = NW == 4 || wave < 4, do_v = NW == 4 || wave >= 4;
     const int unit = tid & 255, unit_wave = wave & 3;  // tiles of keys, blocks of values to a wave
     uint32_t kr[KN], vr[VU][VN], sk[SN], sv[SN];
     auto fetch = [&](int g, int32_t page) {
-        const rsrc_t kp = attn_group(c.k, c, page, head, g, c.group_k), vp = attn_group(c.v, c, page, head, g, c.group_v);
+        const rsrc_t kp = attn_keys(mem, c, page, g), vp = attn_values(mem, c, page, g);
 #pragma unroll
         for (int i = 0; i < SN; ++i) {  // an odd number of blocks: past the end, and zero
             sk[i] = __builtin_amdgcn_raw_buffer_load_b32(kp, (uint32_t)lane * 4 + 256 * i, 1024 * KN, 0);
@@ -178,9 +167,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
                 if (DB % 4 == 0 || unit_wave + 4 * i < DB) load_pieces<VN>(vp, (uint32_t)((unit_wave + 4 * i) * 256 * VN), (uint32_t)lane, vr[i]);
         }
     };
-    // of the 64 tokens that are decoded next, and of those in LDS: exponents taken off keys and values, and
-    // whether a value is not finite
-    int k_expo = 0, v_expo = NONE, new_expo = NONE;
+    // of the 64 tokens that were decoded last: exponents taken off keys and values, and whether a value is not
+    // finite
+    int k_expo = 0, v_expo = NONE;
     bool odd = false;
     auto decode = [&](int g, uint8_t* stage) {
         const bool whole = g * 64 >= glo && g * 64 + 64 <= ghi;
@@ -223,9 +212,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
         // power of two that f16 holds (2^15 at most: the smallest scales become normal with it too)
         const int ke = (int)((top & 0xffffu) >> 10), ve = (int)(top >> 26);
         k_expo = max(ke - 22, -15);
-        new_expo = top >> 16 ? max(v_expo, max(ve - 22, -15)) : v_expo;
+        if (top >> 16) v_expo = max(v_expo, max(ve - 22, -15));
         const _Float16 kd = __builtin_bit_cast(_Float16, (uint16_t)((15 - k_expo) << 10));
-        const _Float16 vd = __builtin_bit_cast(_Float16, (uint16_t)(new_expo == NONE ? 0 : (15 - new_expo) << 10));
+        const _Float16 vd = __builtin_bit_cast(_Float16, (uint16_t)(v_expo == NONE ? 0 : (15 - v_expo) << 10));
 #pragma unroll
         for (int i = 0; i < SN; ++i) {
             const int w = lane + 64 * i;
@@ -277,137 +266,168 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
         }
     };
 
-    int32_t page = -1;
-    int g = next(g0, page), cur = 0;
+    f32x16_t s[RT][2];
+    half8_t p[RT][2][2];
+    auto scores = [&](const uint8_t* stage) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[rt][half][i] = 0.0f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int ks = 0; ks < 2 * DB; ++ks)
+#pragma unroll
+                for (int nk = 0; nk < NK; ++nk) {
+                    const half8_t k = *(const half8_t*)(stage + nk * KB + ((2 * ks + h) * 64 + 32 * half + col) * 16);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) s[rt][half] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[rt][ks], s[rt][half], 0, 0, 0);
+                }
+    };
+    auto sums = [&](const uint8_t* stage) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int b = 0; b < DB; ++b) {
+                    const half8_t v = *(const half8_t*)(stage + KB * NK + ((4 * half + 2 * ks + h) * D + 32 * b + col) * 16);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) o[rt][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[rt][half][ks], o[rt][b], 0, 0, 0);
+                }
+    };
+    auto softmax = [&](int g) {
+        const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
+        const float unit_k = ldexpf(1.0f, k_expo);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float f = fmaxf(factor[rt] * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
+            if (a.cap != 0.0f) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[rt][half][i] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[rt][half][i] * (2.8853900817779268f * f)));
+                f = a.cap;
+            }
+            if (masked) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        // row 8 (i / 4) + 4 h + i % 4 of the tile: quad 2 (i / 4) + h
+                        const int quad = ((i >> 2) & 1) * 4 + (i >> 3) * 2, j = g * 64 + 32 * half + 4 * (quad + h) + (i & 3);
+                        s[rt][half][i] = j >= lo[rt] && j < hi[rt] ? s[rt][half][i] : -__builtin_inff();
+                    }
+            }
+            float best = s[rt][0][0];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) best = fmaxf(best, s[rt][half][i]);
+            const uint32_t u = __builtin_bit_cast(uint32_t, best);
+            const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+            best = f * fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
+            if (__any(best > m[rt] + RAISE)) {
+                const float now = fmaxf(m[rt], best), keep = __builtin_amdgcn_exp2f(m[rt] - now);
+                l[rt] *= keep;
+#pragma unroll
+                for (int b = 0; b < DB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[rt][b][i] *= keep;
+                m[rt] = now;
+            }
+            const float off = LIFT - m[rt];
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][half][i], f, off));
+                    sum[i & 3] += e;
+                    p[rt][half][i >> 3][i & 7] = (_Float16)e;
+                }
+            l[rt] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+    };
+    // values that are not finite: NaN to the rows that see them
+    auto spoil = [&](int g, int32_t page) {
+        const rsrc_t vp = attn_values(mem, c, page, g);
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+            for (int pl = 0; pl < 64; ++pl) {
+                const float x = f16lo(__builtin_amdgcn_raw_buffer_load_b16(vp, 0, 256 * VN * DB + 2 * (64 * b + pl), 0));
+                if (fabsf(x) <= 65504.0f) continue;
+                const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float add = j >= lo[rt] && j < hi[rt] ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[rt][b][i] += add;
+                }
+            }
+    };
+
+    // Time slots between barriers.  Waves 0..3 (one on each SIMD) use the matrix cores in the even ones, scores of
+    // tile j and sums of tile j - 1, and the vector units in the odd ones, softmax of j and the decoding of keys j + 1;
+    // waves 4..7 (again one on each) do the same one slot later, with values j + 1 to decode.  So a SIMD has a
+    // wave for each of its units at any time, where waves in step would wait for each other's: 377 us against
+    // 237 us.  Two buffers do: keys of j are written in slot 2 j - 1 and read in 2 j and 2 j + 1, values in slot 2 j and
+    // in 2 j + 2 and 2 j + 3.  With four waves there is one wave on a SIMD (and another workgroup).
+    const bool late = SKEW && NW == 8 && wave >= 4;
+    int32_t page = g0 < g1 ? entry(g0) : -1;
+    int g = next(g0, page), cur = 0, o_expo = NONE;  // o_expo: taken off the values in o
     if (g < g1) {
         fetch(g, page);
+        if (late) __syncthreads();
         decode(g, smem);
-        int32_t ahead_page = -1;
+        __syncthreads();
+        int32_t ahead_page = entry(g + 1);
         int ahead = next(g + 1, ahead_page);
         if (ahead < g1) fetch(ahead, ahead_page);
+        bool before = false;  // the tile before has sums to come
         while (true) {
-            __syncthreads();
             const uint8_t* stage = smem + cur * STAGE;
-            const float shift = new_expo != v_expo ? ldexpf(1.0f, v_expo - new_expo) : 1.0f;  // 0 the first time
-            const bool rescale = new_expo != v_expo, was_odd = odd;
-            const float unit_k = ldexpf(1.0f, k_expo);
-            v_expo = new_expo;
-            if (rescale) {
+            const bool seen = g * 64 + 64 > wlo && g * 64 < whi;
+            if (seen) scores(stage);
+            if (before) sums(smem + (cur ^ 1) * STAGE);
+            __syncthreads();
+            int32_t then = entry(ahead + 1);  // (here for its latency: the other half waits for LDS)
+            if (o_expo != v_expo) {
+                const float shift = ldexpf(1.0f, o_expo - v_expo);  // 0 the first time
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                     for (int b = 0; b < DB; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
+                o_expo = v_expo;
             }
-            if (g * 64 + 64 > wlo && g * 64 < whi) {
-                f32x16_t s[RT][2];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) s[rt][half][i] = 0.0f;
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int ks = 0; ks < 2 * DB; ++ks)
-#pragma unroll
-                        for (int nk = 0; nk < NK; ++nk) {
-                            const half8_t k = *(const half8_t*)(stage + nk * KB + ((2 * ks + h) * 64 + 32 * half + col) * 16);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) s[rt][half] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[rt][ks], s[rt][half], 0, 0, 0);
-                        }
-                half8_t p[RT][2][2];
-                const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    float f = fmaxf(factor[rt] * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
-                    if (a.cap != 0.0f) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                s[rt][half][i] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[rt][half][i] * (2.8853900817779268f * f)));
-                        f = a.cap;
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                // row 8 (i / 4) + 4 h + i % 4 of the tile: quad 2 (i / 4) + h
-                                const int quad = ((i >> 2) & 1) * 4 + (i >> 3) * 2, j = g * 64 + 32 * half + 4 * (quad + h) + (i & 3);
-                                s[rt][half][i] = j >= lo[rt] && j < hi[rt] ? s[rt][half][i] : -__builtin_inff();
-                            }
-                    }
-                    float best = s[rt][0][0];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) best = fmaxf(best, s[rt][half][i]);
-                    const uint32_t u = __builtin_bit_cast(uint32_t, best);
-                    const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-                    best = f * fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
-                    if (__any(best > m[rt] + RAISE)) {
-                        const float now = fmaxf(m[rt], best), keep = __builtin_amdgcn_exp2f(m[rt] - now);
-                        l[rt] *= keep;
-#pragma unroll
-                        for (int b = 0; b < DB; ++b)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[rt][b][i] *= keep;
-                        m[rt] = now;
-                    }
-                    const float off = LIFT - m[rt];
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][half][i], f, off));
-                            sum += e;
-                            p[rt][half][i >> 3][i & 7] = (_Float16)e;
-                        }
-                    l[rt] += sum;
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                        for (int b = 0; b < DB; ++b) {
-                            const half8_t v = *(const half8_t*)(stage + KB * NK + ((4 * half + 2 * ks + h) * D + 32 * b + col) * 16);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) o[rt][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[rt][half][ks], o[rt][b], 0, 0, 0);
-                        }
-                if (was_odd) {  // values that are not finite: NaN to the rows that see them
-                    const rsrc_t vp = attn_group(c.v, c, page, head, g, c.group_v);
-#pragma unroll
-                    for (int b = 0; b < DB; ++b)
-                        for (int pl = 0; pl < 64; ++pl) {
-                            const float x = f16lo(__builtin_amdgcn_raw_buffer_load_b16(vp, 0, 256 * VN * DB + 2 * (64 * b + pl), 0));
-                            if (fabsf(x) <= 65504.0f) continue;
-                            const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) {
-                                const float add = j >= lo[rt] && j < hi[rt] ? __builtin_nanf("") : 0.0f;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[rt][b][i] += add;
-                            }
-                        }
-                }
+            if (seen) {
+                softmax(g);
+                if (odd) spoil(g, page);
             }
-            if (ahead >= g1) break;
+            before = seen;
+            const bool more = ahead < g1;
+            if (more) {
+                decode(ahead, smem + (cur ^ 1) * STAGE);
+                g = ahead;
+                page = ahead_page;
+                ahead = next(g + 1, then);
+                ahead_page = then;
+                if (ahead < g1) fetch(ahead, ahead_page);
+            }
+            __syncthreads();
+            if (!more) break;
             cur ^= 1;
-            decode(ahead, smem + cur * STAGE);
-            g = ahead;
-            page = ahead_page;
-            ahead = next(g + 1, ahead_page);
-            if (ahead < g1) fetch(ahead, ahead_page);
         }
+        if (before) sums(smem + cur * STAGE);
+        if (SKEW && NW == 8 && !late) __syncthreads();
     }
 
-    const float unit_v = v_expo != NONE ? ldexpf(1.0f, v_expo) : 0.0f;
+    const float unit_v = o_expo != NONE ? ldexpf(1.0f, o_expo) : 0.0f;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const uint32_t u = __builtin_bit_cast(uint32_t, l[rt]);
@@ -437,7 +457,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
     }
 }
 
-template <int FK, int FV, int DB, int NK, int RT, int NW>
+template <int FK, int FV, int DB, int NK, int RT, int NW, bool SKEW = true>
 hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
 {
     constexpr int lds = 2 * 64 * 32 * DB * 2 * (NK + 1) + NW * 2 * DB * 64 * 2;
@@ -447,12 +467,12 @@ hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     if (dev >= 64 || !done[dev]) {
-        e = hipFuncSetAttribute((const void*)attn_tile_kernel<FK, FV, DB, NK, RT, NW>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        e = hipFuncSetAttribute((const void*)attn_tile_kernel<FK, FV, DB, NK, RT, NW, SKEW>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
     const int64_t blocks = (int64_t)a.tiles * a.c.heads * a.pieces;
-    hipLaunchKernelGGL((attn_tile_kernel<FK, FV, DB, NK, RT, NW>), dim3((uint32_t)blocks), dim3(64 * NW), lds, s, a);
+    hipLaunchKernelGGL((attn_tile_kernel<FK, FV, DB, NK, RT, NW, SKEW>), dim3((uint32_t)blocks), dim3(64 * NW), lds, s, a);
     return hipGetLastError();
 }
 
@@ -463,6 +483,8 @@ hipError_t launch_attn_tile_db(const AttnArgs& a, hipStream_t s)
         if (a.tile_rows == 128) return a.c.type == QMM_F16 ? launch_attn_tile<FK, FV, DB, 2, 1, 4>(a, s) : launch_attn_tile<FK, FV, DB, 1, 1, 4>(a, s);
         if (a.c.type == QMM_F16) return launch_attn_tile<FK, FV, DB, 2, 1, 8>(a, s);
     }
+    static const int cfg = getenv("ATTN_CFG") ? atoi(getenv("ATTN_CFG")) : 0;
+    if constexpr (DB == 4) if (cfg == 1) return launch_attn_tile<FK, FV, DB, 1, 1, 8, false>(a, s);
     return launch_attn_tile<FK, FV, DB, 1, 1, 8>(a, s);
 }
 

@@ -75,6 +75,39 @@ QMM_DEV void load8(const void* p, int type, int64_t at, float x[8])
         }
     }
 }
+// N octets of a token's row, `step` values apart, as f32: all loads before the
+// first is waited for.
+template <int N>
+QMM_DEV void load_octets(const void* p, int type, int64_t at, int step, float x[N][8])
+{
+    if (type == QMM_F32) {
+        f32x4_t w[N][2];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            w[n][0] = *(const f32x4_t*)((const float*)p + at + n * step);
+            w[n][1] = *(const f32x4_t*)((const float*)p + at + n * step + 4);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[n][i] = w[n][i >> 2][i & 3];
+        return;
+    }
+    u32x4_t w[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = *(const u32x4_t*)((const uint16_t*)p + at + n * step);
+    if (type == QMM_F16) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[n][i] = i & 1 ? f16hi(w[n][i >> 1]) : f16lo(w[n][i >> 1]);
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[n][i] = __builtin_bit_cast(float, i & 1 ? w[n][i >> 1] & 0xffff0000u : w[n][i >> 1] << 16);
+    }
+}
 // Four, and eight, of an output row.
 QMM_DEV void store4(void* p, int type, int64_t at, const float x[4])
 {
