@@ -99,7 +99,7 @@ int64_t plan_attention(AttnArgs& a, int64_t max_length)
     auto workgroups = [&](int tile_rows) { return (c.T * a.per / tile_rows + c.batch) * c.heads; };
     a.many = c.type != QMM_F32 && rows >= 128 && !(c.type == QMM_F16 && c.dim > 128);
     a.tile_rows = 16;
-    if (a.many) a.tile_rows = c.dim <= 128 && workgroups(256) < 256 ? 128 : 256;
+    if (a.many) a.tile_rows = c.dim > 128 || workgroups(256) < 256 ? 128 : 256;
     else
         while (a.tile_rows < (c.dim > 128 ? 64 : 128) && a.tile_rows < rows && workgroups(a.tile_rows) > 512) a.tile_rows *= 2;
     a.tile_shift = __builtin_ctz(a.tile_rows);

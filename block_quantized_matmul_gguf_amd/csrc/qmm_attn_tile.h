@@ -59,8 +59,8 @@ QMM_DEV half8_t mul8(half8_t a, half2_t s)
     return r;
 }
 
-template <int FK, int FV, int DB, int NK, int RT, int NW, bool SKEW = true>
-__global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
+template <int FK, int FV, int DB, int NK, int RT, int NW>
+__global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(AttnArgs a)
 {
     constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a thread's keys
     constexpr int VN = FV == FMT_Q8_0 ? 8 : 4, VU = (DB * 64 + 255) / 256;  // of a unit of values; units of a thread
@@ -143,46 +143,47 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
 
     const int32_t* row = c.table + (int64_t)t.s * c.width;
     const AttnHead mem = attn_head(c, head);
-    // the next group at or after g that has a page; `page`: the entry of g's, loaded before
+    // the first group at or after g that has a page; `page`: the entry of g, loaded before
     auto entry = [&](int g) { return table_entry(row, cache_page_of(c, (uint32_t)min(g, g1 - 1))); };
     auto next = [&](int g, int32_t& page) {
         while (g < g1 && (page < 0 || page >= c.pages))
             if (++g < g1) page = entry(g);
         return g;
     };
+    // Who decodes: with eight waves the first four keys, the others values.
     const bool do_k = NW == 4 || wave < 4, do_v = NW == 4 || wave >= 4;
     const int unit = tid & 255, unit_wave = wave & 3;  // tiles of keys, blocks of values to a wave
     uint32_t kr[KN], vr[VU][VN], sk[SN], sv[SN];
-    auto fetch = [&](int g, int32_t page) {
-        const rsrc_t kp = attn_keys(mem, c, page, g), vp = attn_values(mem, c, page, g);
+    auto fetch_keys = [&](int g, int32_t page) {  // of no group: zeros
+        const rsrc_t kp = attn_keys(mem, c, page, g, g < g1);
 #pragma unroll
-        for (int i = 0; i < SN; ++i) {  // an odd number of blocks: past the end, and zero
-            sk[i] = __builtin_amdgcn_raw_buffer_load_b32(kp, (uint32_t)lane * 4 + 256 * i, 1024 * KN, 0);
-            sv[i] = __builtin_amdgcn_raw_buffer_load_b32(vp, (uint32_t)lane * 4 + 256 * i, 256 * VN * DB, 0);
-        }
+        for (int i = 0; i < SN; ++i) sk[i] = __builtin_amdgcn_raw_buffer_load_b32(kp, (uint32_t)lane * 4 + 256 * i, 1024 * KN, 0);
         if (do_k) load_pieces<KN>(kp, (uint32_t)(unit_wave * 256 * KN), (uint32_t)lane, kr);
+    };
+    auto fetch_values = [&](int g, int32_t page) {
+        const rsrc_t vp = attn_values(mem, c, page, g, g < g1);
+#pragma unroll
+        for (int i = 0; i < SN; ++i) sv[i] = __builtin_amdgcn_raw_buffer_load_b32(vp, (uint32_t)lane * 4 + 256 * i, 256 * VN * DB, 0);
         if (do_v) {
 #pragma unroll
             for (int i = 0; i < VU; ++i)
                 if (DB % 4 == 0 || unit_wave + 4 * i < DB) load_pieces<VN>(vp, (uint32_t)((unit_wave + 4 * i) * 256 * VN), (uint32_t)lane, vr[i]);
         }
     };
-    // of the 64 tokens that were decoded last: exponents taken off keys and values, and whether a value is not
-    // finite
+    // Scales of the keys of group gk and of the values of group gv, brought to range, into the wave's LDS; the
+    // exponents taken off them, and whether a value is not finite.
     int k_expo = 0, v_expo = NONE;
     bool odd = false;
-    auto decode = [&](int g, uint8_t* stage) {
-        const bool whole = g * 64 >= glo && g * 64 + 64 <= ghi;
-        if (!whole) {  // of tokens that nobody sees anything may lie there
+    auto hide = [&](uint32_t (&w)[SN], int g) {  // of tokens that nobody sees anything may lie there
+        if (g * 64 >= glo && g * 64 + 64 <= ghi) return;
+        const int pl = 2 * (lane & 31), p = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+        const uint32_t keep = (p >= glo && p < ghi ? 0xffffu : 0u) | (p + 1 >= glo && p + 1 < ghi ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int i = 0; i < SN; ++i) {
-                const int pl = 2 * (lane & 31);
-                const int p = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
-                const uint32_t keep = (p >= glo && p < ghi ? 0xffffu : 0u) | (p + 1 >= glo && p + 1 < ghi ? 0xffff0000u : 0u);
-                sk[i] &= keep;
-                sv[i] &= keep;
-            }
-        }
+        for (int i = 0; i < SN; ++i) w[i] &= keep;
+    };
+    auto prepare = [&](int gk, int gv) {
+        hide(sk, gk);
+        hide(sv, gv);
         // the largest magnitude of each, as f16 bits (keys low, values high), over lane and wave
         u16x2_t kt = {0, 0}, vt = {0, 0};
 #pragma unroll
@@ -223,44 +224,44 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
             ((half2_t*)my_scales)[DB * 32 + w] = __builtin_bit_cast(half2_t, sv[i]) * half2_t{vd, vd};
         }
         wave_sync();
-        if (do_k) {  // one token's octet c of every block
-            const int u = unit >> 6, tok = 16 * u + (unit & 15), cc = (unit >> 4) & 3;
-            const int to = (tok & 32) + tile_row(tok & 31);
+    };
+    auto decode_keys = [&](uint8_t* stage) {  // one token's octet c of every block
+        const int u = unit >> 6, tok = 16 * u + (unit & 15), cc = (unit >> 4) & 3;
+        const int to = (tok & 32) + tile_row(tok & 31);
 #pragma unroll
-            for (int b = 0; b < DB; ++b) {
-                half8_t k;
-                if constexpr (FK == FMT_Q8_0) k = codes8_q8(kr[2 * b], kr[2 * b + 1]);
-                else k = codes8_q4(kr[b]);
-                const _Float16 s = my_scales[64 * b + cache_place(tok)];
-                const half8_t x = mul8(k, half2_t{s, s});
-                *(half8_t*)(stage + ((4 * b + cc) * 64 + to) * 16) = x;
-                if constexpr (NK == 2) {  // what the rounding took off, exactly
-                    half8_t y;
+        for (int b = 0; b < DB; ++b) {
+            half8_t k;
+            if constexpr (FK == FMT_Q8_0) k = codes8_q8(kr[2 * b], kr[2 * b + 1]);
+            else k = codes8_q4(kr[b]);
+            const _Float16 s = my_scales[64 * b + cache_place(tok)];
+            const half8_t x = mul8(k, half2_t{s, s});
+            *(half8_t*)(stage + ((4 * b + cc) * 64 + to) * 16) = x;
+            if constexpr (NK == 2) {  // what the rounding took off, exactly
+                half8_t y;
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const half2_t z = __builtin_elementwise_fma(half2_t{k[e], k[e + 1]}, half2_t{s, s}, -half2_t{x[e], x[e + 1]});
-                        y[e] = z[0];
-                        y[e + 1] = z[1];
-                    }
-                    *(half8_t*)(stage + KB + ((4 * b + cc) * 64 + to) * 16) = y;
+                for (int e = 0; e < 8; e += 2) {
+                    const half2_t z = __builtin_elementwise_fma(half2_t{k[e], k[e + 1]}, half2_t{s, s}, -half2_t{x[e], x[e + 1]});
+                    y[e] = z[0];
+                    y[e + 1] = z[1];
                 }
+                *(half8_t*)(stage + KB + ((4 * b + cc) * 64 + to) * 16) = y;
             }
         }
-        if (do_v) {  // sixteen tokens of dimensions n and n + 16 of a block
+    };
+    auto decode_values = [&](uint8_t* stage) {  // sixteen tokens of dimensions n and n + 16 of a block
 #pragma unroll
-            for (int i = 0; i < VU; ++i) {
-                const int v = unit + 256 * i, b = v >> 6, g4 = (v >> 4) & 3, n = v & 15;
-                if (DB % 4 != 0 && v >= 64 * DB) continue;
+        for (int i = 0; i < VU; ++i) {
+            const int b = unit_wave + 4 * i, g4 = (lane >> 4) & 3, n = lane & 15;
+            if (DB % 4 != 0 && b >= DB) continue;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const half8_t sc = *(const half8_t*)(my_scales + DB * 64 + 64 * b + 16 * g4 + 8 * s);
+            for (int s = 0; s < 2; ++s) {
+                const half8_t sc = *(const half8_t*)(my_scales + DB * 64 + 64 * b + 16 * g4 + 8 * s);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        half8_t x;
-                        if constexpr (FV == FMT_Q8_0) x = codes8_q8(vr[i][4 * p + 2 * s], vr[i][4 * p + 2 * s + 1]);
-                        else x = codes8_q4(vr[i][2 * p + s]);
-                        *(half8_t*)(stage + KB * NK + ((4 * s + g4) * D + 32 * b + 16 * p + n) * 16) = x * sc;
-                    }
+                for (int p = 0; p < 2; ++p) {
+                    half8_t x;
+                    if constexpr (FV == FMT_Q8_0) x = codes8_q8(vr[i][4 * p + 2 * s], vr[i][4 * p + 2 * s + 1]);
+                    else x = codes8_q4(vr[i][2 * p + s]);
+                    *(half8_t*)(stage + KB * NK + ((4 * s + g4) * D + 32 * b + 16 * p + n) * 16) = x * sc;
                 }
             }
         }
@@ -298,9 +299,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
                     for (int rt = 0; rt < RT; ++rt) o[rt][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[rt][half][ks], o[rt][b], 0, 0, 0);
                 }
     };
-    auto softmax = [&](int g) {
+    auto softmax = [&](int g, int expo) {
         const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
-        const float unit_k = ldexpf(1.0f, k_expo);
+        const float unit_k = ldexpf(1.0f, expo);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float f = fmaxf(factor[rt] * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
@@ -370,31 +371,49 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
             }
     };
 
-    // Time slots between barriers.  Waves 0..3 (one on each SIMD) use the matrix cores in the even ones, scores of
-    // tile j and sums of tile j - 1, and the vector units in the odd ones, softmax of j and the decoding of keys j + 1;
-    // waves 4..7 (again one on each) do the same one slot later, with values j + 1 to decode.  So a SIMD has a
-    // wave for each of its units at any time, where waves in step would wait for each other's: 377 us against
-    // 237 us.  Two buffers do: keys of j are written in slot 2 j - 1 and read in 2 j and 2 j + 1, values in slot 2 j and
-    // in 2 j + 2 and 2 j + 3.  With four waves there is one wave on a SIMD (and another workgroup).
-    const bool late = SKEW && NW == 8 && wave >= 4;
+    // Time slots between barriers.  Waves 0..3 (one on each SIMD) use the matrix cores in the even ones: scores of
+    // tile j and sums of tile j - 1, and in their shadow they decode keys j + 1; the odd ones are softmax of j.  Waves 4..7
+    // (again one on each SIMD) do the same one slot later, decoding values j.  So a SIMD has a wave for each of
+    // its units at any time.  Two buffers do: keys of j are written in slot 2 j - 2 and read in 2 j and 2 j + 1,
+    // values written in slot 2 j + 1 and read in 2 j + 2 and 2 j + 3.  With four waves there is one on a SIMD (and
+    // another workgroup), which decodes both.
+    // A tile that a wave does not see costs it nothing but time: its scores are all hidden.
+    const bool late = NW == 8 && wave >= 4;
+    int o_expo = NONE;  // taken off the values in o
     int32_t page = g0 < g1 ? entry(g0) : -1;
-    int g = next(g0, page), cur = 0, o_expo = NONE;  // o_expo: taken off the values in o
+    int g = next(g0, page);  // tile j
     if (g < g1) {
-        fetch(g, page);
+        int32_t page_b = entry(g + 1);
+        int g_b = next(g + 1, page_b);  // tile j + 1
+        int32_t page_c = entry(g_b + 1);
+        int g_c = next(g_b + 1, page_c);  // tile j + 2
+        fetch_keys(g, page);
+        fetch_values(g, page);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[rt][i >> 1][i & 1][e] = (_Float16)0.0f;
+        // sums before the first tile: of nothing, and of values that are numbers
+        for (int i = tid; i < KB / 16; i += 64 * NW) *(u32x4_t*)(smem + STAGE + KB * NK + 16 * i) = u32x4_t{0, 0, 0, 0};
         if (late) __syncthreads();
-        decode(g, smem);
+        prepare(g, g);
+        int expo = k_expo, expo_b = 0;
+        if (do_k) decode_keys(smem);
+        fetch_keys(g_b, page_b);
+        prepare(g_b, g);
+        expo_b = k_expo;
         __syncthreads();
-        int32_t ahead_page = entry(g + 1);
-        int ahead = next(g + 1, ahead_page);
-        if (ahead < g1) fetch(ahead, ahead_page);
-        bool before = false;  // the tile before has sums to come
-        while (true) {
-            const uint8_t* stage = smem + cur * STAGE;
-            const bool seen = g * 64 + 64 > wlo && g * 64 < whi;
-            if (seen) scores(stage);
-            if (before) sums(smem + (cur ^ 1) * STAGE);
+        for (int cur = 0;; cur ^= 1) {
+            scores(smem + cur * STAGE);
+            sums(smem + (cur ^ 1) * STAGE);
+            if (do_k) decode_keys(smem + (cur ^ 1) * STAGE);
+            if (do_v) decode_values(smem + cur * STAGE);
+            fetch_keys(g_c, page_c);
+            fetch_values(g_b, page_b);
             __syncthreads();
-            int32_t then = entry(ahead + 1);  // (here for its latency: the other half waits for LDS)
+            int32_t page_d = entry(g_c + 1);  // (here for its latency: the other half waits for LDS)
             if (o_expo != v_expo) {
                 const float shift = ldexpf(1.0f, o_expo - v_expo);  // 0 the first time
 #pragma unroll
@@ -405,26 +424,24 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
                         for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
                 o_expo = v_expo;
             }
-            if (seen) {
-                softmax(g);
-                if (odd) spoil(g, page);
-            }
-            before = seen;
-            const bool more = ahead < g1;
-            if (more) {
-                decode(ahead, smem + (cur ^ 1) * STAGE);
-                g = ahead;
-                page = ahead_page;
-                ahead = next(g + 1, then);
-                ahead_page = then;
-                if (ahead < g1) fetch(ahead, ahead_page);
-            }
+            softmax(g, expo);
+            if (odd) spoil(g, page);
+            prepare(g_c, g_b);
+            expo = expo_b;
+            expo_b = k_expo;
+            g = g_b;
+            page = page_b;
+            g_b = g_c;
+            page_b = page_c;
+            g_c = next(g_c + 1, page_d);
+            page_c = page_d;
             __syncthreads();
-            if (!more) break;
-            cur ^= 1;
+            if (g >= g1) {
+                sums(smem + cur * STAGE);
+                break;
+            }
         }
-        if (before) sums(smem + cur * STAGE);
-        if (SKEW && NW == 8 && !late) __syncthreads();
+        if (NW == 8 && !late) __syncthreads();
     }
 
     const float unit_v = o_expo != NONE ? ldexpf(1.0f, o_expo) : 0.0f;
@@ -457,7 +474,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a)
     }
 }
 
-template <int FK, int FV, int DB, int NK, int RT, int NW, bool SKEW = true>
+template <int FK, int FV, int DB, int NK, int RT, int NW>
 hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
 {
     constexpr int lds = 2 * 64 * 32 * DB * 2 * (NK + 1) + NW * 2 * DB * 64 * 2;
@@ -467,12 +484,12 @@ hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     if (dev >= 64 || !done[dev]) {
-        e = hipFuncSetAttribute((const void*)attn_tile_kernel<FK, FV, DB, NK, RT, NW, SKEW>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        e = hipFuncSetAttribute((const void*)attn_tile_kernel<FK, FV, DB, NK, RT, NW>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
     const int64_t blocks = (int64_t)a.tiles * a.c.heads * a.pieces;
-    hipLaunchKernelGGL((attn_tile_kernel<FK, FV, DB, NK, RT, NW, SKEW>), dim3((uint32_t)blocks), dim3(64 * NW), lds, s, a);
+    hipLaunchKernelGGL((attn_tile_kernel<FK, FV, DB, NK, RT, NW>), dim3((uint32_t)blocks), dim3(64 * NW), lds, s, a);
     return hipGetLastError();
 }
 
@@ -483,9 +500,7 @@ hipError_t launch_attn_tile_db(const AttnArgs& a, hipStream_t s)
         if (a.tile_rows == 128) return a.c.type == QMM_F16 ? launch_attn_tile<FK, FV, DB, 2, 1, 4>(a, s) : launch_attn_tile<FK, FV, DB, 1, 1, 4>(a, s);
         if (a.c.type == QMM_F16) return launch_attn_tile<FK, FV, DB, 2, 1, 8>(a, s);
     }
-    static const int cfg = getenv("ATTN_CFG") ? atoi(getenv("ATTN_CFG")) : 0;
-    if constexpr (DB == 4) if (cfg == 1) return launch_attn_tile<FK, FV, DB, 1, 1, 8, false>(a, s);
-    return launch_attn_tile<FK, FV, DB, 1, 1, 8>(a, s);
+    return launch_attn_tile<FK, FV, DB, 1, 1, DB <= 4 ? 8 : 4>(a, s);
 }
 
 #define QMM_ATTN_TILE(P, FK, FV)                                         \
