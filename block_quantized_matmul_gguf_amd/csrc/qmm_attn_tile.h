@@ -14,6 +14,8 @@
 // code * d rounded to f16; both times a power of two per 64 tokens, so that
 // neither end of f16's range is met.
 #pragma once
+#include <type_traits>
+
 #include "qmm_attn_rows.h"
 
 namespace qmm {
@@ -67,6 +69,7 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     constexpr int SN = (DB + 1) / 2, KB = 64 * D * 2, STAGE = KB * (NK + 1), SCALE = 2 * DB * 64;
     constexpr int ROWS = 32 * RT;
     constexpr int NONE = -1000;  // no exponent yet
+    enum { KEYS, VALUES, BOTH };  // what a wave decodes
     constexpr float RAISE = 8.0f, LIFT = 6.0f;  // powers of two: what m may lag behind, and p at m
     extern __shared__ __align__(16) uint8_t smem[];
     const CacheArgs& c = a.c;
@@ -144,23 +147,21 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     const int32_t* row = c.table + (int64_t)t.s * c.width;
     const AttnHead mem = attn_head(c, head);
     // the first group at or after g that has a page; `page`: the entry of g, loaded before
-    auto entry = [&](int g) { return table_entry(row, cache_page_of(c, (uint32_t)min(g, g1 - 1))); };
-    auto next = [&](int g, int32_t& page) {
+    auto entry = [&](int g) __attribute__((always_inline)) { return table_entry(row, cache_page_of(c, (uint32_t)min(g, g1 - 1))); };
+    auto next = [&](int g, int32_t& page) __attribute__((always_inline)) {
         while (g < g1 && (page < 0 || page >= c.pages))
             if (++g < g1) page = entry(g);
         return g;
     };
-    // Who decodes: with eight waves the first four keys, the others values.
-    const bool do_k = NW == 4 || wave < 4, do_v = NW == 4 || wave >= 4;
     const int unit = tid & 255, unit_wave = wave & 3;  // tiles of keys, blocks of values to a wave
     uint32_t kr[KN], vr[VU][VN], sk[SN], sv[SN];
-    auto fetch_keys = [&](int g, int32_t page) {  // of no group: zeros
+    auto fetch_keys = [&](int g, int32_t page, bool do_k) __attribute__((always_inline)) {  // of no group: zeros
         const rsrc_t kp = attn_keys(mem, c, page, g, g < g1);
 #pragma unroll
         for (int i = 0; i < SN; ++i) sk[i] = __builtin_amdgcn_raw_buffer_load_b32(kp, (uint32_t)lane * 4 + 256 * i, 1024 * KN, 0);
         if (do_k) load_pieces<KN>(kp, (uint32_t)(unit_wave * 256 * KN), (uint32_t)lane, kr);
     };
-    auto fetch_values = [&](int g, int32_t page) {
+    auto fetch_values = [&](int g, int32_t page, bool do_v) __attribute__((always_inline)) {
         const rsrc_t vp = attn_values(mem, c, page, g, g < g1);
 #pragma unroll
         for (int i = 0; i < SN; ++i) sv[i] = __builtin_amdgcn_raw_buffer_load_b32(vp, (uint32_t)lane * 4 + 256 * i, 256 * VN * DB, 0);
@@ -174,14 +175,14 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     // exponents taken off them, and whether a value is not finite.
     int k_expo = 0, v_expo = NONE;
     bool odd = false;
-    auto hide = [&](uint32_t (&w)[SN], int g) {  // of tokens that nobody sees anything may lie there
+    auto hide = [&](uint32_t (&w)[SN], int g) __attribute__((always_inline)) {  // of tokens that nobody sees anything may lie there
         if (g * 64 >= glo && g * 64 + 64 <= ghi) return;
         const int pl = 2 * (lane & 31), p = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
         const uint32_t keep = (p >= glo && p < ghi ? 0xffffu : 0u) | (p + 1 >= glo && p + 1 < ghi ? 0xffff0000u : 0u);
 #pragma unroll
         for (int i = 0; i < SN; ++i) w[i] &= keep;
     };
-    auto prepare = [&](int gk, int gv) {
+    auto prepare = [&](int gk, int gv) __attribute__((always_inline)) {
         hide(sk, gk);
         hide(sv, gv);
         // the largest magnitude of each, as f16 bits (keys low, values high), over lane and wave
@@ -225,81 +226,85 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
         }
         wave_sync();
     };
-    auto decode_keys = [&](uint8_t* stage) {  // one token's octet c of every block
-        const int u = unit >> 6, tok = 16 * u + (unit & 15), cc = (unit >> 4) & 3;
-        const int to = (tok & 32) + tile_row(tok & 31);
+    const int key_tok = 16 * (unit >> 6) + (unit & 15), key_place = cache_place(key_tok);
+    const int key_at = (((unit >> 4) & 3) * 64 + (key_tok & 32) + tile_row(key_tok & 31)) * 16;
+    auto decode_key = [&](uint8_t* stage, int b) __attribute__((always_inline)) {  // one token's octet of block b
+        half8_t k;
+        if constexpr (FK == FMT_Q8_0) k = codes8_q8(kr[2 * b], kr[2 * b + 1]);
+        else k = codes8_q4(kr[b]);
+        const _Float16 s = my_scales[64 * b + key_place];
+        const half8_t x = mul8(k, half2_t{s, s});
+        *(half8_t*)(stage + key_at + 4096 * b) = x;
+        if constexpr (NK == 2) {  // what the rounding took off, exactly
+            half8_t y;
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
-            half8_t k;
-            if constexpr (FK == FMT_Q8_0) k = codes8_q8(kr[2 * b], kr[2 * b + 1]);
-            else k = codes8_q4(kr[b]);
-            const _Float16 s = my_scales[64 * b + cache_place(tok)];
-            const half8_t x = mul8(k, half2_t{s, s});
-            *(half8_t*)(stage + ((4 * b + cc) * 64 + to) * 16) = x;
-            if constexpr (NK == 2) {  // what the rounding took off, exactly
-                half8_t y;
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const half2_t z = __builtin_elementwise_fma(half2_t{k[e], k[e + 1]}, half2_t{s, s}, -half2_t{x[e], x[e + 1]});
-                    y[e] = z[0];
-                    y[e + 1] = z[1];
-                }
-                *(half8_t*)(stage + KB + ((4 * b + cc) * 64 + to) * 16) = y;
+            for (int e = 0; e < 8; e += 2) {
+                const half2_t z = __builtin_elementwise_fma(half2_t{k[e], k[e + 1]}, half2_t{s, s}, -half2_t{x[e], x[e + 1]});
+                y[e] = z[0];
+                y[e + 1] = z[1];
             }
+            *(half8_t*)(stage + KB + key_at + 4096 * b) = y;
         }
     };
-    auto decode_values = [&](uint8_t* stage) {  // sixteen tokens of dimensions n and n + 16 of a block
-#pragma unroll
-        for (int i = 0; i < VU; ++i) {
-            const int b = unit_wave + 4 * i, g4 = (lane >> 4) & 3, n = lane & 15;
-            if (DB % 4 != 0 && b >= DB) continue;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const half8_t sc = *(const half8_t*)(my_scales + DB * 64 + 64 * b + 16 * g4 + 8 * s);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    half8_t x;
-                    if constexpr (FV == FMT_Q8_0) x = codes8_q8(vr[i][4 * p + 2 * s], vr[i][4 * p + 2 * s + 1]);
-                    else x = codes8_q4(vr[i][2 * p + s]);
-                    *(half8_t*)(stage + KB * NK + ((4 * s + g4) * D + 32 * b + 16 * p + n) * 16) = x * sc;
-                }
-            }
-        }
+    // eight tokens (s) of dimensions n (p == 0) or n + 16 of a block
+    const int value_group = lane >> 4, value_at = KB * NK + (value_group * D + 32 * unit_wave + (lane & 15)) * 16;
+    auto decode_value = [&](uint8_t* stage, int i, int s, int p) __attribute__((always_inline)) {
+        const int b = unit_wave + 4 * i;
+        if (DB % 4 != 0 && b >= DB) return;
+        const half8_t sc = *(const half8_t*)(my_scales + DB * 64 + 64 * b + 16 * value_group + 8 * s);
+        half8_t x;
+        if constexpr (FV == FMT_Q8_0) x = codes8_q8(vr[i][4 * p + 2 * s], vr[i][4 * p + 2 * s + 1]);
+        else x = codes8_q4(vr[i][2 * p + s]);
+        *(half8_t*)(stage + value_at + (4 * s * D + 128 * i + 16 * p) * 16) = x * sc;
     };
 
     f32x16_t s[RT][2];
     half8_t p[RT][2][2];
-    auto scores = [&](const uint8_t* stage) {
+    // The matrix products of a slot: scores of the tile in `now`, sums of the one in `other`; and between them, in
+    // steps of four products, what else is to be done.  LDS answers after three or four products' time: an operand
+    // is read eight products ahead, and the steps keep their order.
+    constexpr int NQ = 4 * DB * NK, ALL = NQ + 4 * DB, AHEAD = 8;
+    auto products = [&](const uint8_t* now, const uint8_t* other, int from, auto between) __attribute__((always_inline)) {
+        const uint8_t* keys = now + (h * 64 + col) * 16;
+        const uint8_t* values = other + KB * NK + (h * D + col) * 16;
+        auto operand = [&](int i) __attribute__((always_inline)) {
+            if (i < NQ) return *(const half8_t*)(keys + i % NK * KB + i / NK % 2 * 512 + i / (2 * NK) * 2048);
+            const int v = i - NQ;
+            return *(const half8_t*)(values + v % DB * 512 + v / DB * 2 * D * 16);
+        };
+        half8_t f[AHEAD];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int i = from; i < from + AHEAD; ++i) f[i % AHEAD] = operand(i);
+        if (from == 0) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[rt][half][i] = 0.0f;
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+                    for (int i = 0; i < 16; ++i) s[rt][half][i] = 0.0f;
+        }
 #pragma unroll
-            for (int ks = 0; ks < 2 * DB; ++ks)
+        for (int step = from / 4; step < ALL / 4; ++step) {
 #pragma unroll
-                for (int nk = 0; nk < NK; ++nk) {
-                    const half8_t k = *(const half8_t*)(stage + nk * KB + ((2 * ks + h) * 64 + 32 * half + col) * 16);
+            for (int i = 4 * step; i < 4 * step + 4; ++i) {
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) s[rt][half] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[rt][ks], s[rt][half], 0, 0, 0);
+                for (int rt = 0; rt < RT; ++rt) {
+                    if (i < NQ) {
+                        f32x16_t& x = s[rt][i / NK % 2];
+                        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], q[rt][i / (2 * NK)], x, 0, 0, 0);
+                    } else {
+                        const int v = i - NQ;
+                        f32x16_t& x = o[rt][v % DB];
+                        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], p[rt][v / (2 * DB)][v / DB % 2], x, 0, 0, 0);
+                    }
                 }
+                if (i + AHEAD < ALL) f[i % AHEAD] = operand(i + AHEAD);
+            }
+            between(step);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
-    auto sums = [&](const uint8_t* stage) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                for (int b = 0; b < DB; ++b) {
-                    const half8_t v = *(const half8_t*)(stage + KB * NK + ((4 * half + 2 * ks + h) * D + 32 * b + col) * 16);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) o[rt][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[rt][half][ks], o[rt][b], 0, 0, 0);
-                }
-    };
-    auto softmax = [&](int g, int expo) {
+    auto softmax = [&](int g, int expo) __attribute__((always_inline)) {
         const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
         const float unit_k = ldexpf(1.0f, expo);
 #pragma unroll
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
         }
     };
     // values that are not finite: NaN to the rows that see them
-    auto spoil = [&](int g, int32_t page) {
+    auto spoil = [&](int g, int32_t page) __attribute__((always_inline)) {
         const rsrc_t vp = attn_values(mem, c, page, g);
 #pragma unroll
         for (int b = 0; b < DB; ++b)
@@ -378,71 +383,86 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     // values written in slot 2 j + 1 and read in 2 j + 2 and 2 j + 3.  With four waves there is one on a SIMD (and
     // another workgroup), which decodes both.
     // A tile that a wave does not see costs it nothing but time: its scores are all hidden.
-    const bool late = NW == 8 && wave >= 4;
     int o_expo = NONE;  // taken off the values in o
-    int32_t page = g0 < g1 ? entry(g0) : -1;
-    int g = next(g0, page);  // tile j
-    if (g < g1) {
-        int32_t page_b = entry(g + 1);
-        int g_b = next(g + 1, page_b);  // tile j + 1
-        int32_t page_c = entry(g_b + 1);
-        int g_c = next(g_b + 1, page_c);  // tile j + 2
-        fetch_keys(g, page);
-        fetch_values(g, page);
+    auto run = [&](auto role) __attribute__((always_inline)) {
+        constexpr bool LATE = role.value == VALUES, DO_K = role.value != VALUES, DO_V = role.value != KEYS;
+        int32_t page = g0 < g1 ? entry(g0) : -1;
+        int g = next(g0, page);  // tile j
+        if (g < g1) {
+            int32_t page_b = entry(g + 1);
+            int g_b = next(g + 1, page_b);  // tile j + 1
+            int32_t page_c = entry(g_b + 1);
+            int g_c = next(g_b + 1, page_c);  // tile j + 2
+            fetch_keys(g, page, DO_K);
+            fetch_values(g, page, DO_V);
+    #pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+    #pragma unroll
+                for (int i = 0; i < 4; ++i)
+    #pragma unroll
+                    for (int e = 0; e < 8; ++e) p[rt][i >> 1][i & 1][e] = (_Float16)0.0f;
+            // sums before the first tile: of nothing, and of values that are numbers
+            for (int i = tid; i < KB / 16; i += 64 * NW) *(u32x4_t*)(smem + STAGE + KB * NK + 16 * i) = u32x4_t{0, 0, 0, 0};
+            if constexpr (LATE) __syncthreads();
+            prepare(g, g);
+            int expo = k_expo, expo_b = 0;
+            if constexpr (DO_K) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[rt][i >> 1][i & 1][e] = (_Float16)0.0f;
-        // sums before the first tile: of nothing, and of values that are numbers
-        for (int i = tid; i < KB / 16; i += 64 * NW) *(u32x4_t*)(smem + STAGE + KB * NK + 16 * i) = u32x4_t{0, 0, 0, 0};
-        if (late) __syncthreads();
-        prepare(g, g);
-        int expo = k_expo, expo_b = 0;
-        if (do_k) decode_keys(smem);
-        fetch_keys(g_b, page_b);
-        prepare(g_b, g);
-        expo_b = k_expo;
-        __syncthreads();
-        for (int cur = 0;; cur ^= 1) {
-            scores(smem + cur * STAGE);
-            sums(smem + (cur ^ 1) * STAGE);
-            if (do_k) decode_keys(smem + (cur ^ 1) * STAGE);
-            if (do_v) decode_values(smem + cur * STAGE);
-            fetch_keys(g_c, page_c);
-            fetch_values(g_b, page_b);
-            __syncthreads();
-            int32_t page_d = entry(g_c + 1);  // (here for its latency: the other half waits for LDS)
-            if (o_expo != v_expo) {
-                const float shift = ldexpf(1.0f, o_expo - v_expo);  // 0 the first time
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int b = 0; b < DB; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
-                o_expo = v_expo;
+                for (int b = 0; b < DB; ++b) decode_key(smem, b);
             }
-            softmax(g, expo);
-            if (odd) spoil(g, page);
-            prepare(g_c, g_b);
-            expo = expo_b;
+            fetch_keys(g_b, page_b, DO_K);
+            prepare(g_b, g);
             expo_b = k_expo;
-            g = g_b;
-            page = page_b;
-            g_b = g_c;
-            page_b = page_c;
-            g_c = next(g_c + 1, page_d);
-            page_c = page_d;
             __syncthreads();
-            if (g >= g1) {
-                sums(smem + cur * STAGE);
-                break;
+            for (int cur = 0;; cur ^= 1) {
+                uint8_t *now = smem + cur * STAGE, *other = smem + (cur ^ 1) * STAGE;
+                products(now, other, 0, [&](int step) __attribute__((always_inline)) {
+                    // keys: an octet in every (NK + 1)th step; values: 4 VU eights in DB (NK + 1) steps
+                    if constexpr (DO_K)
+                        if (step % (NK + 1) == 0) decode_key(other, step / (NK + 1));
+                    if constexpr (DO_V) {
+#pragma unroll
+                        for (int i = 0; i < 4 * VU; ++i)
+                            if (i * (DB * (NK + 1)) / (4 * VU) == step) decode_value(now, i >> 2, (i >> 1) & 1, i & 1);
+                    }
+                });
+                fetch_keys(g_c, page_c, DO_K);
+                fetch_values(g_b, page_b, DO_V);
+                __syncthreads();
+                int32_t page_d = entry(g_c + 1);  // (here for its latency: the other half waits for LDS)
+                if (o_expo != v_expo) {
+                    const float shift = ldexpf(1.0f, o_expo - v_expo);  // 0 the first time
+    #pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+    #pragma unroll
+                        for (int b = 0; b < DB; ++b)
+    #pragma unroll
+                            for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
+                    o_expo = v_expo;
+                }
+                softmax(g, expo);
+                if (odd) spoil(g, page);
+                prepare(g_c, g_b);
+                expo = expo_b;
+                expo_b = k_expo;
+                g = g_b;
+                page = page_b;
+                g_b = g_c;
+                page_b = page_c;
+                g_c = next(g_c + 1, page_d);
+                page_c = page_d;
+                __syncthreads();
+                if (g >= g1) {
+                    products(nullptr, now, NQ, [](int) {});
+                    break;
+                }
             }
+            if constexpr (role.value == KEYS) __syncthreads();
         }
-        if (NW == 8 && !late) __syncthreads();
-    }
+    };
+    if constexpr (NW == 4) run(std::integral_constant<int, BOTH>());
+    else if (wave < 4) run(std::integral_constant<int, KEYS>());
+    else run(std::integral_constant<int, VALUES>());
 
     const float unit_v = o_expo != NONE ? ldexpf(1.0f, o_expo) : 0.0f;
 #pragma unroll
