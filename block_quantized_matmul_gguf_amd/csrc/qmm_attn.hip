@@ -109,7 +109,7 @@ int64_t plan_attention(AttnArgs& a, int64_t max_length)
     if (a.window) span = std::min(span, (int64_t)a.window + a.tile_rows + 126);
     const int64_t groups = std::max<int64_t>(1, (span + CACHE_GROUP - 1) / CACHE_GROUP);
     const int64_t base = (int64_t)a.tiles * c.heads;
-    const int64_t target = a.tile_rows == 256 ? 256 : a.many ? 1024 : 512, least = a.many ? 4 : 8;
+    const int64_t target = a.tile_rows == 256 ? 256 : a.many ? 768 : 512, least = a.many ? 4 : 8;
     const int64_t want = std::min((target + base - 1) / base, (groups + least - 1) / least);
     a.piece_groups = (int)((groups + want - 1) / want);
     a.pieces = (int)((groups + a.piece_groups - 1) / a.piece_groups);
@@ -141,7 +141,7 @@ hipError_t launch_attention(AttnArgs& a, void* ws, hipStream_t s)
     if (e != hipSuccess || a.pieces == 1) return e;
     const int lanes = c.dim <= 64 ? 16 : c.dim <= 128 ? 32 : 64;
     int share = 1;
-    while (share * 2 * lanes <= 256 && share * 2 <= a.pieces) share *= 2;
+    while (share * 2 * lanes <= 256 && share * 2 <= a.pieces && all * lanes * share < 512 * 256) share *= 2;
     const int64_t per_block = 256 / (lanes * share);
     hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)((all + per_block - 1) / per_block)), dim3(256), 0, s, a, lanes, share);
     return hipGetLastError();

@@ -395,11 +395,11 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
             int g_c = next(g_b + 1, page_c);  // tile j + 2
             fetch_keys(g, page, DO_K);
             fetch_values(g, page, DO_V);
-    #pragma unroll
+#pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 4; ++i)
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 8; ++e) p[rt][i >> 1][i & 1][e] = (_Float16)0.0f;
             // sums before the first tile: of nothing, and of values that are numbers
             for (int i = tid; i < KB / 16; i += 64 * NW) *(u32x4_t*)(smem + STAGE + KB * NK + 16 * i) = u32x4_t{0, 0, 0, 0};
@@ -415,6 +415,7 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
             expo_b = k_expo;
             __syncthreads();
             for (int cur = 0;; cur ^= 1) {
+                __builtin_amdgcn_s_setprio(1);  // before the other wave of the SIMD, which has many instructions to choose from
                 uint8_t *now = smem + cur * STAGE, *other = smem + (cur ^ 1) * STAGE;
                 products(now, other, 0, [&](int step) __attribute__((always_inline)) {
                     // keys: an octet in every (NK + 1)th step; values: 4 VU eights in DB (NK + 1) steps
@@ -426,17 +427,18 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
                             if (i * (DB * (NK + 1)) / (4 * VU) == step) decode_value(now, i >> 2, (i >> 1) & 1, i & 1);
                     }
                 });
+                __builtin_amdgcn_s_setprio(0);
                 fetch_keys(g_c, page_c, DO_K);
                 fetch_values(g_b, page_b, DO_V);
                 __syncthreads();
                 int32_t page_d = entry(g_c + 1);  // (here for its latency: the other half waits for LDS)
                 if (o_expo != v_expo) {
                     const float shift = ldexpf(1.0f, o_expo - v_expo);  // 0 the first time
-    #pragma unroll
+#pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
-    #pragma unroll
+#pragma unroll
                         for (int b = 0; b < DB; ++b)
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
                     o_expo = v_expo;
                 }

@@ -521,6 +521,9 @@ extern "C" int qmatmul_cache_attention(const qmm_cache* cache, int64_t T, int64_
     if (st != QMM_OK) return st;
     if (!std::isfinite(scale)) return bad("scale must be finite");
     if (!std::isfinite(softcap) || softcap < 0.0f) return bad("softcap must be finite and not negative");
+    const float log2e = 1.4426950408889634f;
+    if (!std::isfinite(scale * log2e) || !std::isfinite(softcap * log2e) || (softcap > 0.0f && !std::isfinite(scale / softcap)))
+        return bad("scale or softcap out of range");
     if (T == 0 || cache->batch == 0) return QMM_OK;
     if ((st = check_pointers(cache)) != QMM_OK) return st;
     const int64_t row = q_heads * cache->dim;
@@ -530,7 +533,6 @@ extern "C" int qmatmul_cache_attention(const qmm_cache* cache, int64_t T, int64_
     AttnArgs a = attention_args(cache, T, q_heads, type, causal, window);
     a.q = q;
     a.q_stride = q_stride;
-    const float log2e = 1.4426950408889634f;
     a.scale = softcap > 0.0f ? scale / softcap : scale * log2e;
     a.cap = softcap * log2e;
     a.out = out;

@@ -66,7 +66,8 @@ def test_load_refusals(kw):
 
 @pytest.mark.parametrize("kw", [dict(q_heads=0), dict(q_heads=3), dict(q_heads=1026), dict(window=-1), dict(window=1 << 31),
                                 dict(window=5, causal=0), dict(max_length=-1), dict(scale=float("nan")), dict(scale=float("inf")),
-                                dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(out=None),
+                                dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(softcap=1e-42),
+                                dict(scale=3e38), dict(softcap=3e38), dict(out=None),
                                 dict(out=OUT + 8), dict(lse=Y + 2), dict(xs=255), dict(xs=258), dict(out=X), dict(out=K),
                                 dict(lse=X), dict(lse=OUT), dict(out=V + 256), dict(lse=LENGTHS), dict(T=1 << 18, q_heads=1024)], ids=str)
 def test_attention_refusals(kw):
