@@ -95,22 +95,40 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 int64_t plan_attention(AttnArgs& a, int64_t max_length)
 {
     const CacheArgs& c = a.c;
-    const int64_t rows = (c.T * a.per + c.batch - 1) / c.batch;
-    auto workgroups = [&](int tile_rows) { return (c.T * a.per / tile_rows + c.batch) * c.heads; };
-    a.many = c.type != QMM_F32 && rows >= 128 && !(c.type == QMM_F16 && c.dim > 128);
-    a.tile_rows = 16;
-    if (a.many) a.tile_rows = c.dim > 128 || workgroups(256) < 256 ? 128 : 256;
-    else
-        while (a.tile_rows < (c.dim > 128 ? 64 : 128) && a.tile_rows < rows && workgroups(a.tile_rows) > 512) a.tile_rows *= 2;
+    const int64_t rows = (c.T * a.per + c.batch - 1) / c.batch;  // of a sequence
+    // workgroups without pieces, if the sequences have as many rows each
+    auto workgroups = [&](int tile_rows) { return (rows + tile_rows - 1) / tile_rows * c.batch * c.heads; };
+    // Decoding once for all rows pays where a tile of 128 is mostly full and there is work for the whole card.  In us,
+    // rows kernel : this one, 8 heads over 4096 positions: bf16, dim 128: 8 sequences of 64 rows 39 : 40, 96 rows 55 :
+    // 41, 128 rows 56 : 42, 256 rows 102 : 58; one of 128 rows 20 : 25, four of 96 36 : 32; dim 256, 4 heads over 2048
+    // positions: four sequences of 128 rows 30 : 35, eight 43 : 40.  f16 has one and a half times the products, and the
+    // keys' parts leave room for one workgroup to a compute unit: 8 of 128 rows 55 : 69, of 192 82 : 77, of 256 102 :
+    // 80; one of 256 24 : 30, of 1024 55 : 53.  Of 256 dimensions the f16 parts do not fit; f32's are the rows kernel's.
+    const bool half = c.type == QMM_F16;
+    a.many = c.type != QMM_F32 && !(half && c.dim > 128) && rows >= (half ? 192 : 96) && workgroups(16) >= (half ? 512 : 192);
+    a.tile_rows = ATTN_ROWS;
+    if (a.many) {
+        // 256 rows share the decoding of two tiles of 128, one workgroup to a compute unit, not two (128 : 256, bf16,
+        // dim 128): 512 rows 99 : 93, 2048 rows of one sequence 62 : 58.  Not where they fill up with more than an
+        // eighth of empty rows: 384 rows 87 : 96, 600 rows of f16 and dim 96 38 : 42; nor bf16 of 64 dimensions, with
+        // little to decode: 8192 rows 107 : 114.  f16 of 128 has one workgroup either way: 384 rows 168 : 129.
+        auto padded = [&](int64_t tile) { return (rows + tile - 1) / tile * tile; };
+        const bool wide = c.dim <= 128 && (half ? c.dim == 128 || padded(256) * 8 <= padded(128) * 9
+                                                : c.dim > 64 && padded(256) * 8 <= padded(128) * 9);
+        a.tile_rows = wide ? 256 : 128;
+    }
     a.tile_shift = __builtin_ctz(a.tile_rows);
     a.tiles = (int)(c.T * a.per / a.tile_rows + c.batch);
     int64_t span = (int64_t)c.width * c.page_size;
     if (max_length > 0) span = std::min(span, max_length);
     if (a.window) span = std::min(span, (int64_t)a.window + a.tile_rows + 126);
     const int64_t groups = std::max<int64_t>(1, (span + CACHE_GROUP - 1) / CACHE_GROUP);
-    const int64_t base = (int64_t)a.tiles * c.heads;
-    const int64_t target = a.tile_rows == 256 ? 256 : a.many ? 768 : 512, least = a.many ? 4 : 8;
-    const int64_t want = std::min((target + base - 1) / base, (groups + least - 1) / least);
+    // Pieces: as many as let every compute unit have what it can hold, one or two workgroups (by LDS and registers),
+    // in one go, of four groups or more (a wave of the rows kernel has one then: one sequence of 4096 positions 11.6 us,
+    // with eight groups 13.0).  Up to eight groups the second launch costs more than it gives (307 positions: 9.6 us
+    // whole, 13.5 in two).
+    const bool one = a.many ? a.tile_rows == 256 || c.dim > 128 || (half && c.dim == 128) : c.dim > 128 || (c.type == QMM_F32 && c.dim == 128);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((one ? 256 : 512) / workgroups(a.tile_rows), groups > 8 ? (groups + 3) / 4 : 1));
     a.piece_groups = (int)((groups + want - 1) / want);
     a.pieces = (int)((groups + a.piece_groups - 1) / a.piece_groups);
     if (a.pieces <= 1) {
@@ -130,14 +148,12 @@ hipError_t launch_attention(AttnArgs& a, void* ws, hipStream_t s)
         a.part_ml = (float*)((char*)ws + align256(a.pieces * all * c.dim * 4));
         a.part_n = (int32_t*)((char*)a.part_ml + align256(a.pieces * all * 8));
     }
-    const bool two = c.type == QMM_F32;
-    const int rt = a.tile_rows > 16 && c.dim <= 128 ? 2 : 1;
     hipError_t e;
     if (a.many) {
         if (c.fmt_k == FMT_Q8_0) e = c.fmt_v == FMT_Q8_0 ? launch_attn_tile_q8q8(a, s) : launch_attn_tile_q8q4(a, s);
         else e = c.fmt_v == FMT_Q8_0 ? launch_attn_tile_q4q8(a, s) : launch_attn_tile_q4q4(a, s);
-    } else if (c.fmt_k == FMT_Q8_0) e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q8q8(a, two, rt, s) : launch_attn_rows_q8q4(a, two, rt, s);
-    else e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q4q8(a, two, rt, s) : launch_attn_rows_q4q4(a, two, rt, s);
+    } else if (c.fmt_k == FMT_Q8_0) e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q8q8(a, s) : launch_attn_rows_q8q4(a, s);
+    else e = c.fmt_v == FMT_Q8_0 ? launch_attn_rows_q4q8(a, s) : launch_attn_rows_q4q4(a, s);
     if (e != hipSuccess || a.pieces == 1) return e;
     const int lanes = c.dim <= 64 ? 16 : c.dim <= 128 ? 32 : 64;
     int share = 1;

@@ -17,8 +17,10 @@
 // and so does one whose values are not finite; the rows that see it get NaN
 // directly.
 //
-// The waves of a workgroup take row tiles of 16 RT rows, and where there are
-// fewer of these than waves they share the tokens and join in LDS.
+// The four waves of a workgroup have the same 16 rows, take the groups in turn
+// and join in LDS.  (Two row tiles to a wave share the decoding but leave half
+// the workgroups: 8 sequences of 4096 positions, dim 128, bf16, with 32 rows each
+// 34 us against 54 us, with 128 58 us against 82 us.)
 #pragma once
 #include "../../include/qmatmul.h"
 #include "qmm_act.h"
@@ -26,7 +28,7 @@
 
 namespace qmm {
 
-constexpr int ATTN_WAVES = 4;
+constexpr int ATTN_WAVES = 4, ATTN_ROWS = 16;  // of a workgroup
 
 QMM_DEV half8_t codes8_q8(uint32_t w0, uint32_t w1)
 {
@@ -126,14 +128,14 @@ QMM_DEV void load_pieces(rsrc_t p, uint32_t at, uint32_t lane, uint32_t r[N])
     static_assert(N % 4 != 1, "no such piece");
 }
 
-template <int FK, int FV, int DB, int NP, int RT>
-__global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void attn_rows_kernel(AttnArgs a)
+template <int FK, int FV, int DB, int NP>
+__global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP <= 4 ? 2 : 1) void attn_rows_kernel(AttnArgs a)
 {
     constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a lane per key tile
     constexpr int VN = FV == FMT_Q8_0 ? 8 : 4;                     // and per block of values
     constexpr int SN = (DB + 1) / 2;                               // of scales per lane
     constexpr int SCALES = 2 * DB * 64;                            // f32 of a wave
-    constexpr int ROWS = 16 * RT;
+    constexpr int ROWS = ATTN_ROWS;
     extern __shared__ __align__(16) float lds[];
     const CacheArgs& c = a.c;
     const int lane = (int)__lane_id(), g4 = lane >> 4;
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
     // head fastest: the tiles of one head follow each other in steps of `heads` workgroups
     const int head = (int)(blockIdx.x % (uint32_t)c.heads);
     const uint32_t rest = blockIdx.x / (uint32_t)c.heads;
-    const int id = (int)(rest % (uint32_t)a.tiles), piece = (int)(rest / (uint32_t)a.tiles);
+    const int id = (int)(rest / (uint32_t)a.pieces), piece = (int)(rest % (uint32_t)a.pieces);
     AttnTile t;
     if (!attn_tile(a, id, t)) return;
     const int last = min(t.r0 + a.tile_rows, t.rows) - 1;
@@ -152,64 +154,49 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
     if (piece > 0) g0 += piece * a.piece_groups;
     if (piece + 1 < pieces) g1 = min(g1, g0 + a.piece_groups);
 
-    // waves: `along` of them share the tokens of a row tile
-    const int tiles = (last - t.r0) / ROWS + 1;
-    const int along = tiles == 1 ? ATTN_WAVES : tiles == 2 ? ATTN_WAVES / 2 : 1;
-    const int wr = wave / along, wt = wave % along;
-    const int w0 = t.r0 + wr * ROWS, w1 = min(w0 + ROWS - 1, last);
-    const bool work = w0 <= last;
-    const int wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
-    // every row of the wave sees [flo, fhi)
-    const int flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
+    const int wlo = t.lo(a, t.r0), whi = t.hi(a, last);
+    // every row sees [flo, fhi)
+    const int flo = t.lo(a, last), fhi = t.hi(a, t.r0);
 
-    // rows of this lane: their queries as f16 parts, what they see
-    half8_t q[RT][DB][NP];
-    float factor[RT], m[RT], l[RT];
-    int hi[RT], lo[RT];
-    int64_t at[RT];  // output row (token, query head), or -1
-    f32x4_t o[RT][2 * DB];
+    // the row of this lane: its queries as f16 parts, what it sees
+    half8_t q[DB][NP];
+    float m = -3.402823466e38f, l = 0.0f;
+    f32x4_t o[2 * DB];
+    const int r = t.r0 + (lane & 15);
+    const bool live = r <= last;
+    const int token = live ? r / a.per : 0, h = live ? r - token * a.per : 0;
+    const int hi = live ? t.hi(a, r) : 0, lo = live ? t.lo(a, r) : 0;
+    const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + h) * D;
+    float x[DB][8], top = 0.0f;
+    bool fine = true;
+    load_octets<DB>(a.q, c.type, from + 8 * g4, 32, x);  // (a row past the last: the sequence's first)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = w0 + 16 * rt + (lane & 15);
-        const bool live = r <= last;
-        const int token = live ? r / a.per : 0, h = live ? r - token * a.per : 0;
-        at[rt] = live ? (t.n0 + token) * a.q_heads + head * a.per + h : -1;
-        hi[rt] = live ? t.hi(a, r) : 0;
-        lo[rt] = live ? t.lo(a, r) : 0;
-        const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + h) * D;
-        float x[DB][8], top = 0.0f;
-        bool fine = true;
-        load_octets<DB>(a.q, c.type, from + 8 * g4, 32, x);  // (a row past the last: the sequence's first)
+    for (int b = 0; b < DB; ++b) {
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[b][e] = live ? x[b][e] : 0.0f;
-                top = fmaxf(top, fabsf(x[b][e]));
-                fine = fine && fabsf(x[b][e]) <= 3.402823466e38f;
-            }
+        for (int e = 0; e < 8; ++e) {
+            x[b][e] = live ? x[b][e] : 0.0f;
+            top = fmaxf(top, fabsf(x[b][e]));
+            fine = fine && fabsf(x[b][e]) <= 3.402823466e38f;
         }
-        top = rows_max(top);
-        fine = rows_max(fine ? 0.0f : 1.0f) == 0.0f;
-        // f16 rows enter as they are, others scaled by a power of two (exact)
-        const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
-        const float up = ldexpf(1.0f, e2);
-        factor[rt] = a.scale * ldexpf(1.0f, -e2);
-#pragma unroll
-        for (int b = 0; b < DB; ++b)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                _Float16 hi16, lo16;
-                float xs;
-                split_one(fine ? x[b][e] : __builtin_nanf(""), up, hi16, lo16, xs);
-                q[rt][b][0][e] = hi16;
-                if constexpr (NP == 2) q[rt][b][1][e] = lo16;
-            }
-        m[rt] = -3.402823466e38f;
-        l[rt] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2 * DB; ++i) o[rt][i] = f32x4_t{0, 0, 0, 0};
     }
+    top = rows_max(top);
+    fine = rows_max(fine ? 0.0f : 1.0f) == 0.0f;
+    // f16 rows enter as they are, others scaled by a power of two (exact)
+    const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
+    const float up = ldexpf(1.0f, e2);
+    const float factor = a.scale * ldexpf(1.0f, -e2);
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            _Float16 hi16, lo16;
+            float xs;
+            split_one(fine ? x[b][e] : __builtin_nanf(""), up, hi16, lo16, xs);
+            q[b][0][e] = hi16;
+            if constexpr (NP == 2) q[b][1][e] = lo16;
+        }
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) o[i] = f32x4_t{0, 0, 0, 0};
 
     // scales of the wave: keys [DB][64], values [DB][64]
     float* ks = lds + wave * SCALES;
@@ -219,9 +206,8 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
     int expo = -1000;  // E
 
     // the wave's groups, and those of them that have a page
-    const int wg0 = max(g0, (int)(wlo / CACHE_GROUP)), wg1 = work ? min(g1, (int)((whi + CACHE_GROUP - 1) / CACHE_GROUP)) : 0;
     auto next = [&](int g, int32_t& page) {
-        for (; g < wg1; g += along) {
+        for (; g < g1; g += ATTN_WAVES) {
             page = table_entry(row, cache_page_of(c, (uint32_t)g));
             if (page >= 0 && page < c.pages) break;
         }
@@ -247,13 +233,13 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
         for (int b = 0; b < DB; ++b) load_pieces<VN>(vp, b * 256 * VN, (uint32_t)lane, vr[b]);
     };
     int32_t page = -1, ahead_page = -1;
-    int ahead = next(g0 + (wg0 - g0 + along - 1 - wt) / along * along + wt, ahead_page);
-    fetch_keys(ahead, ahead_page, ahead < wg1);
-    fetch_values(ahead, ahead_page, ahead < wg1);
-    while (ahead < wg1) {
+    int ahead = next(g0 + wave, ahead_page);
+    fetch_keys(ahead, ahead_page, ahead < g1);
+    fetch_values(ahead, ahead_page, ahead < g1);
+    while (ahead < g1) {
         const int g = ahead;
         page = ahead_page;
-        ahead = next(g + along, ahead_page);
+        ahead = next(g + ATTN_WAVES, ahead_page);
 
         // scales to LDS: word w holds places 2 (w % 32), + 1 of block w / 32
         const bool whole = g * 64 >= wlo && g * 64 + 64 <= whi;
@@ -295,11 +281,9 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
         const bool rescale = was != expo;
         const float shift = rescale ? ldexpf(1.0f, was - expo) : 1.0f;  // 0 the first time
 
-        float p[RT][16];
+        float p[16];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[rt][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) p[i] = 0.0f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
@@ -308,64 +292,56 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
                 if constexpr (FK == FMT_Q8_0) k = codes8_q8(kr[u][2 * b], kr[u][2 * b + 1]);
                 else k = codes8_q4(kr[u][b]);
                 const f32x4_t s = *(const f32x4_t*)(ks + 64 * b + 16 * g4 + 4 * u);
+                f32x4_t x = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[b][0], f32x4_t{0, 0, 0, 0}, 0, 0, 0);
+                if constexpr (NP == 2) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[b][1], x, 0, 0, 0);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    f32x4_t x = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[rt][b][0], f32x4_t{0, 0, 0, 0}, 0, 0, 0);
-                    if constexpr (NP == 2) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[rt][b][1], x, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[rt][4 * u + i] = fmaf(s[i], x[i], p[rt][4 * u + i]);
-                }
+                for (int i = 0; i < 4; ++i) p[4 * u + i] = fmaf(s[i], x[i], p[4 * u + i]);
             }
             if constexpr (DB > 4) {
                 // sums of one tile at a time: with all four in flight their parts and scales fill the registers (24
                 // to 120 of them were kept in memory).  Up to dim 128 they fit, and a wave that has them in flight
                 // is faster: 142 us against 180 us for 64 sequences.
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-                    asm volatile("" : "+v"(p[rt][4 * u]), "+v"(p[rt][4 * u + 1]), "+v"(p[rt][4 * u + 2]), "+v"(p[rt][4 * u + 3]));
+                    asm volatile("" : "+v"(p[4 * u]), "+v"(p[4 * u + 1]), "+v"(p[4 * u + 2]), "+v"(p[4 * u + 3]));
             }
             __builtin_amdgcn_sched_barrier(0);
         }
 
-        fetch_keys(ahead, ahead_page, ahead < wg1);
+        fetch_keys(ahead, ahead_page, ahead < g1);
         const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[rt][i] *= factor[rt];
-            if (a.cap != 0.0f) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if constexpr (NP == 2) p[rt][i] = a.cap * tanhf(p[rt][i]);
-                    else p[rt][i] = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * p[rt][i])));
-                }
-            }
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = g * 64 + 16 * (i >> 2) + 4 * g4 + (i & 3);
-                    p[rt][i] = j >= lo[rt] && j < hi[rt] ? p[rt][i] : -__builtin_inff();
-                }
-            }
-            float best = -3.402823466e38f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) best = fmaxf(best, p[rt][i]);
-            best = rows_max(best);
-            const float now = fmaxf(m[rt], best), keep = __builtin_amdgcn_exp2f(m[rt] - now);
-            if (__any(now > m[rt]) || rescale) {
-                const float both = keep * shift;
-                l[rt] *= keep;
-#pragma unroll
-                for (int i = 0; i < 2 * DB; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[rt][i][k] *= both;
-                m[rt] = now;
-            }
+        for (int i = 0; i < 16; ++i) p[i] *= factor;
+        if (a.cap != 0.0f) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                p[rt][i] = __builtin_amdgcn_exp2f(p[rt][i] - m[rt]);
-                l[rt] += p[rt][i];
+                if constexpr (NP == 2) p[i] = a.cap * tanhf(p[i]);
+                else p[i] = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * p[i])));
             }
+        }
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int j = g * 64 + 16 * (i >> 2) + 4 * g4 + (i & 3);
+                p[i] = j >= lo && j < hi ? p[i] : -__builtin_inff();
+            }
+        }
+        float best = -3.402823466e38f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) best = fmaxf(best, p[i]);
+        best = rows_max(best);
+        const float now = fmaxf(m, best), keep = __builtin_amdgcn_exp2f(m - now);
+        if (__any(now > m) || rescale) {
+            const float both = keep * shift;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < 2 * DB; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[i][k] *= both;
+            m = now;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(p[i] - m);
+            l += p[i];
         }
 
 #pragma unroll
@@ -374,36 +350,31 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
             for (int b = 0; b < DB; ++b) {
                 const f32x4_t s0 = *(const f32x4_t*)(vs + 64 * b + 16 * g4 + 8 * s);
                 const f32x4_t s1 = *(const f32x4_t*)(vs + 64 * b + 16 * g4 + 8 * s + 4);
-                half8_t pv[RT][NP];
+                half8_t pv[NP];
+                u32x4_t part[2];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    u32x4_t part[2];
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        uint32_t h, r = 0;
-                        split_products<NP == 2>(p[rt][8 * s + e], e < 4 ? s0[e & 3] : s1[e & 3], p[rt][8 * s + e + 1],
-                                                e < 4 ? s0[(e & 3) + 1] : s1[(e & 3) + 1], h, r);
-                        part[0][e >> 1] = h;
-                        part[1][e >> 1] = r;
-                    }
-#pragma unroll
-                    for (int np = 0; np < NP; ++np) pv[rt][np] = __builtin_bit_cast(half8_t, part[np]);
+                for (int e = 0; e < 8; e += 2) {
+                    uint32_t h, r = 0;
+                    split_products<NP == 2>(p[8 * s + e], e < 4 ? s0[e & 3] : s1[e & 3], p[8 * s + e + 1],
+                                            e < 4 ? s0[(e & 3) + 1] : s1[(e & 3) + 1], h, r);
+                    part[0][e >> 1] = h;
+                    part[1][e >> 1] = r;
                 }
+#pragma unroll
+                for (int np = 0; np < NP; ++np) pv[np] = __builtin_bit_cast(half8_t, part[np]);
 #pragma unroll
                 for (int par = 0; par < 2; ++par) {
                     half8_t v;
                     if constexpr (FV == FMT_Q8_0) v = codes8_q8(vr[b][4 * par + 2 * s], vr[b][4 * par + 2 * s + 1]);
                     else v = codes8_q4(vr[b][2 * par + s]);
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
                         for (int np = 0; np < NP; ++np)
-                            o[rt][2 * b + par] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pv[rt][np], o[rt][2 * b + par], 0, 0, 0);
+                            o[2 * b + par] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pv[np], o[2 * b + par], 0, 0, 0);
                 }
                 if (b % 2) __builtin_amdgcn_sched_barrier(0);
             }
 
-        fetch_values(ahead, ahead_page, ahead < wg1);
+        fetch_values(ahead, ahead_page, ahead < g1);
         if (__any(odd)) {  // values that are not finite: NaN to the rows that see them
             const rsrc_t vp = attn_values(mem, c, page, g);
 #pragma unroll
@@ -412,58 +383,51 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
                     const float s = f16lo(__builtin_amdgcn_raw_buffer_load_b16(vp, 0, 256 * VN * DB + 2 * (64 * b + pl), 0));
                     if (fabsf(s) <= 65504.0f) continue;
                     const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+                    const float add = j >= lo && j < hi ? __builtin_nanf("") : 0.0f;
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const float add = j >= lo[rt] && j < hi[rt] ? __builtin_nanf("") : 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[rt][2 * b + (k >> 2)][k & 3] += add;
-                    }
+                    for (int k = 0; k < 8; ++k) o[2 * b + (k >> 2)][k & 3] += add;
                 }
         }
     }
 
-    // join: every wave's sums as one with the maximum over the waves that share its rows
+    // join: every wave's sums as one with the maximum over the waves
     float* all = lds + ATTN_WAVES * SCALES;                  // [waves][ROWS][2] maximum, sum
     float* sums = lds + ATTN_WAVES * (SCALES + 2 * ROWS);    // [waves][ROWS][D]
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        l[rt] = rows_sum(l[rt]);
-        if (g4 == 0) {
-            all[(wave * ROWS + 16 * rt + lane) * 2] = m[rt];
-            all[(wave * ROWS + 16 * rt + lane) * 2 + 1] = l[rt];
-        }
+    l = rows_sum(l);
+    if (g4 == 0) {
+        all[(wave * ROWS + lane) * 2] = m;
+        all[(wave * ROWS + lane) * 2 + 1] = l;
     }
     __syncthreads();
     const float unit = expo > -1000 ? ldexpf(1.0f, expo) : 0.0f;
+    float most = m;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = 16 * rt + (lane & 15);
-        float top = m[rt];
-        for (int w = 0; w < along; ++w) top = fmaxf(top, all[((wr * along + w) * ROWS + r) * 2]);
-        const float f = __builtin_amdgcn_exp2f(m[rt] - top) * unit;
+    for (int w = 0; w < ATTN_WAVES; ++w) most = fmaxf(most, all[(w * ROWS + (lane & 15)) * 2]);
+    const float f = __builtin_amdgcn_exp2f(m - most) * unit;
 #pragma unroll
-        for (int i = 0; i < 2 * DB; ++i) {
-            f32x4_t v = o[rt][i];
+    for (int i = 0; i < 2 * DB; ++i) {
+        f32x4_t v = o[i];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] *= f;
-            *(f32x4_t*)(sums + (wave * ROWS + r) * D + 16 * i + 4 * g4) = v;
-        }
+        for (int k = 0; k < 4; ++k) v[k] *= f;
+        *(f32x4_t*)(sums + (wave * ROWS + (lane & 15)) * D + 16 * i + 4 * g4) = v;
     }
     __syncthreads();
     const int rows = last - t.r0 + 1;
     for (int i = (int)threadIdx.x; i < rows * (D / 4); i += 64 * ATTN_WAVES) {
-        const int r = i / (D / 4), d = 4 * (i - r * (D / 4)), first = r / ROWS * along, rr = r % ROWS;
+        const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
         float top = -3.402823466e38f, sum = 0.0f;
-        for (int w = first; w < first + along; ++w) top = fmaxf(top, all[(w * ROWS + rr) * 2]);
+#pragma unroll
+        for (int w = 0; w < ATTN_WAVES; ++w) top = fmaxf(top, all[(w * ROWS + rr) * 2]);
         f32x4_t v = f32x4_t{0, 0, 0, 0};
-        for (int w = first; w < first + along; ++w) {
+#pragma unroll
+        for (int w = 0; w < ATTN_WAVES; ++w) {
             sum += all[(w * ROWS + rr) * 2 + 1] * __builtin_amdgcn_exp2f(all[(w * ROWS + rr) * 2] - top);
             const f32x4_t x = *(const f32x4_t*)(sums + (w * ROWS + rr) * D + d);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] += x[k];
         }
-        const int token = (t.r0 + r) / a.per, h = t.r0 + r - token * a.per;
-        const int64_t to = (t.n0 + token) * a.q_heads + head * a.per + h;
+        const int n = (t.r0 + rr) / a.per;
+        const int64_t to = (t.n0 + n) * a.q_heads + head * a.per + (t.r0 + rr - n * a.per);
         if (pieces == 1) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const float y[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
@@ -482,42 +446,34 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP * RT <= 4 ? 2 : 1) void at
     }
 }
 
-template <int FK, int FV, int DB, int NP, int RT>
+template <int FK, int FV, int DB, int NP>
 hipError_t launch_attn_rows(const AttnArgs& a, hipStream_t s)
 {
-    constexpr int lds = ATTN_WAVES * (2 * DB * 64 + 2 * 16 * RT + 16 * RT * 32 * DB) * 4;
+    constexpr int lds = ATTN_WAVES * (2 * DB * 64 + 2 * ATTN_ROWS + ATTN_ROWS * 32 * DB) * 4;
     static bool done[64] = {};
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     if (lds > 65536 && (dev >= 64 || !done[dev])) {
-        e = hipFuncSetAttribute((const void*)attn_rows_kernel<FK, FV, DB, NP, RT>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        e = hipFuncSetAttribute((const void*)attn_rows_kernel<FK, FV, DB, NP>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
     const int64_t blocks = (int64_t)a.tiles * a.c.heads * a.pieces;
-    hipLaunchKernelGGL((attn_rows_kernel<FK, FV, DB, NP, RT>), dim3((uint32_t)blocks), dim3(64 * ATTN_WAVES), lds, s, a);
+    hipLaunchKernelGGL((attn_rows_kernel<FK, FV, DB, NP>), dim3((uint32_t)blocks), dim3(64 * ATTN_WAVES), lds, s, a);
     return hipGetLastError();
 }
 
-template <int FK, int FV, int DB>
-hipError_t launch_attn_rows_db(const AttnArgs& a, bool two_parts, int rt, hipStream_t s)
-{
-    if constexpr (DB <= 4) {
-        if (rt == 2) return two_parts ? launch_attn_rows<FK, FV, DB, 2, 2>(a, s) : launch_attn_rows<FK, FV, DB, 1, 2>(a, s);
-    }
-    return two_parts ? launch_attn_rows<FK, FV, DB, 2, 1>(a, s) : launch_attn_rows<FK, FV, DB, 1, 1>(a, s);
-}
-
-#define QMM_ATTN_ROWS(P, FK, FV)                                                            \
-    hipError_t launch_attn_rows_##P(const AttnArgs& a, bool two_parts, int rt, hipStream_t s) \
-    {                                                                                       \
-        switch (a.c.dim) {                                                                  \
-        case 64: return launch_attn_rows_db<FK, FV, 2>(a, two_parts, rt, s);                \
-        case 96: return launch_attn_rows_db<FK, FV, 3>(a, two_parts, rt, s);                \
-        case 128: return launch_attn_rows_db<FK, FV, 4>(a, two_parts, rt, s);               \
-        default: return launch_attn_rows_db<FK, FV, 8>(a, two_parts, rt, s);                \
-        }                                                                                   \
+#define QMM_ATTN_ROWS(P, FK, FV)                                                                                         \
+    hipError_t launch_attn_rows_##P(const AttnArgs& a, hipStream_t s)                                                    \
+    {                                                                                                                    \
+        const bool f32 = a.c.type == QMM_F32;                                                                            \
+        switch (a.c.dim) {                                                                                               \
+        case 64: return f32 ? launch_attn_rows<FK, FV, 2, 2>(a, s) : launch_attn_rows<FK, FV, 2, 1>(a, s);               \
+        case 96: return f32 ? launch_attn_rows<FK, FV, 3, 2>(a, s) : launch_attn_rows<FK, FV, 3, 1>(a, s);               \
+        case 128: return f32 ? launch_attn_rows<FK, FV, 4, 2>(a, s) : launch_attn_rows<FK, FV, 4, 1>(a, s);              \
+        default: return f32 ? launch_attn_rows<FK, FV, 8, 2>(a, s) : launch_attn_rows<FK, FV, 8, 1>(a, s);               \
+        }                                                                                                                \
     }
 
 }  // namespace qmm

@@ -1,6 +1,6 @@
 // qmm_attn_tile.h -- attention over the quantized cache for many rows.
 //
-// A workgroup of NW waves takes NW * 32 RT rows of one sequence and head of the
+// A workgroup of NW waves takes NW * 32 rows of one sequence and head of the
 // cache; 64 tokens at a time are decoded to f16 once for all of them, into LDS
 // in operand order, while the matrix cores work on the 64 before:
 //   S^T = K Q^T     v_mfma_f32_32x32x16_f16, 32 tokens by 32 rows
@@ -61,13 +61,13 @@ QMM_DEV half8_t mul8(half8_t a, half2_t s)
     return r;
 }
 
-template <int FK, int FV, int DB, int NK, int RT, int NW>
+template <int FK, int FV, int DB, int NK, int NW>
 __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(AttnArgs a)
 {
     constexpr int D = 32 * DB, KN = FK == FMT_Q8_0 ? 2 * DB : DB;  // dwords of a thread's keys
     constexpr int VN = FV == FMT_Q8_0 ? 8 : 4, VU = (DB * 64 + 255) / 256;  // of a unit of values; units of a thread
     constexpr int SN = (DB + 1) / 2, KB = 64 * D * 2, STAGE = KB * (NK + 1), SCALE = 2 * DB * 64;
-    constexpr int ROWS = 32 * RT;
+    constexpr int ROWS = 32;
     constexpr int NONE = -1000;  // no exponent yet
     enum { KEYS, VALUES, BOTH };  // what a wave decodes
     constexpr float RAISE = 8.0f, LIFT = 6.0f;  // powers of two: what m may lag behind, and p at m
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
 
     const int head = (int)(blockIdx.x % (uint32_t)c.heads);
     const uint32_t rest = blockIdx.x / (uint32_t)c.heads;
-    const int id = (int)(rest % (uint32_t)a.tiles), piece = (int)(rest / (uint32_t)a.tiles);
+    const int id = (int)(rest / (uint32_t)a.pieces), piece = (int)(rest % (uint32_t)a.pieces);
     AttnTile t;
     if (!attn_tile(a, id, t)) return;
     const int last = min(t.r0 + a.tile_rows, t.rows) - 1;
@@ -95,54 +95,46 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     const int wlo = work ? t.lo(a, w0) : 0, whi = work ? t.hi(a, w1) : 0;
     const int flo = work ? t.lo(a, w1) : 0, fhi = work ? t.hi(a, w0) : 0;
 
-    half8_t q[RT][2 * DB];
-    float factor[RT], m[RT], l[RT];
-    int hi[RT], lo[RT];
-    int64_t at[RT];
-    f32x16_t o[RT][DB];
+    half8_t q[2 * DB];
+    float m = -3.0e38f, l = 0.0f;
+    f32x16_t o[DB];
+    const int r = w0 + col;
+    const bool live = r <= last;
+    const int token = live ? r / a.per : 0, qh = live ? r - token * a.per : 0;
+    const int64_t at = live ? (t.n0 + token) * a.q_heads + head * a.per + qh : -1;
+    const int hi = live ? t.hi(a, r) : 0, lo = live ? t.lo(a, r) : 0;
+    const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + qh) * D;
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+    float top = 0.0f;
+    bool fine = true;
+    float x[2 * DB][8];
+    load_octets<2 * DB>(a.q, c.type, from + 8 * h, 16, x);  // (a row past the last: the sequence's first)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = w0 + 32 * rt + col;
-        const bool live = r <= last;
-        const int token = live ? r / a.per : 0, qh = live ? r - token * a.per : 0;
-        at[rt] = live ? (t.n0 + token) * a.q_heads + head * a.per + qh : -1;
-        hi[rt] = live ? t.hi(a, r) : 0;
-        lo[rt] = live ? t.lo(a, r) : 0;
-        const int64_t from = (t.n0 + token) * a.q_stride + (int64_t)(head * a.per + qh) * D;
-        const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
-        float top = 0.0f;
-        bool fine = true;
-        float x[2 * DB][8];
-        load_octets<2 * DB>(a.q, c.type, from + 8 * h, 16, x);  // (a row past the last: the sequence's first)
+    for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < 2 * DB; ++ks)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[ks][e] = live ? x[ks][e] : 0.0f;
-                top = fmaxf(top, fabsf(x[ks][e]));
-                fine = fine && fabsf(x[ks][e]) <= 3.402823466e38f;
-            }
-        {
-            const uint32_t u = __builtin_bit_cast(uint32_t, top), f = fine ? 0u : 1u;
-            const auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-            const auto y = __builtin_amdgcn_permlane32_swap(f, f, false, false);
-            top = fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
-            fine = ((uint32_t)y[0] | (uint32_t)y[1]) == 0;
+        for (int e = 0; e < 8; ++e) {
+            x[ks][e] = live ? x[ks][e] : 0.0f;
+            top = fmaxf(top, fabsf(x[ks][e]));
+            fine = fine && fabsf(x[ks][e]) <= 3.402823466e38f;
         }
-        const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
-        const float up = sign * ldexpf(1.0f, e2);
-        factor[rt] = fabsf(a.scale) * ldexpf(1.0f, -e2);
-#pragma unroll
-        for (int ks = 0; ks < 2 * DB; ++ks)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[rt][ks][e] = (_Float16)(fine ? x[ks][e] * up : __builtin_nanf(""));
-        m[rt] = -3.0e38f;
-        l[rt] = 0.0f;
-#pragma unroll
-        for (int b = 0; b < DB; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[rt][b][i] = 0.0f;
+    {
+        const uint32_t u = __builtin_bit_cast(uint32_t, top), f = fine ? 0u : 1u;
+        const auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(f, f, false, false);
+        top = fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
+        fine = ((uint32_t)y[0] | (uint32_t)y[1]) == 0;
     }
+    const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
+    const float up = sign * ldexpf(1.0f, e2);
+    const float factor = fabsf(a.scale) * ldexpf(1.0f, -e2);
+#pragma unroll
+    for (int ks = 0; ks < 2 * DB; ++ks)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[ks][e] = (_Float16)(fine ? x[ks][e] * up : __builtin_nanf(""));
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
 
     const int32_t* row = c.table + (int64_t)t.s * c.width;
     const AttnHead mem = attn_head(c, head);
@@ -258,8 +250,8 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
         *(half8_t*)(stage + value_at + (4 * s * D + 128 * i + 16 * p) * 16) = x * sc;
     };
 
-    f32x16_t s[RT][2];
-    half8_t p[RT][2][2];
+    f32x16_t s[2];
+    half8_t p[NK][2][2];  // f16 rows: hi and lo
     // The matrix products of a slot: scores of the tile in `now`, sums of the one in `other`; and between them, in
     // steps of four products, what else is to be done.  LDS answers after three or four products' time: an operand
     // is read eight products ahead, and the steps keep their order.
@@ -277,26 +269,23 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
         for (int i = from; i < from + AHEAD; ++i) f[i % AHEAD] = operand(i);
         if (from == 0) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[rt][half][i] = 0.0f;
+                    for (int i = 0; i < 16; ++i) s[half][i] = 0.0f;
         }
 #pragma unroll
         for (int step = from / 4; step < ALL / 4; ++step) {
 #pragma unroll
             for (int i = 4 * step; i < 4 * step + 4; ++i) {
+                if (i < NQ) {
+                    f32x16_t& x = s[i / NK % 2];
+                    x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], q[i / (2 * NK)], x, 0, 0, 0);
+                } else {
+                    const int v = i - NQ;
+                    f32x16_t& x = o[v % DB];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if (i < NQ) {
-                        f32x16_t& x = s[rt][i / NK % 2];
-                        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], q[rt][i / (2 * NK)], x, 0, 0, 0);
-                    } else {
-                        const int v = i - NQ;
-                        f32x16_t& x = o[rt][v % DB];
-                        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], p[rt][v / (2 * DB)][v / DB % 2], x, 0, 0, 0);
-                    }
+                    for (int n = 0; n < NK; ++n)
+                        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], p[n][v / (2 * DB)][v / DB % 2], x, 0, 0, 0);
                 }
                 if (i + AHEAD < ALL) f[i % AHEAD] = operand(i + AHEAD);
             }
@@ -307,56 +296,62 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     auto softmax = [&](int g, int expo) __attribute__((always_inline)) {
         const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
         const float unit_k = ldexpf(1.0f, expo);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float f = fmaxf(factor[rt] * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
-            if (a.cap != 0.0f) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[rt][half][i] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[rt][half][i] * (2.8853900817779268f * f)));
-                f = a.cap;
-            }
-            if (masked) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        // row 8 (i / 4) + 4 h + i % 4 of the tile: quad 2 (i / 4) + h
-                        const int quad = ((i >> 2) & 1) * 4 + (i >> 3) * 2, j = g * 64 + 32 * half + 4 * (quad + h) + (i & 3);
-                        s[rt][half][i] = j >= lo[rt] && j < hi[rt] ? s[rt][half][i] : -__builtin_inff();
-                    }
-            }
-            float best = s[rt][0][0];
+        float f = fmaxf(factor * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
+        if (a.cap != 0.0f) {
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) best = fmaxf(best, s[rt][half][i]);
-            const uint32_t u = __builtin_bit_cast(uint32_t, best);
-            const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-            best = f * fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
-            if (__any(best > m[rt] + RAISE)) {
-                const float now = fmaxf(m[rt], best), keep = __builtin_amdgcn_exp2f(m[rt] - now);
-                l[rt] *= keep;
-#pragma unroll
-                for (int b = 0; b < DB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[rt][b][i] *= keep;
-                m[rt] = now;
-            }
-            const float off = LIFT - m[rt];
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < 16; ++i)
+                    s[half][i] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[half][i] * (2.8853900817779268f * f)));
+            f = a.cap;
+        }
+        if (masked) {
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][half][i], f, off));
-                    sum[i & 3] += e;
-                    p[rt][half][i >> 3][i & 7] = (_Float16)e;
+                    // row 8 (i / 4) + 4 h + i % 4 of the tile: quad 2 (i / 4) + h
+                    const int quad = ((i >> 2) & 1) * 4 + (i >> 3) * 2, j = g * 64 + 32 * half + 4 * (quad + h) + (i & 3);
+                    s[half][i] = j >= lo && j < hi ? s[half][i] : -__builtin_inff();
                 }
-            l[rt] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
+        float best = s[0][0];
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) best = fmaxf(best, s[half][i]);
+        const uint32_t u = __builtin_bit_cast(uint32_t, best);
+        const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        best = f * fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
+        if (__any(best > m + RAISE)) {
+            const float now = fmaxf(m, best), keep = __builtin_amdgcn_exp2f(m - now);
+            l *= keep;
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[b][i] *= keep;
+            m = now;
+        }
+        const float off = LIFT - m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float e0 = __builtin_amdgcn_exp2f(fmaf(s[half][i], f, off));
+                const float e1 = __builtin_amdgcn_exp2f(fmaf(s[half][i + 1], f, off));
+                sum[i & 3] += e0;
+                sum[i + 1 & 3] += e1;
+                uint32_t part[2];
+                split_products<NK == 2>(e0, 1.0f, e1, 1.0f, part[0], part[1]);
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    const half2_t x = __builtin_bit_cast(half2_t, part[n]);
+                    p[n][half][i >> 3][i & 7] = x[0];
+                    p[n][half][i >> 3][(i & 7) + 1] = x[1];
+                }
+            }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
     // values that are not finite: NaN to the rows that see them
     auto spoil = [&](int g, int32_t page) __attribute__((always_inline)) {
@@ -367,12 +362,9 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
                 const float x = f16lo(__builtin_amdgcn_raw_buffer_load_b16(vp, 0, 256 * VN * DB + 2 * (64 * b + pl), 0));
                 if (fabsf(x) <= 65504.0f) continue;
                 const int j = g * 64 + ((pl >> 3) & 1) * 32 + ((pl >> 2) & 1) * 16 + (pl >> 4) * 4 + (pl & 3);
+                const float add = j >= lo && j < hi ? __builtin_nanf("") : 0.0f;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const float add = j >= lo[rt] && j < hi[rt] ? __builtin_nanf("") : 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[rt][b][i] += add;
-                }
+                for (int i = 0; i < 16; ++i) o[b][i] += add;
             }
     };
 
@@ -396,11 +388,9 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
             fetch_keys(g, page, DO_K);
             fetch_values(g, page, DO_V);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int i = 0; i < 4 * NK; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) p[rt][i >> 1][i & 1][e] = (_Float16)0.0f;
+                for (int e = 0; e < 8; ++e) p[i >> 2][i >> 1 & 1][i & 1][e] = (_Float16)0.0f;
             // sums before the first tile: of nothing, and of values that are numbers
             for (int i = tid; i < KB / 16; i += 64 * NW) *(u32x4_t*)(smem + STAGE + KB * NK + 16 * i) = u32x4_t{0, 0, 0, 0};
             if constexpr (LATE) __syncthreads();
@@ -435,11 +425,9 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
                 if (o_expo != v_expo) {
                     const float shift = ldexpf(1.0f, o_expo - v_expo);  // 0 the first time
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
                         for (int b = 0; b < DB; ++b)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[rt][b][i] *= shift;
+                            for (int i = 0; i < 16; ++i) o[b][i] *= shift;
                     o_expo = v_expo;
                 }
                 softmax(g, expo);
@@ -467,36 +455,33 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     else run(std::integral_constant<int, VALUES>());
 
     const float unit_v = o_expo != NONE ? ldexpf(1.0f, o_expo) : 0.0f;
+    const uint32_t u = __builtin_bit_cast(uint32_t, l);
+    const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const float sum = __builtin_bit_cast(float, (uint32_t)both[0]) + __builtin_bit_cast(float, (uint32_t)both[1]);
+    if (at < 0) return;
+    const float f = pieces > 1 ? unit_v : sum == 0.0f ? 0.0f : unit_v / sum;
+    const int64_t to = piece * (c.T * a.q_heads) + at;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t u = __builtin_bit_cast(uint32_t, l[rt]);
-        const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-        const float sum = __builtin_bit_cast(float, (uint32_t)both[0]) + __builtin_bit_cast(float, (uint32_t)both[1]);
-        if (at[rt] < 0) continue;
-        const float f = pieces > 1 ? unit_v : sum == 0.0f ? 0.0f : unit_v / sum;
-        const int64_t p = piece * (c.T * a.q_heads) + at[rt];
+    for (int b = 0; b < DB; ++b)
 #pragma unroll
-        for (int b = 0; b < DB; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const int d = 32 * b + 2 * i + 4 * h;
-                const float y[4] = {o[rt][b][i] * f, o[rt][b][i + 1] * f, o[rt][b][i + 2] * f, o[rt][b][i + 3] * f};
-                if (pieces == 1) store4(a.out, c.type, at[rt] * D + d, y);
-                else *(f32x4_t*)(a.part + p * D + d) = f32x4_t{y[0], y[1], y[2], y[3]};
-            }
-        if (h == 0) {
-            if (a.pieces > 1 && piece == 0) a.part_n[at[rt]] = pieces;
-            if (pieces > 1) {
-                a.part_ml[2 * p] = m[rt] - LIFT;
-                a.part_ml[2 * p + 1] = sum;
-            } else if (a.lse) {
-                a.lse[at[rt]] = sum == 0.0f ? -__builtin_inff() : (m[rt] - LIFT + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
-            }
+        for (int i = 0; i < 16; i += 4) {
+            const int d = 32 * b + 2 * i + 4 * h;
+            const float y[4] = {o[b][i] * f, o[b][i + 1] * f, o[b][i + 2] * f, o[b][i + 3] * f};
+            if (pieces == 1) store4(a.out, c.type, at * D + d, y);
+            else *(f32x4_t*)(a.part + to * D + d) = f32x4_t{y[0], y[1], y[2], y[3]};
+        }
+    if (h == 0) {
+        if (a.pieces > 1 && piece == 0) a.part_n[at] = pieces;
+        if (pieces > 1) {
+            a.part_ml[2 * to] = m - LIFT;
+            a.part_ml[2 * to + 1] = sum;
+        } else if (a.lse) {
+            a.lse[at] = sum == 0.0f ? -__builtin_inff() : (m - LIFT + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
         }
     }
 }
 
-template <int FK, int FV, int DB, int NK, int RT, int NW>
+template <int FK, int FV, int DB, int NK, int NW>
 hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
 {
     constexpr int lds = 2 * 64 * 32 * DB * 2 * (NK + 1) + NW * 2 * DB * 64 * 2;
@@ -506,12 +491,12 @@ hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     if (dev >= 64 || !done[dev]) {
-        e = hipFuncSetAttribute((const void*)attn_tile_kernel<FK, FV, DB, NK, RT, NW>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        e = hipFuncSetAttribute((const void*)attn_tile_kernel<FK, FV, DB, NK, NW>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
     const int64_t blocks = (int64_t)a.tiles * a.c.heads * a.pieces;
-    hipLaunchKernelGGL((attn_tile_kernel<FK, FV, DB, NK, RT, NW>), dim3((uint32_t)blocks), dim3(64 * NW), lds, s, a);
+    hipLaunchKernelGGL((attn_tile_kernel<FK, FV, DB, NK, NW>), dim3((uint32_t)blocks), dim3(64 * NW), lds, s, a);
     return hipGetLastError();
 }
 
@@ -519,10 +504,10 @@ template <int FK, int FV, int DB>
 hipError_t launch_attn_tile_db(const AttnArgs& a, hipStream_t s)
 {
     if constexpr (DB <= 4) {
-        if (a.tile_rows == 128) return a.c.type == QMM_F16 ? launch_attn_tile<FK, FV, DB, 2, 1, 4>(a, s) : launch_attn_tile<FK, FV, DB, 1, 1, 4>(a, s);
-        if (a.c.type == QMM_F16) return launch_attn_tile<FK, FV, DB, 2, 1, 8>(a, s);
+        if (a.tile_rows == 128) return a.c.type == QMM_F16 ? launch_attn_tile<FK, FV, DB, 2, 4>(a, s) : launch_attn_tile<FK, FV, DB, 1, 4>(a, s);
+        if (a.c.type == QMM_F16) return launch_attn_tile<FK, FV, DB, 2, 8>(a, s);
     }
-    return launch_attn_tile<FK, FV, DB, 1, 1, DB <= 4 ? 8 : 4>(a, s);
+    return launch_attn_tile<FK, FV, DB, 1, DB <= 4 ? 8 : 4>(a, s);
 }
 
 #define QMM_ATTN_TILE(P, FK, FV)                                         \
