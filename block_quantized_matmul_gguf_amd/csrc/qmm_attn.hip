@@ -113,8 +113,8 @@ int64_t plan_attention(AttnArgs& a, int64_t max_length)
         // eighth of empty rows: 384 rows 87 : 96, 600 rows of f16 and dim 96 38 : 42; nor bf16 of 64 dimensions, with
         // little to decode: 8192 rows 107 : 114.  f16 of 128 has one workgroup either way: 384 rows 168 : 129.
         auto padded = [&](int64_t tile) { return (rows + tile - 1) / tile * tile; };
-        const bool wide = c.dim <= 128 && (half ? c.dim == 128 || padded(256) * 8 <= padded(128) * 9
-                                                : c.dim > 64 && padded(256) * 8 <= padded(128) * 9);
+        const bool full = padded(256) * 8 <= padded(128) * 9;
+        const bool wide = half ? c.dim == 128 || full : c.dim > 64 && c.dim <= 128 && full;
         a.tile_rows = wide ? 256 : 128;
     }
     a.tile_shift = __builtin_ctz(a.tile_rows);
@@ -127,7 +127,7 @@ int64_t plan_attention(AttnArgs& a, int64_t max_length)
     // in one go, of four groups or more (a wave of the rows kernel has one then: one sequence of 4096 positions 11.6 us,
     // with eight groups 13.0).  Up to eight groups the second launch costs more than it gives (307 positions: 9.6 us
     // whole, 13.5 in two).
-    const bool one = a.many ? a.tile_rows == 256 || c.dim > 128 || (half && c.dim == 128) : c.dim > 128 || (c.type == QMM_F32 && c.dim == 128);
+    const bool one = a.many ? a.tile_rows == 256 || c.dim > 128 : c.dim > 128 || (c.type == QMM_F32 && c.dim == 128);
     const int64_t want = std::max<int64_t>(1, std::min<int64_t>((one ? 256 : 512) / workgroups(a.tile_rows), groups > 8 ? (groups + 3) / 4 : 1));
     a.piece_groups = (int)((groups + want - 1) / want);
     a.pieces = (int)((groups + a.piece_groups - 1) / a.piece_groups);

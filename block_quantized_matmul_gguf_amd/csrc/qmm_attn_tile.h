@@ -9,10 +9,17 @@
 //   O^T += V^T P^T  P^T straight from the registers that S^T left it in: row r of
 //                   an S^T tile is the token whose place in the values' order of
 //                   tokens fits the operand
-// Keys are code * d rounded to f16 once (NK == 1: bf16 queries, whose own
-// rounding is eight times that) or hi + lo, which is exact (f16 queries); values
-// code * d rounded to f16; both times a power of two per 64 tokens, so that
-// neither end of f16's range is met.
+// bf16 rows (NK == 1): keys are code * d rounded to f16, and so are p, which is an
+// eighth of the rounding that q had.  f16 rows (NK == 2): keys are hi + lo, which
+// is exact, and p is hi + lo, to 2^-22; with one part of each the output of 300
+// rows over 3500 positions is off by 3.5e-4 of its size, with two 2.6e-4.  Values
+// are code * d rounded to f16.  Keys and values are times a power of two per 64
+// tokens, so that neither end of f16's range is met.
+//
+// 2048 rows of 32 heads over 10240 positions, dim 128, bf16: 342 us, 904 TF/s (a
+// large library product reaches 1108 to 1390).  The matrix cores are busy 48% of
+// the cycles, at a clock that falls to 1.7 GHz under this load; the slots last as
+// long as a wave's softmax and decoding, not the other's products.
 #pragma once
 #include <type_traits>
 
@@ -269,9 +276,9 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
         for (int i = from; i < from + AHEAD; ++i) f[i % AHEAD] = operand(i);
         if (from == 0) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[half][i] = 0.0f;
+                for (int i = 0; i < 16; ++i) s[half][i] = 0.0f;
         }
 #pragma unroll
         for (int step = from / 4; step < ALL / 4; ++step) {
@@ -401,7 +408,9 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
                 for (int b = 0; b < DB; ++b) decode_key(smem, b);
             }
             fetch_keys(g_b, page_b, DO_K);
+            const bool first_odd = odd;  // (sv has lost them by now)
             prepare(g_b, g);
+            odd = first_odd;
             expo_b = k_expo;
             __syncthreads();
             for (int cur = 0;; cur ^= 1) {
@@ -425,9 +434,9 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
                 if (o_expo != v_expo) {
                     const float shift = ldexpf(1.0f, o_expo - v_expo);  // 0 the first time
 #pragma unroll
-                        for (int b = 0; b < DB; ++b)
+                    for (int b = 0; b < DB; ++b)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[b][i] *= shift;
+                        for (int i = 0; i < 16; ++i) o[b][i] *= shift;
                     o_expo = v_expo;
                 }
                 softmax(g, expo);
@@ -500,14 +509,19 @@ hipError_t launch_attn_tile(const AttnArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
+// (the sizes and types that the plan asks for)
 template <int FK, int FV, int DB>
 hipError_t launch_attn_tile_db(const AttnArgs& a, hipStream_t s)
 {
-    if constexpr (DB <= 4) {
-        if (a.tile_rows == 128) return a.c.type == QMM_F16 ? launch_attn_tile<FK, FV, DB, 2, 4>(a, s) : launch_attn_tile<FK, FV, DB, 1, 4>(a, s);
-        if (a.c.type == QMM_F16) return launch_attn_tile<FK, FV, DB, 2, 8>(a, s);
-    }
-    return launch_attn_tile<FK, FV, DB, 1, DB <= 4 ? 8 : 4>(a, s);
+    if constexpr (DB <= 4)
+        if (a.c.type == QMM_F16) {
+            if constexpr (DB < 4)
+                if (a.tile_rows == 128) return launch_attn_tile<FK, FV, DB, 2, 4>(a, s);
+            return launch_attn_tile<FK, FV, DB, 2, 8>(a, s);
+        }
+    if constexpr (DB == 3 || DB == 4)
+        if (a.tile_rows == 256) return launch_attn_tile<FK, FV, DB, 1, 8>(a, s);
+    return launch_attn_tile<FK, FV, DB, 1, 4>(a, s);
 }
 
 #define QMM_ATTN_TILE(P, FK, FV)                                         \

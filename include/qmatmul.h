@@ -455,8 +455,13 @@ int qmatmul_cache_load(const qmm_cache* cache, int64_t T, int type, void* k, voi
  * exp(score), by which results over parts of a sequence can be joined.  A row
  * that sees nothing has out 0 and lse -inf.
  * Scores and sums are f32; q enters as f16 parts (f32 as two: 2^-22 of the
- * row's largest), probabilities times value scales as f16 (f32: as two parts),
- * which leaves at most 2^-37 of the largest value in the cache per position.
+ * row's largest), and codes are exact.  Probabilities times value scales enter
+ * as f16 (f32: as two parts), off by at most 2^-37 of the largest value in the
+ * cache per position beside their rounding; where f16 or bf16 rows are many
+ * (some hundred, with work for the whole card) values are rounded to f16 and
+ * probabilities to f16 (f16 rows: as two parts), for bf16 rows also keys.  How
+ * the sums are cut depends on the sizes of the call, so that a row's last bits
+ * can differ between batches; the same call gives the same bits again.
  * A NaN or infinity in q, or a NaN in a key that a row sees, makes that row NaN;
  * a NaN in a value that a row sees makes the dimensions of its block NaN; what
  * a row does not see does not touch it.
