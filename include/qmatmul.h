@@ -434,8 +434,8 @@ typedef struct qmm_cache {
  * qmatmul_cache_store: the call's T rows of keys and values (device, `type`
  * QMM_F32, QMM_F16 or QMM_BF16, [T][heads][dim] with k_stride and v_stride
  * values from token to token) into the cache.  Bytes of other tokens keep their
- * values.  Where two rows of a call have the same place (two sequences that
- * share a page and both write it), the place holds codes of either.
+ * values.  Where two sequences of a call write into the same 64 neighbouring
+ * tokens of a page, each of those 64 holds codes of either or what it held.
  * qmatmul_cache_load: the rows read back, contiguous [T][heads][dim] of `type`,
  * each value rounded once; with lengths = starts[s + 1] - starts[s] these are
  * whole sequences.
