@@ -287,7 +287,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP <= 4 ? 2 : 1) void attn_ro
 
         float p[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) p[i] = 0.0f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP <= 4 ? 2 : 1) void attn_ro
                 // sums of one tile at a time: with all four in flight their parts and scales fill the registers (24
                 // to 120 of them were kept in memory).  Up to dim 128 they fit, and a wave that has them in flight
                 // is faster: 142 us against 180 us for 64 sequences.
-                    asm volatile("" : "+v"(p[4 * u]), "+v"(p[4 * u + 1]), "+v"(p[4 * u + 2]), "+v"(p[4 * u + 3]));
+                asm volatile("" : "+v"(p[4 * u]), "+v"(p[4 * u + 1]), "+v"(p[4 * u + 2]), "+v"(p[4 * u + 3]));
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -372,8 +372,8 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP <= 4 ? 2 : 1) void attn_ro
                     if constexpr (FV == FMT_Q8_0) v = codes8_q8(vr[b][4 * par + 2 * s], vr[b][4 * par + 2 * s + 1]);
                     else v = codes8_q4(vr[b][2 * par + s]);
 #pragma unroll
-                        for (int np = 0; np < NP; ++np)
-                            o[2 * b + par] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pv[np], o[2 * b + par], 0, 0, 0);
+                    for (int np = 0; np < NP; ++np)
+                        o[2 * b + par] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pv[np], o[2 * b + par], 0, 0, 0);
                 }
                 if (b % 2) __builtin_amdgcn_sched_barrier(0);
             }
