@@ -86,7 +86,6 @@ __device__ __forceinline__ int wave_prefix_sum(int v)
 __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int id, AttnTile& t)
 {
     const CacheArgs& c = a.c;
-    const int32_t base = c.starts[0];
     CacheSequence q;
     if (c.batch <= 64) {
         const int lane = (int)__lane_id(), s = min(lane, c.batch - 1);
@@ -100,6 +99,7 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int id, AttnTile& t
         q = {pick, __builtin_amdgcn_readlane(behind - count, pick), __builtin_amdgcn_readlane(n0, pick),
              __builtin_amdgcn_readlane(n1, pick), __builtin_amdgcn_readlane(length, pick)};
     } else {
+        const int32_t base = c.starts[0];
         q = cache_sequence(c, id, [&](int32_t start, int s) { return (int)(((int64_t)start - base) * a.per >> a.tile_shift) + s; });
     }
     const int64_t n0 = q.n0, n1 = q.n1;
