@@ -13,8 +13,8 @@ struct AttnArgs {
     const void* q;
     int64_t q_stride;
     int q_heads, per;  // query heads, and of them to one head of the cache
-    float scale;       // of the scores times log2(e); with a cap: 1 / cap of them
-    float cap;         // cap * log2(e), or 0
+    float scale;       // of the scores times log2(e)
+    float cap, ratio;  // cap * log2(e) and scale / cap, or 0
     int causal, window;
     void* out;
     float* lse;

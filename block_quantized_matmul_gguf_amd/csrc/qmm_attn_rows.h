@@ -87,6 +87,37 @@ QMM_DEV float rows_sum(float v)
     return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
 }
 
+// Capped scores: s becomes cap tanh(x) with x = ratio s, of which y = factor s is
+// the score itself, cap x.  Up to 1/2 as y (tanh x / x), an even polynomial with
+// the least relative error (fitted here, 2^-25.9), so that a score keeps its bits
+// however far the cap lies above it, also where x itself has none left; further
+// out, where tanh is 0.46 or more, by the exponential.  Off by 2^-21 of the result.
+// Mostly no score of a wave's 64 tokens is far out, and none pays for the
+// exponential then: 16 sequences of 1 to 5 rows, dim 256, a window of 1024, a cap of
+// 50, 23.9 us; with both forms for every score (the near one a quotient) 25.1 us.
+template <int N, class T>
+QMM_DEV void cap_scores(T& s, float ratio, float factor, float cap)
+{
+    constexpr float NEAR = 0.5f;
+    auto near = [&](float x, float y) {
+        const float u = x * x;
+        return y * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0x1.1a7c0cp-6f, -0x1.b28c76p-5f), 0x1.10e9fcp-3f), -0x1.5554d6p-2f), 1.0f);
+    };
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(s[i]));
+    if (!__any(most * fabsf(ratio) > NEAR)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = near(s[i] * ratio, s[i] * factor);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float x = s[i] * ratio, far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * x));
+            s[i] = fabsf(x) <= NEAR ? near(x, s[i] * factor) : cap * far;
+        }
+    }
+}
+
 // p s for two neighbours as f16, hi and (TWO) what hi lacks: hi + lo = p s to
 // 2^-22.  hi is fixed before lo is formed: the compiler may round p s to f16
 // once in one place and by way of f32 in another, and a lo of the other hi would
@@ -188,7 +219,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP <= 4 ? 2 : 1) void attn_ro
     // f16 rows enter as they are, others scaled by a power of two (exact)
     const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
     const float up = ldexpf(1.0f, e2);
-    const float factor = a.scale * ldexpf(1.0f, -e2);
+    const float factor = a.scale * ldexpf(1.0f, -e2), ratio = a.ratio * ldexpf(1.0f, -e2);
 #pragma unroll
     for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -312,14 +343,11 @@ __global__ __launch_bounds__(64 * ATTN_WAVES, DB * NP <= 4 ? 2 : 1) void attn_ro
 
         fetch_keys(ahead, ahead_page, ahead < g1);
         const bool masked = g * 64 < flo || g * 64 + 64 > fhi;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] *= factor;
         if (a.cap != 0.0f) {
+            cap_scores<16>(p, ratio, factor, a.cap);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if constexpr (NP == 2) p[i] = a.cap * tanhf(p[i]);
-                else p[i] = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.8853900817779268f * p[i])));
-            }
+            for (int i = 0; i < 16; ++i) p[i] *= factor;
         }
         if (masked) {
 #pragma unroll

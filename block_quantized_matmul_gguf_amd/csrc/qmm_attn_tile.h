@@ -133,7 +133,7 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
     }
     const int e2 = c.type == QMM_F16 || !fine ? 0 : split_exp(top);
     const float up = sign * ldexpf(1.0f, e2);
-    const float factor = fabsf(a.scale) * ldexpf(1.0f, -e2);
+    const float factor = fabsf(a.scale) * ldexpf(1.0f, -e2), ratio = fabsf(a.ratio) * ldexpf(1.0f, -e2);
 #pragma unroll
     for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
@@ -306,11 +306,8 @@ __global__ __launch_bounds__(64 * NW, DB <= 4 ? 2 : 1) void attn_tile_kernel(Att
         float f = fmaxf(factor * unit_k, 1e-37f);  // not 0: a hidden score stays -inf
         if (a.cap != 0.0f) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[half][i] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[half][i] * (2.8853900817779268f * f)));
-            f = a.cap;
+            for (int half = 0; half < 2; ++half) cap_scores<16>(s[half], ratio * unit_k, f, a.cap);
+            f = 1.0f;
         }
         if (masked) {
 #pragma unroll

@@ -536,8 +536,9 @@ extern "C" int qmatmul_cache_attention(const qmm_cache* cache, int64_t T, int64_
     AttnArgs a = attention_args(cache, T, q_heads, type, causal, window);
     a.q = q;
     a.q_stride = q_stride;
-    a.scale = softcap > 0.0f ? scale / softcap : scale * log2e;
+    a.scale = scale * log2e;
     a.cap = softcap * log2e;
+    a.ratio = softcap > 0.0f ? scale / softcap : 0.0f;
     a.out = out;
     a.lse = lse;
     const int64_t need = plan_attention(a, max_length);

@@ -449,7 +449,8 @@ int qmatmul_cache_load(const qmm_cache* cache, int64_t T, int type, void* k, voi
  * positions j that row n sees of c(scale * q[n][h] . k_j); query heads h to one
  * head of the cache: h / (q_heads / heads).  Row n at position p sees 0 <= j <
  * lengths[s]; causal: j <= p; window > 0 (causal only): j > p - window.  c is
- * the identity, or softcap * tanh(x / softcap) where softcap > 0.  q: device
+ * the identity, or softcap * tanh(x / softcap) where softcap > 0 (to 2^-20 of x,
+ * whatever the cap's size).  q: device
  * `type` [T][q_heads][dim], q_stride values from token to token; out: the same
  * type, contiguous.  lse: device f32 [T][q_heads] or NULL: ln of the sum of
  * exp(score), by which results over parts of a sequence can be joined.  A row
