@@ -100,7 +100,7 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int id, AttnTile& t
              __builtin_amdgcn_readlane(n1, pick), __builtin_amdgcn_readlane(length, pick)};
     } else {
         const int32_t base = c.starts[0];
-        q = cache_sequence(c, id, [&](int32_t start, int s) { return (int)(((int64_t)start - base) * a.per >> a.tile_shift) + s; });
+        q = cache_sequence(c, id, [&](int32_t start, int s) { return (int)(cache_start(c, start, base) * a.per >> a.tile_shift) + s; });
     }
     const int64_t n0 = q.n0, n1 = q.n1;
     if (n0 < 0 || n1 > c.T || n1 <= n0) return false;  // no rows, or starts that name rows that are not there

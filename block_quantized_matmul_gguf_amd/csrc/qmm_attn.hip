@@ -27,7 +27,24 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int lanes, i
     float top = none, sum = 0.0f;
     f32x4_t v = f32x4_t{0, 0, 0, 0};
     int pieces = 0;
-    const int64_t first = (int64_t)c.starts[0] * a.q_heads, behind = (int64_t)c.starts[c.batch] * a.q_heads;
+    int32_t n0 = c.starts[0], n1 = c.starts[c.batch];
+    if (n0 < 0 || n1 > c.T) {  // sequences with rows that are not there have no sums: from the first start at 0 or
+        int lo = 0, hi = c.batch;  // later to the last one that is at most T
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (c.starts[mid] < 0) lo = mid + 1;
+            else hi = mid;
+        }
+        n0 = c.starts[lo];
+        lo = 0, hi = c.batch;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (c.starts[mid] <= c.T) lo = mid;
+            else hi = mid - 1;
+        }
+        n1 = c.starts[lo];
+    }
+    const int64_t first = (int64_t)n0 * a.q_heads, behind = (int64_t)n1 * a.q_heads;
     if (row < all && d < c.dim && row >= first && row < behind) {  // others belong to no sequence
         pieces = min(a.part_n[row], a.pieces);
         if (pieces > 1)

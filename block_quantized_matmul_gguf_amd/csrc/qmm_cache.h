@@ -133,6 +133,15 @@ __device__ __forceinline__ uint32_t cache_page_of(const CacheArgs& c, uint32_t g
     return c.page_magic ? __umulhi(group, c.page_magic) : group;
 }
 
+// A start as the tile ids count it, from row 0 or the first sequence's: starts that
+// name rows which are not there (their sequences are left out) neither pass the ids
+// of the others nor 31 bits.
+__device__ __forceinline__ int64_t cache_start(const CacheArgs& c, int32_t start, int32_t base)
+{
+    const int64_t from = base > 0 ? base : 0, s = start > from ? start : from;
+    return (s < c.T ? s : c.T) - from;
+}
+
 // The sequence of tile `id`: the last s whose first(starts[s], s) is at or below
 // it, the same in every lane of the wave.  A step compares 64 sequences, so the
 // chain of dependent loads is one for up to 64 of them.  With it come the bounds

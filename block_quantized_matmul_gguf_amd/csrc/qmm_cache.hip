@@ -35,7 +35,7 @@ struct CacheTile {
 QMM_DEV bool cache_tile(const CacheArgs& c, int id, CacheTile& t)
 {
     const int32_t base = c.starts[0];
-    const CacheSequence q = cache_sequence(c, id, [&](int32_t start, int s) { return (int)(((int64_t)start - base) >> 6) + 2 * s; });
+    const CacheSequence q = cache_sequence(c, id, [&](int32_t start, int s) { return (int)(cache_start(c, start, base) >> 6) + 2 * s; });
     const int64_t n0 = q.n0, n1 = q.n1;
     if (n0 < 0 || n1 > c.T || n1 <= n0) return false;  // no rows, or starts that name rows that are not there
     const int64_t p0 = q.length - (n1 - n0);
