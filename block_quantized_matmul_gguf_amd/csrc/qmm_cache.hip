@@ -366,7 +366,8 @@ int check_cache(const qmm_cache* c, int64_t T, int type)
 }
 int check_pointers(const qmm_cache* c)
 {
-    if (!c->k || !c->v || !c->table || !c->starts || !c->lengths) return bad("null pointer");
+    // (no page is read without pages, no entry without columns: an empty tensor's pointer is null)
+    if (((!c->k || !c->v) && c->pages > 0) || (!c->table && c->table_width > 0) || !c->starts || !c->lengths) return bad("null pointer");
     if (off16(c->k) || off16(c->v)) return bad("the caches must be 16-byte aligned");
     if ((uintptr_t)c->table % 4 || (uintptr_t)c->starts % 4 || (uintptr_t)c->lengths % 4) return bad("table, starts and lengths must be 4-byte aligned");
     return QMM_OK;

@@ -422,10 +422,10 @@ typedef struct qmm_cache {
     int format_k, format_v;    /* QMM_Q8_0 or QMM_Q4_0 each */
     int64_t pages, page_size;  /* page_size: a multiple of 64, at most 8192 */
     int64_t heads, dim;        /* dim: 64, 96, 128 or 256 */
-    void* k;                   /* device, 16-byte aligned */
+    void* k;                   /* device, 16-byte aligned; NULL is fine for 0 pages */
     void* v;
     int64_t batch, table_width; /* batch <= 2^20, batch * heads <= 2^21, table_width * page_size < 2^31 */
-    const int32_t* table;      /* device [batch][table_width] */
+    const int32_t* table;      /* device [batch][table_width]; NULL is fine for 0 columns */
     const int32_t* starts;     /* device [batch + 1] */
     const int32_t* lengths;    /* device [batch] */
 } qmm_cache;
