@@ -759,7 +759,9 @@ def cache_attention(fmt_k: int, fmt_v: int, k_cache, v_cache, q, table, starts, 
     sqrt(dim) unless given.  Cache, table, starts and lengths as in
     ``cache_store``: one new token per sequence, many, or both side by side.
     max_length: a bound on lengths if known (0: what the table can hold), by which
-    the work is split.  Returns [T, q_heads, dim] in q's type; rows that see
+    the work is split (results are right under any, but one far above the lengths
+    costs time: 4096 positions 13 us, with a table of 131072 and no bound 25 us).
+    Returns [T, q_heads, dim] in q's type; rows that see
     nothing are zeros, rows of no sequence are not written.  lse: float32 [T,
     q_heads] to be filled with ln sum exp(score)."""
     torch = _torch()

@@ -460,15 +460,22 @@ int qmatmul_cache_load(const qmm_cache* cache, int64_t T, int type, void* k, voi
  * as f16 (f32: as two parts), off by at most 2^-37 of the largest value in the
  * cache per position beside their rounding; where f16 or bf16 rows are many
  * (some hundred, with work for the whole card) values are rounded to f16 and
- * probabilities to f16 (f16 rows: as two parts), for bf16 rows also keys.  How
- * the sums are cut depends on the sizes of the call, so that a row's last bits
+ * probabilities to f16 (f16 rows: as two parts), for bf16 rows also keys, and
+ * that end of f16 lies at 2^-30.  Outputs of f16 rows are off by 2.6e-4 of their
+ * size where rows are few and 2.2e-4 where they are many, 2.1e-4 of it their own
+ * rounding; of bf16 rows by 1.67e-3 and 1.72e-3 (1.66e-3).  Which of both a call
+ * takes and how its sums are cut depends on its sizes, so that a row's last bits
  * can differ between batches; the same call gives the same bits again.
  * A NaN or infinity in q, or a NaN in a key that a row sees, makes that row NaN;
  * a NaN in a value that a row sees makes the dimensions of its block NaN; what
  * a row does not see does not touch it.
  * max_length: at least the largest of lengths where the caller knows it (0:
  * table_width * page_size); it goes into how the work is split and the size of
- * the workspace; results are right also for longer sequences.
+ * the workspace; results are right also for longer sequences.  Work is split by
+ * this bound and by the batch's average rows, not by each length: one token over
+ * 4096 positions takes 13 us with the bound 4096 and 25 us with a table of 131072
+ * and no bound, and a long sequence among many short ones, or a prompt among
+ * single tokens, takes longer than in a call of its own.
  * Limits: q_heads a multiple of heads, at most 1024; T <= 2^24, T * q_heads <=
  * 2^25.  Outputs and ws must not overlap inputs or each other (QMM_EINVAL).
  */

@@ -10,9 +10,9 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import block_quantized_matmul_gguf_amd as qmm  # noqa: E402
-from attention_bounds import run_close  # noqa: E402
+from attention_bounds import bounds, run_close  # noqa: E402
 from exact_values import cancelling  # noqa: E402
-from test_gpu_attention import FMTS  # noqa: E402
+from test_gpu_attention import FMTS, check, gpu, largest, starts_of  # noqa: E402
 
 CODES = {"f32": qmm.F32, "f16": qmm.F16, "bf16": qmm.BF16}
 FORMATS = [("q8", "q8"), ("q4", "q4"), ("q8", "q4"), ("q4", "q8")]
@@ -72,3 +72,26 @@ def test_more_than_64_sequences(kw, fk, fv, dim, kernel, dtype, count, new, leng
     a = run_close(kernel, c, dtype, per, m, seed=351, **kw)
     b = run_close(kernel, c, dtype, per, m, seed=351, **kw)
     assert torch.equal(a[0].nan_to_num(7), b[0].nan_to_num(7)) and torch.equal(a[1].nan_to_num(7), b[1].nan_to_num(7))
+
+
+@pytest.mark.parametrize("kernel,dtype,lengths,new,heads,per", ROWS + MANY)
+@pytest.mark.parametrize("fk,fv", FORMATS)
+@pytest.mark.parametrize("low", [10.0, 16.0, 22.0])
+def test_small_probabilities_of_large_values(low, fk, fv, kernel, dtype, lengths, new, heads, per):
+    """Each row sees a token of value 0 and one of a large value whose probability is e^-low: what is left of it where
+    f16 ends, 2^-37 of the value in the rows kernel and 2^-30 in the one for many rows."""
+    dim = 64
+    c = ref.Cache(360, FMTS[fk], FMTS[fv], heads, dim, 64, lengths)
+    g = np.random.default_rng(361)
+    for s, n in enumerate(lengths):
+        large = (np.arange(n) % 2 == 1)[:, None, None]
+        c.k[s] = np.broadcast_to(np.where(large, -low * dim ** -0.5, 0.0), (n, heads, dim)).astype(np.float32)
+        c.v[s] = np.where(large, g.uniform(1e4, 4e4, (n, heads, dim)), 0.0).astype(np.float32)
+    c.write()
+    dt, st = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype], starts_of(new)
+    q = torch.ones((int(st[-1]), heads * per, dim), dtype=dt)
+    out = qmm.cache_attention(c.fmt_k, c.fmt_v, gpu(c.k_cache), gpu(c.v_cache), q.cuda(), gpu(c.table), gpu(st), gpu(c.lengths), window=2)
+    for s, n in enumerate(lengths):
+        rows, m = slice(st[s], st[s + 1]), new[s]
+        o, l, big, top = ref.attention(q[rows].double().numpy(), c.kq[s], c.vq[s], np.arange(n - m, n), dim ** -0.5, window=2)
+        check(out[rows], o, bounds(kernel, dt, dim, 2, big, top, largest(c.vq[s]), l)[0], f"out of sequence {s}")
