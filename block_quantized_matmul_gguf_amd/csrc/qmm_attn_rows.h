@@ -27,7 +27,7 @@
 // 34 us against 54 us, with 128 58 us against 82 us.)  The next group's codes are
 // on their way while one is computed.  Bound by the cache's bytes: one token of
 // each of 64 sequences of 8192 positions and less, 8 heads of the cache with four
-// each, dim 128, bf16, Q8_0: 674 MB in 144 to 148 us (4.6 TB/s; a copy reaches
+// each, dim 128, bf16, Q8_0: 674 MB in 144 to 151 us (4.6 TB/s; a copy reaches
 // 4.8); one sequence of 131 072 positions in Q4_0 37 us (4.1 TB/s).
 #pragma once
 #include "../../include/qmatmul.h"

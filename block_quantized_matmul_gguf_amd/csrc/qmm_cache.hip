@@ -20,7 +20,7 @@ namespace {
 // of a token (128 bytes or a multiple apart) lie in different LDS banks.
 // 6518 tokens of 8 x 128, bf16, to Q8_0 keys and Q4_0 values: 15 us (38 MB, 2.5
 // TB/s: half of the time the SIMDs issue instructions), back 10 us (3.6 TB/s);
-// 52 528 tokens from Q4_0 to f16: 61 us (276 MB, 4.5 TB/s; a copy reaches 4.8).
+// 52 528 tokens from Q4_0 to f16: 61 to 63 us (276 MB, 4.4 TB/s; a copy reaches 4.8).
 QMM_DEV int padded(int byte) { return byte + (byte >> 7) * 16; }
 
 // The rows of a call that lie in one group: tile ids of sequence s begin at
