@@ -1,5 +1,6 @@
 """Soft caps of any size: softcap * tanh(x / softcap) keeps x's relative accuracy
 however far the cap lies above the scores, and a cap out of their reach is none."""
+import numpy as np
 import pytest
 
 import cache_ref as ref
@@ -31,3 +32,16 @@ def test_scales_with_a_cap(scale, kernel, dtype, lengths, new, heads, per):
     c = ref.Cache(310, FMTS["q8"], FMTS["q4"], heads, 64, 64, lengths)
     for cap in (2.0, 1e8):
         run_close(kernel, c, dtype, per, new, seed=311, scale=scale, softcap=cap)
+
+
+@pytest.mark.parametrize("kernel,dtype,lengths,new,heads,per", ROWS + MANY)
+@pytest.mark.parametrize("cap", [3.0, 1e8])
+def test_what_is_not_finite_under_a_cap(cap, kernel, dtype, lengths, new, heads, per):
+    """A cap does not turn a NaN into a number, nor let a key or value touch a row that does not see it."""
+    c = ref.Cache(320, FMTS["q8"], FMTS["q8"], heads, 64, 64, lengths)
+    c.v[0][lengths[0] - 1, 0, 40] = np.nan
+    c.k[0][lengths[0] - 2, 1, 5] = np.inf
+    c.k[1][0, 0, 9] = np.nan
+    c.write()
+    out, _ = run_close(kernel, c, dtype, per, new, seed=321, window=30, softcap=cap)
+    assert torch.isnan(out).any() and not torch.isnan(out).all()
