@@ -413,7 +413,8 @@ int qmatmul_w4_run(int64_t N, int64_t K, int64_t M, int64_t group, int type, int
  * starts[s] + i of the call's tensors is its token at position lengths[s] -
  * (starts[s + 1] - starts[s]) + i.  starts must not decrease; rows before
  * starts[0] and from starts[batch] on belong to no sequence and are neither
- * read nor written, and so are those of a sequence that has rows outside 0..T - 1.  Position p lies in page table[s][p / page_size].  A
+ * read nor written, and neither are those of a sequence that has rows outside
+ * 0..T - 1.  Position p lies in page table[s][p / page_size].  A
  * position without a page (negative, past the table, or where the entry is not
  * in 0..pages - 1) holds nothing: it is not stored, reads back as zeros, and
  * attention does not see it.
